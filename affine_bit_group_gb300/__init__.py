@@ -1,6 +1,7 @@
 """Python binding of libabg.so: the GB300 affine 4-bit group-quantized
-matrix-vector product (q4mv), its activation producers (rmsq, swq, gsum) and
-the decode-token stage graph.
+matrix-vector product (q4mv), its activation producers (rmsq, swq, gsum), the
+decode-token stage graph, and the calls that check drafted tokens over a paged
+cache (page_plan, tree_plan, kv_put, tree_attn, tree_accept).
 
 This module only marshals arguments: tensors become device pointers, the
 current torch stream becomes a cudaStream_t, and status codes become
@@ -19,10 +20,14 @@ import threading
 __all__ = [
     "TREE", "FAST", "AbgError", "library", "q4mv", "q4mv_ex", "q4mm", "gsum", "rmsq", "swq", "StageGraph", "Node",
     "device_status", "set_q4mv_tuning", "MAX_COLS", "SB_F32", "SB_BF16", "SB_F16", "SB_TYPES", "swiglu_mlp_static",
+    "page_plan", "tree_plan", "kv_put", "tree_attn", "tree_attn_workspace", "tree_accept", "tree_accept_workspace",
+    "MAX_SPAN", "MAX_REQUESTS",
 ]
 
 TREE, FAST = 0, 1
 MAX_COLS = 16384
+MAX_SPAN = 256
+MAX_REQUESTS = 8192
 NODE_Q4MV, NODE_RMSQ, NODE_SWQ, NODE_GSUM, NODE_GDN, NODE_ATQ, NODE_COPY = 0, 1, 2, 3, 4, 5, 6
 PRO_NONE, PRO_GSUM, PRO_RMSQ, PRO_SWQ = 0, 1, 2, 3
 SB_F32, SB_BF16, SB_F16 = 0, 1, 2
@@ -77,6 +82,24 @@ class _AtqArgs(ctypes.Structure):
                [(f, ctypes.c_int64) for f in ("Hq", "Hkv", "D", "P", "pos")] + [("eps", ctypes.c_float)]
 
 
+class _KvPutArgs(ctypes.Structure):
+    """Mirror of struct abg_kv_put_args in include/abg.h."""
+    _fields_ = [(f, ctypes.c_void_p) for f in ("q", "k", "v")] + \
+               [(f, ctypes.c_int64) for f in ("q_row", "q_head", "k_row", "k_head", "v_row", "v_head")] + \
+               [(f, ctypes.c_void_p) for f in ("rows", "slots", "qn_w", "kn_w", "cos", "sin", "pos", "qo", "Kc", "Vc")] + \
+               [(f, ctypes.c_int64) for f in ("N", "src_rows", "Hq", "Hkv", "D", "page", "pages", "cos_rows")] + \
+               [("eps", ctypes.c_float), ("src_type", ctypes.c_int32), ("type", ctypes.c_int32)]
+
+
+class _TreeAttnArgs(ctypes.Structure):
+    """Mirror of struct abg_tree_attn_args in include/abg.h."""
+    _fields_ = [(f, ctypes.c_void_p) for f in ("q", "Kc", "Vc", "table", "lens", "cu", "Kd", "Vd", "mask", "gate", "y",
+                                               "ysum")] + \
+               [(f, ctypes.c_int64) for f in ("B", "N", "Hq", "Hkv", "D", "page", "pages", "width", "drafts", "words",
+                                              "max_span")] + \
+               [("type", ctypes.c_int32), ("y_type", ctypes.c_int32)]
+
+
 def library(build_if_missing: bool = True) -> ctypes.CDLL:
     """Loads libabg.so (building it with nvcc first if it is missing or stale)."""
     global _lib
@@ -110,6 +133,13 @@ def library(build_if_missing: bool = True) -> ctypes.CDLL:
             F = ctypes.c_float
             lib.abg_gdn.argtypes = [P, P, P, P, P, P, P, P, P, P, P, P, I64, I64, I64, F, F, I, P]
             lib.abg_atq.argtypes = [P, P, P, P, P, P, P, P, P, P, P, P, I64, I64, I64, I64, I64, F, I, P]
+            lib.abg_page_plan.argtypes = [P] * 13 + [I64] * 5 + [P]
+            lib.abg_tree_plan.argtypes = [P] * 5 + [I64] * 3 + [P]
+            lib.abg_kv_put.argtypes = [P, P]
+            lib.abg_tree_attn_workspace.argtypes = [I64, I64, I64, I64, I, ctypes.POINTER(I64)]
+            lib.abg_tree_attn.argtypes = [P, P, I64, P]
+            lib.abg_tree_accept_workspace.argtypes = [I64, I64, ctypes.POINTER(I64)]
+            lib.abg_tree_accept.argtypes = [P, I64] + [P] * 7 + [I64] * 3 + [P, I64, P]
             lib.abg_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), I]
             lib.abg_selftest_wait_timeout.argtypes = [P]
             lib.abg_set_q4mv_tuning.argtypes = [I, I, I, I]
@@ -121,7 +151,9 @@ def library(build_if_missing: bool = True) -> ctypes.CDLL:
                       "abg_swq_ex", "abg_stage_graph_create",
                       "abg_stage_graph_launch", "abg_stage_graph_launches", "abg_stage_graph_swiglu_pairs",
                       "abg_stage_graph_destroy", "abg_swiglu_mlp_static", "abg_gdn", "abg_atq",
-                      "abg_device_status", "abg_set_q4mv_tuning", "abg_selftest_wait_timeout"):
+                      "abg_device_status", "abg_set_q4mv_tuning", "abg_selftest_wait_timeout", "abg_page_plan",
+                      "abg_tree_plan", "abg_kv_put", "abg_tree_attn_workspace", "abg_tree_attn",
+                      "abg_tree_accept_workspace", "abg_tree_accept"):
                 getattr(lib, f).restype = ctypes.c_int
             _lib = lib
     return _lib
@@ -266,6 +298,188 @@ def atq(q, gate, k, v, qn_w, kn_w, cos, sin, Kc, Vc, y, ysum, pos: int, eps: flo
                            t.Hq, t.Hkv, t.D, t.P, t.pos, ctypes.c_float(eps), mode, _stream(stream))
     _check(st, "abg_atq")
     return y
+
+
+_TYPE_OF = None  # torch dtype -> abg_sb_type
+
+
+def _type_of(t, name):
+    global _TYPE_OF
+    if _TYPE_OF is None:
+        import torch
+        _TYPE_OF = {torch.float32: SB_F32, torch.bfloat16: SB_BF16, torch.float16: SB_F16}
+    if t.dtype not in _TYPE_OF:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
+    return _TYPE_OF[t.dtype]
+
+
+def _need(t, dtype, numel, name):
+    """Device pointer of a contiguous CUDA tensor of this dtype with at least numel elements."""
+    if not (t.is_cuda and t.dtype == dtype and t.is_contiguous() and t.numel() >= numel):
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of at least {numel} elements")
+    return t.data_ptr()
+
+
+def _strided(t, shape, dtype, name):
+    """Device pointer and the strides of the first two dimensions of a [rows][heads][D] CUDA tensor."""
+    if not (t.is_cuda and t.dtype == dtype and t.dim() == 3 and t.shape[1:] == shape and t.stride(2) == 1):
+        raise ValueError(f"{name} must be a {dtype} CUDA tensor [rows][{shape[0]}][{shape[1]}] with contiguous columns")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def _cache(Kc, Vc):
+    if Kc.dim() != 4 or Vc.shape != Kc.shape or Vc.dtype != Kc.dtype:
+        raise ValueError("the caches must be [pages][Hkv][page][D] tensors of one shape and type")
+    return _type_of(Kc, "Kc")
+
+
+def page_plan(lens, add, cu, held, ends, ring, table, page: int, slots, pos, lens_out, held_out, ends_out, info,
+              stream=None):
+    """Pages and cache slots of add[b] more tokens of each request b, which has
+    lens[b] tokens in held[b] pages; add[b] < 0 gives its pages back (see
+    abg_page_plan).  table [B][width] and ring are updated in place; slots, pos,
+    lens_out, held_out, ends_out and info are written.  slots and ends are
+    int64, everything else is int32."""
+    import torch
+    i32, i64 = torch.int32, torch.int64
+    B, N = lens.numel(), slots.numel()
+    width = table.numel() // max(1, B)
+    st = library().abg_page_plan(
+        _need(lens, i32, B, "lens"), _need(add, i32, B, "add"), _need(cu, i32, B + 1, "cu"),
+        _need(held, i32, B, "held"), _need(ends, i64, 2, "ends"), _need(ring, i32, 1, "ring"),
+        _need(table, i32, B * width, "table"), _need(slots, i64, N, "slots"), _need(pos, i32, N, "pos"),
+        _need(lens_out, i32, B, "lens_out"), _need(held_out, i32, B, "held_out"), _need(ends_out, i64, 2, "ends_out"),
+        _need(info, i32, 2, "info"), B, N, page, width, ring.numel(), _stream(stream))
+    _check(st, "abg_page_plan")
+    return slots, pos
+
+
+def tree_plan(parent, lens, cu, mask, pos, stream=None):
+    """Ancestor masks [N][words] (int64 bit words) and positions [N] of drafts
+    from their parents' indices (see abg_tree_plan)."""
+    import torch
+    i32 = torch.int32
+    B, N = lens.numel(), parent.numel()
+    if mask.dim() != 2 or mask.shape[0] != N:
+        raise ValueError("mask must be [N][words]")
+    st = library().abg_tree_plan(_need(parent, i32, N, "parent"), _need(lens, i32, B, "lens"),
+                                 _need(cu, i32, B + 1, "cu"), _need(mask, torch.int64, N, "mask"),
+                                 _need(pos, i32, N, "pos"), B, N, mask.shape[1], _stream(stream))
+    _check(st, "abg_tree_plan")
+    return mask, pos
+
+
+def kv_put(k, v, Kc, Vc, slots=None, rows=None, q=None, qo=None, qn_w=None, kn_w=None, cos=None, sin=None, pos=None,
+           eps: float = 1e-6, stream=None):
+    """Key and value rows k, v [rows][Hkv][D] (any strides over rows and heads)
+    into the caches Kc, Vc [pages][Hkv][page][D] (see abg_kv_put): token n's row
+    rows[n] (default n) to slot slots[n] (default n), k and q [rows][Hq][D] with
+    RMS norm (qn_w, kn_w [D]) and rotation (cos, sin [positions][D/2], pos [N])
+    where given; q goes to qo [N][Hq][D].  k, v and q are float32 or of the
+    caches' type."""
+    import torch
+    f32 = torch.float32
+    pages, Hkv, page, D = Kc.shape
+    ty = _cache(Kc, Vc)
+    N = rows.numel() if rows is not None else slots.numel() if slots is not None else k.shape[0]
+    a = _KvPutArgs(N=N, src_rows=min(k.shape[0], v.shape[0]), Hkv=Hkv, D=D, page=page, pages=pages, eps=eps,
+                   src_type=_type_of(k, "k"), type=ty)
+    a.k, a.k_row, a.k_head = _strided(k, (Hkv, D), k.dtype, "k")
+    a.v, a.v_row, a.v_head = _strided(v, (Hkv, D), k.dtype, "v")
+    a.Kc, a.Vc = _need(Kc, Kc.dtype, 0, "Kc"), _need(Vc, Kc.dtype, 0, "Vc")
+    if q is not None:
+        a.Hq = q.shape[1]
+        a.q, a.q_row, a.q_head = _strided(q, (a.Hq, D), k.dtype, "q")
+        a.src_rows = min(a.src_rows, q.shape[0])
+        a.qo = _need(qo, Kc.dtype, N * a.Hq * D, "qo")
+        if qn_w is not None:
+            a.qn_w = _need(qn_w, f32, D, "qn_w")
+    if rows is not None:
+        a.rows = _need(rows, torch.int32, N, "rows")
+    if slots is not None:
+        a.slots = _need(slots, torch.int64, N, "slots")
+    if kn_w is not None:
+        a.kn_w = _need(kn_w, f32, D, "kn_w")
+    if cos is not None:
+        a.cos_rows = cos.shape[0]
+        a.cos, a.sin = _need(cos, f32, a.cos_rows * (D // 2), "cos"), _need(sin, f32, a.cos_rows * (D // 2), "sin")
+        a.pos = _need(pos, torch.int32, N, "pos")
+    _check(library().abg_kv_put(ctypes.byref(a), _stream(stream)), "abg_kv_put")
+    return Kc, Vc
+
+
+def tree_attn_workspace(q, Kc, max_span: int) -> int:
+    """Bytes of tree_attn's workspace for queries and caches like these."""
+    n = ctypes.c_int64()
+    _check(library().abg_tree_attn_workspace(q.shape[1], Kc.shape[1], q.shape[2], max_span, _type_of(Kc, "Kc"),
+                                             ctypes.byref(n)), "abg_tree_attn_workspace")
+    return n.value
+
+
+def tree_attn(q, Kc, Vc, table, lens, cu, Kd, Vd, mask, y, max_span: int | None = None, gate=None, ysum=None, ws=None,
+              stream=None):
+    """Attention of the drafts q [N][Hq][D] over their requests' cached tokens
+    (Kc, Vc, table [B][width], lens) and over the drafts their masks [N][words]
+    name (Kd, Vd [Hkv][drafts][D]), into y [N][Hq][D] (the caches' type or
+    float32) and, with a float32 y, its 64-value group sums ysum (see
+    abg_tree_attn).  max_span defaults to the most that the masks can hold.  ws
+    is a uint8 tensor of tree_attn_workspace() bytes; by default the call takes
+    one from torch's allocator on the current stream (give ws for a call on
+    another stream)."""
+    import torch
+    i32, f32 = torch.int32, torch.float32
+    pages, Hkv, page, D = Kc.shape
+    ty = _cache(Kc, Vc)
+    dt = Kc.dtype
+    N, Hq = q.shape[0], q.shape[1]
+    B, words, drafts = lens.numel(), mask.shape[1], Kd.shape[1]
+    if max_span is None:
+        max_span = 64 * words
+    if ws is None:
+        ws = torch.empty(tree_attn_workspace(q, Kc, max_span), dtype=torch.uint8, device=q.device)
+    width = table.numel() // max(1, B)
+    a = _TreeAttnArgs(
+        _need(q, dt, N * Hq * D, "q"), _need(Kc, dt, 0, "Kc"), _need(Vc, dt, 0, "Vc"),
+        _need(table, i32, B * width, "table"), _need(lens, i32, B, "lens"), _need(cu, i32, B + 1, "cu"),
+        _need(Kd, dt, Hkv * drafts * D, "Kd"), _need(Vd, dt, Hkv * drafts * D, "Vd"),
+        _need(mask, torch.int64, N * words, "mask"), None if gate is None else _need(gate, f32, N * Hq * D, "gate"),
+        _need(y, y.dtype, N * Hq * D, "y"), None if ysum is None else _need(ysum, f32, N * Hq * D // 64, "ysum"),
+        B, N, Hq, Hkv, D, page, pages, width, drafts, words, max_span, ty, _type_of(y, "y"))
+    if q.dim() != 3 or q.shape[2] != D or Kd.dim() != 3 or Kd.shape[0] != Hkv or Vd.shape != Kd.shape:
+        raise ValueError("q must be [N][Hq][D], Kd and Vd [Hkv][drafts][D]")
+    _check(library().abg_tree_attn(ctypes.byref(a), _need(ws, torch.uint8, 0, "ws"), ws.numel(), _stream(stream)),
+           "abg_tree_attn")
+    return y
+
+
+def tree_accept_workspace(logits) -> int:
+    """Bytes of tree_accept's workspace for logits [N][V] like these."""
+    n = ctypes.c_int64()
+    _check(library().abg_tree_accept_workspace(logits.shape[0], logits.shape[1], ctypes.byref(n)),
+           "abg_tree_accept_workspace")
+    return n.value
+
+
+def tree_accept(logits, tok, parent, cu, best, rows, add, last, ws=None, stream=None):
+    """The greedy check of drafts against float32 logits [N][V] (any row
+    stride): best [N], the accepted rows of each request rows [N] and their
+    number add [B], and the next tokens last [B] (see abg_tree_accept); all
+    int32.  ws as in tree_attn."""
+    import torch
+    i32 = torch.int32
+    N, V = logits.shape
+    B = add.numel()
+    if not (logits.is_cuda and logits.dtype == torch.float32 and (V < 2 or logits.stride(1) == 1)):
+        raise ValueError("logits must be a float32 CUDA tensor [N][V] with contiguous rows")
+    if ws is None:
+        ws = torch.empty(tree_accept_workspace(logits), dtype=torch.uint8, device=logits.device)
+    st = library().abg_tree_accept(
+        logits.data_ptr(), logits.stride(0) if N > 1 else V, _need(tok, i32, N, "tok"),
+        _need(parent, i32, N, "parent"), _need(cu, i32, B + 1, "cu"), _need(best, i32, N, "best"),
+        _need(rows, i32, N, "rows"), _need(add, i32, B, "add"), _need(last, i32, B, "last"), B, N, V,
+        _need(ws, torch.uint8, 0, "ws"), ws.numel(), _stream(stream))
+    _check(st, "abg_tree_accept")
+    return rows, add, last
 
 
 def swiglu_mlp_static(gate, up, down, x, xsum, y, cols: int, mode: int = TREE, stream=None):

@@ -11,6 +11,7 @@
 // the one wait.
 #include "../../include/abg.h"
 #include "abg_kernels.cuh"
+#include "draft.cuh"
 #include "mixer.cuh"
 
 #include <algorithm>
@@ -491,6 +492,10 @@ bool pdl_enabled() {
 }
 
 }  // namespace
+
+namespace abg {
+abg_status cuda_status(cudaError_t e, const char *where) { return cuda_fail(e, where); }
+}  // namespace abg
 
 extern "C" {
 

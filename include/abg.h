@@ -485,6 +485,189 @@ abg_status abg_swiglu_mlp_static(const uint32_t *wg, const float *sg, const floa
                                  const float *x, const float *xsum, float *y,
                                  int64_t n, int64_t cols, int64_t rows, int mode, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Draft verification: several guessed tokens of each of B requests checked in
+ * one step, over a paged key/value cache.  The calls of a step, in order:
+ *
+ *   abg_page_plan    pages and cache slots of the tokens that enter the cache
+ *   abg_tree_plan    ancestor masks and positions of the drafts
+ *   abg_kv_put       q/k norm and rotation, k/v rows into the cache's layout
+ *   abg_tree_attn    attention of the drafts over the cache and one another
+ *   abg_tree_accept  the drafts that the logits agree with
+ *
+ * A request's drafts stay outside the cache, in rows of draft buffers, until
+ * they are accepted: a rejected draft costs no page and nothing is moved.  One
+ * draft a request is ordinary decoding; a prompt is tokens that enter the
+ * cache at once.
+ *
+ * Shared by these calls:
+ *   cu     i32 [B+1]  request b owns rows cu[b] .. cu[b+1]-1 of the N draft
+ *          rows (its span), draft i of it is row cu[b]+i; cu[0] = 0,
+ *          nondecreasing, cu[B] <= N.  Rows from cu[B] on are padding.
+ *   cache  [pages][Hkv][page][D] of f32, bf16 or f16 (an abg_sb_type), page >=
+ *          1 tokens a page; slot s is row s % page of page s / page.  A draft
+ *          buffer [Hkv][rows][D] is a cache of one page of `rows` tokens, and
+ *          the caches of abg_atq are one page of P tokens.
+ *   table  i32 [B][width]  page of tokens page*j .. page*j+page-1 of request b
+ * Lengths, spans, tables and slots are read on the GPU; what they name out of
+ * range is not touched (each call says what it does instead).  These calls
+ * have no mode: whole numbers are exact, kv_put's f32 results are those of
+ * abg_atq's steps bit for bit, tree_attn's are within the bounds given there
+ * and the same on every run.  None of them uses an atomic on global memory.
+ * ------------------------------------------------------------------------- */
+
+/* Largest span of a request, and largest number of mask words of a draft
+ * (64 drafts a word). */
+#define ABG_MAX_SPAN 256
+/* Largest B of abg_page_plan (its scan is held in shared memory). */
+#define ABG_MAX_REQUESTS 8192
+
+/*
+ * page_plan: request b, which has lens[b] tokens in the cache and held[b]
+ * pages in its table row, gets the pages and slots for add[b] more tokens, or
+ * gives its pages back (add[b] < 0).
+ *   Free pages are entries head .. tail-1 (taken modulo ring_len) of `ring`,
+ *   ends = {head, tail}.  need = ceil((lens + add) / page), extra = max(0,
+ *   need - held); requests take their extra pages from the head in request
+ *   order.  A request is granted if extra is 0 or the extras up to and
+ *   including its own fit in tail - head; it is refused if they do not, or if
+ *   add exceeds its span, need or held exceeds width, lens or held is
+ *   negative, or lens + add exceeds 2^31 - 1.  Pages given back go to the
+ *   tail in request order (none of them is granted in the same call); a
+ *   request whose held is out of range gives nothing back and counts as
+ *   refused.
+ *   table  in place: entries held .. need-1 of granted requests
+ *   ring   in place: entries from tail on, for pages given back
+ *   slots  i64 [N]  slot of token lens+i for i < add of granted requests, else -1
+ *   pos    i32 [N]  lens + i there, else 0
+ *   lens_out, held_out i32 [B], ends_out i64 [2]: the values for the next call
+ *          (refused: unchanged; given back: 0)
+ *   info   i32 [2]  pages taken, requests refused
+ * Integers only.  The call can be repeated: it reads nothing that it writes.
+ * 1 <= B <= ABG_MAX_REQUESTS, 0 <= N < 2^31, page, width, ring_len in 1 .. 2^31-1.
+ */
+abg_status abg_page_plan(const int32_t *lens, const int32_t *add, const int32_t *cu, const int32_t *held,
+                         const int64_t *ends, int32_t *ring, int32_t *table, int64_t *slots, int32_t *pos,
+                         int32_t *lens_out, int32_t *held_out, int64_t *ends_out, int32_t *info, int64_t B, int64_t N,
+                         int64_t page, int64_t width, int64_t ring_len, void *stream);
+
+/*
+ * tree_plan: each draft's ancestors and position from its parent.
+ *   parent i32 [N]  index of the parent among the request's drafts; -1 (or an
+ *          index that is no other draft of the request) for a root; below -1
+ *          for padding.  Any order; a cycle makes its members one another's
+ *          ancestors.
+ *   mask   u64 [N][words]  bit j: draft j of the request is the draft itself
+ *          or an ancestor of it (0 for padding)
+ *   pos    i32 [N]  lens[b] + the number of ancestors (0 for padding)
+ * 1 <= words <= 4.  Drafts from 64*words on in a span are padding, as are rows
+ * from cu[B] on.
+ */
+abg_status abg_tree_plan(const int32_t *parent, const int32_t *lens, const int32_t *cu, uint64_t *mask, int32_t *pos,
+                         int64_t B, int64_t N, int64_t words, void *stream);
+
+/*
+ * kv_put: key and value rows of N tokens into a cache, with abg_atq's RMS norm
+ * and rotation of q and k (each optional), rounded once to the cache's type.
+ *   k, v   source row i, head h at k + i*k_row + h*k_head (in elements), of
+ *          src_type (f32, or the cache's type)
+ *   rows   i32 [N] or null: token n reads source row rows[n] (null: n).  A
+ *          token whose row is outside 0 .. src_rows-1 is skipped.
+ *   slots  i64 [N] or null: token n goes to slot slots[n] (null: n).  A slot
+ *          outside 0 .. pages*page-1 is not written.
+ *   q, qo  q as k (q_row, q_head, Hq heads, src_type); qo [N][Hq][D] of the
+ *          cache's type; both null for none
+ *   qn_w, kn_w  f32 [D] or null: x <- (x * 1/sqrt(tree(x*x)/D + eps)) * w
+ *   cos, sin    f32 [cos_rows][D/2] or both null: rotation of the column
+ *          pairs (i, i + D/2) of q and k by row pos[n] (the rows are NaN where
+ *          pos[n] is outside 0 .. cos_rows-1)
+ *   pos    i32 [N], with cos and sin only
+ * D = 64, 128 or 256.  Two tokens of one slot leave either's row.  Rows, row
+ * strides and head strides are multiples of 16 bytes.
+ */
+typedef struct abg_kv_put_args {
+    const void *q, *k, *v;
+    int64_t q_row, q_head, k_row, k_head, v_row, v_head;
+    const int32_t *rows;
+    const int64_t *slots;
+    const float *qn_w, *kn_w, *cos, *sin;
+    const int32_t *pos;
+    void *qo, *Kc, *Vc;
+    int64_t N, src_rows, Hq, Hkv, D, page, pages, cos_rows;
+    float eps;
+    int32_t src_type, type;
+} abg_kv_put_args;
+abg_status abg_kv_put(const abg_kv_put_args *a, void *stream);
+
+/*
+ * tree_attn: attention of every draft over its request's cached tokens and
+ * over the drafts of its request that its mask names (query head h reads
+ * key/value head h / (Hq/Hkv)):
+ *   s_t = q.K_t / sqrt(D)  for the lens[b] cached tokens,
+ *   s_j = q.Kd_j / sqrt(D) for the drafts j whose bit is set,
+ *   y   = sum_t p_t V_t / sum_t p_t,  p = exp(s - max s),
+ * then, with a gate, y * 1/(1 + exp(-gate)).  A draft that sees no token (no
+ * cached token and an empty mask, or scores of -infinity only) gives 0.  What
+ * a draft does not see does not reach it, not a NaN either.
+ *   q      [N][Hq][D]   Kc, Vc  the cache   Kd, Vd [Hkv][drafts][D], drafts >=
+ *          N: draft row n's key and value; all of `type`
+ *   lens   i32 [B]  (at most width*page is used; a page outside 0 .. pages-1
+ *          reads as zeros)
+ *   mask   u64 [N][words], 1 <= words <= 4; drafts of a span from 64*words on
+ *          are neither attended to nor computed
+ *   gate   f32 [N][Hq][D] or null
+ *   y      [N][Hq][D] of y_type: `type` or f32
+ *   ysum   f32 [N][Hq*D/64] or null, with y_type f32 only: y's 64-value group
+ *          sums, for abg_q4mv's xsum
+ *   max_span  the largest span (1 .. 64*words): a hint that picks the tiling
+ *   ws     abg_tree_attn_workspace() bytes of device memory, for this call's
+ *          stream until it is done; its contents need not be kept or cleared
+ * Rows outside the spans are not written.
+ * Sums, softmax statistics and the work split's partial results are f32.  f32
+ * operands are multiplied in f32.  16-bit operands are multiplied exactly and
+ * the weights p are rounded to the operands' type before they meet V, so y
+ * carries about one more rounding of that type than the formula: relative to
+ * max_t |V_t|, 2^-8 (bf16) or 2^-11 (f16) at most, before y's own.
+ * D = 64, 128 or 256; Hq a multiple of Hkv; every matrix 16-byte aligned.
+ */
+typedef struct abg_tree_attn_args {
+    const void *q, *Kc, *Vc;
+    const int32_t *table, *lens, *cu;
+    const void *Kd, *Vd;
+    const uint64_t *mask;
+    const float *gate;
+    void *y;
+    float *ysum;
+    int64_t B, N, Hq, Hkv, D, page, pages, width, drafts, words, max_span;
+    int32_t type, y_type;
+} abg_tree_attn_args;
+/* Bytes of workspace; it depends on D, type, Hq/Hkv and max_span only (and on
+ * the device). */
+abg_status abg_tree_attn_workspace(int64_t Hq, int64_t Hkv, int64_t D, int64_t max_span, int type, int64_t *bytes);
+abg_status abg_tree_attn(const abg_tree_attn_args *a, void *ws, int64_t ws_bytes, void *stream);
+
+/*
+ * tree_accept: the greedy check of the drafts.  best[n] is the index of the
+ * largest of row n's V logits (the lowest such index; a NaN counts as
+ * -infinity).  Draft 0 of a request is its last known token and is accepted;
+ * from an accepted draft c the walk goes to the first later draft whose parent
+ * is c and whose token is best[c], until there is none.
+ *   logits f32, row n at logits + n*ld   tok, parent i32 [N] (as tree_plan's;
+ *          a child comes after its parent)
+ *   best   i32 [N]  (all N rows)
+ *   rows   i32 [N]  rows[cu[b]+i] = row of the i-th accepted draft of request
+ *          b (for abg_kv_put), -1 after the last and outside the spans
+ *   add    i32 [B]  number of accepted drafts (for abg_page_plan)
+ *   last   i32 [B]  best of the last accepted draft: the next token (-1 for an
+ *          empty span)
+ *   ws     abg_tree_accept_workspace() bytes, as tree_attn's
+ * Drafts from ABG_MAX_SPAN on in a span are not accepted.
+ */
+abg_status abg_tree_accept_workspace(int64_t N, int64_t V, int64_t *bytes);
+abg_status abg_tree_accept(const float *logits, int64_t ld, const int32_t *tok, const int32_t *parent,
+                           const int32_t *cu, int32_t *best, int32_t *rows, int32_t *add, int32_t *last, int64_t B,
+                           int64_t N, int64_t V, void *ws, int64_t ws_bytes, void *stream);
+
 const char *abg_status_str(int status);
 /* Text of the last CUDA error seen by any call on this thread ("" if none). */
 const char *abg_last_cuda_error(void);
