@@ -894,6 +894,7 @@ abg_status abg_device_status(uint32_t *bits, int clear) {
     if (e == cudaSuccess) e = vec_status(&v, clear != 0);
     if (e == cudaSuccess) e = q4mm_status(&v, clear != 0);
     if (e == cudaSuccess) e = mixer_status(&v, clear != 0);
+    if (e == cudaSuccess) e = tree_attn16_status(&v, clear != 0);
     if (e != cudaSuccess) return cuda_fail(e);
     *bits = v;
     return (v & 1u) ? ABG_ETIMEOUT : ABG_OK;  // bit 0: a bounded wait timed out

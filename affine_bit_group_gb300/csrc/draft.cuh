@@ -64,6 +64,9 @@ cudaError_t launch_tree_accept(const float *logits, int64_t ld, const int32_t *t
 size_t tree_attn_bytes(int Hq, int Hkv, int D, int max_span, int type);
 cudaError_t launch_tree_attn(const abg_tree_attn_args &a, void *ws, cudaStream_t stream);
 
+// the 16-bit kernel's device status word (OR-ed into *bits)
+cudaError_t tree_attn16_status(unsigned *bits, bool clear);
+
 // Records e as the calling thread's last CUDA error (api.cu) and returns the
 // call's status.
 abg_status cuda_status(cudaError_t e, const char *where);

@@ -149,7 +149,7 @@ abg_status abg_tree_attn(const abg_tree_attn_args *args, void *ws, int64_t ws_by
     if (a.ysum && a.y_type != ABG_SB_F32) return ABG_EINVAL;
     if (a.words < 1 || a.words > ABG_MAX_SPAN / 64 || a.B < 1 || a.B > kMax32 - 1 || a.N < 0 || a.N > kMax32 ||
         a.page < 1 || a.page > kMax32 || a.pages < 0 || a.pages > kMax32 || a.width < 0 || a.width > kMax32 ||
-        !bounded({a.B, a.width, 4}) || !bounded({a.width, a.page, 2}) || a.width * a.page > kMax32 || a.drafts < a.N || a.drafts > kMax32 ||
+        !bounded({a.pages, a.Hkv}) || a.pages * a.Hkv > kMax32 || !bounded({a.B, a.width, 4}) || !bounded({a.width, a.page, 2}) || a.width * a.page > kMax32 || a.drafts < a.N || a.drafts > kMax32 ||
         a.max_span > 64 * a.words || !bounded({a.pages, a.page, a.Hkv, a.D, 4}) ||
         !bounded({a.drafts, a.Hq, a.D, 4}))
         return ABG_ESHAPE;

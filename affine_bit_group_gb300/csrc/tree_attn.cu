@@ -1,9 +1,13 @@
 // tree_attn: attention of drafted tokens over a paged cache and one another
-// (formulas in include/abg.h, the work split in tree_attn.cuh).
+// (formulas in include/abg.h, the work split in tree_attn.cuh).  This file holds
+// the f32 kernel, whose products are f32 on the CUDA cores: the tensor cores
+// would round its operands.
 #include "abg_kernels.cuh"
 #include "tree_attn.cuh"
+#include "tree_attn16.cuh"
 
 #include <algorithm>
+#include <cmath>
 
 namespace abg {
 
@@ -14,18 +18,6 @@ constexpr int kKT = 64;  // tokens a tile
 
 // Rows of one query tile: 16 where a request has no more, else 64.
 constexpr int kFewRows = 16, kManyRows = 64;
-
-template <typename T>
-__device__ __forceinline__ float4 widen4(const T *p) {
-    if constexpr (sizeof(T) == 4) {
-        return *reinterpret_cast<const float4 *>(p);
-    } else {
-        alignas(8) T t[4];
-        *reinterpret_cast<uint2 *>(t) = *reinterpret_cast<const uint2 *>(p);
-        return make_float4(static_cast<float>(t[0]), static_cast<float>(t[1]), static_cast<float>(t[2]),
-                           static_cast<float>(t[3]));
-    }
-}
 
 __device__ __forceinline__ void cp16(void *dst, const void *src, bool real) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(real ? 16 : 0)
@@ -68,16 +60,12 @@ __device__ __forceinline__ int64_t row_offset(const abg_tree_attn_args &a, const
     return key < s.req.T ? (s.h * a.drafts + s.req.n0 + key) * static_cast<int64_t>(D) : -1;
 }
 
-template <typename T, int D>
-__device__ __forceinline__ void load_tile(float *dst, int ld, const T *src, const int64_t *off) {
+template <int D>
+__device__ __forceinline__ void load_tile(float *dst, int ld, const float *src, const int64_t *off) {
     for (int i = threadIdx.x; i < kKT * (D / 4); i += kThreads) {
         const int r = i / (D / 4), c = 4 * (i % (D / 4));
         const int64_t o = off[r];
-        if constexpr (sizeof(T) == 4) {
-            cp16(dst + r * ld + c, src + max(o, int64_t(0)) + c, o >= 0);
-        } else {
-            *reinterpret_cast<float4 *>(dst + r * ld + c) = o >= 0 ? widen4(src + o + c) : make_float4(0, 0, 0, 0);
-        }
+        cp16(dst + r * ld + c, src + max(o, int64_t(0)) + c, o >= 0);
     }
     cp_commit();
 }
@@ -85,7 +73,7 @@ __device__ __forceinline__ void load_tile(float *dst, int ld, const T *src, cons
 // One part of the work line.  Thread (ty, tx) = (tid / 16, tid % 16) holds the
 // scores of kRPS rows and tokens tx + 16 j; for the sums, a thread holds four
 // columns of kRPO rows over every kKS-th token.
-template <typename T, int D, int kRT>
+template <int D, int kRT>
 __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ AttnArgs p) {
     using S = Smem<D, kRT>;
     extern __shared__ __align__(16) unsigned char raw[];
@@ -104,27 +92,28 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
     AttnSplit split{};
     AttnSeg s;
     while (line.next(p, s)) {
-        const T *kt, *vt;
+        const float *kt, *vt;
         auto source = [&](int t) {
             const bool cache = t < s.ctiles;
-            kt = static_cast<const T *>(cache ? a.Kc : a.Kd);
-            vt = static_cast<const T *>(cache ? a.Vc : a.Vd);
+            kt = static_cast<const float *>(cache ? a.Kc : a.Kd);
+            vt = static_cast<const float *>(cache ? a.Vc : a.Vd);
         };
         __syncthreads();  // the last stretch's shared memory is done with
         for (int i = tid; i < kRT * (D / 4); i += kThreads) {
             const int r = i / (D / 4), c = 4 * (i % (D / 4)), row = s.r0 + r;
             float4 v = make_float4(0, 0, 0, 0);
             if (r < s.rows)
-                v = widen4(static_cast<const T *>(a.q) +
-                           ((static_cast<int64_t>(s.req.n0) + row / p.G) * a.Hq + s.h * p.G + row % p.G) * D + c);
+                v = *reinterpret_cast<const float4 *>(
+                    static_cast<const float *>(a.q) +
+                    ((static_cast<int64_t>(s.req.n0) + row / p.G) * a.Hq + s.h * p.G + row % p.G) * D + c);
             *reinterpret_cast<float4 *>(&sm.q[r][c]) = v;
         }
         if (tid < ABG_MAX_SPAN / 32) sm.bad[tid] = 0;
         if (tid < kKT) sm.off[s.t0 & 1][tid] = row_offset<D>(a, s, s.t0, tid);
         __syncthreads();
         source(s.t0);
-        load_tile<T, D>(&sm.k[0][0], S::kLd, kt, sm.off[s.t0 & 1]);
-        load_tile<T, D>(&sm.v[0][0], D, vt, sm.off[s.t0 & 1]);
+        load_tile<D>(&sm.k[0][0], S::kLd, kt, sm.off[s.t0 & 1]);
+        load_tile<D>(&sm.v[0][0], D, vt, sm.off[s.t0 & 1]);
         float m[kRPS], l[kRPS], o[kRPO][4];
 #pragma unroll
         for (int i = 0; i < kRPS; ++i) m[i] = -INFINITY, l[i] = 0.0f;
@@ -183,7 +172,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
             }
             if (more) {
                 source(t + 1);
-                load_tile<T, D>(&sm.k[0][0], S::kLd, kt, sm.off[(t + 1) & 1]);
+                load_tile<D>(&sm.k[0][0], S::kLd, kt, sm.off[(t + 1) & 1]);
             } else {
                 cp_commit();
             }
@@ -260,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
             }
             __syncthreads();
             if (more) {
-                load_tile<T, D>(&sm.v[0][0], D, vt, sm.off[(t + 1) & 1]);
+                load_tile<D>(&sm.v[0][0], D, vt, sm.off[(t + 1) & 1]);
             } else {
                 cp_commit();
             }
@@ -295,15 +284,15 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
             const int64_t n = static_cast<int64_t>(s.req.n0) + (s.r0 + r) / p.G;
             for (int k = 0; k < s.req.T; ++k)
                 if (sm.bad[k >> 5] >> (k & 31) & 1 && attn_sees(a.mask + n * a.words, k)) {
-                    const T *row = static_cast<const T *>(a.Vd) + (s.h * a.drafts + s.req.n0 + k) * static_cast<int64_t>(D);
+                    const float *row = static_cast<const float *>(a.Vd) + (s.h * a.drafts + s.req.n0 + k) * static_cast<int64_t>(D);
 #pragma unroll
                     for (int i = 0; i < E; ++i) {
-                        const float x = static_cast<float>(row[lane * E + i]);
+                        const float x = row[lane * E + i];
                         if (!(fabsf(x) < INFINITY)) v[i] += x;
                     }
                 }
             if (whole) {
-                attn_finish<T, D>(a, n, s.h * p.G + (s.r0 + r) % p.G, v, sm.l[r]);
+                attn_finish<float, D>(a, n, s.h * p.G + (s.r0 + r) % p.G, v, sm.l[r]);
             } else {
                 float *po = p.part_o + (slot * kRT + r) * D + lane * E;
 #pragma unroll
@@ -319,13 +308,13 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
 
 int row_tile(int64_t G, int64_t max_span) { return G * max_span <= kFewRows ? kFewRows : kManyRows; }
 
-template <typename T, int D, int kRT>
+template <int D, int kRT>
 int grid_of() {
     static const int blocks = [] {
         int per = 0;
-        if (cudaFuncSetAttribute(attn_kernel<T, D, kRT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(attn_kernel<D, kRT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  sizeof(Smem<D, kRT>)) != cudaSuccess ||
-            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, attn_kernel<T, D, kRT>, kThreads,
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, attn_kernel<D, kRT>, kThreads,
                                                           sizeof(Smem<D, kRT>)) != cudaSuccess)
             per = 1;
         return std::max(1, per) * sm_count();
@@ -333,57 +322,35 @@ int grid_of() {
     return blocks;
 }
 
-template <typename T, int D, int kRT>
+template <int D, int kRT>
 cudaError_t go(AttnArgs p, void *ws, cudaStream_t stream) {
-    const int C = grid_of<T, D, kRT>();
+    const int C = grid_of<D, kRT>();
     const AttnLayout l = attn_layout(C, kRT, D);
     unsigned char *w = static_cast<unsigned char *>(ws);
     p.part_o = reinterpret_cast<float *>(w + l.o);
     p.part_ml = reinterpret_cast<float2 *>(w + l.ml);
     p.split = reinterpret_cast<AttnSplit *>(w + l.split);
     const cudaError_t e =
-        launch_kernel(attn_kernel<T, D, kRT>, dim3(C), dim3(kThreads), sizeof(Smem<D, kRT>), stream, false, p);
+        launch_kernel(attn_kernel<D, kRT>, dim3(C), dim3(kThreads), sizeof(Smem<D, kRT>), stream, false, p);
     if (e != cudaSuccess) return e;
-    return launch_kernel(attn_join_kernel<T, D, kRT>, dim3(C, kRT / 8), dim3(256), 0, stream, true, p);
+    return launch_kernel(attn_join_kernel<float, D, kRT>, dim3(C, kRT / 8), dim3(256), 0, stream, true, p);
 }
 
-// calls f.template operator()<T, D, kRT>()
-template <typename F>
-auto pick(int type, int D, int rt, F f) {
-    auto by_rows = [&](auto t, auto d) {
-        using T = decltype(t);
-        constexpr int kD = decltype(d)::value;
-        return rt == kFewRows ? f.template operator()<T, kD, kFewRows>() : f.template operator()<T, kD, kManyRows>();
-    };
-    auto by_width = [&](auto t) {
-        return D == 64    ? by_rows(t, std::integral_constant<int, 64>{})
-               : D == 128 ? by_rows(t, std::integral_constant<int, 128>{})
-                          : by_rows(t, std::integral_constant<int, 256>{});
-    };
-    return type == ABG_SB_F32 ? by_width(0.0f) : type == ABG_SB_BF16 ? by_width(__nv_bfloat16{}) : by_width(__half{});
+template <int D>
+size_t bytes_of(int rt) {
+    return attn_layout(rt == kFewRows ? grid_of<D, kFewRows>() : grid_of<D, kManyRows>(), rt, D).total;
 }
-
-struct GridOf {
-    template <typename T, int D, int kRT>
-    int operator()() const {
-        return grid_of<T, D, kRT>();
-    }
-};
-struct Go {
-    AttnArgs p;
-    void *ws;
-    cudaStream_t stream;
-    template <typename T, int D, int kRT>
-    cudaError_t operator()() const {
-        return go<T, D, kRT>(p, ws, stream);
-    }
-};
+template <int D>
+cudaError_t go_rows(const AttnArgs &p, int rt, void *ws, cudaStream_t stream) {
+    return rt == kFewRows ? go<D, kFewRows>(p, ws, stream) : go<D, kManyRows>(p, ws, stream);
+}
 
 }  // namespace
 
 size_t tree_attn_bytes(int Hq, int Hkv, int D, int max_span, int type) {
+    if (type != ABG_SB_F32) return tree_attn16_bytes(D);
     const int rt = row_tile(Hq / Hkv, max_span);
-    return attn_layout(pick(type, D, rt, GridOf{}), rt, D).total;
+    return D == 64 ? bytes_of<64>(rt) : D == 128 ? bytes_of<128>(rt) : bytes_of<256>(rt);
 }
 
 cudaError_t launch_tree_attn(const abg_tree_attn_args &a, void *ws, cudaStream_t stream) {
@@ -391,7 +358,11 @@ cudaError_t launch_tree_attn(const abg_tree_attn_args &a, void *ws, cudaStream_t
     p.a = a;
     p.G = static_cast<int>(a.Hq / a.Hkv);
     p.scale2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(a.D)));
-    return pick(a.type, static_cast<int>(a.D), row_tile(p.G, a.max_span), Go{p, ws, stream});
+    if (a.type != ABG_SB_F32) return launch_tree_attn16(p, ws, stream);
+    const int rt = row_tile(p.G, a.max_span);
+    return a.D == 64    ? go_rows<64>(p, rt, ws, stream)
+           : a.D == 128 ? go_rows<128>(p, rt, ws, stream)
+                        : go_rows<256>(p, rt, ws, stream);
 }
 
 }  // namespace abg

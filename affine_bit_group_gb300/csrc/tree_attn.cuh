@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
         const float *po = p.part_o + at * D + lane * E;
         L += ml.y * w;
 #pragma unroll
-        for (int i = 0; i < E; ++i) o[i] += po[i] * w;
+        for (int i = 0; i < E; ++i) o[i] += ml.y == 0.0f ? 0.0f : po[i] * w;
     }
     const int row = s.r0 + r;
     attn_finish<T, D>(p.a, static_cast<int64_t>(s.n0) + row / p.G, s.h * p.G + row % p.G, o, L);

@@ -1,0 +1,11 @@
+// Host launcher of the 16-bit tree_attn kernel (tree_attn16.cu).
+#pragma once
+
+#include "tree_attn.cuh"
+
+namespace abg {
+
+size_t tree_attn16_bytes(int D);
+cudaError_t launch_tree_attn16(const AttnArgs &p, void *ws, cudaStream_t stream);
+
+}  // namespace abg

@@ -422,7 +422,8 @@ abg_status abg_stage_graph_destroy(void *graph);
 /* Reads (and, if clear != 0, resets) the device status word on the current
  * device: bit 0 = a device-side wait timed out; bits 4.. name the wait that
  * gave up (16: a stage's release, 32: a stage's arrival, 64: the partial sums
- * of a tile, 128: a final drain of copies).  Synchronizes the device.
+ * of a tile, 128: a final drain of copies, 256: a wait of the 16-bit
+ * abg_tree_attn kernel).  Synchronizes the device.
  * Returns ABG_ETIMEOUT when bit 0 was set, else ABG_OK. */
 abg_status abg_device_status(uint32_t *bits, int clear);
 
@@ -628,7 +629,8 @@ abg_status abg_kv_put(const abg_kv_put_args *a, void *stream);
  * the weights p are rounded to the operands' type before they meet V, so y
  * carries about one more rounding of that type than the formula: relative to
  * max_t |V_t|, 2^-8 (bf16) or 2^-11 (f16) at most, before y's own.
- * D = 64, 128 or 256; Hq a multiple of Hkv; every matrix 16-byte aligned.
+ * D = 64, 128 or 256; Hq a multiple of Hkv; pages*Hkv and width*page below 2^31;
+ * every matrix 16-byte aligned.
  */
 typedef struct abg_tree_attn_args {
     const void *q, *Kc, *Vc;
