@@ -42,6 +42,7 @@ struct Smem {
     float corr[kRT];
     int64_t off[2][kKT];                 // a tile's row offsets in elements (-1: none)
     float m[kRT], l[kRT];
+    AttnScan scan;
     uint32_t bad[ABG_MAX_SPAN / 32];     // drafts whose V holds an infinity or a NaN
 };
 
@@ -88,7 +89,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
     grid_dep_wait();
     grid_dep_launch();
     AttnLine<kRT, kKT> line;
-    line.template init<kThreads>(p, blockIdx.x, gridDim.x);
+    line.template init<kThreads>(p, blockIdx.x, gridDim.x, sm.scan);
     AttnSplit split{};
     AttnSeg s;
     while (line.next(p, s)) {
@@ -317,7 +318,7 @@ int grid_of() {
             cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, attn_kernel<D, kRT>, kThreads,
                                                           sizeof(Smem<D, kRT>)) != cudaSuccess)
             per = 1;
-        return std::max(1, per) * sm_count();
+        return std::min(std::max(1, per) * sm_count(), kJoinMax);
     }();
     return blocks;
 }
@@ -333,7 +334,8 @@ cudaError_t go(AttnArgs p, void *ws, cudaStream_t stream) {
     const cudaError_t e =
         launch_kernel(attn_kernel<D, kRT>, dim3(C), dim3(kThreads), sizeof(Smem<D, kRT>), stream, false, p);
     if (e != cudaSuccess) return e;
-    return launch_kernel(attn_join_kernel<float, D, kRT>, dim3(C, kRT / 8), dim3(256), 0, stream, true, p);
+    return launch_kernel(attn_join_kernel<float, D, kRT, false>, dim3(kJoinBlocksPerSm * sm_count()),
+                         dim3(32 * kJoinWarps), 0, stream, true, p, C);
 }
 
 template <int D>

@@ -37,7 +37,7 @@ struct AttnArgs {
     float scale2;  // log2(e) / sqrt(D): scores are kept in base 2
     // workspace: per block two pieces (0: of a unit begun earlier, 1: of a
     // unit that goes on) of kRT rows
-    float *part_o;    // [C][2][kRT][D]
+    float *part_o;    // [C][2] pieces of kRT * D (attn_piece_at)
     float2 *part_ml;  // [C][2][kRT]  (maximum, weight sum)
     AttnSplit *split;  // [C]
 };
@@ -82,6 +82,12 @@ struct AttnSeg {
     int64_t unit;            // the unit's place on the line
 };
 
+// Shared memory of AttnLine::init.
+struct AttnScan {
+    int64_t w[32], ex;
+    int b;
+};
+
 // A block's part of the line; every thread holds the same values.
 template <int kRT, int kKT>
 struct AttnLine {
@@ -91,10 +97,7 @@ struct AttnLine {
     // By a whole block of kThreads threads: part c of the line.  Blocks get at
     // least two tiles each, so that a short call is not all joining.
     template <int kThreads>
-    __device__ void init(const AttnArgs &p, int c, int grid) {
-        __shared__ int64_t s_w[kThreads / 32];
-        __shared__ int64_t s_ex;
-        __shared__ int s_b;
+    __device__ void init(const AttnArgs &p, int c, int grid, AttnScan &sm) {
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
         const int B = static_cast<int>(p.a.B);
         const int64_t w0 = tid < B ? attn_weight<kRT, kKT>(p, attn_req(p.a, tid)) : 0;
@@ -102,12 +105,12 @@ struct AttnLine {
         for (int i = kThreads + tid; i < B; i += kThreads) sum += attn_weight<kRT, kKT>(p, attn_req(p.a, i));
 #pragma unroll
         for (int d = 16; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (lane == 0) s_w[warp] = sum;
-        if (tid == 0) s_b = B;
+        if (lane == 0) sm.w[warp] = sum;
+        if (tid == 0) sm.b = B;
         __syncthreads();
         W = 0;
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) W += s_w[w];
+        for (int w = 0; w < kThreads / 32; ++w) W += sm.w[w];
         C = static_cast<int>(min(static_cast<int64_t>(grid), max(int64_t(1), W / 2)));
         cur = c < C ? W * c / C : W;
         end = c < C ? W * (c + 1) / C : W;
@@ -124,22 +127,22 @@ struct AttnLine {
                 const int64_t u = __shfl_up_sync(0xffffffffu, x, d);
                 if (lane >= d) x += u;
             }
-            __syncthreads();  // s_w's last readers are done
-            if (lane == 31) s_w[warp] = x;
+            __syncthreads();  // sm.w's last readers are done
+            if (lane == 31) sm.w[warp] = x;
             __syncthreads();
             int64_t all = 0;
 #pragma unroll
             for (int v = 0; v < kThreads / 32; ++v) {
                 if (v == warp) x += before + all;
-                all += s_w[v];
+                all += sm.w[v];
             }
             before += all;
-            if (i < B && x - w <= cur && cur < x) s_b = i, s_ex = x - w;
+            if (i < B && x - w <= cur && cur < x) sm.b = i, sm.ex = x - w;
             __syncthreads();
-            if (s_b < B) break;
+            if (sm.b < B) break;
         }
-        b = s_b;
-        ex = s_ex;
+        b = sm.b;
+        ex = sm.ex;
     }
 
     // The next stretch (false: the part is done).
@@ -218,36 +221,120 @@ __device__ __forceinline__ void attn_finish(const abg_tree_attn_args &a, int64_t
     }
 }
 
-// Joins the pieces of split units: a block a (unit, 8 rows), a warp a row.
-template <typename T, int D, int kRT>
-__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnArgs p) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31, c = blockIdx.x;
-    const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
-    grid_dep_wait();
-    const AttnSplit s = p.split[c];
-    if (r >= s.rows) return;
-    // piece k of the unit: block c's second piece, then the first pieces of c+1 .. last
-    const int pieces = s.last - c + 1;
-    float M = -INFINITY;
-    for (int k = lane; k < pieces; k += 32)
-        M = fmaxf(M, p.part_ml[(static_cast<int64_t>(2) * (c + k) + (k == 0)) * kRT + r].x);
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-    if (M == -INFINITY) M = 0.0f;
-    float o[E] = {}, L = 0.0f;
-#pragma unroll 4
-    for (int k = 0; k < pieces; ++k) {
-        const int64_t at = (static_cast<int64_t>(2) * (c + k) + (k == 0)) * kRT + r;
-        const float2 ml = p.part_ml[at];
-        const float w = exp2f(ml.x - M);
-        const float *po = p.part_o + at * D + lane * E;
-        L += ml.y * w;
-#pragma unroll
-        for (int i = 0; i < E; ++i) o[i] += ml.y == 0.0f ? 0.0f : po[i] * w;
-    }
-    const int row = s.r0 + r;
-    attn_finish<T, D>(p.a, static_cast<int64_t>(s.n0) + row / p.G, s.h * p.G + row % p.G, o, L);
+// Where four columns 4q .. 4q+3 of row r of a piece lie (in floats).  The
+// kernel with a thread a row writes them quad by quad with the rows side by
+// side (kByQuad), the one with a warp a row writes whole rows.
+template <int D, int kRT, bool kByQuad>
+__device__ __forceinline__ int64_t attn_piece_at(int64_t piece, int r, int q) {
+    return kByQuad ? ((piece * (D / 4) + q) * kRT + r) * 4 : (piece * kRT + r) * D + 4 * q;
 }
+
+// Joins the pieces of split units.  The rows of all split units are dealt out
+// to all blocks (few units may hold all of them): eight rows a block, a warp
+// each, where a unit has up to eight pieces; else one row a block, whose warps
+// take every eighth piece each and meet in shared memory.
+constexpr int kJoinWarps = 8;
+
+__device__ __forceinline__ int join_tasks(const AttnSplit &s, int c) {
+    return s.last - c < kJoinWarps ? (s.rows + kJoinWarps - 1) / kJoinWarps : s.rows;
+}
+constexpr int kJoinMax = 1024;  // split units at most (one a block of the first launch)
+
+template <typename T, int D, int kRT, bool kByQuad>
+__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid_constant__ AttnArgs p, int C) {
+    constexpr int E = D / 32, kThreads = 32 * kJoinWarps;
+    __shared__ int s_upto[kJoinMax];  // tasks of units 0 .. c
+    __shared__ int s_warp[kJoinWarps];
+    __shared__ __align__(16) float s_o[kJoinWarps][D];
+    __shared__ float s_l[kJoinWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    grid_dep_wait();
+    int total = 0;
+    for (int c0 = 0; c0 < C; c0 += kThreads) {
+        const int c = c0 + tid;
+        int x = c < C ? join_tasks(p.split[c], c) : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, x, d);
+            if (lane >= d) x += u;
+        }
+        if (lane == 31) s_warp[warp] = x;
+        __syncthreads();
+        int all = 0;
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+            if (w == warp) x += total + all;
+            all += s_warp[w];
+        }
+        total += all;
+        if (c < C) s_upto[c] = x;
+        __syncthreads();
+    }
+    for (int i = blockIdx.x; i < total; i += gridDim.x) {
+        int lo = 0, hi = C - 1;  // the first unit with upto > i
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (s_upto[mid] > i) {
+                hi = mid;
+            } else {
+                lo = mid + 1;
+            }
+        }
+        const AttnSplit s = p.split[lo];
+        const int task = i - (lo ? s_upto[lo - 1] : 0);
+        // piece k of the unit: block lo's second piece, then the first pieces of lo+1 .. last
+        const int pieces = s.last - lo + 1;
+        const bool few = pieces <= kJoinWarps;
+        const int r = few ? task * kJoinWarps + warp : task;
+        if (few && r >= s.rows) continue;  // no barrier follows
+        auto piece = [&](int k) { return static_cast<int64_t>(2) * (lo + k) + (k == 0); };
+        float M = -INFINITY;
+        for (int k = lane; k < pieces; k += 32) M = fmaxf(M, p.part_ml[piece(k) * kRT + r].x);
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+        if (M == -INFINITY) M = 0.0f;
+        float o[E] = {}, L = 0.0f;
+#pragma unroll 4
+        for (int k = few ? 0 : warp; k < pieces; k += few ? 1 : kJoinWarps) {
+            const float2 ml = p.part_ml[piece(k) * kRT + r];
+            const float w = exp2f(ml.x - M);
+            L += ml.y * w;
+            if constexpr (E == 2) {
+                const float2 v = *reinterpret_cast<const float2 *>(
+                    p.part_o + attn_piece_at<D, kRT, kByQuad>(piece(k), r, lane / 2) + 2 * (lane & 1));
+                o[0] += ml.y == 0.0f ? 0.0f : v.x * w, o[1] += ml.y == 0.0f ? 0.0f : v.y * w;
+            } else {
+#pragma unroll
+                for (int q = 0; q < E / 4; ++q) {
+                    const float4 v = *reinterpret_cast<const float4 *>(
+                        p.part_o + attn_piece_at<D, kRT, kByQuad>(piece(k), r, lane * (E / 4) + q));
+                    const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[4 * q + e] += ml.y == 0.0f ? 0.0f : x[e] * w;
+                }
+            }
+        }
+        if (!few) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
+            if (lane == 0) s_l[warp] = L;
+            __syncthreads();
+            if (warp == 0)
+                for (int w = 1; w < kJoinWarps; ++w) {
+                    L += s_l[w];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) o[e] += s_o[w][lane * E + e];
+                }
+        }
+        if (few || warp == 0) {
+            const int row = s.r0 + r;
+            attn_finish<T, D>(p.a, static_cast<int64_t>(s.n0) + row / p.G, s.h * p.G + row % p.G, o, L);
+        }
+        if (!few) __syncthreads();
+    }
+}
+
+// Blocks of the joining launch: about as many as fit at once.
+constexpr int kJoinBlocksPerSm = 4;
 
 }  // namespace abg

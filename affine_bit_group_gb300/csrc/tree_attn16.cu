@@ -1,24 +1,30 @@
 // tree_attn for 16-bit types on the tensor cores (formulas in include/abg.h,
 // the work split in tree_attn.cuh).
 //
-// A block holds 128 query rows (drafts x heads of one key/value head) and
-// streams token tiles past them, one pass with a running maximum:
+// A block streams a unit's token tiles past its query rows (drafts x heads of
+// one key/value head), one pass with a running maximum.  A step is
 //
 //   S = Q K^T     tcgen05.mma, Q and K in shared memory, S (f32) in TMEM
-//   P = 2^(S - m) four warps, a thread a row, from TMEM through registers back
+//   P = 2^(S - m) a warpgroup, a thread a row, from TMEM through registers back
 //                 into TMEM as 16-bit values over S's own columns
 //   O += P V      tcgen05.mma with P read from TMEM, V from shared memory
 //
-// Warps 0-3 are the softmax rows (TMEM lanes 32w ..), warp 4 brings K and V
-// tiles with TMA into a ring of tile-sized slots, lane 0 of warp 5 issues the
-// matrix instructions.  S has two buffers: the product of tile j+1 runs while
-// the weights of tile j are taken.  The pages of the cache need not be aligned
+// for 128 rows and one tile.  Two warpgroups take turns, each with its own S and
+// O columns of TMEM, so that one's exponentials run beside the other's products:
+// with more than 128 rows in the unit each has 128 of the rows and both use
+// every tile (each tile is read once for 256 rows); with fewer, each has every
+// second tile and the two results are joined at the end.  256 columns a head
+// leave TMEM for one O only: there one warpgroup takes every step, with two S
+// buffers.
+//
+// One warp brings K and V tiles with TMA into a ring of tile-sized slots, one
+// issues the matrix instructions.  The pages of the cache need not be aligned
 // to tiles: a tile is copied in boxes of the largest power of two of rows that
 // divides the page, each from its own page.
 //
-// Why 128 rows even for a few drafts: the matrix unit has 128 rows, and a tile's
-// product with all of them takes 0.65 us of an SM's tensor time per 64 KB of
-// cache, less than half of the 1.5 us its share of the memory bandwidth takes
+// Why 128 rows a step even for a few drafts: the matrix unit has 128 rows, and a
+// tile's products with all of them take 0.65 us of an SM's tensor time per 64 KB
+// of cache, less than half of the 1.5 us its share of the memory bandwidth takes
 // to deliver them.  Rows past the unit's are not loaded, and warps without rows
 // skip the softmax.
 #include "abg_kernels.cuh"
@@ -34,20 +40,22 @@ namespace abg {
 
 namespace {
 
-constexpr int kRT = 128;
-constexpr int kThreads16 = 192;
 constexpr int kDraftBox = 16;  // rows of a box of the draft buffers
 
 template <int D>
 struct Shape {
-    static constexpr int kKT = D == 256 ? 64 : 128;      // tokens a tile
+    static constexpr int kGroups = D == 256 ? 1 : 2;      // warpgroups of rows
+    static constexpr int kRT = 128 * kGroups;             // rows of a unit
+    static constexpr int kThreads = 128 * kGroups + 64;
+    static constexpr int kKT = D == 256 ? 64 : 128;       // tokens a tile
     static constexpr int kCols = D / 64;                  // 128-byte column blocks
-    static constexpr uint32_t kQBytes = kRT * D * 2;
+    static constexpr uint32_t kQTile = 128 * D * 2;
+    static constexpr uint32_t kQBytes = kQTile * kGroups;
     static constexpr uint32_t kTile = kKT * D * 2;        // a K or V tile: a ring slot
-    static constexpr int kSlots = D == 64 ? 12 : D == 128 ? 6 : 5;
-    static constexpr uint32_t kSmem = 1024 + kQBytes + kSlots * kTile;
+    static constexpr int kSlots = D == 64 ? 12 : 5;
 };
-constexpr uint32_t kTmemO = 256;  // TMEM columns: S buffers at 0 and 128, O from 256 on
+// TMEM columns: the S buffers at 0 and 128, O at 256 and (two groups) 384
+constexpr uint32_t kTmemO = 256;
 
 struct Maps {
     CUtensorMap k, v, kd, vd;
@@ -56,8 +64,25 @@ struct Maps {
 struct Bars {
     uint64_t full[12], empty[12];
     uint64_t s_full[2], p_full[2], pv_done[2];
-    uint64_t q_full, o_free, drain;
+    uint64_t q_full, o_free, ml_full, drain;
 };
+
+// Shared memory: the swizzled operands first (1024-byte aligned), all of it
+// dynamic, since the ring takes all that is left of the 227 KB.
+template <int D>
+struct Smem16 {
+    unsigned char q[Shape<D>::kQBytes];
+    unsigned char ring[Shape<D>::kSlots * Shape<D>::kTile];
+    float2 ml[2][128];                      // (maximum, weight) of each group's rows
+    Bars bars;
+    AttnScan scan;
+    uint32_t bad[2][ABG_MAX_SPAN / 32];     // drafts whose V holds an infinity or a NaN, of alternate stretches
+    uint32_t tmem;
+    volatile int gone;                      // a wait has given up
+};
+static_assert(sizeof(Smem16<64>) <= 227 * 1024 && sizeof(Smem16<128>) <= 227 * 1024 &&
+                  sizeof(Smem16<256>) <= 227 * 1024,
+              "shared memory of a block");
 
 // ------------------------------------------------------------ PTX wrappers --
 __device__ __forceinline__ void tma_3d(void *dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
@@ -170,229 +195,279 @@ __device__ __forceinline__ int tile_tokens(const AttnSeg &s, int t) {
     return t < s.ctiles ? min(kKT, s.req.len - t * kKT) : min(kKT, s.req.T - (t - s.ctiles) * kKT);
 }
 
-// A place on the block's tile stream.
-template <int kKT>
-struct Cursor {
-    AttnLine<kRT, kKT> line;
-    AttnSeg s;
-    int t;
-    bool on;
-    __device__ __forceinline__ void start(const AttnArgs &p, const AttnLine<kRT, kKT> &l) {
-        line = l;
-        on = line.next(p, s);
-        t = s.t0;
-    }
-    __device__ __forceinline__ void step(const AttnArgs &p) {
-        if (++t == s.t1) {
-            on = line.next(p, s);
-            t = s.t0;
-        }
-    }
-};
+// Which of a stretch's ring items hold K and V of its tile j (of n), in the
+// order the issuing warp first needs them.  Rows in both groups: K0 V0 K1 V1 ..;
+// otherwise a step ahead: K0 K1 V0 K2 V1 .. V(n-1).
+__device__ __forceinline__ int item_k(bool both, int j) { return both ? 2 * j : j == 0 ? 0 : 2 * j - 1; }
+__device__ __forceinline__ int item_v(bool both, int j, int n) {
+    return both || j == n - 1 ? 2 * j + 1 : 2 * j + 2;
+}
+
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads16, 1) attn16_kernel(const __grid_constant__ AttnArgs p,
-                                                              const __grid_constant__ Maps maps, int box) {
+__global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __grid_constant__ AttnArgs p,
+                                                                      const __grid_constant__ Maps maps, int box) {
     using S = Shape<D>;
-    constexpr int kKT = S::kKT, kSlots = S::kSlots, kCols = S::kCols;
-    extern __shared__ unsigned char raw[];
-    __shared__ Bars bars;
-    __shared__ uint32_t s_tmem;
-    __shared__ uint32_t s_bad[2][ABG_MAX_SPAN / 32];
-    __shared__ volatile int s_gone;
+    constexpr int kKT = S::kKT, kSlots = S::kSlots, kCols = S::kCols, kRT = S::kRT, kGroups = S::kGroups;
+    constexpr int kCopyWarp = 4 * kGroups, kIssueWarp = kCopyWarp + 1;
+    extern __shared__ __align__(1024) unsigned char raw[];
+    Smem16<D> &sm = *reinterpret_cast<Smem16<D> *>(raw);
+    Bars &bars = sm.bars;
     const abg_tree_attn_args &a = p.a;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    unsigned char *base = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-    unsigned char *sm_q = base, *sm_ring = base + S::kQBytes;
-    if (warp == 5) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem))
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    if (warp == kIssueWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sm.tmem))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     if (tid == 0) {
-        s_gone = 0;
+        sm.gone = 0;
         for (int i = 0; i < kSlots; ++i) mbar_init(&bars.full[i], 1), mbar_init(&bars.empty[i], 1);
         for (int i = 0; i < 2; ++i)
             mbar_init(&bars.s_full[i], 1), mbar_init(&bars.p_full[i], 4), mbar_init(&bars.pv_done[i], 1);
-        mbar_init(&bars.q_full, 4), mbar_init(&bars.o_free, 4), mbar_init(&bars.drain, 1);
+        mbar_init(&bars.q_full, 4 * kGroups), mbar_init(&bars.o_free, 4 * kGroups);
+        mbar_init(&bars.ml_full, 4 * kGroups), mbar_init(&bars.drain, 1);
         fence_mbar_init();
     }
     tc_before();
     grid_dep_wait();
     grid_dep_launch();
     AttnLine<kRT, kKT> line;
-    line.template init<kThreads16>(p, blockIdx.x, gridDim.x);
+    line.template init<S::kThreads>(p, blockIdx.x, gridDim.x, sm.scan);
     __syncthreads();
     tc_after();
-    const uint32_t tmem = s_tmem;
-    const int n_tiles = static_cast<int>(line.end - line.cur);
-    // ring items: K0, then K(j+1), V(j) in turn
-    auto item_k = [](int j) { return j == 0 ? 0 : 2 * j - 1; };
-    auto item_v = [n_tiles](int j) { return j < n_tiles - 1 ? 2 * j + 2 : 2 * j + 1; };
-    auto slot = [&](int i) { return sm_ring + static_cast<uint32_t>(i % kSlots) * S::kTile; };
+    const uint32_t tmem = sm.tmem;
+    AttnSeg s{};
+    bool live = true;
 
-    if (warp == 4) {
+    if (warp == kCopyWarp) {
         // ------------------------------------------------- the copying warp
-        Cursor<kKT> ck, cv;
-        ck.start(p, line);
-        cv.start(p, line);
-        int items = 0;
-        bool live = true;
-        auto bring = [&](const Cursor<kKT> &c, bool value) {
-            const AttnSeg &s = c.s;
-            const bool cache = c.t < s.ctiles;
-            const int step = cache ? box : kDraftBox;
-            const int boxes = (tile_tokens<kKT>(s, c.t) + step - 1) / step;
-            const CUtensorMap *map = cache ? (value ? &maps.v : &maps.k) : (value ? &maps.vd : &maps.kd);
-            unsigned char *to = slot(items);
-            uint64_t *bar = &bars.full[items % kSlots];
-            const int key0 = c.t * kKT, page = static_cast<int>(a.page);
-            // where the lane's first box lies (the load is in flight during the wait)
-            auto where = [&](int i, int &y, int &z) {
-                if (cache) {
-                    const int key = key0 + i * step, j = key / page;
+        // The lane's box of a tile: its row and page.  Taken a tile ahead of
+        // the tile's K, so that the table's latency is not in the way.
+        struct At {
+            int y, z;
+        };
+        const int page = static_cast<int>(a.page);
+        auto where = [&](int t, int i) {
+            At at{0, 0};
+            if (t < s.ctiles) {
+                const int key = t * kKT + i * box;
+                if (key < s.req.len) {
+                    const int j = key / page;
                     const int64_t id = a.table[static_cast<int64_t>(s.b) * a.width + j];
-                    y = key - j * page;
-                    z = id >= 0 && id < a.pages ? static_cast<int>(id * a.Hkv) + s.h : -1;  // -1: zeros
-                } else {
-                    y = s.req.n0 + (c.t - s.ctiles) * kKT + i * step;
-                    z = s.h;
+                    at.y = key - j * page;
+                    at.z = id >= 0 && id < a.pages ? static_cast<int>(id * a.Hkv) + s.h : -1;  // -1: zeros
                 }
-            };
-            int y = 0, z = 0;
-            if (lane < boxes) where(lane, y, z);
-            if (items >= kSlots && live) live = wait16(&bars.empty[items % kSlots], (items / kSlots - 1) & 1, &s_gone);
-            live = __all_sync(0xffffffffu, live);
+            } else {
+                at.y = s.req.n0 + (t - s.ctiles) * kKT + i * kDraftBox;
+                at.z = s.h;
+            }
+            return at;
+        };
+        int slot = 0, issued = 0;
+        uint32_t phase = 1;  // a slot's first wait passes
+        auto bring = [&](int t, bool value, At at) {
+            const bool cache = t < s.ctiles;
+            const int step = cache ? box : kDraftBox, boxes = (tile_tokens<kKT>(s, t) + step - 1) / step;
+            const CUtensorMap *map = cache ? (value ? &maps.v : &maps.k) : (value ? &maps.vd : &maps.kd);
+            unsigned char *to = sm.ring + static_cast<uint32_t>(slot) * S::kTile;
+            uint64_t *bar = &bars.full[slot];
+            live = __all_sync(0xffffffffu, wait16(&bars.empty[slot], phase, &sm.gone));
             if (!live) return;
             if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes * step) * D * 2);
             __syncwarp();
             for (int i = lane; i < boxes; i += 32) {
-                if (i != lane) where(i, y, z);
+                if (i != lane) at = where(t, i);
 #pragma unroll
                 for (int cb = 0; cb < kCols; ++cb)
                     tma_3d(to + static_cast<uint32_t>(cb) * kKT * 128 + static_cast<uint32_t>(i * step) * 128, map,
-                           64 * cb, y, z, bar);
+                           64 * cb, at.y, at.z, bar);
             }
-            ++items;
+            ++issued;
+            if (++slot == kSlots) slot = 0, phase ^= 1;
         };
-        if (n_tiles > 0) {
-            bring(ck, false);
-            for (int j = 0; j < n_tiles && live; ++j) {
-                if (j + 1 < n_tiles) {
-                    ck.step(p);
-                    bring(ck, false);
+        while (live && line.next(p, s)) {
+            const bool both = s.rows > 128;
+            At now = where(s.t0, lane), next = now;
+            if (s.t0 + 1 < s.t1) next = where(s.t0 + 1, lane);
+            if (!both) bring(s.t0, false, now);
+            for (int t = s.t0; live && t < s.t1; ++t) {
+                const At after = t + 2 < s.t1 ? where(t + 2, lane) : next;
+                if (both) {
+                    bring(t, false, now);
+                } else if (t + 1 < s.t1) {
+                    bring(t + 1, false, next);
                 }
-                if (live) bring(cv, true);
-                cv.step(p);
+                if (live) bring(t, true, now);
+                now = next;
+                next = after;
             }
         }
-        if (!live)  // what was issued must have landed before the block ends
-            for (int i = max(0, items - kSlots); i < items; ++i) mbar_wait(&bars.full[i % kSlots], (i / kSlots) & 1);
-    } else if (warp == 5) {
-        // --------------------------------------------- the issuing thread
-        if (lane == 0 && n_tiles > 0) {
-            constexpr uint32_t kQK = instr_desc<T>(kRT, kKT, false), kPV = instr_desc<T>(kRT, D, true);
-            const uint32_t q = smem_u32(sm_q);
-            int seg = 0;
-            bool live = true;
-            auto product = [&](int j) {  // S(j) = Q K(j)^T
-                const int i = item_k(j);
-                live = live && wait16(&bars.full[i % kSlots], (i / kSlots) & 1, &s_gone) &&
-                       (j < 2 || wait16(&bars.pv_done[j & 1], ((j - 2) >> 1) & 1, &s_gone));
+        if (!live) {  // what was issued must have landed before the block ends
+            for (int i = 0; i < min(issued, kSlots); ++i) {
+                if (--slot < 0) slot = kSlots - 1, phase ^= 1;
+                mbar_wait(&bars.full[slot], phase ^ 1);
+            }
+        }
+    } else if (warp == kIssueWarp) {
+        // ------------------------------------------------- the issuing warp
+        // All lanes keep the same place and wait; one elected lane issues.
+        constexpr uint32_t kQK = instr_desc<T>(128, kKT, false), kPV = instr_desc<T>(128, D, true);
+        const uint64_t dq = smem_desc(smem_u32(sm.q), 16), dk = smem_desc(smem_u32(sm.ring), 16),
+                       dv = smem_desc(smem_u32(sm.ring), kKT * 128);
+        const bool one = elect();
+        int first_item = 0, seg = 0;        // ring item of the stretch's first tile
+        // bit b: next phase of buffer b's pv_done (the first wait passes), p_full
+        uint32_t done = 3, weights = 0;
+        for (; live && line.next(p, s); ++seg) {
+            const bool both = s.rows > 128;
+            const int n = s.t1 - s.t0, steps = both ? 2 * n : n;
+            live = wait16(&bars.q_full, seg & 1, &sm.gone);
+            // S of step i (buffer i & 1): row group i & 1 and tile i / 2, or tile i
+            auto product = [&](int i) {
+                const int b = i & 1, item = first_item + item_k(both, both ? i >> 1 : i), at = item % kSlots;
+                live = live && wait16(&bars.full[at], (item / kSlots) & 1, &sm.gone) &&
+                       wait16(&bars.pv_done[b], done >> b & 1, &sm.gone);
+                live = __all_sync(0xffffffffu, live);
                 if (!live) return;
+                done ^= 1u << b;
                 tc_after();
-                const uint32_t k = smem_u32(slot(i));
+                if (one) {
+                    const uint64_t q = dq + (both && b ? S::kQTile >> 4 : 0u), k = dk + at * (S::kTile >> 4);
 #pragma unroll
-                for (int d = 0; d < D / 16; ++d)
-                    mma_ss(tmem + (j & 1) * 128, smem_desc(q + (d / 4) * (kRT * 128) + (d % 4) * 32, 16),
-                           smem_desc(k + (d / 4) * (kKT * 128) + (d % 4) * 32, 16), kQK, d > 0);
-                tc_commit(&bars.s_full[j & 1]);
-                tc_commit(&bars.empty[i % kSlots]);
-            };
-            AttnSeg s;
-            for (int j = 0; live && line.next(p, s); ++seg) {
-                live = wait16(&bars.q_full, seg & 1, &s_gone);
-                product(j);
-                for (int t = s.t0; live && t < s.t1; ++t, ++j) {
-                    if (t + 1 < s.t1) product(j + 1);  // ahead of this tile's sums
-                    const int i = item_v(j);
-                    live = live && wait16(&bars.full[i % kSlots], (i / kSlots) & 1, &s_gone) &&
-                           wait16(&bars.p_full[j & 1], (j >> 1) & 1, &s_gone) &&
-                           (t > s.t0 || seg == 0 || wait16(&bars.o_free, (seg - 1) & 1, &s_gone));
-                    if (!live) break;
-                    tc_after();
-                    const uint32_t v = smem_u32(slot(i));
-                    const int steps = (tile_tokens<kKT>(s, t) + 15) / 16;  // past the tokens there is no weight
-                    for (int k = 0; k < steps; ++k)
-                        mma_ts(tmem + kTmemO, tmem + (j & 1) * 128 + k * 8, smem_desc(v + k * 2048, kKT * 128), kPV,
-                               t > s.t0 || k > 0);
-                    tc_commit(&bars.pv_done[j & 1]);
-                    tc_commit(&bars.empty[i % kSlots]);
+                    for (int d = 0; d < D / 16; ++d)
+                        mma_ss(tmem + b * 128, q + (((d / 4) * (128 * 128) + (d % 4) * 32) >> 4),
+                               k + (((d / 4) * (kKT * 128) + (d % 4) * 32) >> 4), kQK, d > 0);
+                    tc_commit(&bars.s_full[b]);
+                    if (!both || b) tc_commit(&bars.empty[at]);
                 }
+                __syncwarp();
+            };
+            product(0);
+            if (steps > 1) product(1);
+            for (int i = 0; live && i < steps; ++i) {
+                const int b = i & 1, j = both ? i >> 1 : i;
+                const int item = first_item + item_v(both, j, n), at = item % kSlots;
+                live = wait16(&bars.full[at], (item / kSlots) & 1, &sm.gone) &&
+                       wait16(&bars.p_full[b], weights >> b & 1, &sm.gone) &&
+                       (i > 0 || seg == 0 || wait16(&bars.o_free, (seg - 1) & 1, &sm.gone));
+                live = __all_sync(0xffffffffu, live);
+                if (!live) break;
+                weights ^= 1u << b;
+                tc_after();
+                if (one) {
+                    const uint64_t v = dv + at * (S::kTile >> 4);
+                    const uint32_t o = tmem + kTmemO + (kGroups == 2 && b ? 128u : 0u), w = tmem + b * 128;
+                    const bool add = i >= kGroups;  // not the first into this O
+                    const int tokens = tile_tokens<kKT>(s, s.t0 + j);
+                    if (tokens > kKT - 16) {
+#pragma unroll
+                        for (int k = 0; k < kKT / 16; ++k) mma_ts(o, w + k * 8, v + k * 128, kPV, add || k > 0);
+                    } else {  // past the tokens there is no weight
+                        for (int k = 0; k < (tokens + 15) / 16; ++k)
+                            mma_ts(o, w + k * 8, v + k * 128, kPV, add || k > 0);
+                    }
+                    tc_commit(&bars.pv_done[b]);
+                    if (!both || b) tc_commit(&bars.empty[at]);
+                }
+                __syncwarp();
+                if (i + 2 < steps) product(i + 2);
             }
-            if (!live) {  // matrix instructions in flight read this block's memory
-                tc_commit(&bars.drain);
-                mbar_wait(&bars.drain, 0);
-            }
+            first_item += 2 * n;
+        }
+        if (!live) {  // matrix instructions in flight read this block's memory
+            if (one) tc_commit(&bars.drain);
+            mbar_wait(&bars.drain, 0);
         }
     } else {
-        // ------------------------------------------------ the softmax rows
+        // ------------------------------------------------- the softmax rows
         AttnSplit split{};
-        AttnSeg s;
-        const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-        const int r = tid;  // row of the tile
-        bool live = true;
-        int j = 0, seg = 0;
+        const int group = kGroups == 2 ? warp >> 2 : 0;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        int first_item = 0, seg = 0;
+        // bit b: next phase of buffer b's s_full; phase of pv_done that the
+        // buffer's last step completes
+        uint32_t scores = 0, done = 3;
         for (; live && line.next(p, s); ++seg) {
-            const bool busy = warp * 32 < s.rows, mine = r < s.rows;
-            uint32_t *bad = s_bad[seg & 1];
+            const bool both = s.rows > 128;
+            const int n = s.t1 - s.t0, steps = both ? 2 * n : n;
+            const int r = (tid & 127) + (both ? 128 * group : 0);  // row of the unit
+            const bool busy = r - lane < s.rows, mine = r < s.rows;
+            uint32_t *bad = sm.bad[seg & 1];
             if (tid < ABG_MAX_SPAN / 32) bad[tid] = 0;
             // Q, swizzled: 16-byte chunk ch of row q at chunk ch ^ (q % 8).  The
             // products that read the last stretch's Q are done (their S was).
-            for (int i = tid; i < s.rows * (D / 8); i += 128) {
-                const int q = i / (D / 8), ch = i % (D / 8), row = s.r0 + q;
-                const uint4 v = *reinterpret_cast<const uint4 *>(
-                    static_cast<const T *>(a.q) +
-                    ((static_cast<int64_t>(s.req.n0) + row / p.G) * a.Hq + s.h * p.G + row % p.G) * D + ch * 8);
-                *reinterpret_cast<uint4 *>(sm_q + (ch / 8) * (kRT * 128) + q * 128 + ((ch % 8) ^ (q % 8)) * 16) = v;
+            const int chunks = s.rows * (D / 8);
+            for (int i0 = tid; i0 < chunks; i0 += 4 * 128 * kGroups) {
+                uint4 v[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {  // four loads in flight
+                    const int i = i0 + u * 128 * kGroups, row = s.r0 + i / (D / 8);
+                    if (i < chunks)
+                        v[u] = *reinterpret_cast<const uint4 *>(
+                            static_cast<const T *>(a.q) +
+                            ((static_cast<int64_t>(s.req.n0) + row / p.G) * a.Hq + s.h * p.G + row % p.G) * D +
+                            i % (D / 8) * 8);
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int i = i0 + u * 128 * kGroups, q = i / (D / 8), ch = i % (D / 8);
+                    if (i < chunks)
+                        *reinterpret_cast<uint4 *>(sm.q + (q / 128) * S::kQTile + (ch / 8) * (128 * 128) +
+                                                   (q % 128) * 128 + ((ch % 8) ^ (q % 8)) * 16) = v[u];
+                }
             }
             fence_async();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.q_full);
-            const int64_t n = static_cast<int64_t>(s.req.n0) + (s.r0 + (mine ? r : 0)) / p.G;
-            const uint64_t *seen = a.mask + n * a.words;
+            const int64_t row = static_cast<int64_t>(s.req.n0) + (s.r0 + (mine ? r : 0)) / p.G;
+            const uint64_t *seen = a.mask + row * a.words;
             float ref = -INFINITY, l = 0.0f;
-            for (int t = s.t0; t < s.t1; ++t, ++j) {
+            const uint32_t o_at = tmem + kTmemO + lanes;  // group 0's O
+            const uint32_t o_mine = o_at + group * 128;
+            for (int i = kGroups == 2 ? group : 0; i < steps; i += kGroups) {
+                const int b = i & 1, j = both ? i >> 1 : i, t = s.t0 + j;
                 const bool drafts = t >= s.ctiles;
                 const int tokens = tile_tokens<kKT>(s, t), key0 = (t - s.ctiles) * kKT;
-                const uint32_t sbuf = tmem + (j & 1) * 128 + lanes;
-                live = wait16(&bars.s_full[j & 1], (j >> 1) & 1, &s_gone);
-                live = __all_sync(0xffffffffu, live);
+                const uint32_t sbuf = tmem + b * 128 + lanes;
+                live = __all_sync(0xffffffffu, wait16(&bars.s_full[b], scores >> b & 1, &sm.gone));
                 if (!live) break;
+                scores ^= 1u << b;
                 tc_after();
                 if (busy) {
-                    float x[kKT];
-#pragma unroll
-                    for (int k = 0; k < kKT; k += 32) tmem_ld32(sbuf + k, *reinterpret_cast<float(*)[32]>(x + k));
-                    tmem_ld_wait();
-                    if (drafts) {
-#pragma unroll
-                        for (int w = 0; w < kKT / 64; ++w) {
-                            uint64_t bits = key0 / 64 + w < a.words ? seen[key0 / 64 + w] : 0;
-                            const int left = tokens - 64 * w;
+                    // 64 scores at a time: the last ones are read for the maximum,
+                    // then again for their weights, which keeps the row in 168
+                    // registers without spills
+                    float x[64];
+                    auto read = [&](int h) {
+                        tmem_ld32(sbuf + 64 * h, *reinterpret_cast<float(*)[32]>(x));
+                        tmem_ld32(sbuf + 64 * h + 32, *reinterpret_cast<float(*)[32]>(x + 32));
+                        tmem_ld_wait();
+                        if (drafts || tokens < kKT) {
+                            uint64_t bits = ~0ull;
+                            if (drafts) bits = key0 / 64 + h < a.words ? seen[key0 / 64 + h] : 0;
+                            const int left = tokens - 64 * h;
                             if (left < 64) bits &= left > 0 ? (1ull << left) - 1 : 0;
 #pragma unroll
                             for (int k = 0; k < 64; ++k)
-                                if (!(bits >> k & 1)) x[64 * w + k] = -INFINITY;
+                                if (!(bits >> k & 1)) x[k] = -INFINITY;
                         }
-                    } else if (tokens < kKT) {
+                    };
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int k = 0; k < kKT; ++k)
-                            if (k >= tokens) x[k] = -INFINITY;
+                    for (int h = kKT / 64 - 1; h >= 0; --h) {
+                        read(h);
+#pragma unroll
+                        for (int k = 0; k < 64; k += 8)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) top[e] = max3(top[e], x[k + e], x[k + 4 + e]);
                     }
-                    float top[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-                    for (int k = 4; k < kKT; ++k) top[k & 3] = fmaxf(top[k & 3], x[k]);
                     const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.scale2;
                     // The reference follows the maximum only when it is 2^8
                     // behind: weights up to 256 lose nothing in 16 bits, and
@@ -403,55 +478,59 @@ __global__ void __launch_bounds__(kThreads16, 1) attn16_kernel(const __grid_cons
                         const float f = up ? ex2(ref - to) : 1.0f;
                         ref = to;
                         l *= f;
-                        if (t > s.t0) {
-                            live = wait16(&bars.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, &s_gone);
-                            live = __all_sync(0xffffffffu, live);
+                        if (i >= kGroups) {  // O holds this group's earlier steps
+                            // the last one used the other buffer if there is one group
+                            const int pb = kGroups == 2 ? b : b ^ 1;
+                            live = __all_sync(0xffffffffu, wait16(&bars.pv_done[pb], done >> pb & 1, &sm.gone));
                             if (!live) break;
                             tc_after();
 #pragma unroll 1
                             for (int k = 0; k < D; k += 32) {
                                 float o[32];
-                                tmem_ld32(tmem + kTmemO + lanes + k, o);
+                                tmem_ld32(o_mine + k, o);
                                 tmem_ld_wait();
 #pragma unroll
-                                for (int i = 0; i < 32; ++i) o[i] *= f;
-                                tmem_st32(tmem + kTmemO + lanes + k, *reinterpret_cast<uint32_t(*)[32]>(o));
+                                for (int e = 0; e < 32; ++e) o[e] *= f;
+                                tmem_st32(o_mine + k, *reinterpret_cast<uint32_t(*)[32]>(o));
                             }
                         }
                     }
                     const float sub = ref == -INFINITY ? 0.0f : ref;
-                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    const float2 mul = make_float2(p.scale2, p.scale2), off = make_float2(-sub, -sub);
+                    float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-                    for (int k = 0; k < kKT; k += 64) {
+                    for (int h = 0; h < kKT / 64; ++h) {
+                        if (h > 0) read(h);
                         uint32_t w[32];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float e0 = ex2(fmaf(x[k + 2 * i], p.scale2, -sub));
-                            const float e1 = ex2(fmaf(x[k + 2 * i + 1], p.scale2, -sub));
-                            sum[(2 * i) & 3] += e0;
-                            sum[(2 * i + 1) & 3] += e1;
-                            w[i] = pack2<T>(e0, e1);
+                        for (int e = 0; e < 32; ++e) {
+                            float2 v = fma2(make_float2(x[2 * e], x[2 * e + 1]), mul, off);
+                            v.x = ex2(v.x);
+                            v.y = ex2(v.y);
+                            sum[e & 1] = add2(sum[e & 1], v);
+                            w[e] = pack2<T>(v.x, v.y);
                         }
-                        tmem_st32(sbuf + k / 2, w);
+                        tmem_st32(sbuf + 32 * h, w);
                     }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
                     tmem_st_wait();
                 }
-                if (drafts || tokens < kKT) {
+                if ((drafts || tokens < kKT) && !(both && group)) {
                     // V rows past the tile's tokens hold what was there before,
                     // and a draft's V may hold an infinity or a NaN that only
                     // the rows that see it may get: 0 * NaN is NaN, so both are
-                    // cleared here (the latter is added back at the end).
-                    const int i = item_v(j), all = (tokens + 15) / 16 * 16;
-                    live = wait16(&bars.full[i % kSlots], (i / kSlots) & 1, &s_gone);
-                    live = __all_sync(0xffffffffu, live);
+                    // cleared here (the latter is added back at the end).  With
+                    // rows in both groups the first clears for both: its
+                    // product is issued first.
+                    const int item = first_item + item_v(both, j, n), all = (tokens + 15) / 16 * 16;
+                    live = __all_sync(0xffffffffu, wait16(&bars.full[item % kSlots], (item / kSlots) & 1, &sm.gone));
                     if (!live) break;
-                    unsigned char *v = slot(i);
-                    for (int e = tid; e < all * (D / 8); e += 128) {
-                        const int row = e / (D / 8), ch = e % (D / 8);
-                        uint4 *at = reinterpret_cast<uint4 *>(v + (ch / 8) * (kKT * 128) + row * 128 +
-                                                              ((ch % 8) ^ (row % 8)) * 16);
-                        if (row >= tokens) {
+                    unsigned char *v = sm.ring + static_cast<uint32_t>(item % kSlots) * S::kTile;
+                    for (int e = tid & 127; e < all * (D / 8); e += 128) {
+                        const int q = e / (D / 8), ch = e % (D / 8);
+                        uint4 *at = reinterpret_cast<uint4 *>(v + (ch / 8) * (kKT * 128) + q * 128 +
+                                                              ((ch % 8) ^ (q % 8)) * 16);
+                        if (q >= tokens) {
                             *at = make_uint4(0, 0, 0, 0);
                         } else if (drafts) {
                             constexpr uint32_t kExp = std::is_same_v<T, __nv_bfloat16> ? 0x7f80u : 0x7c00u;
@@ -459,13 +538,13 @@ __global__ void __launch_bounds__(kThreads16, 1) attn16_kernel(const __grid_cons
                             uint32_t *h = reinterpret_cast<uint32_t *>(&u);
                             bool hit = false;
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                if ((h[q] & kExp) == kExp) h[q] &= 0xffff0000u, hit = true;
-                                if ((h[q] >> 16 & kExp) == kExp) h[q] &= 0xffffu, hit = true;
+                            for (int k = 0; k < 4; ++k) {
+                                if ((h[k] & kExp) == kExp) h[k] &= 0xffff0000u, hit = true;
+                                if ((h[k] >> 16 & kExp) == kExp) h[k] &= 0xffffu, hit = true;
                             }
                             if (hit) {
                                 *at = u;
-                                atomicOr(&bad[(key0 + row) >> 5], 1u << ((key0 + row) & 31));
+                                atomicOr(&bad[(key0 + q) >> 5], 1u << ((key0 + q) & 31));
                             }
                         }
                     }
@@ -473,27 +552,63 @@ __global__ void __launch_bounds__(kThreads16, 1) attn16_kernel(const __grid_cons
                 }
                 tc_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.p_full[j & 1]);
+                if (lane == 0) mbar_arrive(&bars.p_full[b]);
+                done ^= 1u << b;
             }
             if (!live) break;
-            // the stretch's sums: tile j-1 was its last
-            live = wait16(&bars.pv_done[(j - 1) & 1], ((j - 1) >> 1) & 1, &s_gone);
+            // phases of the other group's buffer
+            if (kGroups == 2) {
+                const int others = group ? (steps + 1) / 2 : steps / 2;
+                if (others & 1) scores ^= 2u >> group, done ^= 2u >> group;
+            }
+            first_item += 2 * n;
+            const bool joined = kGroups == 2 && !both;  // both groups worked for the same rows
+            float2 mine_ml = make_float2(ref, l), other_ml = make_float2(-INFINITY, 0.0f);
+            if (kGroups == 2) {
+                if (joined) sm.ml[group][tid & 127] = mine_ml;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars.ml_full);
+                if (joined) {
+                    live = __all_sync(0xffffffffu, wait16(&bars.ml_full, seg & 1, &sm.gone));
+                    if (!live) break;
+                    other_ml = sm.ml[group ^ 1][tid & 127];
+                }
+            }
+            // the products of the stretch's last steps
+            live = wait16(&bars.pv_done[0], done & 1, &sm.gone) &&
+                   (steps < 2 || wait16(&bars.pv_done[1], done >> 1 & 1, &sm.gone));
             live = __all_sync(0xffffffffu, live);
             if (!live) break;
             tc_after();
             const bool whole = s.t0 == 0 && s.t1 == s.tiles;
-            const int64_t piece = (static_cast<int64_t>(2) * blockIdx.x + (s.t0 == 0)) * kRT + r;
-            const int64_t at = (n * a.Hq + s.h * p.G + (s.r0 + (mine ? r : 0)) % p.G) * D;
+            const int64_t piece = static_cast<int64_t>(2) * blockIdx.x + (s.t0 == 0);
+            const int64_t at = (row * a.Hq + s.h * p.G + (s.r0 + (mine ? r : 0)) % p.G) * D;
+            // joined: each group takes half of the columns of both O (of 64
+            // columns the first takes all: a group sum has 64)
+            const bool two = joined && steps > 1;
+            const int k0 = joined && D > 64 ? group * (D / 2) : 0;
+            const int k1 = !joined ? D : D > 64 ? k0 + D / 2 : group ? 0 : D;
+            const float M = fmaxf(ref, other_ml.x);
+            const float fm = l == 0.0f ? 0.0f : ex2(ref - M);
+            const float fo = other_ml.y == 0.0f ? 0.0f : ex2(other_ml.x - M);
+            const float L = l * fm + other_ml.y * fo;
+            // in O's order: group 0's factor first
+            const float f0 = joined && group ? fo : fm, f1 = joined && group ? fm : fo;
             if (busy) {
-                float group = 0.0f;
-                const float scale = l == 0.0f ? 0.0f : 1.0f / l;
+                float sums = 0.0f;
+                const float scale = 1.0f / L;
 #pragma unroll 1
-                for (int k = 0; k < D; k += 32) {
-                    float o[32];
+                for (int k = k0; k < k1; k += 32) {
+                    float o[32], o1[32];
                     __syncwarp();  // rows past the unit's have skipped ahead
-                    tmem_ld32(tmem + kTmemO + lanes + k, o);
+                    tmem_ld32((joined ? o_at : o_mine) + k, o);
+                    if (two) tmem_ld32(o_at + 128 + k, o1);
                     tmem_ld_wait();
                     if (!mine) continue;
+                    if (two)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = (f0 == 0.0f ? 0.0f : o[e] * f0) + (f1 == 0.0f ? 0.0f : o1[e] * f1);
                     for (int w = 0; w < (s.req.T + 31) / 32; ++w)
                         for (uint32_t m = bad[w]; m; m &= m - 1) {
                             const int d = 32 * w + __ffs(static_cast<int>(m)) - 1;
@@ -501,48 +616,49 @@ __global__ void __launch_bounds__(kThreads16, 1) attn16_kernel(const __grid_cons
                             const T *vd = static_cast<const T *>(a.Vd) +
                                           (s.h * a.drafts + s.req.n0 + d) * static_cast<int64_t>(D) + k;
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) {
-                                const float v = static_cast<float>(vd[i]);
-                                if (!(fabsf(v) < INFINITY)) o[i] += v;
+                            for (int e = 0; e < 32; ++e) {
+                                const float v = static_cast<float>(vd[e]);
+                                if (!(fabsf(v) < INFINITY)) o[e] += v;
                             }
                         }
                     if (!whole) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<float4 *>(p.part_o + piece * D + k + i) =
-                                make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4 *>(p.part_o +
+                                                        attn_piece_at<D, kRT, true>(piece, r, (k + e) / 4)) =
+                                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                         continue;
                     }
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = l == 0.0f ? 0.0f : o[i] * scale;
+                    for (int e = 0; e < 32; ++e) o[e] = L == 0.0f ? 0.0f : o[e] * scale;
                     if (a.gate)
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4) {
-                            const float4 g = *reinterpret_cast<const float4 *>(a.gate + at + k + i);
-                            o[i] /= 1.0f + __expf(-g.x), o[i + 1] /= 1.0f + __expf(-g.y);
-                            o[i + 2] /= 1.0f + __expf(-g.z), o[i + 3] /= 1.0f + __expf(-g.w);
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 g = *reinterpret_cast<const float4 *>(a.gate + at + k + e);
+                            o[e] /= 1.0f + __expf(-g.x), o[e + 1] /= 1.0f + __expf(-g.y);
+                            o[e + 2] /= 1.0f + __expf(-g.z), o[e + 3] /= 1.0f + __expf(-g.w);
                         }
                     if (a.y_type == ABG_SB_F32) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<float4 *>(static_cast<float *>(a.y) + at + k + i) =
-                                make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4 *>(static_cast<float *>(a.y) + at + k + e) =
+                                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8)
-                            *reinterpret_cast<uint4 *>(static_cast<T *>(a.y) + at + k + i) =
-                                make_uint4(pack2<T>(o[i], o[i + 1]), pack2<T>(o[i + 2], o[i + 3]),
-                                           pack2<T>(o[i + 4], o[i + 5]), pack2<T>(o[i + 6], o[i + 7]));
+                        for (int e = 0; e < 32; e += 8)
+                            *reinterpret_cast<uint4 *>(static_cast<T *>(a.y) + at + k + e) =
+                                make_uint4(pack2<T>(o[e], o[e + 1]), pack2<T>(o[e + 2], o[e + 3]),
+                                           pack2<T>(o[e + 4], o[e + 5]), pack2<T>(o[e + 6], o[e + 7]));
                     }
                     if (a.ysum) {
                         float sum = 0.0f;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) sum += o[i];
-                        group += sum;
-                        if (k & 32) a.ysum[(at + k) / 64] = group, group = 0.0f;
+                        for (int e = 0; e < 32; ++e) sum += o[e];
+                        sums += sum;
+                        if (k & 32) a.ysum[(at + k) / 64] = sums, sums = 0.0f;
                     }
                 }
-                if (mine && !whole) p.part_ml[piece] = make_float2(ref, l);
+                if (mine && !whole && k0 == 0 && k1 > 0) p.part_ml[piece * kRT + r] = make_float2(M, L);
             }
             if (s.t0 == 0 && s.t1 < s.tiles)
                 split = AttnSplit{s.req.n0, s.h, s.r0, s.rows, line.block_of_end(s.unit + s.tiles)};
@@ -556,7 +672,7 @@ __global__ void __launch_bounds__(kThreads16, 1) attn16_kernel(const __grid_cons
     tc_before();
     __syncthreads();
     tc_after();
-    if (warp == 5)
+    if (warp == kIssueWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
@@ -597,7 +713,7 @@ template <typename T, int D>
 cudaError_t go16(AttnArgs p, void *ws, cudaStream_t stream) {
     using S = Shape<D>;
     static const cudaError_t attr =
-        cudaFuncSetAttribute(attn16_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+        cudaFuncSetAttribute(attn16_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem16<D>));
     if (attr != cudaSuccess) return attr;
     if (!encoder()) return cudaErrorSymbolNotFound;
     const abg_tree_attn_args &a = p.a;
@@ -611,20 +727,24 @@ cudaError_t go16(AttnArgs p, void *ws, cudaStream_t stream) {
         !row_map<T>(&m.vd, a.Vd, D, a.drafts, a.Hkv, kDraftBox))
         return cudaErrorInvalidValue;
     const int C = sm_count();
-    const AttnLayout l = attn_layout(C, kRT, D);
+    const AttnLayout l = attn_layout(C, S::kRT, D);
     unsigned char *w = static_cast<unsigned char *>(ws);
     p.part_o = reinterpret_cast<float *>(w + l.o);
     p.part_ml = reinterpret_cast<float2 *>(w + l.ml);
     p.split = reinterpret_cast<AttnSplit *>(w + l.split);
     const cudaError_t e =
-        launch_kernel(attn16_kernel<T, D>, dim3(C), dim3(kThreads16), S::kSmem, stream, false, p, m, box);
+        launch_kernel(attn16_kernel<T, D>, dim3(C), dim3(S::kThreads), sizeof(Smem16<D>), stream, false, p, m, box);
     if (e != cudaSuccess) return e;
-    return launch_kernel(attn_join_kernel<T, D, kRT>, dim3(C, kRT / 8), dim3(256), 0, stream, true, p);
+    return launch_kernel(attn_join_kernel<T, D, S::kRT, true>, dim3(kJoinBlocksPerSm * sm_count()),
+                         dim3(32 * kJoinWarps), 0, stream, true, p, C);
 }
 
 }  // namespace
 
-size_t tree_attn16_bytes(int D) { return attn_layout(sm_count(), kRT, D).total; }
+size_t tree_attn16_bytes(int D) {
+    const int rt = D == 64 ? Shape<64>::kRT : D == 128 ? Shape<128>::kRT : Shape<256>::kRT;
+    return attn_layout(sm_count(), rt, D).total;
+}
 
 cudaError_t launch_tree_attn16(const AttnArgs &p, void *ws, cudaStream_t stream) {
     const bool bf = p.a.type == ABG_SB_BF16;
