@@ -495,6 +495,7 @@ bool pdl_enabled() {
 
 namespace abg {
 abg_status cuda_status(cudaError_t e, const char *where) { return cuda_fail(e, where); }
+bool early_launches() { return pdl_enabled(); }
 }  // namespace abg
 
 extern "C" {

@@ -25,6 +25,13 @@ cudaError_t launch_kernel(void (*fn)(P...), dim3 grid, dim3 block, size_t smem, 
     return cudaLaunchKernelEx(&cfg, fn, static_cast<P>(args)...);
 }
 
+// Whether the stream is being captured: then a call's first launch does not
+// start early, since the node ahead of it need not be a kernel.
+inline bool capturing(cudaStream_t stream) {
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    return cudaStreamIsCapturing(stream, &st) != cudaSuccess || st != cudaStreamCaptureStatusNone;
+}
+
 // The request that owns row n: the last b with cu[b] <= n, in 0 .. B-1.
 __device__ __forceinline__ int request_of(const int32_t *cu, int B, int n) {
     int lo = 0, hi = B - 1;
@@ -62,10 +69,13 @@ cudaError_t launch_tree_accept(const float *logits, int64_t ld, const int32_t *t
                                int N, int64_t V, void *ws, cudaStream_t stream);
 
 size_t tree_attn_bytes(int Hq, int Hkv, int D, int max_span, int type);
-cudaError_t launch_tree_attn(const abg_tree_attn_args &a, void *ws, cudaStream_t stream);
+cudaError_t launch_tree_attn(const abg_tree_attn_args &a, void *ws, bool pdl, cudaStream_t stream);
 
 // the 16-bit kernel's device status word (OR-ed into *bits)
 cudaError_t tree_attn16_status(unsigned *bits, bool clear);
+
+// Whether launches may start early (the environment's ABG_PDL; api.cu).
+bool early_launches();
 
 // Records e as the calling thread's last CUDA error (api.cu) and returns the
 // call's status.

@@ -170,7 +170,7 @@ abg_status abg_tree_attn(const abg_tree_attn_args *args, void *ws, int64_t ws_by
                 span(a.lens, a.B, 4), span(a.cu, a.B + 1, 4), span(a.Kd, a.Hkv * a.drafts * a.D, te),
                 span(a.Vd, a.Hkv * a.drafts * a.D, te), span(a.mask, a.N * a.words, 8), span(a.gate, io, 4)}))
         return ABG_EALIAS;
-    return cuda_status(launch_tree_attn(a, ws, to_stream(stream)), "tree_attn launch");
+    return cuda_status(launch_tree_attn(a, ws, early_launches(), to_stream(stream)), "tree_attn launch");
 }
 
 abg_status abg_tree_accept_workspace(int64_t N, int64_t V, int64_t *bytes) {

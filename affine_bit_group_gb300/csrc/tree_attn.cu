@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
     grid_dep_launch();
     AttnLine<kRT, kKT> line;
     line.template init<kThreads>(p, blockIdx.x, gridDim.x, sm.scan);
-    AttnSplit split{};
+    bool left = false;
     AttnSeg s;
     while (line.next(p, s)) {
         const float *kt, *vt;
@@ -301,10 +301,9 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
                 if (lane == 0) p.part_ml[slot * kRT + r] = make_float2(sm.m[r], sm.l[r]);
             }
         }
-        if (s.t0 == 0 && s.t1 < s.tiles)
-            split = AttnSplit{s.req.n0, s.h, s.r0, s.rows, line.block_of_end(s.unit + s.tiles)};
+        if (tid == 0) line.leave_entry(p, s, blockIdx.x, left);
     }
-    if (tid == 0) p.split[blockIdx.x] = split;
+    if (tid == 0) line.end_entries(p, blockIdx.x, left);
 }
 
 int row_tile(int64_t G, int64_t max_span) { return G * max_span <= kFewRows ? kFewRows : kManyRows; }
@@ -318,24 +317,24 @@ int grid_of() {
             cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, attn_kernel<D, kRT>, kThreads,
                                                           sizeof(Smem<D, kRT>)) != cudaSuccess)
             per = 1;
-        return std::min(std::max(1, per) * sm_count(), kJoinMax);
+        return std::min(std::max(1, per) * sm_count(), kMaxBlocks);
     }();
     return blocks;
 }
 
 template <int D, int kRT>
-cudaError_t go(AttnArgs p, void *ws, cudaStream_t stream) {
+cudaError_t go(AttnArgs p, void *ws, bool early, bool pdl, cudaStream_t stream) {
     const int C = grid_of<D, kRT>();
     const AttnLayout l = attn_layout(C, kRT, D);
     unsigned char *w = static_cast<unsigned char *>(ws);
     p.part_o = reinterpret_cast<float *>(w + l.o);
     p.part_ml = reinterpret_cast<float2 *>(w + l.ml);
     p.split = reinterpret_cast<AttnSplit *>(w + l.split);
+    attn_entries(p, C, kRT);
     const cudaError_t e =
-        launch_kernel(attn_kernel<D, kRT>, dim3(C), dim3(kThreads), sizeof(Smem<D, kRT>), stream, false, p);
+        launch_kernel(attn_kernel<D, kRT>, dim3(C), dim3(kThreads), sizeof(Smem<D, kRT>), stream, early, p);
     if (e != cudaSuccess) return e;
-    return launch_kernel(attn_join_kernel<float, D, kRT, false>, dim3(kJoinBlocksPerSm * sm_count()),
-                         dim3(32 * kJoinWarps), 0, stream, true, p, C);
+    return launch_join<float, D, kRT, false>(p, C, pdl, stream);
 }
 
 template <int D>
@@ -343,8 +342,8 @@ size_t bytes_of(int rt) {
     return attn_layout(rt == kFewRows ? grid_of<D, kFewRows>() : grid_of<D, kManyRows>(), rt, D).total;
 }
 template <int D>
-cudaError_t go_rows(const AttnArgs &p, int rt, void *ws, cudaStream_t stream) {
-    return rt == kFewRows ? go<D, kFewRows>(p, ws, stream) : go<D, kManyRows>(p, ws, stream);
+cudaError_t go_rows(const AttnArgs &p, int rt, void *ws, bool early, bool pdl, cudaStream_t stream) {
+    return rt == kFewRows ? go<D, kFewRows>(p, ws, early, pdl, stream) : go<D, kManyRows>(p, ws, early, pdl, stream);
 }
 
 }  // namespace
@@ -355,16 +354,17 @@ size_t tree_attn_bytes(int Hq, int Hkv, int D, int max_span, int type) {
     return D == 64 ? bytes_of<64>(rt) : D == 128 ? bytes_of<128>(rt) : bytes_of<256>(rt);
 }
 
-cudaError_t launch_tree_attn(const abg_tree_attn_args &a, void *ws, cudaStream_t stream) {
+cudaError_t launch_tree_attn(const abg_tree_attn_args &a, void *ws, bool pdl, cudaStream_t stream) {
     AttnArgs p{};
     p.a = a;
     p.G = static_cast<int>(a.Hq / a.Hkv);
     p.scale2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(a.D)));
-    if (a.type != ABG_SB_F32) return launch_tree_attn16(p, ws, stream);
+    const bool early = pdl && !capturing(stream);
+    if (a.type != ABG_SB_F32) return launch_tree_attn16(p, ws, early, pdl, stream);
     const int rt = row_tile(p.G, a.max_span);
-    return a.D == 64    ? go_rows<64>(p, rt, ws, stream)
-           : a.D == 128 ? go_rows<128>(p, rt, ws, stream)
-                        : go_rows<256>(p, rt, ws, stream);
+    return a.D == 64    ? go_rows<64>(p, rt, ws, early, pdl, stream)
+           : a.D == 128 ? go_rows<128>(p, rt, ws, early, pdl, stream)
+                        : go_rows<256>(p, rt, ws, early, pdl, stream);
 }
 
 }  // namespace abg

@@ -19,16 +19,19 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
 namespace abg {
 
 // A unit that ends in another block than it began in, left by the block it
 // began in (rows 0: none).
 struct AttnSplit {
-    int n0;    // first draft row of the request
-    int h;     // key/value head
-    int r0;    // first row of the unit's tile
-    int rows;  // its rows
-    int last;  // block it ends in
+    int n0;     // first draft row of the request
+    int h;      // key/value head
+    int r0;     // first row of the unit's tile
+    int rows;   // its rows
+    int first;  // block it begins in
+    int last;   // block it ends in
 };
 
 struct AttnArgs {
@@ -39,12 +42,25 @@ struct AttnArgs {
     // unit that goes on) of kRT rows
     float *part_o;    // [C][2] pieces of kRT * D (attn_piece_at)
     float2 *part_ml;  // [C][2][kRT]  (maximum, weight sum)
-    AttnSplit *split;  // [C]
+    // per unit, or per block where a call may have more units than blocks
+    AttnSplit *split;
+    int units;      // entries of split
+    int per_head;   // entries a (request, head) has; 0: entry c is block c's
 };
+
+// A call has at most B * Hkv * per_head units, where a request's rows fill at
+// most per_head tiles.  If that is no more than the blocks, a unit's entry is
+// its own; otherwise it is that of the block that it begins in.
+inline void attn_entries(AttnArgs &p, int C, int rt) {
+    const int64_t per_head = (64 * p.a.words * p.G + rt - 1) / rt, units = p.a.B * p.a.Hkv * per_head;
+    p.per_head = p.a.B <= C && p.a.Hkv <= C && units <= C ? static_cast<int>(per_head) : 0;
+    p.units = p.per_head ? static_cast<int>(units) : C;
+}
 
 struct AttnLayout {
     size_t o, ml, split, total;
 };
+constexpr int kMaxBlocks = 1024;  // of the first launch
 inline AttnLayout attn_layout(int C, int rt, int D) {
     AttnLayout l;
     l.o = 0;
@@ -70,7 +86,13 @@ __device__ __forceinline__ AttnReq attn_req(const abg_tree_attn_args &a, int b) 
 template <int kRT, int kKT>
 __device__ __forceinline__ int64_t attn_weight(const AttnArgs &p, const AttnReq &r) {
     const int64_t units = p.a.Hkv * ((static_cast<int64_t>(r.T) * p.G + kRT - 1) / kRT);
-    return units * ((static_cast<int64_t>(r.len) + kKT - 1) / kKT + (r.T + kKT - 1) / kKT);
+    return units * ((static_cast<uint32_t>(r.len) + kKT - 1) / kKT + (r.T + kKT - 1) / kKT);
+}
+
+// a / b of nonnegative numbers; 64-bit division is a long subroutine, and the
+// line of all but enormous calls fits in 32 bits.
+__device__ __forceinline__ int64_t attn_div(int64_t a, int64_t b) {
+    return (a | b) >> 32 ? a / b : static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
 }
 
 // One stretch of a unit's token tiles.
@@ -97,7 +119,35 @@ struct AttnLine {
     // By a whole block of kThreads threads: part c of the line.  Blocks get at
     // least two tiles each, so that a short call is not all joining.
     template <int kThreads>
-    __device__ void init(const AttnArgs &p, int c, int grid, AttnScan &sm) {
+    __device__ __forceinline__ void init(const AttnArgs &p, int c, int grid, AttnScan &sm) {
+        const int tid = threadIdx.x, lane = tid & 31;
+        const int B = static_cast<int>(p.a.B);
+        if (B <= 32) {  // every warp for itself
+            int64_t x = lane < B ? attn_weight<kRT, kKT>(p, attn_req(p.a, lane)) : 0;
+            const int64_t w = x;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t u = __shfl_up_sync(0xffffffffu, x, d);
+                if (lane >= d) x += u;
+            }
+            part(__shfl_sync(0xffffffffu, x, 31), c, grid);
+            const unsigned here = __ballot_sync(0xffffffffu, x - w <= cur && cur < x);
+            b = here ? __ffs(static_cast<int>(here)) - 1 : B;
+            ex = __shfl_sync(0xffffffffu, x - w, b & 31);
+        } else {
+            scan<kThreads>(p, c, grid, sm);
+        }
+    }
+
+    __device__ __forceinline__ void part(int64_t all, int c, int grid) {
+        W = all;
+        C = static_cast<int>(min(static_cast<int64_t>(grid), max(int64_t(1), W / 2)));
+        cur = c < C ? attn_div(W * c, C) : W;
+        end = c < C ? attn_div(W * (c + 1), C) : W;
+    }
+
+    template <int kThreads>
+    __device__ __forceinline__ void scan(const AttnArgs &p, int c, int grid, AttnScan &sm) {
         const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
         const int B = static_cast<int>(p.a.B);
         const int64_t w0 = tid < B ? attn_weight<kRT, kKT>(p, attn_req(p.a, tid)) : 0;
@@ -108,12 +158,10 @@ struct AttnLine {
         if (lane == 0) sm.w[warp] = sum;
         if (tid == 0) sm.b = B;
         __syncthreads();
-        W = 0;
+        sum = 0;
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) W += sm.w[w];
-        C = static_cast<int>(min(static_cast<int64_t>(grid), max(int64_t(1), W / 2)));
-        cur = c < C ? W * c / C : W;
-        end = c < C ? W * (c + 1) / C : W;
+        for (int w = 0; w < kThreads / 32; ++w) sum += sm.w[w];
+        part(sum, c, grid);
         ex = 0;
         b = B;
         if (cur >= end) return;  // uniform
@@ -155,9 +203,9 @@ struct AttnLine {
             if (cur - ex < w) break;
         }
         const int R = s.req.T * p.G, nrt = (R + kRT - 1) / kRT;
-        s.ctiles = (s.req.len + kKT - 1) / kKT;
+        s.ctiles = static_cast<int>((static_cast<uint32_t>(s.req.len) + kKT - 1) / kKT);
         s.tiles = s.ctiles + (s.req.T + kKT - 1) / kKT;
-        const int64_t u = (cur - ex) / s.tiles;
+        const int64_t u = attn_div(cur - ex, s.tiles);
         s.unit = ex + u * s.tiles;
         s.t0 = static_cast<int>(cur - s.unit);
         s.t1 = static_cast<int>(min(static_cast<int64_t>(s.tiles), s.t0 + (end - cur)));
@@ -169,8 +217,28 @@ struct AttnLine {
         return true;
     }
 
-    __device__ __forceinline__ int block_of_end(int64_t e) const {  // block that holds tile e-1
-        return static_cast<int>((e * C + W - 1) / W - 1);
+    // where a unit that begins in this block leaves what it is
+    __device__ __forceinline__ AttnSplit *entry(const AttnArgs &p, const AttnSeg &s, int c) const {
+        return p.split +
+               (p.per_head ? (static_cast<int64_t>(s.b) * p.a.Hkv + s.h) * p.per_head + s.r0 / kRT : int64_t(c));
+    }
+    // By one thread, once a stretch: says whether and where the unit that
+    // begins here goes on.  Units in one block have an entry too where entries
+    // are per unit (nothing else writes it).
+    __device__ __forceinline__ void leave_entry(const AttnArgs &p, const AttnSeg &s, int c, bool &left) const {
+        if (s.t0 != 0) return;
+        AttnSplit sp{};
+        if (s.t1 < s.tiles) {
+            // the block that holds the unit's last tile
+            const int last = static_cast<int>(attn_div((s.unit + s.tiles) * C + W - 1, W) - 1);
+            sp = AttnSplit{s.req.n0, s.h, s.r0, s.rows, c, last};
+            left = true;
+        }
+        if (p.per_head || s.t1 < s.tiles) *entry(p, s, c) = sp;
+    }
+    // By the same thread at the end: a block's entry says so if there is none.
+    __device__ __forceinline__ void end_entries(const AttnArgs &p, int c, bool left) const {
+        if (!p.per_head && !left) p.split[c] = AttnSplit{};
     }
 };
 
@@ -229,112 +297,120 @@ __device__ __forceinline__ int64_t attn_piece_at(int64_t piece, int r, int q) {
     return kByQuad ? ((piece * (D / 4) + q) * kRT + r) * 4 : (piece * kRT + r) * D + 4 * q;
 }
 
-// Joins the pieces of split units.  The rows of all split units are dealt out
-// to all blocks (few units may hold all of them): eight rows a block, a warp
-// each, where a unit has up to eight pieces; else one row a block, whose warps
-// take every eighth piece each and meet in shared memory.
-constexpr int kJoinWarps = 8;
-
-__device__ __forceinline__ int join_tasks(const AttnSplit &s, int c) {
-    return s.last - c < kJoinWarps ? (s.rows + kJoinWarps - 1) / kJoinWarps : s.rows;
-}
-constexpr int kJoinMax = 1024;  // split units at most (one a block of the first launch)
-
-template <typename T, int D, int kRT, bool kByQuad>
-__global__ void __launch_bounds__(32 * kJoinWarps) attn_join_kernel(const __grid_constant__ AttnArgs p, int C) {
-    constexpr int E = D / 32, kThreads = 32 * kJoinWarps;
-    __shared__ int s_upto[kJoinMax];  // tasks of units 0 .. c
-    __shared__ int s_warp[kJoinWarps];
-    __shared__ __align__(16) float s_o[kJoinWarps][D];
-    __shared__ float s_l[kJoinWarps];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// Joins the pieces of split units: block (u, y) the rows y * 8/kWarps .. of
+// entry u, kWarps warps a row.  A warp takes every kWarps-th piece, with a
+// running maximum (so that no load waits for another), and the warps of a row
+// meet in shared memory.
+template <typename T, int D, int kRT, bool kByQuad, int kWarps>
+__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnArgs p) {
+    constexpr int E = D / 32, kRows = 8 / kWarps;
+    __shared__ __align__(16) float s_o[8][D];
+    __shared__ float2 s_ml[8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % kWarps;
     grid_dep_wait();
-    int total = 0;
-    for (int c0 = 0; c0 < C; c0 += kThreads) {
-        const int c = c0 + tid;
-        int x = c < C ? join_tasks(p.split[c], c) : 0;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, x, d);
-            if (lane >= d) x += u;
-        }
-        if (lane == 31) s_warp[warp] = x;
-        __syncthreads();
-        int all = 0;
-#pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) {
-            if (w == warp) x += total + all;
-            all += s_warp[w];
-        }
-        total += all;
-        if (c < C) s_upto[c] = x;
-        __syncthreads();
+    grid_dep_launch();
+    AttnSplit s = p.split[blockIdx.x];
+    if (p.per_head) {  // a request without drafts, or a tile past its rows, has no entry
+        const int64_t per = p.a.Hkv * p.per_head;
+        const int b = static_cast<int>(blockIdx.x / per);
+        if (static_cast<int64_t>(attn_req(p.a, b).T) * p.G <= static_cast<int64_t>(blockIdx.x % p.per_head) * kRT) return;
     }
-    for (int i = blockIdx.x; i < total; i += gridDim.x) {
-        int lo = 0, hi = C - 1;  // the first unit with upto > i
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (s_upto[mid] > i) {
-                hi = mid;
-            } else {
-                lo = mid + 1;
-            }
-        }
-        const AttnSplit s = p.split[lo];
-        const int task = i - (lo ? s_upto[lo - 1] : 0);
-        // piece k of the unit: block lo's second piece, then the first pieces of lo+1 .. last
-        const int pieces = s.last - lo + 1;
-        const bool few = pieces <= kJoinWarps;
-        const int r = few ? task * kJoinWarps + warp : task;
-        if (few && r >= s.rows) continue;  // no barrier follows
-        auto piece = [&](int k) { return static_cast<int64_t>(2) * (lo + k) + (k == 0); };
-        float M = -INFINITY;
-        for (int k = lane; k < pieces; k += 32) M = fmaxf(M, p.part_ml[piece(k) * kRT + r].x);
+    // piece k of the unit: the first block's second piece, then the first pieces of the others
+    const int pieces = s.last - s.first + 1;
+    for (int r0 = blockIdx.y * kRows; r0 < s.rows; r0 += gridDim.y * kRows) {
+        const int r = r0 + warp / kWarps;
+        float m = -INFINITY, L = 0.0f, o[E] = {};
+        if (r < s.rows) {
+            constexpr int kBatch = 4;
+            for (int k0 = sub; k0 < pieces; k0 += kBatch * kWarps) {
+                float2 ml[kBatch];
+                float v[kBatch][E];
 #pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-        if (M == -INFINITY) M = 0.0f;
-        float o[E] = {}, L = 0.0f;
-#pragma unroll 4
-        for (int k = few ? 0 : warp; k < pieces; k += few ? 1 : kJoinWarps) {
-            const float2 ml = p.part_ml[piece(k) * kRT + r];
-            const float w = exp2f(ml.x - M);
-            L += ml.y * w;
-            if constexpr (E == 2) {
-                const float2 v = *reinterpret_cast<const float2 *>(
-                    p.part_o + attn_piece_at<D, kRT, kByQuad>(piece(k), r, lane / 2) + 2 * (lane & 1));
-                o[0] += ml.y == 0.0f ? 0.0f : v.x * w, o[1] += ml.y == 0.0f ? 0.0f : v.y * w;
-            } else {
+                for (int u = 0; u < kBatch; ++u) {
+                    const int k = k0 + u * kWarps;
+                    ml[u] = make_float2(-INFINITY, 0.0f);
+                    if (k >= pieces) continue;
+                    const int64_t piece = static_cast<int64_t>(2) * (s.first + k) + (k == 0);
+                    ml[u] = p.part_ml[piece * kRT + r];
+                    if constexpr (E == 2) {
+                        const float2 x = *reinterpret_cast<const float2 *>(
+                            p.part_o + attn_piece_at<D, kRT, kByQuad>(piece, r, lane / 2) + 2 * (lane & 1));
+                        v[u][0] = x.x, v[u][1] = x.y;
+                    } else {
 #pragma unroll
-                for (int q = 0; q < E / 4; ++q) {
-                    const float4 v = *reinterpret_cast<const float4 *>(
-                        p.part_o + attn_piece_at<D, kRT, kByQuad>(piece(k), r, lane * (E / 4) + q));
-                    const float x[4] = {v.x, v.y, v.z, v.w};
+                        for (int q = 0; q < E / 4; ++q) {
+                            const float4 x = *reinterpret_cast<const float4 *>(
+                                p.part_o + attn_piece_at<D, kRT, kByQuad>(piece, r, lane * (E / 4) + q));
+                            v[u][4 * q] = x.x, v[u][4 * q + 1] = x.y, v[u][4 * q + 2] = x.z, v[u][4 * q + 3] = x.w;
+                        }
+                    }
+                }
+                float top = m;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[4 * q + e] += ml.y == 0.0f ? 0.0f : x[e] * w;
+                for (int u = 0; u < kBatch; ++u) top = fmaxf(top, ml[u].x);
+                const float ref = top == -INFINITY ? 0.0f : top, f = exp2f(m - ref);
+                m = top;
+                L *= f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] *= f;
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    if (ml[u].y == 0.0f) continue;  // no weight: nothing to add, not a NaN either
+                    const float w = exp2f(ml[u].x - ref);
+                    L += ml[u].y * w;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) o[e] += v[u][e] * w;
                 }
             }
         }
-        if (!few) {
+        if constexpr (kWarps > 1) {
 #pragma unroll
             for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
-            if (lane == 0) s_l[warp] = L;
+            if (lane == 0) s_ml[warp] = make_float2(m, L);
             __syncthreads();
-            if (warp == 0)
-                for (int w = 1; w < kJoinWarps; ++w) {
-                    L += s_l[w];
+            if (sub == 0) {
+                float top = m;
 #pragma unroll
-                    for (int e = 0; e < E; ++e) o[e] += s_o[w][lane * E + e];
+                for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_ml[warp + w].x);
+                const float ref = top == -INFINITY ? 0.0f : top;
+                const float f = L == 0.0f ? 0.0f : exp2f(m - ref);
+                L *= f;
+#pragma unroll
+                for (int e = 0; e < E; ++e) o[e] = f == 0.0f ? 0.0f : o[e] * f;
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) {
+                    const float2 ml = s_ml[warp + w];
+                    if (ml.y == 0.0f) continue;
+                    const float g = exp2f(ml.x - ref);
+                    L += ml.y * g;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) o[e] += s_o[warp + w][lane * E + e] * g;
                 }
+            }
         }
-        if (few || warp == 0) {
+        if (r < s.rows && sub == 0) {
             const int row = s.r0 + r;
             attn_finish<T, D>(p.a, static_cast<int64_t>(s.n0) + row / p.G, s.h * p.G + row % p.G, o, L);
         }
-        if (!few) __syncthreads();
+        if constexpr (kWarps > 1) __syncthreads();
     }
 }
 
-// Blocks of the joining launch: about as many as fit at once.
-constexpr int kJoinBlocksPerSm = 4;
+// The joining launch, early (it waits for the first).  Few units are many
+// pieces each: more warps a row.
+template <typename T, int D, int kRT, bool kByQuad>
+cudaError_t launch_join(const AttnArgs &p, int C, bool pdl, cudaStream_t stream) {
+    const int64_t units = p.per_head ? p.units : C;
+    const int64_t rows = std::min<int64_t>(kRT, p.a.max_span * p.G);
+    const int64_t pieces = C / units + 1;
+    auto go = [&](auto w) {
+        constexpr int kWarps = decltype(w)::value;
+        const dim3 grid(static_cast<unsigned>(units), static_cast<unsigned>((rows * kWarps + 7) / 8));
+        return launch_kernel(attn_join_kernel<T, D, kRT, kByQuad, kWarps>, grid, dim3(256), 0, stream, pdl, p);
+    };
+    return pieces > 32  ? go(std::integral_constant<int, 8>{})
+           : pieces > 6 ? go(std::integral_constant<int, 4>{})
+                        : go(std::integral_constant<int, 1>{});
+}
 
 }  // namespace abg

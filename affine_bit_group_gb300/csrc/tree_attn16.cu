@@ -17,8 +17,8 @@
 // leave TMEM for one O only: there one warpgroup takes every step, with two S
 // buffers.
 //
-// One warp brings K and V tiles with TMA into a ring of tile-sized slots, one
-// issues the matrix instructions.  The pages of the cache need not be aligned
+// Three warps (two, with one group) bring K and V tiles with TMA into a ring of
+// tile-sized slots, one issues the matrix instructions.  The pages of the cache need not be aligned
 // to tiles: a tile is copied in boxes of the largest power of two of rows that
 // divides the page, each from its own page.
 //
@@ -46,7 +46,8 @@ template <int D>
 struct Shape {
     static constexpr int kGroups = D == 256 ? 1 : 2;      // warpgroups of rows
     static constexpr int kRT = 128 * kGroups;             // rows of a unit
-    static constexpr int kThreads = 128 * kGroups + 64;
+    static constexpr int kCopyWarps = kGroups == 2 ? 3 : 2;
+    static constexpr int kThreads = 128 * kGroups + 32 * (1 + kCopyWarps);
     static constexpr int kKT = D == 256 ? 64 : 128;       // tokens a tile
     static constexpr int kCols = D / 64;                  // 128-byte column blocks
     static constexpr uint32_t kQTile = 128 * D * 2;
@@ -76,7 +77,7 @@ struct Smem16 {
     float2 ml[2][128];                      // (maximum, weight) of each group's rows
     Bars bars;
     AttnScan scan;
-    uint32_t bad[2][ABG_MAX_SPAN / 32];     // drafts whose V holds an infinity or a NaN, of alternate stretches
+    uint32_t bad[4][ABG_MAX_SPAN / 32];     // drafts whose V holds an infinity or a NaN, of stretches in turn
     uint32_t tmem;
     volatile int gone;                      // a wait has given up
 };
@@ -139,6 +140,9 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t (&r)[32]
 }
 __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cp16(void *dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -215,7 +219,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
                                                                       const __grid_constant__ Maps maps, int box) {
     using S = Shape<D>;
     constexpr int kKT = S::kKT, kSlots = S::kSlots, kCols = S::kCols, kRT = S::kRT, kGroups = S::kGroups;
-    constexpr int kCopyWarp = 4 * kGroups, kIssueWarp = kCopyWarp + 1;
+    constexpr int kIssueWarp = 4 * kGroups, kCopyWarp = kIssueWarp + 1, kCopyWarps = S::kCopyWarps;
     extern __shared__ __align__(1024) unsigned char raw[];
     Smem16<D> &sm = *reinterpret_cast<Smem16<D> *>(raw);
     Bars &bars = sm.bars;
@@ -231,9 +235,13 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
         for (int i = 0; i < kSlots; ++i) mbar_init(&bars.full[i], 1), mbar_init(&bars.empty[i], 1);
         for (int i = 0; i < 2; ++i)
             mbar_init(&bars.s_full[i], 1), mbar_init(&bars.p_full[i], 4), mbar_init(&bars.pv_done[i], 1);
-        mbar_init(&bars.q_full, 4 * kGroups), mbar_init(&bars.o_free, 4 * kGroups);
+        mbar_init(&bars.q_full, 4), mbar_init(&bars.o_free, 4 * kGroups);
         mbar_init(&bars.ml_full, 4 * kGroups), mbar_init(&bars.drain, 1);
         fence_mbar_init();
+    }
+    if (warp == kCopyWarp && lane < 4) {
+        const CUtensorMap *map = lane == 0 ? &maps.k : lane == 1 ? &maps.v : lane == 2 ? &maps.kd : &maps.vd;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
     }
     tc_before();
     grid_dep_wait();
@@ -246,10 +254,12 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
     AttnSeg s{};
     bool live = true;
 
-    if (warp == kCopyWarp) {
-        // ------------------------------------------------- the copying warp
-        // The lane's box of a tile: its row and page.  Taken a tile ahead of
-        // the tile's K, so that the table's latency is not in the way.
+    if (warp >= kCopyWarp) {
+        // ------------------------------------------------ the copying warps
+        // Item i of the ring is brought by warp i % kCopyWarps: a tile of small
+        // pages is many boxes, and a warp issues one at a time.
+        // The lane's box of a tile: its row and page.  Taken before the wait
+        // for the slot, so that the table's latency is not in the way.
         struct At {
             int y, z;
         };
@@ -270,15 +280,16 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
             }
             return at;
         };
-        int slot = 0, issued = 0;
-        uint32_t phase = 1;  // a slot's first wait passes
-        auto bring = [&](int t, bool value, At at) {
+        int first_item = 0, last = -1;  // last: this warp's last item so far
+        auto bring = [&](int t, bool value, int item) {
             const bool cache = t < s.ctiles;
             const int step = cache ? box : kDraftBox, boxes = (tile_tokens<kKT>(s, t) + step - 1) / step;
             const CUtensorMap *map = cache ? (value ? &maps.v : &maps.k) : (value ? &maps.vd : &maps.kd);
+            const int slot = item % kSlots;
             unsigned char *to = sm.ring + static_cast<uint32_t>(slot) * S::kTile;
             uint64_t *bar = &bars.full[slot];
-            live = __all_sync(0xffffffffu, wait16(&bars.empty[slot], phase, &sm.gone));
+            At at = where(t, lane);
+            live = __all_sync(0xffffffffu, wait16(&bars.empty[slot], (item / kSlots + 1) & 1, &sm.gone));
             if (!live) return;
             if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes * step) * D * 2);
             __syncwarp();
@@ -289,32 +300,23 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
                     tma_3d(to + static_cast<uint32_t>(cb) * kKT * 128 + static_cast<uint32_t>(i * step) * 128, map,
                            64 * cb, at.y, at.z, bar);
             }
-            ++issued;
-            if (++slot == kSlots) slot = 0, phase ^= 1;
+            last = item;
         };
         while (live && line.next(p, s)) {
             const bool both = s.rows > 128;
-            At now = where(s.t0, lane), next = now;
-            if (s.t0 + 1 < s.t1) next = where(s.t0 + 1, lane);
-            if (!both) bring(s.t0, false, now);
-            for (int t = s.t0; live && t < s.t1; ++t) {
-                const At after = t + 2 < s.t1 ? where(t + 2, lane) : next;
-                if (both) {
-                    bring(t, false, now);
-                } else if (t + 1 < s.t1) {
-                    bring(t + 1, false, next);
-                }
-                if (live) bring(t, true, now);
-                now = next;
-                next = after;
+            const int n = s.t1 - s.t0;
+            // the warp's items of the stretch, in order
+            int i = (warp - kCopyWarp) - first_item % kCopyWarps;
+            for (i += i < 0 ? kCopyWarps : 0; live && i < 2 * n; i += kCopyWarps) {
+                const bool value = both ? i & 1 : i > 0 && (!(i & 1) || i == 2 * n - 1);
+                const int j = both ? i >> 1 : !value ? (i + 1) >> 1 : i == 2 * n - 1 ? n - 1 : (i >> 1) - 1;
+                bring(s.t0 + j, value, first_item + i);
             }
+            first_item += 2 * n;
         }
-        if (!live) {  // what was issued must have landed before the block ends
-            for (int i = 0; i < min(issued, kSlots); ++i) {
-                if (--slot < 0) slot = kSlots - 1, phase ^= 1;
-                mbar_wait(&bars.full[slot], phase ^ 1);
-            }
-        }
+        if (!live)  // what was issued must have landed before the block ends
+            for (int i = last; i >= 0 && i > last - kSlots; i -= kCopyWarps)
+                mbar_wait(&bars.full[i % kSlots], (i / kSlots) & 1);
     } else if (warp == kIssueWarp) {
         // ------------------------------------------------- the issuing warp
         // All lanes keep the same place and wait; one elected lane issues.
@@ -387,45 +389,38 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
         }
     } else {
         // ------------------------------------------------- the softmax rows
-        AttnSplit split{};
+        bool left = false;
         const int group = kGroups == 2 ? warp >> 2 : 0;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         int first_item = 0, seg = 0;
         // bit b: next phase of buffer b's s_full; phase of pv_done that the
         // buffer's last step completes
         uint32_t scores = 0, done = 3;
-        for (; live && line.next(p, s); ++seg) {
+        // By one group: a stretch's Q, swizzled (16-byte chunk ch of row q at
+        // chunk ch ^ (q % 8)), and its list of bad drafts, emptied.
+        auto bring_q = [&](const AttnSeg &g, int of) {
+            if ((tid & 127) < ABG_MAX_SPAN / 32) sm.bad[of & 3][tid & 127] = 0;
+            for (int i = tid & 127; i < g.rows * (D / 8); i += 128) {
+                const int q = i / (D / 8), ch = i % (D / 8), row = g.r0 + q;
+                cp16(sm.q + (q / 128) * S::kQTile + (ch / 8) * (128 * 128) + (q % 128) * 128 + ((ch % 8) ^ (q % 8)) * 16,
+                     static_cast<const T *>(a.q) +
+                         ((static_cast<int64_t>(g.req.n0) + row / p.G) * a.Hq + g.h * p.G + row % p.G) * D + ch * 8);
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.q_full);
+        };
+        AttnSeg next{};
+        bool more = line.next(p, next);
+        if (more && group == 0) bring_q(next, 0);
+        for (; live && more; ++seg) {
+            s = next;
             const bool both = s.rows > 128;
             const int n = s.t1 - s.t0, steps = both ? 2 * n : n;
             const int r = (tid & 127) + (both ? 128 * group : 0);  // row of the unit
             const bool busy = r - lane < s.rows, mine = r < s.rows;
-            uint32_t *bad = sm.bad[seg & 1];
-            if (tid < ABG_MAX_SPAN / 32) bad[tid] = 0;
-            // Q, swizzled: 16-byte chunk ch of row q at chunk ch ^ (q % 8).  The
-            // products that read the last stretch's Q are done (their S was).
-            const int chunks = s.rows * (D / 8);
-            for (int i0 = tid; i0 < chunks; i0 += 4 * 128 * kGroups) {
-                uint4 v[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {  // four loads in flight
-                    const int i = i0 + u * 128 * kGroups, row = s.r0 + i / (D / 8);
-                    if (i < chunks)
-                        v[u] = *reinterpret_cast<const uint4 *>(
-                            static_cast<const T *>(a.q) +
-                            ((static_cast<int64_t>(s.req.n0) + row / p.G) * a.Hq + s.h * p.G + row % p.G) * D +
-                            i % (D / 8) * 8);
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int i = i0 + u * 128 * kGroups, q = i / (D / 8), ch = i % (D / 8);
-                    if (i < chunks)
-                        *reinterpret_cast<uint4 *>(sm.q + (q / 128) * S::kQTile + (ch / 8) * (128 * 128) +
-                                                   (q % 128) * 128 + ((ch % 8) ^ (q % 8)) * 16) = v[u];
-                }
-            }
-            fence_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.q_full);
+            uint32_t *bad = sm.bad[seg & 3];
             const int64_t row = static_cast<int64_t>(s.req.n0) + (s.r0 + (mine ? r : 0)) / p.G;
             const uint64_t *seen = a.mask + row * a.words;
             float ref = -INFINITY, l = 0.0f;
@@ -562,9 +557,22 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
                 if (others & 1) scores ^= 2u >> group, done ^= 2u >> group;
             }
             first_item += 2 * n;
+            // The group of the last step has seen its S, and with it the end of
+            // every product that reads Q: the next stretch's Q comes before
+            // this one's results are written.
+            more = line.next(p, next);
+            if (more && group == (kGroups == 2 ? (steps - 1) & 1 : 0)) bring_q(next, seg + 1);
+            // the products of the stretch's last steps
+            live = wait16(&bars.pv_done[0], done & 1, &sm.gone) &&
+                   (steps < 2 || wait16(&bars.pv_done[1], done >> 1 & 1, &sm.gone));
+            live = __all_sync(0xffffffffu, live);
+            if (!live) break;
+            tc_after();
             const bool joined = kGroups == 2 && !both;  // both groups worked for the same rows
             float2 mine_ml = make_float2(ref, l), other_ml = make_float2(-INFINITY, 0.0f);
             if (kGroups == 2) {
+                // (a product of this stretch is done, so every row has read
+                // the last one's O, and sm.ml before it)
                 if (joined) sm.ml[group][tid & 127] = mine_ml;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars.ml_full);
@@ -574,12 +582,6 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
                     other_ml = sm.ml[group ^ 1][tid & 127];
                 }
             }
-            // the products of the stretch's last steps
-            live = wait16(&bars.pv_done[0], done & 1, &sm.gone) &&
-                   (steps < 2 || wait16(&bars.pv_done[1], done >> 1 & 1, &sm.gone));
-            live = __all_sync(0xffffffffu, live);
-            if (!live) break;
-            tc_after();
             const bool whole = s.t0 == 0 && s.t1 == s.tiles;
             const int64_t piece = static_cast<int64_t>(2) * blockIdx.x + (s.t0 == 0);
             const int64_t at = (row * a.Hq + s.h * p.G + (s.r0 + (mine ? r : 0)) % p.G) * D;
@@ -660,13 +662,12 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
                 }
                 if (mine && !whole && k0 == 0 && k1 > 0) p.part_ml[piece * kRT + r] = make_float2(M, L);
             }
-            if (s.t0 == 0 && s.t1 < s.tiles)
-                split = AttnSplit{s.req.n0, s.h, s.r0, s.rows, line.block_of_end(s.unit + s.tiles)};
+            if (tid == 0) line.leave_entry(p, s, blockIdx.x, left);
             tc_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.o_free);
         }
-        if (tid == 0) p.split[blockIdx.x] = split;
+        if (tid == 0) line.end_entries(p, blockIdx.x, left);
     }
     __syncwarp();
     tc_before();
@@ -710,7 +711,7 @@ bool row_map(CUtensorMap *map, const void *p, int64_t D, int64_t rows, int64_t o
 }
 
 template <typename T, int D>
-cudaError_t go16(AttnArgs p, void *ws, cudaStream_t stream) {
+cudaError_t go16(AttnArgs p, void *ws, bool early, bool pdl, cudaStream_t stream) {
     using S = Shape<D>;
     static const cudaError_t attr =
         cudaFuncSetAttribute(attn16_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem16<D>));
@@ -732,11 +733,11 @@ cudaError_t go16(AttnArgs p, void *ws, cudaStream_t stream) {
     p.part_o = reinterpret_cast<float *>(w + l.o);
     p.part_ml = reinterpret_cast<float2 *>(w + l.ml);
     p.split = reinterpret_cast<AttnSplit *>(w + l.split);
+    attn_entries(p, C, S::kRT);
     const cudaError_t e =
-        launch_kernel(attn16_kernel<T, D>, dim3(C), dim3(S::kThreads), sizeof(Smem16<D>), stream, false, p, m, box);
+        launch_kernel(attn16_kernel<T, D>, dim3(C), dim3(S::kThreads), sizeof(Smem16<D>), stream, early, p, m, box);
     if (e != cudaSuccess) return e;
-    return launch_kernel(attn_join_kernel<T, D, S::kRT, true>, dim3(kJoinBlocksPerSm * sm_count()),
-                         dim3(32 * kJoinWarps), 0, stream, true, p, C);
+    return launch_join<T, D, S::kRT, true>(p, C, pdl, stream);
 }
 
 }  // namespace
@@ -746,12 +747,12 @@ size_t tree_attn16_bytes(int D) {
     return attn_layout(sm_count(), rt, D).total;
 }
 
-cudaError_t launch_tree_attn16(const AttnArgs &p, void *ws, cudaStream_t stream) {
+cudaError_t launch_tree_attn16(const AttnArgs &p, void *ws, bool early, bool pdl, cudaStream_t stream) {
     const bool bf = p.a.type == ABG_SB_BF16;
     switch (p.a.D) {
-    case 64: return bf ? go16<__nv_bfloat16, 64>(p, ws, stream) : go16<__half, 64>(p, ws, stream);
-    case 128: return bf ? go16<__nv_bfloat16, 128>(p, ws, stream) : go16<__half, 128>(p, ws, stream);
-    default: return bf ? go16<__nv_bfloat16, 256>(p, ws, stream) : go16<__half, 256>(p, ws, stream);
+    case 64: return bf ? go16<__nv_bfloat16, 64>(p, ws, early, pdl, stream) : go16<__half, 64>(p, ws, early, pdl, stream);
+    case 128: return bf ? go16<__nv_bfloat16, 128>(p, ws, early, pdl, stream) : go16<__half, 128>(p, ws, early, pdl, stream);
+    default: return bf ? go16<__nv_bfloat16, 256>(p, ws, early, pdl, stream) : go16<__half, 256>(p, ws, early, pdl, stream);
     }
 }
 
