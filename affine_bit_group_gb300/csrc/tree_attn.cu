@@ -19,8 +19,8 @@ constexpr int kThreads = 512;
 // 8 us of an SM), the even split counts more than the tile.
 constexpr int kKT = 32, kTile = 64;
 
-// Rows of a unit: up to 4 or 16 where a request has no more, else 64.
-constexpr int kOneRows = 4, kFewRows = 16, kManyRows = 64;
+// Rows of a unit: up to 4, 16 or 32 where a request has no more, else 64.
+constexpr int kOneRows = 4, kFewRows = 16, kSomeRows = 32, kManyRows = 64;
 
 __device__ __forceinline__ void cp16(void *dst, const void *src, bool real) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(real ? 16 : 0)
@@ -36,12 +36,14 @@ template <int D, int kRT>
 struct Smem {
     static constexpr int kLd = D + 4;                       // rows of Q and K start in different banks
     static constexpr int kPLd = kRT + 4;
-    static constexpr int kParts = kRT == kManyRows ? 0 : 8;  // column parts of the scores
+    static constexpr int kWide = kRT > kFewRows;             // score tiles of 4 x 4 a thread
+    static constexpr int kParts = kWide ? 8 * 16 / kRT : 8;  // column parts of the scores
     float q[kRT][kLd];
     float k[kTile][kLd];
     float v[kTile][D];
     float p[kTile][kPLd];                     // weights, token-major
-    float part[kParts][kTile][kRT];           // partial scores
+    // partial scores: of all parts, or (wide) of the third part on
+    float part[kWide ? kParts - 2 : kParts][kTile][kWide ? kPLd : kRT];
     float corr[kRT];
     int64_t off[2][kTile];                    // a tile's row offsets in elements (-1: none)
     float m[kRT], l[kRT];
@@ -89,8 +91,8 @@ __device__ __forceinline__ Tile tile_at(const AttnSeg &s, int t) {
 
 // One part of the work line.  Scores: up to 16 rows, a thread holds an eighth of
 // the columns of one token for all rows, and the eighths meet in shared memory;
-// 64 rows, two rows by four tokens a thread.  Then thread (ty, tx) = (tid / 16,
-// tid % 16) has the scores of kRPS rows and tokens tx + 16 j.  Sums: a thread
+// 32 or 64 rows, a quarter or half of the columns of four rows by four tokens.  Then thread (ty,
+// tx) = (tid / 16, tid % 16) has the scores of kRPS rows and tokens tx + 16 j.  Sums: a thread
 // holds four columns of kRPO rows, two rows to a packed pair, over every
 // kKS-th token.  f32 arithmetic is what bounds it above about 16 rows (0.5
 // multiply-adds a byte and row against 11 a byte that an SM can do); below,
@@ -101,11 +103,13 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
     extern __shared__ __align__(16) unsigned char raw[];
     S &sm = *reinterpret_cast<S *>(raw);
     const abg_tree_attn_args &a = p.a;
-    constexpr int kRPS = kRT <= 32 ? 1 : kRT / 32;  // rows of a softmax thread
+    constexpr int kRPS = S::kWide ? 4 : 1;           // rows of a softmax thread
+    constexpr int kTY = S::kWide ? kRT / 4 : 32;     // thread rows of a score tile
+    constexpr int kParts = S::kParts;
     constexpr int kRPO = kRT < 8 ? kRT : 8;        // rows of a thread's sums
     constexpr int kQuads = D / 4, kRG = kRT / kRPO, kKS = kThreads / (kQuads * kRG);
     constexpr int E = D / 32;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tx = tid % 16, ty = tid / 16;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tx = tid % 16, ty = (tid % (16 * kTY)) / 16;
     const int quad = tid % kQuads, rg = tid / kQuads % kRG, ks = tid / (kQuads * kRG);
     grid_dep_wait();
     grid_dep_launch();
@@ -115,6 +119,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
     AttnSeg s;
     while (line.next(p, s)) {
         const bool rows_here = 2 * kRPS * warp < s.rows;  // the warp has softmax rows (whole warps: they shuffle)
+        const int part = tid / (S::kWide ? 16 * kTY : kTile);  // of the columns
         auto source = [&](const Tile &x, bool value) {
             return static_cast<const float *>(x.cache ? (value ? a.Vc : a.Kc) : (value ? a.Vd : a.Kd));
         };
@@ -147,8 +152,8 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
             __syncthreads();
             // scores
             float sc[kRPS][4];
-            if constexpr (kRT != kManyRows) {
-                const int key = tid % kTile, part = tid / kTile;
+            if constexpr (!S::kWide) {
+                const int key = tid % kTile;
                 if (key < now.tokens) {
                     float2 acc[kRT];
 #pragma unroll
@@ -179,6 +184,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
                         sc[0][j] = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
                     }
             } else {
+                const bool work = 8 * (warp % (kTY / 2)) < s.rows;  // the warp's eight rows
                 auto scores = [&](auto keys) {
                     constexpr int kKeys = decltype(keys)::value;
                     float2 acc[kRPS][kKeys];
@@ -186,8 +192,8 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
                     for (int i = 0; i < kRPS; ++i)
 #pragma unroll
                         for (int j = 0; j < kKeys; ++j) acc[i][j] = make_float2(0.0f, 0.0f);
-#pragma unroll 4
-                    for (int c = 0; c < D; c += 4) {
+#pragma unroll 2
+                    for (int c = part * (D / kParts); c < (part + 1) * (D / kParts); c += 4) {
                         float4 kv[kKeys];
 #pragma unroll
                         for (int j = 0; j < kKeys; ++j)
@@ -205,17 +211,35 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
 #pragma unroll
                     for (int i = 0; i < kRPS; ++i)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) sc[i][j] = j < kKeys ? acc[i][j < kKeys ? j : 0].x + acc[i][j < kKeys ? j : 0].y : 0.0f;
+                        for (int j = 0; j < 4; ++j)
+                            sc[i][j] = j < kKeys ? acc[i][j < kKeys ? j : 0].x + acc[i][j < kKeys ? j : 0].y : 0.0f;
                 };
-                // (a warp has rows 4 * warp .. 4 * warp + 3)
-                if (4 * warp < s.rows) {
+                if (work) {
                     if (now.tokens > 32) {
                         scores(std::integral_constant<int, 4>{});
                     } else {
                         scores(std::integral_constant<int, 2>{});
                     }
+                    // the second part's go through the weights' memory
+                    if (part)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            float *to = &sm.p[tx + 16 * j][ty * 4];
+                            if (kParts > 2 && part > 1) to = &sm.part[part - 2][tx + 16 * j][ty * 4];
+                            *reinterpret_cast<float4 *>(to) = make_float4(sc[0][j], sc[1][j], sc[2][j], sc[3][j]);
+                        }
                 }
                 __syncthreads();
+                if (rows_here)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int h = 1; h < kParts; ++h) {
+                            const float *from = h == 1 ? &sm.p[tx + 16 * j][ty * 4]
+                                                       : &sm.part[h > 1 ? h - 2 : 0][tx + 16 * j][ty * 4];
+                            const float4 x = *reinterpret_cast<const float4 *>(from);
+                            sc[0][j] += x.x, sc[1][j] += x.y, sc[2][j] += x.z, sc[3][j] += x.w;
+                        }
             }
             if (more) {
                 load_tile<D>(&sm.k[0][0], S::kLd, source(next, false), sm.off[buf ^ 1], next.tokens);
@@ -245,15 +269,23 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
                     float sum = 0.0f;
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const float e = exp2f(sc[i][j] - ref);
-                        sum += e;
-                        sm.p[tx + 16 * j][r] = e;
+                        sc[i][j] = exp2f(sc[i][j] - ref);
+                        sum += sc[i][j];
                     }
 #pragma unroll
                     for (int d = 8; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
                     l[i] = l[i] * corr + sum;
                     m[i] = top;
                     if (tx == 0) sm.corr[r] = corr;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float *to = &sm.p[tx + 16 * j][ty * kRPS];
+                    if constexpr (kRPS == 4) {
+                        *reinterpret_cast<float4 *>(to) = make_float4(sc[0][j], sc[1][j], sc[2][j], sc[3][j]);
+                    } else {
+                        *to = sc[0][j];
+                    }
                 }
             }
             cp_wait<1>();
@@ -372,7 +404,8 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
 }
 
 int row_tile(int64_t G, int64_t max_span) {
-    return G * max_span <= kOneRows ? kOneRows : G * max_span <= kFewRows ? kFewRows : kManyRows;
+    const int64_t rows = G * max_span;
+    return rows <= kOneRows ? kOneRows : rows <= kFewRows ? kFewRows : rows <= kSomeRows ? kSomeRows : kManyRows;
 }
 
 template <int D, int kRT>
@@ -409,6 +442,7 @@ template <int D, typename F>
 auto by_rows(int rt, F f) {
     return rt == kOneRows   ? f.template operator()<D, kOneRows>()
            : rt == kFewRows ? f.template operator()<D, kFewRows>()
+           : rt == kSomeRows ? f.template operator()<D, kSomeRows>()
                             : f.template operator()<D, kManyRows>();
 }
 template <typename F>
