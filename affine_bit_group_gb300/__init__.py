@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 __all__ = [
@@ -183,10 +184,26 @@ def _ptr(t, dtype=None, numel=None, name="tensor"):
     return t.data_ptr()
 
 
+_raw_stream = None  # () -> the current stream's handle
+
+
+def _find_raw_stream():
+    """torch.cuda.current_stream() builds a Stream object (about 3.5 us a call);
+    torch also hands out the bare handle, which is all a call needs."""
+    import torch
+    get, device = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    torch.cuda.current_stream()  # initializes CUDA
+    if get is None or device is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: get(device())
+
+
 def _stream(stream):
+    global _raw_stream
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _raw_stream is None:
+            _raw_stream = _find_raw_stream()
+        return _raw_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -300,35 +317,62 @@ def atq(q, gate, k, v, qn_w, kn_w, cos, sin, Kc, Vc, y, ysum, pos: int, eps: flo
     return y
 
 
-_TYPE_OF = None  # torch dtype -> abg_sb_type
+class _Torch:
+    """What the calls below need of torch, looked up once."""
+
+    def __init__(self):
+        import torch
+        self.i32, self.i64, self.f32, self.u8 = torch.int32, torch.int64, torch.float32, torch.uint8
+        self.empty = torch.empty
+        self.type_of = {torch.float32: SB_F32, torch.bfloat16: SB_BF16, torch.float16: SB_F16}
+
+
+_torch = None
+
+
+def _th():
+    global _torch
+    if _torch is None:
+        _torch = _Torch()
+    return _torch
+
+
+def _packer(struct_type):
+    """Packs a struct's fields, in order, into its C layout (building the ctypes
+    structure field by field costs several times as much)."""
+    codes = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_float: "f"}
+    return struct.Struct("@" + "".join(codes[t] for _, t in struct_type._fields_) + "0q").pack
+
+
+_pack_kv_put, _pack_tree_attn = _packer(_KvPutArgs), _packer(_TreeAttnArgs)
 
 
 def _type_of(t, name):
-    global _TYPE_OF
-    if _TYPE_OF is None:
-        import torch
-        _TYPE_OF = {torch.float32: SB_F32, torch.bfloat16: SB_BF16, torch.float16: SB_F16}
-    if t.dtype not in _TYPE_OF:
+    ty = _th().type_of.get(t.dtype)
+    if ty is None:
         raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
-    return _TYPE_OF[t.dtype]
+    return ty
 
 
 def _need(t, dtype, numel, name):
     """Device pointer of a contiguous CUDA tensor of this dtype with at least numel elements."""
-    if not (t.is_cuda and t.dtype == dtype and t.is_contiguous() and t.numel() >= numel):
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of at least {numel} elements")
-    return t.data_ptr()
+    if t.dtype is dtype and t.numel() >= numel and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of at least {numel} elements")
 
 
-def _strided(t, shape, dtype, name):
-    """Device pointer and the strides of the first two dimensions of a [rows][heads][D] CUDA tensor."""
-    if not (t.is_cuda and t.dtype == dtype and t.dim() == 3 and t.shape[1:] == shape and t.stride(2) == 1):
-        raise ValueError(f"{name} must be a {dtype} CUDA tensor [rows][{shape[0]}][{shape[1]}] with contiguous columns")
-    return t.data_ptr(), t.stride(0), t.stride(1)
+def _strided(t, heads, D, dtype, name):
+    """Rows, device pointer, row and head stride of a [rows][heads][D] CUDA tensor with contiguous columns."""
+    if t.dtype is dtype and t.is_cuda and t.dim() == 3:
+        n, h, d = t.shape
+        row, head, col = t.stride()
+        if h == heads and d == D and col == 1:
+            return n, t.data_ptr(), row, head
+    raise ValueError(f"{name} must be a {dtype} CUDA tensor [rows][{heads}][{D}] with contiguous columns")
 
 
 def _cache(Kc, Vc):
-    if Kc.dim() != 4 or Vc.shape != Kc.shape or Vc.dtype != Kc.dtype:
+    if Kc.dim() != 4 or Vc.shape != Kc.shape or Vc.dtype is not Kc.dtype:
         raise ValueError("the caches must be [pages][Hkv][page][D] tensors of one shape and type")
     return _type_of(Kc, "Kc")
 
@@ -340,32 +384,34 @@ def page_plan(lens, add, cu, held, ends, ring, table, page: int, slots, pos, len
     abg_page_plan).  table [B][width] and ring are updated in place; slots, pos,
     lens_out, held_out, ends_out and info are written.  slots and ends are
     int64, everything else is int32."""
-    import torch
-    i32, i64 = torch.int32, torch.int64
-    B, N = lens.numel(), slots.numel()
+    th = _th()
+    i32, i64 = th.i32, th.i64
+    B, N, R = lens.numel(), slots.numel(), ring.numel()
     width = table.numel() // max(1, B)
     st = library().abg_page_plan(
         _need(lens, i32, B, "lens"), _need(add, i32, B, "add"), _need(cu, i32, B + 1, "cu"),
-        _need(held, i32, B, "held"), _need(ends, i64, 2, "ends"), _need(ring, i32, 1, "ring"),
-        _need(table, i32, B * width, "table"), _need(slots, i64, N, "slots"), _need(pos, i32, N, "pos"),
+        _need(held, i32, B, "held"), _need(ends, i64, 2, "ends"), _need(ring, i32, R, "ring"),
+        _need(table, i32, 0, "table"), _need(slots, i64, N, "slots"), _need(pos, i32, N, "pos"),
         _need(lens_out, i32, B, "lens_out"), _need(held_out, i32, B, "held_out"), _need(ends_out, i64, 2, "ends_out"),
-        _need(info, i32, 2, "info"), B, N, page, width, ring.numel(), _stream(stream))
-    _check(st, "abg_page_plan")
+        _need(info, i32, 2, "info"), B, N, page, width, R, _stream(stream))
+    if st:
+        _check(st, "abg_page_plan")
     return slots, pos
 
 
 def tree_plan(parent, lens, cu, mask, pos, stream=None):
     """Ancestor masks [N][words] (int64 bit words) and positions [N] of drafts
     from their parents' indices (see abg_tree_plan)."""
-    import torch
-    i32 = torch.int32
+    th = _th()
+    i32 = th.i32
     B, N = lens.numel(), parent.numel()
     if mask.dim() != 2 or mask.shape[0] != N:
         raise ValueError("mask must be [N][words]")
     st = library().abg_tree_plan(_need(parent, i32, N, "parent"), _need(lens, i32, B, "lens"),
-                                 _need(cu, i32, B + 1, "cu"), _need(mask, torch.int64, N, "mask"),
+                                 _need(cu, i32, B + 1, "cu"), _need(mask, th.i64, N, "mask"),
                                  _need(pos, i32, N, "pos"), B, N, mask.shape[1], _stream(stream))
-    _check(st, "abg_tree_plan")
+    if st:
+        _check(st, "abg_tree_plan")
     return mask, pos
 
 
@@ -377,34 +423,35 @@ def kv_put(k, v, Kc, Vc, slots=None, rows=None, q=None, qo=None, qn_w=None, kn_w
     RMS norm (qn_w, kn_w [D]) and rotation (cos, sin [positions][D/2], pos [N])
     where given; q goes to qo [N][Hq][D].  k, v and q are float32 or of the
     caches' type."""
-    import torch
-    f32 = torch.float32
-    pages, Hkv, page, D = Kc.shape
+    th = _th()
+    f32, dt, src = th.f32, Kc.dtype, k.dtype
     ty = _cache(Kc, Vc)
-    N = rows.numel() if rows is not None else slots.numel() if slots is not None else k.shape[0]
-    a = _KvPutArgs(N=N, src_rows=min(k.shape[0], v.shape[0]), Hkv=Hkv, D=D, page=page, pages=pages, eps=eps,
-                   src_type=_type_of(k, "k"), type=ty)
-    a.k, a.k_row, a.k_head = _strided(k, (Hkv, D), k.dtype, "k")
-    a.v, a.v_row, a.v_head = _strided(v, (Hkv, D), k.dtype, "v")
-    a.Kc, a.Vc = _need(Kc, Kc.dtype, 0, "Kc"), _need(Vc, Kc.dtype, 0, "Vc")
+    pages, Hkv, page, D = Kc.shape
+    src_rows, kp, k_row, k_head = _strided(k, Hkv, D, src, "k")
+    v_rows, vp, v_row, v_head = _strided(v, Hkv, D, src, "v")
+    src_rows = min(src_rows, v_rows)
+    N = rows.numel() if rows is not None else slots.numel() if slots is not None else src_rows
+    Hq = qp = q_row = q_head = qop = qn = kn = cp = sp = pp = cos_rows = 0
     if q is not None:
-        a.Hq = q.shape[1]
-        a.q, a.q_row, a.q_head = _strided(q, (a.Hq, D), k.dtype, "q")
-        a.src_rows = min(a.src_rows, q.shape[0])
-        a.qo = _need(qo, Kc.dtype, N * a.Hq * D, "qo")
+        Hq = q.shape[1]
+        q_rows, qp, q_row, q_head = _strided(q, Hq, D, src, "q")
+        src_rows = min(src_rows, q_rows)
+        qop = _need(qo, dt, N * Hq * D, "qo")
         if qn_w is not None:
-            a.qn_w = _need(qn_w, f32, D, "qn_w")
-    if rows is not None:
-        a.rows = _need(rows, torch.int32, N, "rows")
-    if slots is not None:
-        a.slots = _need(slots, torch.int64, N, "slots")
+            qn = _need(qn_w, f32, D, "qn_w")
     if kn_w is not None:
-        a.kn_w = _need(kn_w, f32, D, "kn_w")
+        kn = _need(kn_w, f32, D, "kn_w")
     if cos is not None:
-        a.cos_rows = cos.shape[0]
-        a.cos, a.sin = _need(cos, f32, a.cos_rows * (D // 2), "cos"), _need(sin, f32, a.cos_rows * (D // 2), "sin")
-        a.pos = _need(pos, torch.int32, N, "pos")
-    _check(library().abg_kv_put(ctypes.byref(a), _stream(stream)), "abg_kv_put")
+        cos_rows = cos.shape[0]
+        cp, sp = _need(cos, f32, cos_rows * (D // 2), "cos"), _need(sin, f32, cos_rows * (D // 2), "sin")
+        pp = _need(pos, th.i32, N, "pos")
+    st = library().abg_kv_put(_pack_kv_put(
+        qp, kp, vp, q_row, q_head, k_row, k_head, v_row, v_head,
+        0 if rows is None else _need(rows, th.i32, N, "rows"), 0 if slots is None else _need(slots, th.i64, N, "slots"),
+        qn, kn, cp, sp, pp, qop, _need(Kc, dt, 0, "Kc"), _need(Vc, dt, 0, "Vc"), N, src_rows, Hq, Hkv, D, page, pages,
+        cos_rows, eps, _type_of(k, "k"), ty), _stream(stream))
+    if st:
+        _check(st, "abg_kv_put")
     return Kc, Vc
 
 
@@ -426,29 +473,28 @@ def tree_attn(q, Kc, Vc, table, lens, cu, Kd, Vd, mask, y, max_span: int | None 
     is a uint8 tensor of tree_attn_workspace() bytes; by default the call takes
     one from torch's allocator on the current stream (give ws for a call on
     another stream)."""
-    import torch
-    i32, f32 = torch.int32, torch.float32
-    pages, Hkv, page, D = Kc.shape
+    th = _th()
+    i32, f32, dt = th.i32, th.f32, Kc.dtype
     ty = _cache(Kc, Vc)
-    dt = Kc.dtype
-    N, Hq = q.shape[0], q.shape[1]
-    B, words, drafts = lens.numel(), mask.shape[1], Kd.shape[1]
+    pages, Hkv, page, D = Kc.shape
+    N, Hq, qd = q.shape
+    drafts, words = Kd.shape[1], mask.shape[1]
+    B, n = lens.numel(), N * Hq * D
+    if qd != D or Kd.shape != (Hkv, drafts, D) or Vd.shape != Kd.shape:
+        raise ValueError("q must be [N][Hq][D], Kd and Vd [Hkv][drafts][D]")
     if max_span is None:
         max_span = 64 * words
     if ws is None:
-        ws = torch.empty(tree_attn_workspace(q, Kc, max_span), dtype=torch.uint8, device=q.device)
-    width = table.numel() // max(1, B)
-    a = _TreeAttnArgs(
-        _need(q, dt, N * Hq * D, "q"), _need(Kc, dt, 0, "Kc"), _need(Vc, dt, 0, "Vc"),
-        _need(table, i32, B * width, "table"), _need(lens, i32, B, "lens"), _need(cu, i32, B + 1, "cu"),
-        _need(Kd, dt, Hkv * drafts * D, "Kd"), _need(Vd, dt, Hkv * drafts * D, "Vd"),
-        _need(mask, torch.int64, N * words, "mask"), None if gate is None else _need(gate, f32, N * Hq * D, "gate"),
-        _need(y, y.dtype, N * Hq * D, "y"), None if ysum is None else _need(ysum, f32, N * Hq * D // 64, "ysum"),
-        B, N, Hq, Hkv, D, page, pages, width, drafts, words, max_span, ty, _type_of(y, "y"))
-    if q.dim() != 3 or q.shape[2] != D or Kd.dim() != 3 or Kd.shape[0] != Hkv or Vd.shape != Kd.shape:
-        raise ValueError("q must be [N][Hq][D], Kd and Vd [Hkv][drafts][D]")
-    _check(library().abg_tree_attn(ctypes.byref(a), _need(ws, torch.uint8, 0, "ws"), ws.numel(), _stream(stream)),
-           "abg_tree_attn")
+        ws = th.empty(tree_attn_workspace(q, Kc, max_span), dtype=th.u8, device=q.device)
+    args = _pack_tree_attn(
+        _need(q, dt, n, "q"), _need(Kc, dt, 0, "Kc"), _need(Vc, dt, 0, "Vc"), _need(table, i32, 0, "table"),
+        _need(lens, i32, B, "lens"), _need(cu, i32, B + 1, "cu"), _need(Kd, dt, 0, "Kd"), _need(Vd, dt, 0, "Vd"),
+        _need(mask, th.i64, N * words, "mask"), 0 if gate is None else _need(gate, f32, n, "gate"),
+        _need(y, y.dtype, n, "y"), 0 if ysum is None else _need(ysum, f32, n // 64, "ysum"),
+        B, N, Hq, Hkv, D, page, pages, table.numel() // max(1, B), drafts, words, max_span, ty, _type_of(y, "y"))
+    st = library().abg_tree_attn(args, _need(ws, th.u8, 0, "ws"), ws.numel(), _stream(stream))
+    if st:
+        _check(st, "abg_tree_attn")
     return y
 
 
@@ -465,20 +511,22 @@ def tree_accept(logits, tok, parent, cu, best, rows, add, last, ws=None, stream=
     stride): best [N], the accepted rows of each request rows [N] and their
     number add [B], and the next tokens last [B] (see abg_tree_accept); all
     int32.  ws as in tree_attn."""
-    import torch
-    i32 = torch.int32
+    th = _th()
+    i32 = th.i32
     N, V = logits.shape
     B = add.numel()
-    if not (logits.is_cuda and logits.dtype == torch.float32 and (V < 2 or logits.stride(1) == 1)):
+    ld, col = logits.stride()
+    if logits.dtype is not th.f32 or not logits.is_cuda or (col != 1 and V > 1):
         raise ValueError("logits must be a float32 CUDA tensor [N][V] with contiguous rows")
     if ws is None:
-        ws = torch.empty(tree_accept_workspace(logits), dtype=torch.uint8, device=logits.device)
+        ws = th.empty(tree_accept_workspace(logits), dtype=th.u8, device=logits.device)
     st = library().abg_tree_accept(
-        logits.data_ptr(), logits.stride(0) if N > 1 else V, _need(tok, i32, N, "tok"),
-        _need(parent, i32, N, "parent"), _need(cu, i32, B + 1, "cu"), _need(best, i32, N, "best"),
-        _need(rows, i32, N, "rows"), _need(add, i32, B, "add"), _need(last, i32, B, "last"), B, N, V,
-        _need(ws, torch.uint8, 0, "ws"), ws.numel(), _stream(stream))
-    _check(st, "abg_tree_accept")
+        logits.data_ptr(), ld if N > 1 else V, _need(tok, i32, N, "tok"), _need(parent, i32, N, "parent"),
+        _need(cu, i32, B + 1, "cu"), _need(best, i32, N, "best"), _need(rows, i32, N, "rows"),
+        _need(add, i32, B, "add"), _need(last, i32, B, "last"), B, N, V, _need(ws, th.u8, 0, "ws"), ws.numel(),
+        _stream(stream))
+    if st:
+        _check(st, "abg_tree_accept")
     return rows, add, last
 
 
