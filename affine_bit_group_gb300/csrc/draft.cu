@@ -58,6 +58,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
     __shared__ int s_bad[kPlanThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dep_wait();
+    const bool wide = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.pos)) & 15) == 0;
     const int64_t head = a.ends[0], tail = a.ends[1];
     const int64_t avail = max(int64_t(0), min(tail - head, static_cast<int64_t>(a.ring_len)));
     int64_t done_x = 0, done_f = 0, taken = 0;  // taken: extras up to the last request that was granted any
@@ -128,22 +129,49 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
         for (int64_t j = lane; j < k.extra; j += 32) row[held + j] = a.ring[(at + j) % a.ring_len];
         for (int64_t j = lane; j < k.freed; j += 32) a.ring[(at + j) % a.ring_len] = row[j];
     }
-    // slots: a thread a token
-    for (int64_t n = static_cast<int64_t>(blockIdx.x) * kPlanThreads + tid; n < a.N;
-         n += static_cast<int64_t>(gridDim.x) * kPlanThreads) {
-        int64_t slot = -1;
-        int32_t pos = 0;
-        const int b = request_of(s_cu, a.B, static_cast<int>(n));
-        const int i = static_cast<int>(n) - s_cu[b], at = s_at[b];
-        if (n < s_cu[a.B] && i >= 0 && at >= 0 && i < a.add[b]) {
-            pos = a.lens[b] + i;
-            const int j = pos / a.page, held = a.held[b];
-            const int32_t id = j < held ? a.table[static_cast<int64_t>(b) * a.width + j]
-                                        : a.ring[(static_cast<int64_t>(at) + j - held) % a.ring_len];
-            slot = static_cast<int64_t>(id) * a.page + (pos - j * a.page);
+    // slots: a thread four tokens in a row, which mostly share a request and a
+    // page, so that the search and the table's latency are paid once for them
+    const int64_t quads = (static_cast<int64_t>(a.N) + 3) / 4;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPlanThreads + tid; i < quads;
+         i += static_cast<int64_t>(gridDim.x) * kPlanThreads) {
+        const int n0 = static_cast<int>(4 * i), end = s_cu[a.B];
+        int64_t slot[4];
+        int32_t pos[4];
+        int b = request_of(s_cu, a.B, n0), page = -1, seen = -1;
+        int32_t lo = 0, at = -1, add = 0, len = 0, held = 0, id = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int n = n0 + k;
+            slot[k] = -1;
+            pos[k] = 0;
+            if (n >= end || n >= a.N) continue;
+            while (b + 1 < a.B && s_cu[b + 1] <= n) ++b;
+            if (b != seen) {
+                seen = b;
+                page = -1;
+                lo = s_cu[b], at = s_at[b], add = a.add[b], len = a.lens[b], held = a.held[b];
+            }
+            const int t = n - lo;
+            if (t < 0 || at < 0 || t >= add) continue;
+            pos[k] = len + t;
+            const int j = pos[k] / a.page;
+            if (j != page) {
+                page = j;
+                id = j < held ? a.table[static_cast<int64_t>(b) * a.width + j]
+                              : a.ring[(static_cast<int64_t>(at) + j - held) % a.ring_len];
+            }
+            slot[k] = static_cast<int64_t>(id) * a.page + (pos[k] - j * a.page);
         }
-        a.slots[n] = slot;
-        a.pos[n] = pos;
+        if (wide && n0 + 3 < a.N) {
+            longlong2 *to = reinterpret_cast<longlong2 *>(a.slots + n0);
+            to[0] = make_longlong2(slot[0], slot[1]);
+            to[1] = make_longlong2(slot[2], slot[3]);
+            *reinterpret_cast<int4 *>(a.pos + n0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (n0 + k < a.N) a.slots[n0 + k] = slot[k], a.pos[n0 + k] = pos[k];
+        }
     }
 }
 
@@ -207,12 +235,16 @@ __global__ void __launch_bounds__(64 * W) tree_plan_kernel(const int32_t *parent
 }
 
 // -------------------------------------------------------------- kv_put -----
-// A warp a token and four of its heads (q heads, then k, then v): lane l holds
-// D/32 consecutive columns, so the squares are summed as the pairwise tree (the
-// lane's values, then the butterfly) and column i + D/2 is in lane l ^ 16.
-// The four heads' loads are issued before the first is used, and the token's
-// rotation is read once for them.
-constexpr int kPutHeads = 4;
+// A warp a token and 8 of its heads (4 of 256 columns), q heads, then k, then v,
+// two at a time: lane l of a half warp holds columns V*l .. V*l+V-1 of a head
+// (V = D/32) and the ones D/2 further on, so that the rotation stays in the
+// lane.  The squares are summed as the pairwise tree: each half of the columns
+// in the lane and over the lanes, then the two halves.  The warps of a full
+// grid go through all units, a unit's heads are loaded at once, beside the
+// token's rotation and before its slot is looked at, and the next unit's row,
+// slot and position are already on their way.  Instructions bound it as much as
+// bytes: a lane a column pair, not a lane a column, and the heads' norm factors
+// (a division, a root and a reciprocal, each rounded) side by side in the lanes.
 constexpr int kPutWarps = 8;
 
 template <typename T>
@@ -232,6 +264,12 @@ __device__ __forceinline__ T narrow(float v) {
     } else {
         return __float2half_rn(v);
     }
+}
+
+// a / b of nonnegative numbers, in 32 bits where they fit (64-bit division is
+// a long subroutine)
+__device__ __forceinline__ int64_t div_up_to_64(int64_t a, int64_t b) {
+    return (a | b) >> 32 ? a / b : static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
 }
 
 // E consecutive values, E * sizeof(T) = 4, 8, 16 or 32 bytes
@@ -267,79 +305,128 @@ __device__ __forceinline__ void store_e(T *p, const float (&v)[E]) {
     }
 }
 
+template <int D>
+struct Put {
+    static constexpr int V = D / 32;                    // columns of a chunk
+    static constexpr int kSteps = D == 256 ? 2 : 4;
+    static constexpr int kHeads = 2 * kSteps;           // of a unit
+};
+
+// Pairwise tree of V values.
+template <int V>
+__device__ __forceinline__ float chunk_tree(const float (&u)[V]) {
+    float x[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = __fmul_rn(u[i], u[i]);
+#pragma unroll
+    for (int k = V / 2; k >= 1; k >>= 1)
+#pragma unroll
+        for (int i = 0; i < k; ++i) x[i] = __fadd_rn(x[2 * i], x[2 * i + 1]);
+    return x[0];
+}
+
 template <typename S, typename T, int D>
-__global__ void __launch_bounds__(32 * kPutWarps) kv_put_kernel(const __grid_constant__ abg_kv_put_args a,
-                                                                int groups) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * kPutWarps + (threadIdx.x >> 5);
-    const int64_t n = unit / groups;
-    const int h0 = static_cast<int>(unit - n * groups) * kPutHeads;
+__global__ void __launch_bounds__(32 * kPutWarps, D == 256 ? 3 : 4) kv_put_kernel(
+    const __grid_constant__ abg_kv_put_args a, int groups) {
+    using P = Put<D>;
+    constexpr int V = P::V, kSteps = P::kSteps;
+    const int lane = threadIdx.x & 31, l = lane & 15, half = lane >> 4;
+    const int64_t units = a.N * groups, stride = static_cast<int64_t>(gridDim.x) * kPutWarps;
+    const int nq = a.q ? static_cast<int>(a.Hq) : 0, nk = static_cast<int>(a.Hkv), heads = nq + 2 * nk;
     grid_dep_wait();
-    if (n >= a.N) return;
-    const int64_t src = a.rows ? a.rows[n] : n;
-    if (src < 0 || src >= a.src_rows) return;
-    const int nq = a.q ? static_cast<int>(a.Hq) : 0, nk = static_cast<int>(a.Hkv);
-    const int64_t slot = a.slots ? a.slots[n] : n;
-    const bool kept = slot >= 0 && slot < a.pages * a.page;
-    float u[kPutHeads][E];
-    bool act[kPutHeads];
+    struct Token {
+        int64_t n, src, slot;
+        int32_t pos;
+        int h0;
+    };
+    auto token = [&](int64_t unit) {
+        Token t{0, -1, -1, 0, 0};
+        if (unit >= units) return t;
+        t.n = div_up_to_64(unit, groups);
+        t.h0 = static_cast<int>(unit - t.n * groups) * P::kHeads;
+        t.src = a.rows ? a.rows[t.n] : t.n;
+        t.slot = a.slots ? a.slots[t.n] : t.n;
+        if (a.cos) t.pos = a.pos[t.n];
+        return t;
+    };
+    int64_t unit = static_cast<int64_t>(blockIdx.x) * kPutWarps + (threadIdx.x >> 5);
+    Token t = token(unit);
+    for (; unit < units; unit += stride) {
+        const Token next = token(unit + stride);
+        if (t.src >= 0 && t.src < a.src_rows) {
+            float u[kSteps][2][V], c[V], s[V];
 #pragma unroll
-    for (int r = 0; r < kPutHeads; ++r) {
-        const int h = h0 + r;
-        act[r] = h < nq || (kept && h < nq + 2 * nk);
-        if (!act[r]) continue;
-        const S *p = h < nq        ? static_cast<const S *>(a.q) + src * a.q_row + h * a.q_head
-                     : h < nq + nk ? static_cast<const S *>(a.k) + src * a.k_row + (h - nq) * a.k_head
-                                   : static_cast<const S *>(a.v) + src * a.v_row + (h - nq - nk) * a.v_head;
-        load_e<S, E>(p + lane * E, u[r]);
-    }
-    float c[E], s[E];
-    if (a.cos) {
-        const int32_t p = a.pos[n];
-        const bool in = p >= 0 && p < a.cos_rows;
-        const int64_t at = (in ? p : 0) * static_cast<int64_t>(D / 2) + (lane & 15) * E;
-        load_e<float, E>(a.cos + at, c);
-        load_e<float, E>(a.sin + at, s);
-        if (!in)
-#pragma unroll
-            for (int i = 0; i < E; ++i) c[i] = s[i] = __int_as_float(0x7fc00000);
-    }
-    const int64_t page = kept ? slot / a.page : 0;
-    const int64_t base = page * a.Hkv * a.page + (slot - page * a.page);
-#pragma unroll
-    for (int r = 0; r < kPutHeads; ++r) {
-        const int h = h0 + r;
-        if (!act[r]) continue;
-        if (h < nq + nk) {
-            const float *w = h < nq ? a.qn_w : a.kn_w;
-            if (w) {
-                float wv[E], t[E];
-                load_e<float, E>(w + lane * E, wv);
-#pragma unroll
-                for (int i = 0; i < E; ++i) t[i] = __fmul_rn(u[r][i], u[r][i]);
-#pragma unroll
-                for (int k = E / 2; k >= 1; k >>= 1)
-#pragma unroll
-                    for (int i = 0; i < k; ++i) t[i] = __fadd_rn(t[2 * i], t[2 * i + 1]);
-                const float ss = warp_tree<32>(t[0]);
-                const float f = __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(ss, static_cast<float>(D)), a.eps)));
-#pragma unroll
-                for (int i = 0; i < E; ++i) u[r][i] = __fmul_rn(__fmul_rn(u[r][i], f), wv[i]);
+            for (int r = 0; r < kSteps; ++r) {
+                const int h = t.h0 + 2 * r + half;
+                if (h >= heads) continue;
+                const S *p = h < nq        ? static_cast<const S *>(a.q) + t.src * a.q_row + h * a.q_head
+                             : h < nq + nk ? static_cast<const S *>(a.k) + t.src * a.k_row + (h - nq) * a.k_head
+                                           : static_cast<const S *>(a.v) + t.src * a.v_row + (h - nq - nk) * a.v_head;
+                load_e<S, V>(p + V * l, u[r][0]);
+                load_e<S, V>(p + D / 2 + V * l, u[r][1]);
             }
-            if (a.cos) {
+            if (a.cos && t.h0 < nq + nk) {
+                const bool in = t.pos >= 0 && t.pos < a.cos_rows;
+                const int64_t at = (in ? t.pos : 0) * static_cast<int64_t>(D / 2) + V * l;
+                load_e<float, V>(a.cos + at, c);
+                load_e<float, V>(a.sin + at, s);
+                if (!in)
 #pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    const float o = __shfl_xor_sync(0xffffffffu, u[r][i], 16);
-                    const float uc = __fmul_rn(u[r][i], c[i]), os = __fmul_rn(o, s[i]);
-                    u[r][i] = lane < 16 ? __fsub_rn(uc, os) : __fadd_rn(uc, os);
+                    for (int i = 0; i < V; ++i) c[i] = s[i] = __int_as_float(0x7fc00000);
+            }
+            float factor = 0.0f;  // lane r of a half: of the half's head of step r
+            if ((a.qn_w && t.h0 < nq) || (a.kn_w && t.h0 < nq + nk && t.h0 + P::kHeads > nq)) {
+                float ss = 0.0f;
+#pragma unroll
+                for (int r = 0; r < kSteps; ++r) {
+                    const float lo = chunk_tree<V>(u[r][0]), hi = chunk_tree<V>(u[r][1]);
+                    // even lanes go on with the lower columns' sum, odd ones with the upper's
+                    const float away = __shfl_xor_sync(0xffffffffu, l & 1 ? lo : hi, 1);
+                    float sum = __fadd_rn(l & 1 ? hi : lo, away);
+#pragma unroll
+                    for (int d = 2; d < 16; d <<= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
+                    sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, 1));
+                    if (l == r) ss = sum;
                 }
+                factor = __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(ss, static_cast<float>(D)), a.eps)));
+            }
+            const bool kept = t.slot >= 0 && t.slot < a.pages * a.page;
+            const int64_t page = kept ? div_up_to_64(t.slot, a.page) : 0;
+            const int64_t base = page * a.Hkv * a.page + (t.slot - page * a.page);
+#pragma unroll
+            for (int r = 0; r < kSteps; ++r) {
+                const int h = t.h0 + 2 * r + half;
+                const float f = __shfl_sync(0xffffffffu, factor, r, 16);
+                if (h >= heads || (h >= nq && !kept)) continue;
+                if (h < nq + nk) {
+                    const float *w = h < nq ? a.qn_w : a.kn_w;
+                    if (w) {
+                        float wv[2][V];
+                        load_e<float, V>(w + V * l, wv[0]);
+                        load_e<float, V>(w + D / 2 + V * l, wv[1]);
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            u[r][0][i] = __fmul_rn(__fmul_rn(u[r][0][i], f), wv[0][i]);
+                            u[r][1][i] = __fmul_rn(__fmul_rn(u[r][1][i], f), wv[1][i]);
+                        }
+                    }
+                    if (a.cos) {
+#pragma unroll
+                        for (int i = 0; i < V; ++i) {
+                            const float x = u[r][0][i], y = u[r][1][i];
+                            u[r][0][i] = __fsub_rn(__fmul_rn(x, c[i]), __fmul_rn(y, s[i]));
+                            u[r][1][i] = __fadd_rn(__fmul_rn(y, c[i]), __fmul_rn(x, s[i]));
+                        }
+                    }
+                }
+                T *to = h < nq        ? static_cast<T *>(a.qo) + (t.n * a.Hq + h) * D
+                        : h < nq + nk ? static_cast<T *>(a.Kc) + (base + (h - nq) * a.page) * D
+                                      : static_cast<T *>(a.Vc) + (base + (h - nq - nk) * a.page) * D;
+                store_e<T, V>(to + V * l, u[r][0]);
+                store_e<T, V>(to + D / 2 + V * l, u[r][1]);
             }
         }
-        T *to = h < nq        ? static_cast<T *>(a.qo) + (n * a.Hq + h) * D
-                : h < nq + nk ? static_cast<T *>(a.Kc) + (base + (h - nq) * a.page) * D
-                              : static_cast<T *>(a.Vc) + (base + (h - nq - nk) * a.page) * D;
-        store_e<T, E>(to + lane * E, u[r]);
+        t = next;
     }
 }
 
@@ -369,12 +456,13 @@ __global__ void __launch_bounds__(kBestThreads) best_kernel(const float *logits,
     uint64_t key = 0;
     const float4 *quads = reinterpret_cast<const float4 *>(row + q0);
     int64_t q = tid;
-    for (; q + 3 * kBestThreads < nq; q += 4 * kBestThreads) {
-        float4 v[4];
+    constexpr int kBatch = 8;  // loads in flight
+    for (; q + (kBatch - 1) * kBestThreads < nq; q += kBatch * kBestThreads) {
+        float4 v[kBatch];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = __ldcs(quads + q + k * kBestThreads);
+        for (int k = 0; k < kBatch; ++k) v[k] = __ldcs(quads + q + k * kBestThreads);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kBatch; ++k) {
             const uint32_t i = static_cast<uint32_t>(q0 + 4 * (q + k * kBestThreads));
             key = max(key, max(max(best_key(v[k].x, i), best_key(v[k].y, i + 1)),
                                max(best_key(v[k].z, i + 2), best_key(v[k].w, i + 3))));
@@ -399,8 +487,8 @@ __global__ void __launch_bounds__(kBestThreads) best_kernel(const float *logits,
     grid_dep_launch();
 }
 
-// A block a request, a thread a draft (block B: the padding rows).  The first
-// right child of every draft is found by all threads at once; one thread then
+// A block a request, a warp a draft for the answers of its slices, then a thread
+// a draft (block B: the padding rows).  The first right child of every draft is found by all threads at once; one thread then
 // follows the chain.
 __global__ void __launch_bounds__(ABG_MAX_SPAN) accept_kernel(const int32_t *tok, const int32_t *parent,
                                                               const int32_t *cu, int32_t *best, int32_t *rows,
@@ -411,12 +499,17 @@ __global__ void __launch_bounds__(ABG_MAX_SPAN) accept_kernel(const int32_t *tok
     grid_dep_wait();
     const int lo = max(0, b < B ? cu[b] : cu[B]), hi = min(N, b < B ? cu[b + 1] : N);
     const int T = b < B ? max(0, min(hi - lo, ABG_MAX_SPAN)) : 0;
-    for (int64_t n = static_cast<int64_t>(lo) + i; n < hi; n += ABG_MAX_SPAN) {
+    for (int64_t n = static_cast<int64_t>(lo) + (i >> 5); n < hi; n += ABG_MAX_SPAN / 32) {
         uint64_t key = 0;
-        for (int s = 0; s < splits; ++s) key = max(key, parts[n * splits + s]);
-        best[n] = static_cast<int32_t>(~static_cast<uint32_t>(key));
-        rows[n] = -1;
-        if (n - lo < T) s_best[n - lo] = best[n];
+        for (int s = i & 31; s < splits; s += 32) key = max(key, parts[n * splits + s]);
+#pragma unroll
+        for (int d = 16; d >= 1; d >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, d));
+        if ((i & 31) == 0) {
+            const int v = static_cast<int32_t>(~static_cast<uint32_t>(key));
+            best[n] = v;
+            rows[n] = -1;
+            if (n - lo < T) s_best[n - lo] = v;
+        }
     }
     if (b >= B) return;
     s_next[i] = ABG_MAX_SPAN;
@@ -438,8 +531,9 @@ __global__ void __launch_bounds__(ABG_MAX_SPAN) accept_kernel(const int32_t *tok
 }
 
 int64_t best_slices(int64_t N, int64_t V) {
-    // about four blocks an SM, slices of 4096 logits at least
-    const int64_t want = std::max<int64_t>(1, 4 * 152 / std::max<int64_t>(1, N));
+    // about twelve blocks an SM (the even share of ever shorter slices against
+    // a block's start), slices of 4096 logits at least
+    const int64_t want = std::max<int64_t>(1, 12 * 152 / std::max<int64_t>(1, N));
     return std::max<int64_t>(1, std::min<int64_t>(want, (V + 4095) / 4096));
 }
 
@@ -465,26 +559,34 @@ cudaError_t launch_tree_plan(const int32_t *parent, const int32_t *lens, const i
                          mask, pos, B, N);
 }
 
+template <typename S, typename T, int D>
+static cudaError_t put_d(const abg_kv_put_args &a, cudaStream_t stream) {
+    // as many blocks as fit at once
+    static const int fit = [] {
+        int per = 0;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kv_put_kernel<S, T, D>, 32 * kPutWarps, 0) !=
+            cudaSuccess)
+            per = 1;
+        return std::max(per, 1) * sm_count();
+    }();
+    const int heads = static_cast<int>((a.q ? a.Hq : 0) + 2 * a.Hkv);
+    const int groups = (heads + Put<D>::kHeads - 1) / Put<D>::kHeads;
+    const int64_t blocks = (a.N * groups + kPutWarps - 1) / kPutWarps;
+    return launch_kernel(kv_put_kernel<S, T, D>, dim3(static_cast<unsigned>(std::min<int64_t>(blocks, fit))),
+                         dim3(32 * kPutWarps), 0, stream, false, a, groups);
+}
 template <typename S, typename T>
-static cudaError_t put_d(const abg_kv_put_args &a, dim3 grid, int groups, cudaStream_t stream) {
-    auto *fn = a.D == 64 ? kv_put_kernel<S, T, 64> : a.D == 128 ? kv_put_kernel<S, T, 128> : kv_put_kernel<S, T, 256>;
-    return launch_kernel(fn, grid, dim3(32 * kPutWarps), 0, stream, false, a, groups);
+static cudaError_t put(const abg_kv_put_args &a, cudaStream_t stream) {
+    return a.D == 64 ? put_d<S, T, 64>(a, stream) : a.D == 128 ? put_d<S, T, 128>(a, stream) : put_d<S, T, 256>(a, stream);
 }
 
 cudaError_t launch_kv_put(const abg_kv_put_args &a, cudaStream_t stream) {
-    const int heads = static_cast<int>((a.q ? a.Hq : 0) + 2 * a.Hkv);
-    const int groups = (heads + kPutHeads - 1) / kPutHeads;
-    const int64_t blocks = (a.N * groups + kPutWarps - 1) / kPutWarps;
-    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    const dim3 grid(static_cast<unsigned>(blocks));
     const bool f32 = a.src_type == ABG_SB_F32;
     switch (a.type) {
-    case ABG_SB_F32: return put_d<float, float>(a, grid, groups, stream);
+    case ABG_SB_F32: return put<float, float>(a, stream);
     case ABG_SB_BF16:
-        return f32 ? put_d<float, __nv_bfloat16>(a, grid, groups, stream)
-                   : put_d<__nv_bfloat16, __nv_bfloat16>(a, grid, groups, stream);
-    default:
-        return f32 ? put_d<float, __half>(a, grid, groups, stream) : put_d<__half, __half>(a, grid, groups, stream);
+        return f32 ? put<float, __nv_bfloat16>(a, stream) : put<__nv_bfloat16, __nv_bfloat16>(a, stream);
+    default: return f32 ? put<float, __half>(a, stream) : put<__half, __half>(a, stream);
     }
 }
 
