@@ -326,7 +326,7 @@ __device__ __forceinline__ float chunk_tree(const float (&u)[V]) {
 }
 
 template <typename S, typename T, int D>
-__global__ void __launch_bounds__(32 * kPutWarps, D == 256 ? 3 : 4) kv_put_kernel(
+__global__ void __launch_bounds__(32 * kPutWarps, D == 256 ? 2 : D == 128 ? 3 : 4) kv_put_kernel(
     const __grid_constant__ abg_kv_put_args a, int groups) {
     using P = Put<D>;
     constexpr int V = P::V, kSteps = P::kSteps;

@@ -199,13 +199,28 @@ __device__ __forceinline__ int tile_tokens(const AttnSeg &s, int t) {
     return t < s.ctiles ? min(kKT, s.req.len - t * kKT) : min(kKT, s.req.T - (t - s.ctiles) * kKT);
 }
 
-// Which of a stretch's ring items hold K and V of its tile j (of n), in the
-// order the issuing warp first needs them.  Rows in both groups: K0 V0 K1 V1 ..;
+// Which of a stretch's ring items holds V of its tile j (of n).  The order is the
+// one the issuing warp first needs them.  Rows in both groups: K0 V0 K1 V1 ..;
 // otherwise a step ahead: K0 K1 V0 K2 V1 .. V(n-1).
-__device__ __forceinline__ int item_k(bool both, int j) { return both ? 2 * j : j == 0 ? 0 : 2 * j - 1; }
 __device__ __forceinline__ int item_v(bool both, int j, int n) {
     return both || j == n - 1 ? 2 * j + 1 : 2 * j + 2;
 }
+
+// A ring slot and the phase of its item.
+struct Place {
+    int slot;
+    uint32_t phase;
+    __device__ __forceinline__ void skip(int items, int slots) {
+        slot += items;
+        if (items > slots) {
+            phase ^= (slot / slots) & 1;
+            slot %= slots;
+        } else if (slot >= slots) {
+            slot -= slots;
+            phase ^= 1;
+        }
+    }
+};
 
 __device__ __forceinline__ bool elect() {
     uint32_t p;
@@ -319,73 +334,74 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
                 mbar_wait(&bars.full[i % kSlots], (i / kSlots) & 1);
     } else if (warp == kIssueWarp) {
         // ------------------------------------------------- the issuing warp
-        // All lanes keep the same place and wait; one elected lane issues.
-        constexpr uint32_t kQK = instr_desc<T>(128, kKT, false), kPV = instr_desc<T>(128, D, true);
-        const uint64_t dq = smem_desc(smem_u32(sm.q), 16), dk = smem_desc(smem_u32(sm.ring), 16),
-                       dv = smem_desc(smem_u32(sm.ring), kKT * 128);
-        const bool one = elect();
-        int first_item = 0, seg = 0;        // ring item of the stretch's first tile
-        // bit b: next phase of buffer b's pv_done (the first wait passes), p_full
-        uint32_t done = 3, weights = 0;
-        for (; live && line.next(p, s); ++seg) {
-            const bool both = s.rows > 128;
-            const int n = s.t1 - s.t0, steps = both ? 2 * n : n;
-            live = wait16(&bars.q_full, seg & 1, &sm.gone);
-            // S of step i (buffer i & 1): row group i & 1 and tile i / 2, or tile i
-            auto product = [&](int i) {
-                const int b = i & 1, item = first_item + item_k(both, both ? i >> 1 : i), at = item % kSlots;
-                live = live && wait16(&bars.full[at], (item / kSlots) & 1, &sm.gone) &&
-                       wait16(&bars.pv_done[b], done >> b & 1, &sm.gone);
-                live = __all_sync(0xffffffffu, live);
-                if (!live) return;
-                done ^= 1u << b;
-                tc_after();
-                if (one) {
-                    const uint64_t q = dq + (both && b ? S::kQTile >> 4 : 0u), k = dk + at * (S::kTile >> 4);
+        // One elected lane does it all: every product waits on it, so that
+        // it keeps its places in the ring instead of working them out.
+        if (elect()) {
+            constexpr uint32_t kQK = instr_desc<T>(128, kKT, false), kPV = instr_desc<T>(128, D, true);
+            const uint64_t dq = smem_desc(smem_u32(sm.q), 16), dk = smem_desc(smem_u32(sm.ring), 16),
+                           dv = smem_desc(smem_u32(sm.ring), kKT * 128);
+            Place first{0, 0};          // of the stretch's first item
+            uint32_t done = 3;          // bit b: next phase of buffer b's pv_done (the first wait passes)
+            uint32_t weights = 0;       // of p_full
+            for (int seg = 0; live && line.next(p, s); ++seg) {
+                const bool both = s.rows > 128;
+                const int n = s.t1 - s.t0, steps = both ? 2 * n : n;
+                Place k = first, v = first;
+                v.skip(both || n == 1 ? 1 : 2, kSlots);
+                // S of step i (buffer i & 1): row group i & 1 and tile i / 2, or tile i
+                auto product = [&](int i) {
+                    const int b = i & 1;
+                    live = wait16(&bars.full[k.slot], k.phase, &sm.gone) &&
+                           wait16(&bars.pv_done[b], done >> b & 1, &sm.gone);
+                    if (!live) return;
+                    done ^= 1u << b;
+                    tc_after();
+                    const uint64_t q = dq + (both && b ? S::kQTile >> 4 : 0u), kd = dk + k.slot * (S::kTile >> 4);
 #pragma unroll
                     for (int d = 0; d < D / 16; ++d)
                         mma_ss(tmem + b * 128, q + (((d / 4) * (128 * 128) + (d % 4) * 32) >> 4),
-                               k + (((d / 4) * (kKT * 128) + (d % 4) * 32) >> 4), kQK, d > 0);
+                               kd + (((d / 4) * (kKT * 128) + (d % 4) * 32) >> 4), kQK, d > 0);
                     tc_commit(&bars.s_full[b]);
-                    if (!both || b) tc_commit(&bars.empty[at]);
-                }
-                __syncwarp();
-            };
-            product(0);
-            if (steps > 1) product(1);
-            for (int i = 0; live && i < steps; ++i) {
-                const int b = i & 1, j = both ? i >> 1 : i;
-                const int item = first_item + item_v(both, j, n), at = item % kSlots;
-                live = wait16(&bars.full[at], (item / kSlots) & 1, &sm.gone) &&
-                       wait16(&bars.p_full[b], weights >> b & 1, &sm.gone) &&
-                       (i > 0 || seg == 0 || wait16(&bars.o_free, (seg - 1) & 1, &sm.gone));
-                live = __all_sync(0xffffffffu, live);
-                if (!live) break;
-                weights ^= 1u << b;
-                tc_after();
-                if (one) {
-                    const uint64_t v = dv + at * (S::kTile >> 4);
+                    if (!both || b) {
+                        tc_commit(&bars.empty[k.slot]);
+                        k.skip(both || i > 0 ? 2 : 1, kSlots);
+                    }
+                };
+                live = wait16(&bars.q_full, seg & 1, &sm.gone);
+                if (live) product(0);
+                if (live && steps > 1) product(1);
+                for (int i = 0; live && i < steps; ++i) {
+                    const int b = i & 1, j = both ? i >> 1 : i;
+                    live = wait16(&bars.full[v.slot], v.phase, &sm.gone) &&
+                           wait16(&bars.p_full[b], weights >> b & 1, &sm.gone) &&
+                           (i > 0 || seg == 0 || wait16(&bars.o_free, (seg - 1) & 1, &sm.gone));
+                    if (!live) break;
+                    weights ^= 1u << b;
+                    tc_after();
+                    const uint64_t vd = dv + v.slot * (S::kTile >> 4);
                     const uint32_t o = tmem + kTmemO + (kGroups == 2 && b ? 128u : 0u), w = tmem + b * 128;
                     const bool add = i >= kGroups;  // not the first into this O
                     const int tokens = tile_tokens<kKT>(s, s.t0 + j);
                     if (tokens > kKT - 16) {
 #pragma unroll
-                        for (int k = 0; k < kKT / 16; ++k) mma_ts(o, w + k * 8, v + k * 128, kPV, add || k > 0);
+                        for (int e = 0; e < kKT / 16; ++e) mma_ts(o, w + e * 8, vd + e * 128, kPV, add || e > 0);
                     } else {  // past the tokens there is no weight
-                        for (int k = 0; k < (tokens + 15) / 16; ++k)
-                            mma_ts(o, w + k * 8, v + k * 128, kPV, add || k > 0);
+                        for (int e = 0; e < (tokens + 15) / 16; ++e)
+                            mma_ts(o, w + e * 8, vd + e * 128, kPV, add || e > 0);
                     }
                     tc_commit(&bars.pv_done[b]);
-                    if (!both || b) tc_commit(&bars.empty[at]);
+                    if (!both || b) {
+                        tc_commit(&bars.empty[v.slot]);
+                        v.skip(both || j + 2 != n ? 2 : 1, kSlots);
+                    }
+                    if (i + 2 < steps) product(i + 2);
                 }
-                __syncwarp();
-                if (i + 2 < steps) product(i + 2);
+                first.skip(2 * n, kSlots);
             }
-            first_item += 2 * n;
-        }
-        if (!live) {  // matrix instructions in flight read this block's memory
-            if (one) tc_commit(&bars.drain);
-            mbar_wait(&bars.drain, 0);
+            if (!live) {  // matrix instructions in flight read this block's memory
+                tc_commit(&bars.drain);
+                mbar_wait(&bars.drain, 0);
+            }
         }
     } else {
         // ------------------------------------------------- the softmax rows
