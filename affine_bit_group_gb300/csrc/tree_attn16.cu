@@ -9,13 +9,15 @@
 //                 into TMEM as 16-bit values over S's own columns
 //   O += P V      tcgen05.mma with P read from TMEM, V from shared memory
 //
-// for 128 rows and one tile.  Two warpgroups take turns, each with its own S and
-// O columns of TMEM, so that one's exponentials run beside the other's products:
-// with more than 128 rows in the unit each has 128 of the rows and both use
-// every tile (each tile is read once for 256 rows); with fewer, each has every
-// second tile and the two results are joined at the end.  256 columns a head
-// leave TMEM for one O only: there one warpgroup takes every step, with two S
-// buffers.
+// for 128 rows and one tile, S in two buffers of TMEM.  With more than 128 rows in
+// the unit two warpgroups have 128 of them each and take turns, one's
+// exponentials beside the other's products, and each tile is read once for 256
+// rows.  With fewer rows both take every tile, one its first 64 tokens and the
+// other the rest, each with a maximum, a weight sum and an O of its own, joined
+// at the end (a step's length is what bounds it there, and this halves its
+// longest part; taking turns by tile measured 2850 cycles a tile against a
+// memory share of 2800).  256 columns a head leave TMEM for one O only: there one
+// warpgroup takes every step.
 //
 // Three warps (two, with one group) bring K and V tiles with TMA into a ring of
 // tile-sized slots, one issues the matrix instructions.  The pages of the cache need not be aligned
@@ -64,7 +66,7 @@ struct Maps {
 
 struct Bars {
     uint64_t full[12], empty[12];
-    uint64_t s_full[2], p_full[2], pv_done[2];
+    uint64_t s_full[2], p_full[2], p_halves[2], pv_done[2];  // p_halves: P by both groups
     uint64_t q_full, o_free, ml_full, drain;
 };
 
@@ -249,7 +251,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
         sm.gone = 0;
         for (int i = 0; i < kSlots; ++i) mbar_init(&bars.full[i], 1), mbar_init(&bars.empty[i], 1);
         for (int i = 0; i < 2; ++i)
-            mbar_init(&bars.s_full[i], 1), mbar_init(&bars.p_full[i], 4), mbar_init(&bars.pv_done[i], 1);
+            mbar_init(&bars.s_full[i], 1), mbar_init(&bars.p_full[i], 4), mbar_init(&bars.pv_done[i], 1),
+                mbar_init(&bars.p_halves[i], 8);
         mbar_init(&bars.q_full, 4), mbar_init(&bars.o_free, 4 * kGroups);
         mbar_init(&bars.ml_full, 4 * kGroups), mbar_init(&bars.drain, 1);
         fence_mbar_init();
@@ -342,7 +345,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
                            dv = smem_desc(smem_u32(sm.ring), kKT * 128);
             Place first{0, 0};          // of the stretch's first item
             uint32_t done = 3;          // bit b: next phase of buffer b's pv_done (the first wait passes)
-            uint32_t weights = 0;       // of p_full
+            uint32_t weights = 0;       // of p_full; from bit 2 on of p_halves
             for (int seg = 0; live && line.next(p, s); ++seg) {
                 const bool both = s.rows > 128;
                 const int n = s.t1 - s.t0, steps = both ? 2 * n : n;
@@ -370,24 +373,34 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
                 live = wait16(&bars.q_full, seg & 1, &sm.gone);
                 if (live) product(0);
                 if (live && steps > 1) product(1);
+                const bool halves = kGroups == 2 && !both;
+                bool upper = false;  // the second half's O has been written
                 for (int i = 0; live && i < steps; ++i) {
-                    const int b = i & 1, j = both ? i >> 1 : i;
+                    const int b = i & 1, j = both ? i >> 1 : i, p_bit = halves ? b + 2 : b;
                     live = wait16(&bars.full[v.slot], v.phase, &sm.gone) &&
-                           wait16(&bars.p_full[b], weights >> b & 1, &sm.gone) &&
+                           wait16(halves ? &bars.p_halves[b] : &bars.p_full[b], weights >> p_bit & 1, &sm.gone) &&
                            (i > 0 || seg == 0 || wait16(&bars.o_free, (seg - 1) & 1, &sm.gone));
                     if (!live) break;
-                    weights ^= 1u << b;
+                    weights ^= 1u << p_bit;
                     tc_after();
                     const uint64_t vd = dv + v.slot * (S::kTile >> 4);
-                    const uint32_t o = tmem + kTmemO + (kGroups == 2 && b ? 128u : 0u), w = tmem + b * 128;
-                    const bool add = i >= kGroups;  // not the first into this O
-                    const int tokens = tile_tokens<kKT>(s, s.t0 + j);
-                    if (tokens > kKT - 16) {
+                    const uint32_t o = tmem + kTmemO, w = tmem + b * 128;
+                    // sums over `count` 16-token steps from step e0 on; past the
+                    // tile's tokens there is no weight
+                    const int count = (tile_tokens<kKT>(s, s.t0 + j) + 15) / 16;
+                    auto sums = [&](uint32_t to, uint32_t from, int e0, int e1, bool add) {
 #pragma unroll
-                        for (int e = 0; e < kKT / 16; ++e) mma_ts(o, w + e * 8, vd + e * 128, kPV, add || e > 0);
-                    } else {  // past the tokens there is no weight
-                        for (int e = 0; e < (tokens + 15) / 16; ++e)
-                            mma_ts(o, w + e * 8, vd + e * 128, kPV, add || e > 0);
+                        for (int e = 0; e < kKT / 16; ++e)
+                            if (e >= e0 && e < e1) mma_ts(to, from + (e - e0) * 8, vd + e * 128, kPV, add || e > e0);
+                    };
+                    if (halves) {
+                        sums(o, w, 0, min(count, 4), i > 0);
+                        if (count > 4) {
+                            sums(o + 128, w + 64, 4, count, upper);
+                            upper = true;
+                        }
+                    } else {
+                        sums(o + (both && b ? 128u : 0u), w, 0, count, both ? i > 1 : i > 0);
                     }
                     tc_commit(&bars.pv_done[b]);
                     if (!both || b) {
@@ -442,7 +455,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
             float ref = -INFINITY, l = 0.0f;
             const uint32_t o_at = tmem + kTmemO + lanes;  // group 0's O
             const uint32_t o_mine = o_at + group * 128;
-            for (int i = kGroups == 2 ? group : 0; i < steps; i += kGroups) {
+            // this group's steps, and its 64-token halves of their tiles
+            const bool halves = kGroups == 2 && !both;
+            const int h0 = halves ? group : 0, nh = halves ? 1 : kKT / 64;
+            for (int i = both ? group : 0; i < steps; i += both ? 2 : 1) {
                 const int b = i & 1, j = both ? i >> 1 : i, t = s.t0 + j;
                 const bool drafts = t >= s.ctiles;
                 const int tokens = tile_tokens<kKT>(s, t), key0 = (t - s.ctiles) * kKT;
@@ -473,7 +489,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
                     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                     for (int h = kKT / 64 - 1; h >= 0; --h) {
-                        read(h);
+                        if (h >= nh) continue;
+                        read(h0 + h);
 #pragma unroll
                         for (int k = 0; k < 64; k += 8)
 #pragma unroll
@@ -489,9 +506,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
                         const float f = up ? ex2(ref - to) : 1.0f;
                         ref = to;
                         l *= f;
-                        if (i >= kGroups) {  // O holds this group's earlier steps
-                            // the last one used the other buffer if there is one group
-                            const int pb = kGroups == 2 ? b : b ^ 1;
+                        if (i > (both ? 1 : 0)) {  // O holds this group's earlier steps
+                            const int pb = both ? b : b ^ 1;  // the last one's buffer
                             live = __all_sync(0xffffffffu, wait16(&bars.pv_done[pb], done >> pb & 1, &sm.gone));
                             if (!live) break;
                             tc_after();
@@ -511,7 +527,8 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
                     float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
                     for (int h = 0; h < kKT / 64; ++h) {
-                        if (h > 0) read(h);
+                        if (h >= nh) continue;
+                        if (h > 0) read(h0 + h);
                         uint32_t w[32];
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
@@ -521,7 +538,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
                             sum[e & 1] = add2(sum[e & 1], v);
                             w[e] = pack2<T>(v.x, v.y);
                         }
-                        tmem_st32(sbuf + 32 * h, w);
+                        tmem_st32(sbuf + 64 * h0 + 32 * h, w);
                     }
                     l += (sum[0].x + sum[1].x) + (sum[0].y + sum[1].y);
                     tmem_st_wait();
@@ -537,7 +554,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
                     live = __all_sync(0xffffffffu, wait16(&bars.full[item % kSlots], (item / kSlots) & 1, &sm.gone));
                     if (!live) break;
                     unsigned char *v = sm.ring + static_cast<uint32_t>(item % kSlots) * S::kTile;
-                    for (int e = tid & 127; e < all * (D / 8); e += 128) {
+                    for (int e = both ? tid & 127 : tid; e < all * (D / 8); e += both ? 128 : 128 * kGroups) {
                         const int q = e / (D / 8), ch = e % (D / 8);
                         uint4 *at = reinterpret_cast<uint4 *>(v + (ch / 8) * (kKT * 128) + q * 128 +
                                                               ((ch % 8) ^ (q % 8)) * 16);
@@ -563,36 +580,31 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
                 }
                 tc_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars.p_full[b]);
+                if (lane == 0) mbar_arrive(halves ? &bars.p_halves[b] : &bars.p_full[b]);
                 done ^= 1u << b;
             }
             if (!live) break;
-            // phases of the other group's buffer
-            if (kGroups == 2) {
-                const int others = group ? (steps + 1) / 2 : steps / 2;
-                if (others & 1) scores ^= 2u >> group, done ^= 2u >> group;
-            }
+            if (both && (n & 1)) scores ^= 2u >> group, done ^= 2u >> group;  // the other group's buffer
             first_item += 2 * n;
             // The group of the last step has seen its S, and with it the end of
             // every product that reads Q: the next stretch's Q comes before
             // this one's results are written.
             more = line.next(p, next);
-            if (more && group == (kGroups == 2 ? (steps - 1) & 1 : 0)) bring_q(next, seg + 1);
+            if (more && group == (both ? 1 : 0)) bring_q(next, seg + 1);
             // the products of the stretch's last steps
             live = wait16(&bars.pv_done[0], done & 1, &sm.gone) &&
                    (steps < 2 || wait16(&bars.pv_done[1], done >> 1 & 1, &sm.gone));
             live = __all_sync(0xffffffffu, live);
             if (!live) break;
             tc_after();
-            const bool joined = kGroups == 2 && !both;  // both groups worked for the same rows
             float2 mine_ml = make_float2(ref, l), other_ml = make_float2(-INFINITY, 0.0f);
             if (kGroups == 2) {
                 // (a product of this stretch is done, so every row has read
                 // the last one's O, and sm.ml before it)
-                if (joined) sm.ml[group][tid & 127] = mine_ml;
+                if (halves) sm.ml[group][tid & 127] = mine_ml;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars.ml_full);
-                if (joined) {
+                if (halves) {
                     live = __all_sync(0xffffffffu, wait16(&bars.ml_full, seg & 1, &sm.gone));
                     if (!live) break;
                     other_ml = sm.ml[group ^ 1][tid & 127];
@@ -601,17 +613,16 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
             const bool whole = s.t0 == 0 && s.t1 == s.tiles;
             const int64_t piece = static_cast<int64_t>(2) * blockIdx.x + (s.t0 == 0);
             const int64_t at = (row * a.Hq + s.h * p.G + (s.r0 + (mine ? r : 0)) % p.G) * D;
-            // joined: each group takes half of the columns of both O (of 64
+            // after halves each group takes half of the columns of both O (of 64
             // columns the first takes all: a group sum has 64)
-            const bool two = joined && steps > 1;
-            const int k0 = joined && D > 64 ? group * (D / 2) : 0;
-            const int k1 = !joined ? D : D > 64 ? k0 + D / 2 : group ? 0 : D;
+            const int k0 = halves && D > 64 ? group * (D / 2) : 0;
+            const int k1 = !halves ? D : D > 64 ? k0 + D / 2 : group ? 0 : D;
             const float M = fmaxf(ref, other_ml.x);
             const float fm = l == 0.0f ? 0.0f : ex2(ref - M);
             const float fo = other_ml.y == 0.0f ? 0.0f : ex2(other_ml.x - M);
             const float L = l * fm + other_ml.y * fo;
             // in O's order: group 0's factor first
-            const float f0 = joined && group ? fo : fm, f1 = joined && group ? fm : fo;
+            const float f0 = halves && group ? fo : fm, f1 = halves && group ? fm : fo;
             if (busy) {
                 float sums = 0.0f;
                 const float scale = 1.0f / L;
@@ -619,11 +630,11 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
                 for (int k = k0; k < k1; k += 32) {
                     float o[32], o1[32];
                     __syncwarp();  // rows past the unit's have skipped ahead
-                    tmem_ld32((joined ? o_at : o_mine) + k, o);
-                    if (two) tmem_ld32(o_at + 128 + k, o1);
+                    tmem_ld32((halves ? o_at : o_mine) + k, o);
+                    if (halves) tmem_ld32(o_at + 128 + k, o1);
                     tmem_ld_wait();
                     if (!mine) continue;
-                    if (two)
+                    if (halves)
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             o[e] = (f0 == 0.0f ? 0.0f : o[e] * f0) + (f1 == 0.0f ? 0.0f : o1[e] * f1);
