@@ -13,14 +13,14 @@ namespace abg {
 
 namespace {
 
-constexpr int kThreads = 512;
-// The work line is cut at every 32 tokens, and a stretch is taken in tiles of
-// up to 64: with the few tiles a block gets of f32 work (a tile of 64 rows is
-// 8 us of an SM), the even split counts more than the tile.
-constexpr int kKT = 32, kTile = 64;
+constexpr int kThreads = 256;
+constexpr int kKT = 32;  // tokens a tile
 
-// Rows of a unit: up to 4, 16 or 32 where a request has no more, else 64.
-constexpr int kOneRows = 4, kFewRows = 16, kSomeRows = 32, kManyRows = 64;
+// Rows of a unit: up to 4 or 16 where a request has no more, else 32.  A block
+// with a tile and 32 rows of 256 columns takes half of an SM's shared memory:
+// two blocks an SM fill the gaps between each other's barriers (one block of 64
+// rows and 64 tokens measured 72 us where these take FIGURE).
+constexpr int kOneRows = 4, kFewRows = 16, kManyRows = 32;
 
 __device__ __forceinline__ void cp16(void *dst, const void *src, bool real) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(real ? 16 : 0)
@@ -34,18 +34,16 @@ __device__ __forceinline__ void cp_wait() {
 
 template <int D, int kRT>
 struct Smem {
-    static constexpr int kLd = D + 4;                       // rows of Q and K start in different banks
+    static constexpr int kLd = D + 4;                        // rows of Q and K start in different banks
     static constexpr int kPLd = kRT + 4;
-    static constexpr int kWide = kRT > kFewRows;             // score tiles of 4 x 4 a thread
-    static constexpr int kParts = kWide ? 8 * 16 / kRT : 8;  // column parts of the scores
+    static constexpr int kParts = kRT == kManyRows ? 2 : 8;  // column parts of the scores
     float q[kRT][kLd];
-    float k[kTile][kLd];
-    float v[kTile][D];
-    float p[kTile][kPLd];                     // weights, token-major
-    // partial scores: of all parts, or (wide) of the third part on
-    float part[kWide ? kParts - 2 : kParts][kTile][kWide ? kPLd : kRT];
+    float k[kKT][kLd];
+    float v[kKT][D];
+    float p[kKT][kPLd];                       // weights, token-major
+    float part[kParts][kRT][kKT + 1];         // partial scores
     float corr[kRT];
-    int64_t off[2][kTile];                    // a tile's row offsets in elements (-1: none)
+    int64_t off[2][kKT];                      // a tile's row offsets in elements (-1: none)
     float m[kRT], l[kRT];
     AttnScan scan;
     uint32_t bad[ABG_MAX_SPAN / 32];          // drafts whose V holds an infinity or a NaN
@@ -74,42 +72,41 @@ __device__ __forceinline__ void load_tile(float *dst, int ld, const float *src, 
     cp_commit();
 }
 
-// A tile: tokens key0 .. key0+tokens-1 of the cache or of the drafts; `to` is
-// the stretch's work after it.
+// Tile t of a stretch: tokens key0 .. key0+tokens-1 of the cache or of the drafts.
 struct Tile {
     bool cache;
-    int key0, tokens, to;
+    int key0, tokens;
 };
 __device__ __forceinline__ Tile tile_at(const AttnSeg &s, int t) {
     Tile x;
     x.cache = t < s.ctiles;
-    x.to = min(t + kTile / kKT, x.cache ? min(s.ctiles, s.t1) : s.t1);
     x.key0 = (x.cache ? t : t - s.ctiles) * kKT;
-    x.tokens = min((x.to - t) * kKT, (x.cache ? s.req.len : s.req.T) - x.key0);
+    x.tokens = min(kKT, (x.cache ? s.req.len : s.req.T) - x.key0);
     return x;
 }
 
 // One part of the work line.  Scores: up to 16 rows, a thread holds an eighth of
-// the columns of one token for all rows, and the eighths meet in shared memory;
-// 32 or 64 rows, a quarter or half of the columns of four rows by four tokens.  Then thread (ty,
-// tx) = (tid / 16, tid % 16) has the scores of kRPS rows and tokens tx + 16 j.  Sums: a thread
-// holds four columns of kRPO rows, two rows to a packed pair, over every
-// kKS-th token.  f32 arithmetic is what bounds it above about 16 rows (0.5
-// multiply-adds a byte and row against 11 a byte that an SM can do); below,
-// latency and the cache's bytes.
+// the columns of one token for all rows; 32 rows, half of the columns of two
+// rows by four tokens.  The parts meet in shared memory, where 32 lanes or
+// fewer take a row each for its maximum, weights and sum.  Weighted sums: a
+// thread holds four columns of kRPO rows, two rows to a packed pair, over every
+// kKS-th token.  Multiply-adds bound it above about 16 rows (half a multiply-add
+// a byte and row, against 11 a byte that an SM can do); below, latency and the
+// cache's bytes.
 template <int D, int kRT>
-__global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ AttnArgs p) {
+__global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant__ AttnArgs p) {
     using S = Smem<D, kRT>;
     extern __shared__ __align__(16) unsigned char raw[];
     S &sm = *reinterpret_cast<S *>(raw);
     const abg_tree_attn_args &a = p.a;
-    constexpr int kRPS = S::kWide ? 4 : 1;           // rows of a softmax thread
-    constexpr int kTY = S::kWide ? kRT / 4 : 32;     // thread rows of a score tile
     constexpr int kParts = S::kParts;
-    constexpr int kRPO = kRT < 8 ? kRT : 8;        // rows of a thread's sums
+    constexpr int kLanes = kThreads / kRT < 32 ? kThreads / kRT : 32;  // of a row's softmax
+    constexpr int kEach = kKT / kLanes;                                // a lane's tokens of it
+    constexpr int kRPO = kRT < 8 ? kRT : 8;                            // rows of a thread's sums
     constexpr int kQuads = D / 4, kRG = kRT / kRPO, kKS = kThreads / (kQuads * kRG);
     constexpr int E = D / 32;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tx = tid % 16, ty = (tid % (16 * kTY)) / 16;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int row = tid / kLanes, col = tid % kLanes;  // softmax
     const int quad = tid % kQuads, rg = tid / kQuads % kRG, ks = tid / (kQuads * kRG);
     grid_dep_wait();
     grid_dep_launch();
@@ -118,48 +115,46 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
     bool left = false;
     AttnSeg s;
     while (line.next(p, s)) {
-        const bool rows_here = 2 * kRPS * warp < s.rows;  // the warp has softmax rows (whole warps: they shuffle)
-        const int part = tid / (S::kWide ? 16 * kTY : kTile);  // of the columns
+        // whole warps (they shuffle) have softmax rows or not
+        const bool rows_here = (32 * warp) / kLanes < s.rows && row < kRT;
         auto source = [&](const Tile &x, bool value) {
             return static_cast<const float *>(x.cache ? (value ? a.Vc : a.Kc) : (value ? a.Vd : a.Kd));
         };
         Tile now = tile_at(s, s.t0);
         __syncthreads();  // the last stretch's shared memory is done with
-        if (tid < kTile) sm.off[0][tid] = row_offset<D>(a, s, now.cache, now.key0 + tid);
+        if (tid < kKT) sm.off[0][tid] = row_offset<D>(a, s, now.cache, now.key0 + tid);
         for (int i = tid; i < kRT * (D / 4); i += kThreads) {
-            const int r = i / (D / 4), c = 4 * (i % (D / 4)), row = s.r0 + r;
+            const int r = i / (D / 4), c = 4 * (i % (D / 4)), q = s.r0 + r;
             const bool in = r < s.rows;
             cp16(&sm.q[r][c],
                  static_cast<const float *>(a.q) +
-                     (in ? ((static_cast<int64_t>(s.req.n0) + row / p.G) * a.Hq + s.h * p.G + row % p.G) * D + c : 0),
+                     (in ? ((static_cast<int64_t>(s.req.n0) + q / p.G) * a.Hq + s.h * p.G + q % p.G) * D + c : 0),
                  in);
         }
         if (tid < ABG_MAX_SPAN / 32) sm.bad[tid] = 0;
         __syncthreads();
         load_tile<D>(&sm.k[0][0], S::kLd, source(now, false), sm.off[0], now.tokens);  // with Q: one group
         load_tile<D>(&sm.v[0][0], D, source(now, true), sm.off[0], now.tokens);
-        float m[kRPS], l[kRPS];
+        float m = -INFINITY, l = 0.0f;
         float2 o[kRPO / 2][4];  // rows 2i and 2i+1, a column
 #pragma unroll
-        for (int i = 0; i < kRPS; ++i) m[i] = -INFINITY, l[i] = 0.0f;
-#pragma unroll
         for (int i = 0; i < kRPO / 2; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = make_float2(0.0f, 0.0f);
-        for (int buf = 0, t = s.t0; t < s.t1; buf ^= 1) {
-            const bool more = now.to < s.t1;
-            const Tile next = more ? tile_at(s, now.to) : now;
-            if (more && tid < kTile) sm.off[buf ^ 1][tid] = row_offset<D>(a, s, next.cache, next.key0 + tid);
+        for (int t = s.t0; t < s.t1; ++t) {
+            const bool more = t + 1 < s.t1;
+            const int buf = (t - s.t0) & 1;
+            const Tile next = more ? tile_at(s, t + 1) : now;
+            if (more && tid < kKT) sm.off[buf ^ 1][tid] = row_offset<D>(a, s, next.cache, next.key0 + tid);
             cp_wait<1>();
             __syncthreads();
             // scores
-            float sc[kRPS][4];
-            if constexpr (!S::kWide) {
-                const int key = tid % kTile;
+            if constexpr (kRT != kManyRows) {
+                const int key = tid % kKT, part = tid / kKT;
                 if (key < now.tokens) {
                     float2 acc[kRT];
 #pragma unroll
                     for (int r = 0; r < kRT; ++r) acc[r] = make_float2(0.0f, 0.0f);
 #pragma unroll 2
-                    for (int c = part * (D / 8); c < (part + 1) * (D / 8); c += 4) {
+                    for (int c = part * (D / kParts); c < (part + 1) * (D / kParts); c += 4) {
                         const float4 kv = *reinterpret_cast<const float4 *>(&sm.k[key][c]);
 #pragma unroll
                         for (int r = 0; r < kRT; ++r) {
@@ -169,78 +164,36 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
                         }
                     }
 #pragma unroll
-                    for (int r = 0; r < kRT; r += 4)
-                        *reinterpret_cast<float4 *>(&sm.part[part][key][r]) =
-                            make_float4(acc[r].x + acc[r].y, acc[r + 1].x + acc[r + 1].y, acc[r + 2].x + acc[r + 2].y,
-                                        acc[r + 3].x + acc[r + 3].y);
+                    for (int r = 0; r < kRT; ++r) sm.part[part][r][key] = acc[r].x + acc[r].y;
                 }
-                __syncthreads();
-                if (rows_here)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        float x[8];
-#pragma unroll
-                        for (int h = 0; h < 8; ++h) x[h] = sm.part[h][tx + 16 * j][ty];
-                        sc[0][j] = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
-                    }
             } else {
-                const bool work = 8 * (warp % (kTY / 2)) < s.rows;  // the warp's eight rows
-                auto scores = [&](auto keys) {
-                    constexpr int kKeys = decltype(keys)::value;
-                    float2 acc[kRPS][kKeys];
+                const int part = tid / 128, tx = tid % 8, ty = tid / 8 % 16;  // rows ty, ty+16, tokens tx+8j
+                float2 acc[2][4];
 #pragma unroll
-                    for (int i = 0; i < kRPS; ++i)
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                        for (int j = 0; j < kKeys; ++j) acc[i][j] = make_float2(0.0f, 0.0f);
-#pragma unroll 2
-                    for (int c = part * (D / kParts); c < (part + 1) * (D / kParts); c += 4) {
-                        float4 kv[kKeys];
+                    for (int j = 0; j < 4; ++j) acc[i][j] = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+                for (int c = part * (D / kParts); c < (part + 1) * (D / kParts); c += 4) {
+                    float4 kv[4];
 #pragma unroll
-                        for (int j = 0; j < kKeys; ++j)
-                            kv[j] = *reinterpret_cast<const float4 *>(&sm.k[tx + 16 * j][c]);
+                    for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4 *>(&sm.k[tx + 8 * j][c]);
 #pragma unroll
-                        for (int i = 0; i < kRPS; ++i) {
-                            const float4 qv = *reinterpret_cast<const float4 *>(&sm.q[ty * kRPS + i][c]);
-#pragma unroll
-                            for (int j = 0; j < kKeys; ++j) {
-                                acc[i][j] = fma2(make_float2(qv.x, qv.y), make_float2(kv[j].x, kv[j].y), acc[i][j]);
-                                acc[i][j] = fma2(make_float2(qv.z, qv.w), make_float2(kv[j].z, kv[j].w), acc[i][j]);
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int i = 0; i < kRPS; ++i)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            sc[i][j] = j < kKeys ? acc[i][j < kKeys ? j : 0].x + acc[i][j < kKeys ? j : 0].y : 0.0f;
-                };
-                if (work) {
-                    if (now.tokens > 32) {
-                        scores(std::integral_constant<int, 4>{});
-                    } else {
-                        scores(std::integral_constant<int, 2>{});
-                    }
-                    // the second part's go through the weights' memory
-                    if (part)
+                    for (int i = 0; i < 2; ++i) {
+                        const float4 qv = *reinterpret_cast<const float4 *>(&sm.q[ty + 16 * i][c]);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            float *to = &sm.p[tx + 16 * j][ty * 4];
-                            if (kParts > 2 && part > 1) to = &sm.part[part - 2][tx + 16 * j][ty * 4];
-                            *reinterpret_cast<float4 *>(to) = make_float4(sc[0][j], sc[1][j], sc[2][j], sc[3][j]);
+                            acc[i][j] = fma2(make_float2(qv.x, qv.y), make_float2(kv[j].x, kv[j].y), acc[i][j]);
+                            acc[i][j] = fma2(make_float2(qv.z, qv.w), make_float2(kv[j].z, kv[j].w), acc[i][j]);
                         }
+                    }
                 }
-                __syncthreads();
-                if (rows_here)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                        for (int h = 1; h < kParts; ++h) {
-                            const float *from = h == 1 ? &sm.p[tx + 16 * j][ty * 4]
-                                                       : &sm.part[h > 1 ? h - 2 : 0][tx + 16 * j][ty * 4];
-                            const float4 x = *reinterpret_cast<const float4 *>(from);
-                            sc[0][j] += x.x, sc[1][j] += x.y, sc[2][j] += x.z, sc[3][j] += x.w;
-                        }
+                    for (int j = 0; j < 4; ++j) sm.part[part][ty + 16 * i][tx + 8 * j] = acc[i][j].x + acc[i][j].y;
             }
+            __syncthreads();
             if (more) {
                 load_tile<D>(&sm.k[0][0], S::kLd, source(next, false), sm.off[buf ^ 1], next.tokens);
             } else {
@@ -248,45 +201,40 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
             }
             // softmax statistics and weights
             if (rows_here) {
+                const uint64_t *seen = nullptr;
+                if (!now.cache && row < s.rows)
+                    seen = a.mask + (static_cast<int64_t>(s.req.n0) + (s.r0 + row) / p.G) * a.words;
+                float sc[kEach], top = m;
 #pragma unroll
-                for (int i = 0; i < kRPS; ++i) {
-                    const int r = ty * kRPS + i;
-                    const uint64_t *seen = nullptr;
-                    if (!now.cache && r < s.rows)
-                        seen = a.mask + (static_cast<int64_t>(s.req.n0) + (s.r0 + r) / p.G) * a.words;
-                    float top = m[i];
+                for (int j = 0; j < kEach; ++j) {
+                    const int k = col + kLanes * j;
+                    float x[kParts];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int k = tx + 16 * j;
-                        const bool in = k < now.tokens && (now.cache || (seen && attn_sees(seen, now.key0 + k)));
-                        sc[i][j] = in ? sc[i][j] * p.scale2 : -INFINITY;
-                        top = fmaxf(top, sc[i][j]);
-                    }
+                    for (int h = 0; h < kParts; ++h) x[h] = sm.part[h][row][k];
 #pragma unroll
-                    for (int d = 8; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                    const float ref = top == -INFINITY ? 0.0f : top;
-                    const float corr = exp2f(m[i] - ref);
-                    float sum = 0.0f;
+                    for (int w = kParts / 2; w >= 1; w /= 2)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        sc[i][j] = exp2f(sc[i][j] - ref);
-                        sum += sc[i][j];
-                    }
-#pragma unroll
-                    for (int d = 8; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                    l[i] = l[i] * corr + sum;
-                    m[i] = top;
-                    if (tx == 0) sm.corr[r] = corr;
+                        for (int h = 0; h < w; ++h) x[h] = x[2 * h] + x[2 * h + 1];
+                    const bool in = k < now.tokens && (now.cache || (seen && attn_sees(seen, now.key0 + k)));
+                    sc[j] = in ? x[0] * p.scale2 : -INFINITY;
+                    top = fmaxf(top, sc[j]);
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float *to = &sm.p[tx + 16 * j][ty * kRPS];
-                    if constexpr (kRPS == 4) {
-                        *reinterpret_cast<float4 *>(to) = make_float4(sc[0][j], sc[1][j], sc[2][j], sc[3][j]);
-                    } else {
-                        *to = sc[0][j];
-                    }
+                for (int d = kLanes / 2; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                const float ref = top == -INFINITY ? 0.0f : top;
+                const float corr = exp2f(m - ref);
+                float sum = 0.0f;
+#pragma unroll
+                for (int j = 0; j < kEach; ++j) {
+                    const float e = exp2f(sc[j] - ref);
+                    sum += e;
+                    sm.p[col + kLanes * j][row] = e;
                 }
+#pragma unroll
+                for (int d = kLanes / 2; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                l = l * corr + sum;
+                m = top;
+                if (col == 0) sm.corr[row] = corr;
             }
             cp_wait<1>();
             __syncthreads();
@@ -312,7 +260,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
                 for (int e = 0; e < 4; ++e) o[i][e] = mul2(o[i][e], f);
             }
 #pragma unroll 4
-            for (int k = rg * kRPO < s.rows ? ks : now.tokens; k < now.tokens; k += kKS) {
+            for (int k = rg * kRPO < s.rows ? ks : kKT; k < now.tokens; k += kKS) {
                 const float4 v = *reinterpret_cast<const float4 *>(&sm.v[k][4 * quad]);
                 const float2 vv[4] = {make_float2(v.x, v.x), make_float2(v.y, v.y), make_float2(v.z, v.z),
                                       make_float2(v.w, v.w)};
@@ -332,7 +280,6 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
             } else {
                 cp_commit();
             }
-            t = now.to;
             now = next;
         }
         cp_wait<0>();
@@ -367,9 +314,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
                 *place(0, i, 0) = make_float4(o[i][0].x, o[i][1].x, o[i][2].x, o[i][3].x);
                 *place(0, i, 1) = make_float4(o[i][0].y, o[i][1].y, o[i][2].y, o[i][3].y);
             }
-        if (tx == 0 && rows_here)
-#pragma unroll
-            for (int i = 0; i < kRPS; ++i) sm.m[ty * kRPS + i] = m[i], sm.l[ty * kRPS + i] = l[i];
+        if (col == 0 && rows_here) sm.m[row] = m, sm.l[row] = l;
         __syncthreads();
         const bool whole = s.t0 == 0 && s.t1 == s.tiles;
         const int64_t slot = static_cast<int64_t>(2) * blockIdx.x + (s.t0 == 0);
@@ -404,8 +349,7 @@ __global__ void __launch_bounds__(kThreads) attn_kernel(const __grid_constant__ 
 }
 
 int row_tile(int64_t G, int64_t max_span) {
-    const int64_t rows = G * max_span;
-    return rows <= kOneRows ? kOneRows : rows <= kFewRows ? kFewRows : rows <= kSomeRows ? kSomeRows : kManyRows;
+    return G * max_span <= kOneRows ? kOneRows : G * max_span <= kFewRows ? kFewRows : kManyRows;
 }
 
 template <int D, int kRT>
@@ -442,7 +386,6 @@ template <int D, typename F>
 auto by_rows(int rt, F f) {
     return rt == kOneRows   ? f.template operator()<D, kOneRows>()
            : rt == kFewRows ? f.template operator()<D, kFewRows>()
-           : rt == kSomeRows ? f.template operator()<D, kSomeRows>()
                             : f.template operator()<D, kManyRows>();
 }
 template <typename F>
