@@ -37,39 +37,35 @@ struct Smem {
     static constexpr int kLd = D + 4;                        // rows of Q and K start in different banks
     static constexpr int kPLd = kRT + 4;
     static constexpr int kParts = kRT == kManyRows ? 2 : 8;  // column parts of the scores
+    // K and V tiles on their way beside the ones in use, where two blocks fit
+    static constexpr int kStages = D == 256 ? 1 : 2;
     float q[kRT][kLd];
-    float k[kKT][kLd];
-    float v[kKT][D];
+    float k[kStages][kKT][kLd];
+    float v[kStages][kKT][D];
     float p[kKT][kPLd];                       // weights, token-major
     float part[kParts][kRT][kKT + 1];         // partial scores
     float corr[kRT];
-    int64_t off[2][kKT];                      // a tile's row offsets in elements (-1: none)
+    int64_t off[4][kKT];                      // row offsets of tiles in turn, in elements (-1: none)
     float m[kRT], l[kRT];
     AttnScan scan;
     uint32_t bad[ABG_MAX_SPAN / 32];          // drafts whose V holds an infinity or a NaN
 };
 
-// Where token `key` of a stretch's request lies (in elements of its tensor), -1: nowhere.
-template <int D>
-__device__ __forceinline__ int64_t row_offset(const abg_tree_attn_args &a, const AttnSeg &s, bool cache, int key) {
-    if (cache) {
-        if (key >= s.req.len) return -1;
-        const int j = static_cast<int>(key / static_cast<unsigned>(a.page));
-        const int64_t id = a.table[static_cast<int64_t>(s.b) * a.width + j];
-        if (id < 0 || id >= a.pages) return -1;
-        return ((id * a.Hkv + s.h) * a.page + (key - static_cast<int64_t>(j) * a.page)) * D;
-    }
-    return key < s.req.T ? (s.h * a.drafts + s.req.n0 + key) * static_cast<int64_t>(D) : -1;
-}
-
 template <int D>
 __device__ __forceinline__ void load_tile(float *dst, int ld, const float *src, const int64_t *off, int tokens) {
-    for (int i = threadIdx.x; i < tokens * (D / 4); i += kThreads) {
-        const int r = i / (D / 4), c = 4 * (i % (D / 4));
-        const int64_t o = off[r];
-        cp16(dst + r * ld + c, src + max(o, int64_t(0)) + c, o >= 0);
+    constexpr int kEach = kKT * (D / 4) / kThreads, kRows = kThreads / (D / 4);  // rows of a round
+    const int r0 = threadIdx.x / (D / 4), c = 4 * (threadIdx.x % (D / 4));
+    if (tokens == kKT) {  // rounds side by side: their places are read before any is needed
+        int64_t o[kEach];
+#pragma unroll
+        for (int u = 0; u < kEach; ++u) o[u] = off[r0 + u * kRows];
+#pragma unroll
+        for (int u = 0; u < kEach; ++u)
+            cp16(dst + (r0 + u * kRows) * ld + c, src + max(o[u], int64_t(0)) + c, o[u] >= 0);
+    } else {
+        for (int r = r0; r < tokens; r += kRows)
+            cp16(dst + r * ld + c, src + max(off[r], int64_t(0)) + c, off[r] >= 0);
     }
-    cp_commit();
 }
 
 // Tile t of a stretch: tokens key0 .. key0+tokens-1 of the cache or of the drafts.
@@ -83,6 +79,23 @@ __device__ __forceinline__ Tile tile_at(const AttnSeg &s, int t) {
     x.key0 = (x.cache ? t : t - s.ctiles) * kKT;
     x.tokens = min(kKT, (x.cache ? s.req.len : s.req.T) - x.key0);
     return x;
+}
+
+// Page of the tile's token i (0 for drafts), and, given it, where the token's row
+// lies (in elements of its tensor; -1: nowhere).  In two steps, so that the
+// table's latency passes during another tile's work.
+__device__ __forceinline__ int32_t page_of(const abg_tree_attn_args &a, const AttnSeg &s, const Tile &x, int i) {
+    if (!x.cache || i >= x.tokens) return 0;
+    return a.table[static_cast<int64_t>(s.b) * a.width + static_cast<uint32_t>(x.key0 + i) / static_cast<uint32_t>(a.page)];
+}
+template <int D>
+__device__ __forceinline__ int64_t row_offset(const abg_tree_attn_args &a, const AttnSeg &s, const Tile &x, int i,
+                                              int32_t id) {
+    if (i >= x.tokens) return -1;
+    if (!x.cache) return (s.h * a.drafts + s.req.n0 + x.key0 + i) * static_cast<int64_t>(D);
+    if (id < 0 || id >= a.pages) return -1;
+    const uint32_t in_page = static_cast<uint32_t>(x.key0 + i) % static_cast<uint32_t>(a.page);
+    return ((static_cast<int64_t>(id) * a.Hkv + s.h) * a.page + in_page) * D;
 }
 
 // One part of the work line.  Scores: up to 16 rows, a thread holds an eighth of
@@ -120,9 +133,19 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
         auto source = [&](const Tile &x, bool value) {
             return static_cast<const float *>(x.cache ? (value ? a.Vc : a.Kc) : (value ? a.Vd : a.Kd));
         };
-        Tile now = tile_at(s, s.t0);
+        constexpr int kStages = S::kStages;
+        const int n = s.t1 - s.t0;
         __syncthreads();  // the last stretch's shared memory is done with
-        if (tid < kKT) sm.off[0][tid] = row_offset<D>(a, s, now.cache, now.key0 + tid);
+        int32_t id = 0;   // page of the token that this thread looks up next
+        if (tid < kKT) {
+#pragma unroll
+            for (int u = 0; u < kStages; ++u)
+                if (u < n) {
+                    const Tile x = tile_at(s, s.t0 + u);
+                    sm.off[u][tid] = row_offset<D>(a, s, x, tid, page_of(a, s, x, tid));
+                }
+            if (kStages < n) id = page_of(a, s, tile_at(s, s.t0 + kStages), tid);
+        }
         for (int i = tid; i < kRT * (D / 4); i += kThreads) {
             const int r = i / (D / 4), c = 4 * (i % (D / 4)), q = s.r0 + r;
             const bool in = r < s.rows;
@@ -133,18 +156,32 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
         }
         if (tid < ABG_MAX_SPAN / 32) sm.bad[tid] = 0;
         __syncthreads();
-        load_tile<D>(&sm.k[0][0], S::kLd, source(now, false), sm.off[0], now.tokens);  // with Q: one group
-        load_tile<D>(&sm.v[0][0], D, source(now, true), sm.off[0], now.tokens);
+        auto bring = [&](int u, bool value) {  // tile u of the stretch (Q goes with the first); a group each
+            if (u < n) {
+                const Tile x = tile_at(s, s.t0 + u);
+                if (value) {
+                    load_tile<D>(&sm.v[u % kStages][0][0], D, source(x, true), sm.off[u & 3], x.tokens);
+                } else {
+                    load_tile<D>(&sm.k[u % kStages][0][0], S::kLd, source(x, false), sm.off[u & 3], x.tokens);
+                }
+            }
+            cp_commit();
+        };
+#pragma unroll
+        for (int u = 0; u < kStages; ++u) bring(u, false), bring(u, true);
         float m = -INFINITY, l = 0.0f;
         float2 o[kRPO / 2][4];  // rows 2i and 2i+1, a column
 #pragma unroll
         for (int i = 0; i < kRPO / 2; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = make_float2(0.0f, 0.0f);
-        for (int t = s.t0; t < s.t1; ++t) {
-            const bool more = t + 1 < s.t1;
-            const int buf = (t - s.t0) & 1;
-            const Tile next = more ? tile_at(s, t + 1) : now;
-            if (more && tid < kKT) sm.off[buf ^ 1][tid] = row_offset<D>(a, s, next.cache, next.key0 + tid);
-            cp_wait<1>();
+        for (int u = 0; u < n; ++u) {
+            const Tile now = tile_at(s, s.t0 + u);
+            const int st = u % kStages;
+            // the places of tile u + kStages, and the pages of the one after it
+            if (tid < kKT && u + kStages < n) {
+                sm.off[(u + kStages) & 3][tid] = row_offset<D>(a, s, tile_at(s, s.t0 + u + kStages), tid, id);
+                if (u + kStages + 1 < n) id = page_of(a, s, tile_at(s, s.t0 + u + kStages + 1), tid);
+            }
+            cp_wait<2 * kStages - 1>();
             __syncthreads();
             // scores
             if constexpr (kRT != kManyRows) {
@@ -155,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
                     for (int r = 0; r < kRT; ++r) acc[r] = make_float2(0.0f, 0.0f);
 #pragma unroll 2
                     for (int c = part * (D / kParts); c < (part + 1) * (D / kParts); c += 4) {
-                        const float4 kv = *reinterpret_cast<const float4 *>(&sm.k[key][c]);
+                        const float4 kv = *reinterpret_cast<const float4 *>(&sm.k[st][key][c]);
 #pragma unroll
                         for (int r = 0; r < kRT; ++r) {
                             const float4 qv = *reinterpret_cast<const float4 *>(&sm.q[r][c]);
@@ -177,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
                 for (int c = part * (D / kParts); c < (part + 1) * (D / kParts); c += 4) {
                     float4 kv[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4 *>(&sm.k[tx + 8 * j][c]);
+                    for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4 *>(&sm.k[st][tx + 8 * j][c]);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const float4 qv = *reinterpret_cast<const float4 *>(&sm.q[ty + 16 * i][c]);
@@ -194,11 +231,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
                     for (int j = 0; j < 4; ++j) sm.part[part][ty + 16 * i][tx + 8 * j] = acc[i][j].x + acc[i][j].y;
             }
             __syncthreads();
-            if (more) {
-                load_tile<D>(&sm.k[0][0], S::kLd, source(next, false), sm.off[buf ^ 1], next.tokens);
-            } else {
-                cp_commit();
-            }
+            bring(u + kStages, false);
             // softmax statistics and weights
             if (rows_here) {
                 const uint64_t *seen = nullptr;
@@ -236,14 +269,14 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
                 m = top;
                 if (col == 0) sm.corr[row] = corr;
             }
-            cp_wait<1>();
+            cp_wait<2 * kStages - 1>();
             __syncthreads();
             if (!now.cache) {
                 // an infinity or a NaN in a draft's V must not reach the rows
                 // that do not see it (0 * NaN): taken out here, and added at the
                 // end to the rows that do
                 for (int i = tid; i < now.tokens * D; i += kThreads) {
-                    float &v = sm.v[i / D][i % D];
+                    float &v = sm.v[st][i / D][i % D];
                     if (!(fabsf(v) < INFINITY)) {
                         v = 0.0f;
                         const int k = now.key0 + i / D;
@@ -261,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
             }
 #pragma unroll 4
             for (int k = rg * kRPO < s.rows ? ks : kKT; k < now.tokens; k += kKS) {
-                const float4 v = *reinterpret_cast<const float4 *>(&sm.v[k][4 * quad]);
+                const float4 v = *reinterpret_cast<const float4 *>(&sm.v[st][k][4 * quad]);
                 const float2 vv[4] = {make_float2(v.x, v.x), make_float2(v.y, v.y), make_float2(v.z, v.z),
                                       make_float2(v.w, v.w)};
 #pragma unroll
@@ -275,17 +308,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
                 }
             }
             __syncthreads();
-            if (more) {
-                load_tile<D>(&sm.v[0][0], D, source(next, true), sm.off[buf ^ 1], next.tokens);
-            } else {
-                cp_commit();
-            }
-            now = next;
+            bring(u + kStages, true);
         }
         cp_wait<0>();
         // the token groups' sums, halving the groups each time, through the
         // memory of the K and V tiles; then [kRT][D] there
-        float *os = &sm.k[0][0];
+        float *os = &sm.k[0][0][0];
         static_assert(sizeof(float) * kRT * D * (kKS > 1 ? kKS / 2 : 1) <= sizeof sm.k + sizeof sm.v, "groups' sums");
         auto place = [&](int g, int i, int h) {
             return reinterpret_cast<float4 *>(os + (g * kRT + rg * kRPO + 2 * i + h) * D + 4 * quad);
