@@ -531,9 +531,8 @@ __global__ void __launch_bounds__(ABG_MAX_SPAN) accept_kernel(const int32_t *tok
 }
 
 int64_t best_slices(int64_t N, int64_t V) {
-    // about twelve blocks an SM (the even share of ever shorter slices against
-    // a block's start), slices of 4096 logits at least
-    const int64_t want = std::max<int64_t>(1, 12 * 152 / std::max<int64_t>(1, N));
+    // four blocks an SM (all at once: 51.7 us for 304 rows against 52.8 with eight), slices of 4096 logits at least
+    const int64_t want = std::max<int64_t>(1, 4 * 152 / std::max<int64_t>(1, N));
     return std::max<int64_t>(1, std::min<int64_t>(want, (V + 4095) / 4096));
 }
 

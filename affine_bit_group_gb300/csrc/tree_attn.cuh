@@ -400,9 +400,10 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
 // pieces each: more warps a row.
 template <typename T, int D, int kRT, bool kByQuad>
 cudaError_t launch_join(const AttnArgs &p, int C, bool pdl, cudaStream_t stream) {
-    const int64_t units = p.per_head ? p.units : C;
-    const int64_t rows = std::min<int64_t>(kRT, p.a.max_span * p.G);
-    const int64_t pieces = C / units + 1;
+    const int64_t units = p.per_head ? p.units : C, span_rows = p.a.max_span * p.G;
+    const int64_t rows = std::min<int64_t>(kRT, span_rows);
+    const int64_t filled = p.a.B * p.a.Hkv * ((span_rows + kRT - 1) / kRT);  // units with rows, of spans as told
+    const int64_t pieces = C / std::max<int64_t>(1, filled) + 1;
     auto go = [&](auto w) {
         constexpr int kWarps = decltype(w)::value;
         const dim3 grid(static_cast<unsigned>(units), static_cast<unsigned>((rows * kWarps + 7) / 8));
