@@ -5,7 +5,7 @@ cache (page_plan, tree_plan, kv_put, tree_attn, tree_accept).
 
 This module only marshals arguments: tensors become device pointers, the
 current torch stream becomes a cudaStream_t, and status codes become
-exceptions.  Every step of the computation runs in the library's CUDA kernels;
+exceptions (for the draft calls in a compiled module, csrc/marshal.cpp).  Every step of the computation runs in the library's CUDA kernels;
 there is no CPU path.  PyTorch supplies device memory and streams.
 
 The C declarations, with the meaning, layout, ownership and error behaviour
@@ -15,7 +15,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 import threading
 
 __all__ = [
@@ -317,64 +316,32 @@ def atq(q, gate, k, v, qn_w, kn_w, cos, sin, Kc, Vc, y, ysum, pos: int, eps: flo
     return y
 
 
-class _Torch:
-    """What the calls below need of torch, looked up once."""
-
-    def __init__(self):
-        import torch
-        self.i32, self.i64, self.f32, self.u8 = torch.int32, torch.int64, torch.float32, torch.uint8
-        self.empty = torch.empty
-        self.type_of = {torch.float32: SB_F32, torch.bfloat16: SB_BF16, torch.float16: SB_F16}
+_marshal = None  # the CPython module that takes the draft calls' tensors apart, once imported
 
 
-_torch = None
+def _load_marshal():
+    library()  # builds both if stale
+    import importlib
 
-
-def _th():
-    global _torch
-    if _torch is None:
-        _torch = _Torch()
-    return _torch
-
-
-def _packer(struct_type):
-    """Packs a struct's fields, in order, into its C layout (building the ctypes
-    structure field by field costs several times as much)."""
-    codes = {ctypes.c_void_p: "P", ctypes.c_int64: "q", ctypes.c_int32: "i", ctypes.c_float: "f"}
-    return struct.Struct("@" + "".join(codes[t] for _, t in struct_type._fields_) + "0q").pack
-
-
-_pack_kv_put, _pack_tree_attn = _packer(_KvPutArgs), _packer(_TreeAttnArgs)
+    import torch  # noqa: F401  (its libraries, which the module uses)
+    return importlib.import_module("._marshal", __name__)  # and sets the name above
 
 
 def _type_of(t, name):
-    ty = _th().type_of.get(t.dtype)
+    ty = {"torch.float32": SB_F32, "torch.bfloat16": SB_BF16, "torch.float16": SB_F16}.get(str(t.dtype))
     if ty is None:
         raise ValueError(f"{name} must be float32, bfloat16 or float16, got {t.dtype}")
     return ty
 
 
-def _need(t, dtype, numel, name):
-    """Device pointer of a contiguous CUDA tensor of this dtype with at least numel elements."""
-    if t.dtype is dtype and t.numel() >= numel and t.is_cuda and t.is_contiguous():
-        return t.data_ptr()
-    raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of at least {numel} elements")
+def _handle(stream):
+    """A stream argument as the module takes it: None for the current stream, or a handle."""
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
-def _strided(t, heads, D, dtype, name):
-    """Rows, device pointer, row and head stride of a [rows][heads][D] CUDA tensor with contiguous columns."""
-    if t.dtype is dtype and t.is_cuda and t.dim() == 3:
-        n, h, d = t.shape
-        row, head, col = t.stride()
-        if h == heads and d == D and col == 1:
-            return n, t.data_ptr(), row, head
-    raise ValueError(f"{name} must be a {dtype} CUDA tensor [rows][{heads}][{D}] with contiguous columns")
-
-
-def _cache(Kc, Vc):
-    if Kc.dim() != 4 or Vc.shape != Kc.shape or Vc.dtype is not Kc.dtype:
-        raise ValueError("the caches must be [pages][Hkv][page][D] tensors of one shape and type")
-    return _type_of(Kc, "Kc")
+def _bytes(numel, device):
+    import torch
+    return torch.empty(numel, dtype=torch.uint8, device=device)
 
 
 def page_plan(lens, add, cu, held, ends, ring, table, page: int, slots, pos, lens_out, held_out, ends_out, info,
@@ -384,16 +351,8 @@ def page_plan(lens, add, cu, held, ends, ring, table, page: int, slots, pos, len
     abg_page_plan).  table [B][width] and ring are updated in place; slots, pos,
     lens_out, held_out, ends_out and info are written.  slots and ends are
     int64, everything else is int32."""
-    th = _th()
-    i32, i64 = th.i32, th.i64
-    B, N, R = lens.numel(), slots.numel(), ring.numel()
-    width = table.numel() // max(1, B)
-    st = library().abg_page_plan(
-        _need(lens, i32, B, "lens"), _need(add, i32, B, "add"), _need(cu, i32, B + 1, "cu"),
-        _need(held, i32, B, "held"), _need(ends, i64, 2, "ends"), _need(ring, i32, R, "ring"),
-        _need(table, i32, 0, "table"), _need(slots, i64, N, "slots"), _need(pos, i32, N, "pos"),
-        _need(lens_out, i32, B, "lens_out"), _need(held_out, i32, B, "held_out"), _need(ends_out, i64, 2, "ends_out"),
-        _need(info, i32, 2, "info"), B, N, page, width, R, _stream(stream))
+    st = (_marshal or _load_marshal()).page_plan(lens, add, cu, held, ends, ring, table, page, slots, pos, lens_out,
+                                                 held_out, ends_out, info, _handle(stream))
     if st:
         _check(st, "abg_page_plan")
     return slots, pos
@@ -402,14 +361,7 @@ def page_plan(lens, add, cu, held, ends, ring, table, page: int, slots, pos, len
 def tree_plan(parent, lens, cu, mask, pos, stream=None):
     """Ancestor masks [N][words] (int64 bit words) and positions [N] of drafts
     from their parents' indices (see abg_tree_plan)."""
-    th = _th()
-    i32 = th.i32
-    B, N = lens.numel(), parent.numel()
-    if mask.dim() != 2 or mask.shape[0] != N:
-        raise ValueError("mask must be [N][words]")
-    st = library().abg_tree_plan(_need(parent, i32, N, "parent"), _need(lens, i32, B, "lens"),
-                                 _need(cu, i32, B + 1, "cu"), _need(mask, th.i64, N, "mask"),
-                                 _need(pos, i32, N, "pos"), B, N, mask.shape[1], _stream(stream))
+    st = (_marshal or _load_marshal()).tree_plan(parent, lens, cu, mask, pos, _handle(stream))
     if st:
         _check(st, "abg_tree_plan")
     return mask, pos
@@ -423,33 +375,8 @@ def kv_put(k, v, Kc, Vc, slots=None, rows=None, q=None, qo=None, qn_w=None, kn_w
     RMS norm (qn_w, kn_w [D]) and rotation (cos, sin [positions][D/2], pos [N])
     where given; q goes to qo [N][Hq][D].  k, v and q are float32 or of the
     caches' type."""
-    th = _th()
-    f32, dt, src = th.f32, Kc.dtype, k.dtype
-    ty = _cache(Kc, Vc)
-    pages, Hkv, page, D = Kc.shape
-    src_rows, kp, k_row, k_head = _strided(k, Hkv, D, src, "k")
-    v_rows, vp, v_row, v_head = _strided(v, Hkv, D, src, "v")
-    src_rows = min(src_rows, v_rows)
-    N = rows.numel() if rows is not None else slots.numel() if slots is not None else src_rows
-    Hq = qp = q_row = q_head = qop = qn = kn = cp = sp = pp = cos_rows = 0
-    if q is not None:
-        Hq = q.shape[1]
-        q_rows, qp, q_row, q_head = _strided(q, Hq, D, src, "q")
-        src_rows = min(src_rows, q_rows)
-        qop = _need(qo, dt, N * Hq * D, "qo")
-        if qn_w is not None:
-            qn = _need(qn_w, f32, D, "qn_w")
-    if kn_w is not None:
-        kn = _need(kn_w, f32, D, "kn_w")
-    if cos is not None:
-        cos_rows = cos.shape[0]
-        cp, sp = _need(cos, f32, cos_rows * (D // 2), "cos"), _need(sin, f32, cos_rows * (D // 2), "sin")
-        pp = _need(pos, th.i32, N, "pos")
-    st = library().abg_kv_put(_pack_kv_put(
-        qp, kp, vp, q_row, q_head, k_row, k_head, v_row, v_head,
-        0 if rows is None else _need(rows, th.i32, N, "rows"), 0 if slots is None else _need(slots, th.i64, N, "slots"),
-        qn, kn, cp, sp, pp, qop, _need(Kc, dt, 0, "Kc"), _need(Vc, dt, 0, "Vc"), N, src_rows, Hq, Hkv, D, page, pages,
-        cos_rows, eps, _type_of(k, "k"), ty), _stream(stream))
+    st = (_marshal or _load_marshal()).kv_put(k, v, Kc, Vc, slots, rows, q, qo, qn_w, kn_w, cos, sin, pos, eps,
+                                              _handle(stream))
     if st:
         _check(st, "abg_kv_put")
     return Kc, Vc
@@ -473,26 +400,12 @@ def tree_attn(q, Kc, Vc, table, lens, cu, Kd, Vd, mask, y, max_span: int | None 
     is a uint8 tensor of tree_attn_workspace() bytes; by default the call takes
     one from torch's allocator on the current stream (give ws for a call on
     another stream)."""
-    th = _th()
-    i32, f32, dt = th.i32, th.f32, Kc.dtype
-    ty = _cache(Kc, Vc)
-    pages, Hkv, page, D = Kc.shape
-    N, Hq, qd = q.shape
-    drafts, words = Kd.shape[1], mask.shape[1]
-    B, n = lens.numel(), N * Hq * D
-    if qd != D or Kd.shape != (Hkv, drafts, D) or Vd.shape != Kd.shape:
-        raise ValueError("q must be [N][Hq][D], Kd and Vd [Hkv][drafts][D]")
     if max_span is None:
-        max_span = 64 * words
+        max_span = 64 * mask.shape[1]
     if ws is None:
-        ws = th.empty(tree_attn_workspace(q, Kc, max_span), dtype=th.u8, device=q.device)
-    args = _pack_tree_attn(
-        _need(q, dt, n, "q"), _need(Kc, dt, 0, "Kc"), _need(Vc, dt, 0, "Vc"), _need(table, i32, 0, "table"),
-        _need(lens, i32, B, "lens"), _need(cu, i32, B + 1, "cu"), _need(Kd, dt, 0, "Kd"), _need(Vd, dt, 0, "Vd"),
-        _need(mask, th.i64, N * words, "mask"), 0 if gate is None else _need(gate, f32, n, "gate"),
-        _need(y, y.dtype, n, "y"), 0 if ysum is None else _need(ysum, f32, n // 64, "ysum"),
-        B, N, Hq, Hkv, D, page, pages, table.numel() // max(1, B), drafts, words, max_span, ty, _type_of(y, "y"))
-    st = library().abg_tree_attn(args, _need(ws, th.u8, 0, "ws"), ws.numel(), _stream(stream))
+        ws = _bytes(tree_attn_workspace(q, Kc, max_span), q.device)
+    st = (_marshal or _load_marshal()).tree_attn(q, Kc, Vc, table, lens, cu, Kd, Vd, mask, y, max_span, gate, ysum, ws,
+                                                 _handle(stream))
     if st:
         _check(st, "abg_tree_attn")
     return y
@@ -511,20 +424,9 @@ def tree_accept(logits, tok, parent, cu, best, rows, add, last, ws=None, stream=
     stride): best [N], the accepted rows of each request rows [N] and their
     number add [B], and the next tokens last [B] (see abg_tree_accept); all
     int32.  ws as in tree_attn."""
-    th = _th()
-    i32 = th.i32
-    N, V = logits.shape
-    B = add.numel()
-    ld, col = logits.stride()
-    if logits.dtype is not th.f32 or not logits.is_cuda or (col != 1 and V > 1):
-        raise ValueError("logits must be a float32 CUDA tensor [N][V] with contiguous rows")
     if ws is None:
-        ws = th.empty(tree_accept_workspace(logits), dtype=th.u8, device=logits.device)
-    st = library().abg_tree_accept(
-        logits.data_ptr(), ld if N > 1 else V, _need(tok, i32, N, "tok"), _need(parent, i32, N, "parent"),
-        _need(cu, i32, B + 1, "cu"), _need(best, i32, N, "best"), _need(rows, i32, N, "rows"),
-        _need(add, i32, B, "add"), _need(last, i32, B, "last"), B, N, V, _need(ws, th.u8, 0, "ws"), ws.numel(),
-        _stream(stream))
+        ws = _bytes(tree_accept_workspace(logits), logits.device)
+    st = (_marshal or _load_marshal()).tree_accept(logits, tok, parent, cu, best, rows, add, last, ws, _handle(stream))
     if st:
         _check(st, "abg_tree_accept")
     return rows, add, last

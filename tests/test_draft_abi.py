@@ -159,3 +159,51 @@ def test_plain_tree_attn_is_softmax_attention():
         s[:, n:][~bits[:, :N]] = -np.inf
         p = np.exp(s - s.max(1, keepdims=True))
         assert np.allclose(y[:, hq], p / p.sum(1, keepdims=True) @ V, rtol=1e-12, atol=1e-13)
+
+
+def bad_calls():
+    """(call, words of the ValueError) with tensors that the binding refuses; all
+    of them are on the CPU, which is the last thing each check looks at."""
+    import torch
+    i32, i64, f32, u8 = torch.int32, torch.int64, torch.float32, torch.uint8
+
+    def z(*shape, dtype=i32):
+        return torch.zeros(shape, dtype=dtype)
+
+    def plan(**kw):
+        a = dict(lens=z(2), add=z(2), cu=z(3), held=z(2), ends=z(2, dtype=i64), ring=z(9), table=z(2, 4), page=16,
+                 slots=z(5, dtype=i64), pos=z(5), lens_out=z(2), held_out=z(2), ends_out=z(2, dtype=i64), info=z(2))
+        return lambda: abg.page_plan(**{**a, **kw})
+
+    def put(**kw):
+        a = dict(k=z(3, 2, 64, dtype=f32), v=z(3, 2, 64, dtype=f32), Kc=z(1, 2, 8, 64, dtype=f32),
+                 Vc=z(1, 2, 8, 64, dtype=f32))
+        return lambda: abg.kv_put(**{**a, **kw})
+
+    def attn(**kw):
+        a = dict(q=z(3, 4, 64, dtype=f32), Kc=z(5, 2, 8, 64, dtype=f32), Vc=z(5, 2, 8, 64, dtype=f32), table=z(1, 4),
+                 lens=z(1), cu=z(2), Kd=z(2, 3, 64, dtype=f32), Vd=z(2, 3, 64, dtype=f32), mask=z(3, 1, dtype=i64),
+                 y=z(3, 4, 64, dtype=f32), ws=z(9, dtype=u8))
+        return lambda: abg.tree_attn(**{**a, **kw})
+
+    def accept(**kw):
+        a = dict(logits=z(3, 9, dtype=f32), tok=z(3), parent=z(3), cu=z(2), best=z(3), rows=z(3), add=z(1), last=z(1),
+                 ws=z(99, dtype=u8))
+        return lambda: abg.tree_accept(**{**a, **kw})
+
+    return [
+        (plan(), "lens must be a contiguous torch.int32 CUDA tensor"), (plan(lens=3), "lens must be a tensor"),
+        (lambda: abg.tree_plan(z(3), z(1), z(2), z(3, dtype=i64), z(3)), r"mask must be \[N\]\[words\]"),
+        (lambda: abg.tree_plan(z(3), z(1), z(2), z(3, 1, dtype=i64), z(3)), "parent must be a contiguous"),
+        (put(), "Kc must be a contiguous torch.float32 CUDA tensor"), (put(Vc=z(1, 2, 9, 64, dtype=f32)), "one shape"),
+        (put(Kc=z(2, 8, 64, dtype=f32)), "one shape"),
+        (put(Kc=z(1, 2, 8, 64), Vc=z(1, 2, 8, 64)), "Kc must be float32, bfloat16 or float16"),
+        (attn(), "Kc must be a contiguous"), (attn(Vd=None), "Vd must be a tensor"),
+        (accept(), "logits must be a float32 CUDA tensor"), (accept(logits=z(3, 9)), "logits must be a float32"),
+        (accept(add=None), "add must be a tensor")]
+
+
+def test_binding_refuses_wrong_tensors():
+    for call, words in bad_calls():
+        with pytest.raises(ValueError, match=words):
+            call()

@@ -522,3 +522,31 @@ def test_calls_record_into_a_cuda_graph():
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(c["y"], want[0]) and torch.equal(rows, want[1]) and torch.equal(add, want[2])
+
+
+# ---------------------------------------------------------------- refusals ----
+def test_binding_refuses_wrong_tensors_on_the_device():
+    c, _ = attn_case(40, "bf16", 4, 2, 64, 16, [20], [3], tail=0)
+    ws = torch.empty(abg.tree_attn_workspace(c["q"], c["Kc"], c["max_span"]), dtype=torch.uint8, device="cuda")
+    for change, words in ((dict(q=c["q"].float()), "q must be a contiguous torch.bfloat16"),
+                          (dict(q=c["q"].transpose(0, 1)), "q must be"), (dict(q=c["q"][:, :, :32]), "q must be"),
+                          (dict(lens=c["lens"].long()), "lens must be a contiguous torch.int32"),
+                          (dict(mask=c["mask"][:, 0]), "mask must be"), (dict(mask=c["mask"][:2]), "mask must be"),
+                          (dict(gate=c["gate"][:2]), "gate must be a contiguous torch.float32 CUDA tensor of at least"),
+                          (dict(Kd=c["Kd"][:, :, :32]), "q must be"), (dict(y=c["y"].int()), "y must be float32"),
+                          (dict(ws=ws.int()), "ws must be a contiguous torch.uint8"), (dict(cu=c["cu"][:1]), "cu must be")):
+        with pytest.raises(ValueError, match=words):
+            abg.tree_attn(**{**c, "ws": ws, **change})
+    with pytest.raises(abg.AbgError, match="bad shape"):
+        abg.tree_attn(**dict(c, ws=ws[:64]))
+    with pytest.raises(abg.AbgError, match="output overlaps"):
+        abg.tree_attn(**dict(c, y=c["q"], ws=ws))
+    k = torch.zeros((3, 2, 128), device="cuda")
+    Kc, Vc = (torch.zeros((1, 2, 3, 64), device="cuda") for _ in range(2))
+    with pytest.raises(ValueError, match=r"k must be a torch.float32 CUDA tensor \[rows\]\[2\]\[64\]"):
+        abg.kv_put(k[:, :, ::2], k[:, :, ::2], Kc, Vc)
+    with pytest.raises(ValueError, match="qo must be"):
+        abg.kv_put(k[:, :, :64], k[:, :, 64:], Kc, Vc, q=k[:, :, :64], qo=torch.zeros(5, device="cuda"))
+    with pytest.raises(abg.AbgError, match="misaligned"):
+        abg.kv_put(k[:, :, 1:65], k[:, :, 64:], Kc, Vc)
+    abg.kv_put(k[:, :, :64], k[:, :, 64:], Kc, Vc)  # rows and heads with strides of their own
