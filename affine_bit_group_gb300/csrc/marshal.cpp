@@ -133,8 +133,8 @@ int tree_plan(PyObject *const *a) {
     if (mask.dim() != 2 || mask.size(0) != N) throw Wrong("mask must be [N][words]");
     auto *parent_p = static_cast<int32_t *>(need(parent, ScalarType::Int, N, "parent"));
     return abg_tree_plan(parent_p, static_cast<int32_t *>(need(lens, ScalarType::Int, B, "lens")),
-                         i32(a[2], B + 1, "cu"), static_cast<uint64_t *>(need(mask, ScalarType::Long, N, "mask")), i32(a[4], N, "pos"), B, N,
-                         mask.size(1), stream_of(a[5], parent));
+                         i32(a[2], B + 1, "cu"), static_cast<uint64_t *>(need(mask, ScalarType::Long, N, "mask")),
+                         i32(a[4], N, "pos"), B, N, mask.size(1), stream_of(a[5], parent));
 }
 
 // k v Kc Vc slots rows q qo qn_w kn_w cos sin pos eps stream

@@ -198,7 +198,7 @@ def bad_calls():
         (put(), "Kc must be a contiguous torch.float32 CUDA tensor"), (put(Vc=z(1, 2, 9, 64, dtype=f32)), "one shape"),
         (put(Kc=z(2, 8, 64, dtype=f32)), "one shape"),
         (put(Kc=z(1, 2, 8, 64), Vc=z(1, 2, 8, 64)), "Kc must be float32, bfloat16 or float16"),
-        (attn(), "Kc must be a contiguous"), (attn(Vd=None), "Vd must be a tensor"),
+        (attn(), "Kc must be a contiguous"), (attn(Kc=3), "Kc must be a tensor"),
         (accept(), "logits must be a float32 CUDA tensor"), (accept(logits=z(3, 9)), "logits must be a float32"),
         (accept(add=None), "add must be a tensor")]
 
