@@ -58,6 +58,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
     __shared__ int s_bad[kPlanThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dep_wait();
+    grid_dep_launch();
     const bool wide = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.pos)) & 15) == 0;
     const int64_t head = a.ends[0], tail = a.ends[1];
     const int64_t avail = max(int64_t(0), min(tail - head, static_cast<int64_t>(a.ring_len)));
@@ -188,6 +189,7 @@ __global__ void __launch_bounds__(64 * W) tree_plan_kernel(const int32_t *parent
     __shared__ int16_t s_up[2][64 * W];
     const int b = blockIdx.x, i = threadIdx.x;
     grid_dep_wait();
+    grid_dep_launch();
     const int lo = max(0, b < B ? cu[b] : cu[B]), hi = min(N, b < B ? cu[b + 1] : N);
     const int T = b < B ? max(0, min(hi - lo, 64 * W)) : 0;
     uint64_t m[W];
@@ -333,6 +335,7 @@ __global__ void __launch_bounds__(32 * kPutWarps, D == 256 ? 2 : D == 128 ? 3 : 
     const int lane = threadIdx.x & 31, l = lane & 15, half = lane >> 4;
     const int64_t units = a.N * groups, stride = static_cast<int64_t>(gridDim.x) * kPutWarps;
     const int nq = a.q ? static_cast<int>(a.Hq) : 0, nk = static_cast<int>(a.Hkv), heads = nq + 2 * nk;
+    // (no launch after this one starts early: abg_atq's reads its key cache before it waits)
     grid_dep_wait();
     struct Token {
         int64_t n, src, slot;
@@ -449,6 +452,7 @@ __global__ void __launch_bounds__(kBestThreads) best_kernel(const float *logits,
     const int64_t n = blockIdx.x / slices;
     const float *row = logits + n * ld;
     grid_dep_wait();
+    grid_dep_launch();
     const int64_t lo = (blockIdx.x - n * slices) * slice, hi = min(V, lo + slice);
     // whole 16-byte quads from the first aligned element on, single ones around them
     const int64_t off = ((16 - (reinterpret_cast<uintptr_t>(row + lo) & 15)) & 15) / 4;
@@ -484,7 +488,6 @@ __global__ void __launch_bounds__(kBestThreads) best_kernel(const float *logits,
         for (int w = 1; w < kBestThreads / 32; ++w) key = max(key, s_key[w]);
         parts[blockIdx.x] = key;
     }
-    grid_dep_launch();
 }
 
 // A block a request, a warp a draft for the answers of its slices, then a thread
@@ -497,6 +500,7 @@ __global__ void __launch_bounds__(ABG_MAX_SPAN) accept_kernel(const int32_t *tok
     __shared__ int s_best[ABG_MAX_SPAN], s_next[ABG_MAX_SPAN], s_path[ABG_MAX_SPAN], s_count;
     const int b = blockIdx.x, i = threadIdx.x;
     grid_dep_wait();
+    grid_dep_launch();
     const int lo = max(0, b < B ? cu[b] : cu[B]), hi = min(N, b < B ? cu[b + 1] : N);
     const int T = b < B ? max(0, min(hi - lo, ABG_MAX_SPAN)) : 0;
     for (int64_t n = static_cast<int64_t>(lo) + (i >> 5); n < hi; n += ABG_MAX_SPAN / 32) {
@@ -538,28 +542,30 @@ int64_t best_slices(int64_t N, int64_t V) {
 
 }  // namespace
 
-cudaError_t launch_page_plan(const PagePlanArgs &a, cudaStream_t stream) {
+cudaError_t launch_page_plan(const PagePlanArgs &a, bool pdl, cudaStream_t stream) {
     const size_t smem = (2 * static_cast<size_t>(a.B) + 1) * sizeof(int32_t);
     static const cudaError_t attr = cudaFuncSetAttribute(
         page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (2 * ABG_MAX_REQUESTS + 1) * sizeof(int32_t));
     if (attr != cudaSuccess) return attr;
-    const int64_t blocks = std::max<int64_t>((a.N + 4ll * kPlanThreads - 1) / (4 * kPlanThreads), (a.B + 63) / 64);
+    // four tokens a thread, a request a warp
+    const int64_t blocks =
+        std::max<int64_t>((a.N + 4ll * kPlanThreads - 1) / (4 * kPlanThreads), (32ll * a.B + kPlanThreads - 1) / kPlanThreads);
     return launch_kernel(page_plan_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(blocks, 2 * sm_count()))),
-                         dim3(kPlanThreads), smem, stream, false, a);
+                         dim3(kPlanThreads), smem, stream, pdl && !capturing(stream), a);
 }
 
 cudaError_t launch_tree_plan(const int32_t *parent, const int32_t *lens, const int32_t *cu, uint64_t *mask,
-                             int32_t *pos, int B, int N, int words, cudaStream_t stream) {
+                             int32_t *pos, int B, int N, int words, bool pdl, cudaStream_t stream) {
     auto *fn = words == 1   ? tree_plan_kernel<1>
                : words == 2 ? tree_plan_kernel<2>
                : words == 3 ? tree_plan_kernel<3>
                             : tree_plan_kernel<4>;
-    return launch_kernel(fn, dim3(static_cast<unsigned>(B) + 1), dim3(64 * words), 0, stream, false, parent, lens, cu,
-                         mask, pos, B, N);
+    return launch_kernel(fn, dim3(static_cast<unsigned>(B) + 1), dim3(64 * words), 0, stream,
+                         pdl && !capturing(stream), parent, lens, cu, mask, pos, B, N);
 }
 
 template <typename S, typename T, int D>
-static cudaError_t put_d(const abg_kv_put_args &a, cudaStream_t stream) {
+static cudaError_t put_d(const abg_kv_put_args &a, bool early, cudaStream_t stream) {
     // as many blocks as fit at once
     static const int fit = [] {
         int per = 0;
@@ -572,20 +578,22 @@ static cudaError_t put_d(const abg_kv_put_args &a, cudaStream_t stream) {
     const int groups = (heads + Put<D>::kHeads - 1) / Put<D>::kHeads;
     const int64_t blocks = (a.N * groups + kPutWarps - 1) / kPutWarps;
     return launch_kernel(kv_put_kernel<S, T, D>, dim3(static_cast<unsigned>(std::min<int64_t>(blocks, fit))),
-                         dim3(32 * kPutWarps), 0, stream, false, a, groups);
+                         dim3(32 * kPutWarps), 0, stream, early, a, groups);
 }
 template <typename S, typename T>
-static cudaError_t put(const abg_kv_put_args &a, cudaStream_t stream) {
-    return a.D == 64 ? put_d<S, T, 64>(a, stream) : a.D == 128 ? put_d<S, T, 128>(a, stream) : put_d<S, T, 256>(a, stream);
+static cudaError_t put(const abg_kv_put_args &a, bool early, cudaStream_t stream) {
+    return a.D == 64    ? put_d<S, T, 64>(a, early, stream)
+           : a.D == 128 ? put_d<S, T, 128>(a, early, stream)
+                        : put_d<S, T, 256>(a, early, stream);
 }
 
-cudaError_t launch_kv_put(const abg_kv_put_args &a, cudaStream_t stream) {
-    const bool f32 = a.src_type == ABG_SB_F32;
+cudaError_t launch_kv_put(const abg_kv_put_args &a, bool pdl, cudaStream_t stream) {
+    const bool f32 = a.src_type == ABG_SB_F32, early = pdl && !capturing(stream);
     switch (a.type) {
-    case ABG_SB_F32: return put<float, float>(a, stream);
+    case ABG_SB_F32: return put<float, float>(a, early, stream);
     case ABG_SB_BF16:
-        return f32 ? put<float, __nv_bfloat16>(a, stream) : put<__nv_bfloat16, __nv_bfloat16>(a, stream);
-    default: return f32 ? put<float, __half>(a, stream) : put<__half, __half>(a, stream);
+        return f32 ? put<float, __nv_bfloat16>(a, early, stream) : put<__nv_bfloat16, __nv_bfloat16>(a, early, stream);
+    default: return f32 ? put<float, __half>(a, early, stream) : put<__half, __half>(a, early, stream);
     }
 }
 
@@ -595,16 +603,16 @@ size_t tree_accept_bytes(int64_t N, int64_t V) {
 
 cudaError_t launch_tree_accept(const float *logits, int64_t ld, const int32_t *tok, const int32_t *parent,
                                const int32_t *cu, int32_t *best, int32_t *rows, int32_t *add, int32_t *last, int B,
-                               int N, int64_t V, void *ws, cudaStream_t stream) {
+                               int N, int64_t V, void *ws, bool pdl, cudaStream_t stream) {
     const int64_t slices = best_slices(N, V);
     const int64_t slice = (V + slices - 1) / slices;
     uint64_t *parts = static_cast<uint64_t *>(ws);
     if (N > 0) {
         const cudaError_t e = launch_kernel(best_kernel, dim3(static_cast<unsigned>(slices * N)), dim3(kBestThreads), 0,
-                                            stream, false, logits, ld, V, slices, slice, parts);
+                                            stream, pdl && !capturing(stream), logits, ld, V, slices, slice, parts);
         if (e != cudaSuccess) return e;
     }
-    return launch_kernel(accept_kernel, dim3(static_cast<unsigned>(B) + 1), dim3(ABG_MAX_SPAN), 0, stream, N > 0, tok,
+    return launch_kernel(accept_kernel, dim3(static_cast<unsigned>(B) + 1), dim3(ABG_MAX_SPAN), 0, stream, pdl && N > 0, tok,
                          parent, cu, best, rows, add, last, B, N, slices, parts);
 }
 

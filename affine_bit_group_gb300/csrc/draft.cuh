@@ -56,17 +56,19 @@ struct PagePlanArgs {
     int32_t *info;
     int B, N, page, width, ring_len;
 };
-cudaError_t launch_page_plan(const PagePlanArgs &a, cudaStream_t stream);
+// pdl: the launches may start before the launch ahead of them has finished
+// (they wait for it before they read anything)
+cudaError_t launch_page_plan(const PagePlanArgs &a, bool pdl, cudaStream_t stream);
 
 cudaError_t launch_tree_plan(const int32_t *parent, const int32_t *lens, const int32_t *cu, uint64_t *mask,
-                             int32_t *pos, int B, int N, int words, cudaStream_t stream);
+                             int32_t *pos, int B, int N, int words, bool pdl, cudaStream_t stream);
 
-cudaError_t launch_kv_put(const abg_kv_put_args &a, cudaStream_t stream);
+cudaError_t launch_kv_put(const abg_kv_put_args &a, bool pdl, cudaStream_t stream);
 
 size_t tree_accept_bytes(int64_t N, int64_t V);
 cudaError_t launch_tree_accept(const float *logits, int64_t ld, const int32_t *tok, const int32_t *parent,
                                const int32_t *cu, int32_t *best, int32_t *rows, int32_t *add, int32_t *last, int B,
-                               int N, int64_t V, void *ws, cudaStream_t stream);
+                               int N, int64_t V, void *ws, bool pdl, cudaStream_t stream);
 
 size_t tree_attn_bytes(int Hq, int Hkv, int D, int max_span, int type);
 cudaError_t launch_tree_attn(const abg_tree_attn_args &a, void *ws, bool pdl, cudaStream_t stream);

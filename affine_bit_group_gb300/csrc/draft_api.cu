@@ -76,7 +76,7 @@ abg_status abg_page_plan(const int32_t *lens, const int32_t *add, const int32_t 
                          ring,     table,    slots, pos,                 lens_out,
                          held_out, ends_out, info, static_cast<int>(B), static_cast<int>(N),
                          static_cast<int>(page), static_cast<int>(width), static_cast<int>(ring_len)};
-    return cuda_status(launch_page_plan(a, to_stream(stream)), "page_plan launch");
+    return cuda_status(launch_page_plan(a, early_launches(), to_stream(stream)), "page_plan launch");
 }
 
 abg_status abg_tree_plan(const int32_t *parent, const int32_t *lens, const int32_t *cu, uint64_t *mask, int32_t *pos,
@@ -89,7 +89,7 @@ abg_status abg_tree_plan(const int32_t *parent, const int32_t *lens, const int32
                {span(parent, N, 4), span(lens, B, 4), span(cu, B + 1, 4)}))
         return ABG_EALIAS;
     return cuda_status(launch_tree_plan(parent, lens, cu, mask, pos, static_cast<int>(B), static_cast<int>(N),
-                                        static_cast<int>(words), to_stream(stream)),
+                                        static_cast<int>(words), early_launches(), to_stream(stream)),
                        "tree_plan launch");
 }
 
@@ -129,7 +129,7 @@ abg_status abg_kv_put(const abg_kv_put_args *args, void *stream) {
                 span(a.pos, a.N, 4), span(a.qn_w, a.D, 4), span(a.kn_w, a.D, 4),
                 span(a.cos, a.cos_rows * (a.D / 2), 4), span(a.sin, a.cos_rows * (a.D / 2), 4)}))
         return ABG_EALIAS;
-    return cuda_status(launch_kv_put(a, to_stream(stream)), "kv_put launch");
+    return cuda_status(launch_kv_put(a, early_launches(), to_stream(stream)), "kv_put launch");
 }
 
 abg_status abg_tree_attn_workspace(int64_t Hq, int64_t Hkv, int64_t D, int64_t max_span, int type, int64_t *bytes) {
@@ -197,7 +197,7 @@ abg_status abg_tree_accept(const float *logits, int64_t ld, const int32_t *tok, 
                 span(cu, B + 1, 4)}))
         return ABG_EALIAS;
     return cuda_status(launch_tree_accept(logits, ld, tok, parent, cu, best, rows, add, last, static_cast<int>(B),
-                                          static_cast<int>(N), V, ws, to_stream(stream)),
+                                          static_cast<int>(N), V, ws, early_launches(), to_stream(stream)),
                        "tree_accept launch");
 }
 
