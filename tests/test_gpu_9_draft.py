@@ -550,3 +550,56 @@ def test_binding_refuses_wrong_tensors_on_the_device():
     with pytest.raises(abg.AbgError, match="misaligned"):
         abg.kv_put(k[:, :, 1:65], k[:, :, 64:], Kc, Vc)
     abg.kv_put(k[:, :, :64], k[:, :, 64:], Kc, Vc)  # rows and heads with strides of their own
+
+
+# ------------------------------------------------------------- far offsets ----
+@pytest.mark.parametrize("kind,pages", [("bf16", 70000), ("f32", 70000)])
+def test_pages_past_two_to_the_31_elements(kind, pages):
+    """A cache of more than 2^31 elements, its last pages in use: rows put there
+    are found there."""
+    T, Hkv, page, D = TYPES[kind], 4, 64, 128
+    assert pages * Hkv * page * D > 2**31
+    Kc, Vc = (torch.empty((pages, Hkv, page, D), dtype=T, device="cuda") for _ in range(2))
+    n = 100
+    table = np.array([[pages - 1, pages - 2]])
+    k, v = (torch.randn((n, Hkv, D), device="cuda") for _ in range(2))
+    t = np.arange(n)
+    slots = table[0, t // page].astype(np.int64) * page + t % page
+    abg.kv_put(k, v, Kc, Vc, slots=i64(slots))
+    assert torch.equal(Kc[-1].transpose(0, 1), k[:page].to(T)) and torch.equal(Vc[-2, :, :n - page].transpose(0, 1), v[page:].to(T))
+    c, _ = attn_case(50, kind, 8, 4, D, page, [n], [5], gate=False)
+    c.update(Kc=Kc, Vc=Vc, table=i32(table))
+    abg.tree_attn(**c)
+    far = c["y"].clone()
+    c.update(Kc=Kc[-2:].clone(), Vc=Vc[-2:].clone(), table=i32([[1, 0]]))
+    abg.tree_attn(**c)
+    assert torch.equal(far[:5], c["y"][:5])
+    check_attn(c, kind)
+
+
+def test_early_start_off_gives_the_same_bits(tmp_path):
+    """ABG_PDL=0 in a process of its own: plain stream order, the same results."""
+    import os
+    import subprocess
+    import sys
+    prog = tmp_path / "run.py"
+    prog.write_text(
+        "import sys, torch\n"
+        f"sys.path[:0] = {[os.path.dirname(os.path.dirname(os.path.abspath(__file__))), os.path.dirname(os.path.abspath(__file__))]!r}\n"
+        "import test_gpu_9_draft as t\n"
+        "out = []\n"
+        "for kind in ('f32', 'bf16'):\n"
+        "    c, _ = t.attn_case(60, kind, 8, 2, 128, 16, [900, 40], [9, 30], tail=0)\n"
+        "    t.abg.tree_attn(**c)\n"
+        "    out.append(c['y'].cpu())\n"
+        "x, tok, parent, cu = t.accept_case(t.np.random.default_rng(1), [9, 30], 5000, tail=0)\n"
+        "r = [t.i32(t.np.zeros(39)), t.i32(t.np.zeros(39)), t.i32([0, 0]), t.i32([0, 0])]\n"
+        "t.abg.tree_accept(t.dev(x), t.i32(tok), t.i32(parent), t.i32(cu), *r)\n"
+        "torch.save(out + [v.cpu() for v in r], sys.argv[1])\n")
+    got = []
+    for v in ("0", "1"):
+        path = tmp_path / v
+        env = dict(os.environ, ABG_PDL=v)
+        subprocess.run([sys.executable, str(prog), str(path)], check=True, env=env, timeout=120)
+        got.append(torch.load(path))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
