@@ -20,37 +20,48 @@ namespace {
 // ---------------------------------------------------------- page_plan ------
 // One launch: every block scans all requests (a few loads a thread: at most
 // 8192 requests) and keeps each one's place in the ring in shared memory, so
-// that no block waits for another; the blocks then share the tokens.  A token
-// of a fresh page takes the page from the ring itself, not from the table
-// entry that another block writes.
+// that no block waits for another; the first blocks then share the tokens, the
+// others the tables (a warp a request).  A token of a fresh page takes the page
+// from the ring itself, not from the table entry that another block writes.
+// Latency bounds it: 384 tokens of 48 requests take 5 us (3 of them from launch
+// to launch), 768000 tokens of 512 requests 10.3 us, 0.9 TB/s.
 constexpr int kPlanThreads = 512;
 
-__device__ __forceinline__ int ring_at(int64_t i, int len) {
-    const int r = static_cast<int>(i % len);
-    return r < 0 ? r + len : r;
+// Entry i of the ring, 0 <= i < 2^62, from an entry `base` in 0 .. len-1 on.
+__device__ __forceinline__ int ring_at(int base, int64_t i, int len) {
+    const int64_t at = base + i;
+    return static_cast<int>(at < len ? at : at < 2ll * len ? at - len : at % len);
 }
 
 struct Ask {
-    int64_t total, need;
+    int64_t total, extra, freed;
     bool gone, bad;
-    int64_t extra, freed;
 };
 
 __device__ __forceinline__ Ask ask_of(const PagePlanArgs &a, int b) {
     Ask k;
-    const int64_t len = a.lens[b], add = a.add[b], held = a.held[b];
+    const int64_t len = a.lens[b], add = a.add[b];
+    const int held = a.held[b];
     const int64_t span = static_cast<int64_t>(a.cu[b + 1]) - a.cu[b];
     k.gone = add < 0;
     k.total = len + add;
-    k.need = (k.total + a.page - 1) / a.page;
-    k.bad = len < 0 || held < 0 || held > a.width ||
-            (!k.gone && (add > span || k.need > a.width || k.total > 0x7fffffff));
-    k.extra = k.gone || k.bad ? 0 : max(int64_t(0), k.need - held);
+    k.bad = len < 0 || held < 0 || held > a.width;
+    int need = 0;
+    if (!k.gone && !k.bad) {
+        k.bad = add > span || k.total > 0x7fffffff;
+        if (!k.bad) {
+            need = static_cast<int>((static_cast<uint32_t>(k.total) + static_cast<uint32_t>(a.page - 1)) /
+                                    static_cast<uint32_t>(a.page));
+            k.bad = need > a.width;
+        }
+    }
+    k.extra = k.gone || k.bad ? 0 : max(0, need - held);
     k.freed = k.gone && !k.bad ? held : 0;
     return k;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_constant__ PagePlanArgs a) {
+__global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_constant__ PagePlanArgs a,
+                                                                 int token_blocks) {
     extern __shared__ int32_t sm[];
     int32_t *s_cu = sm;              // [B+1]
     int32_t *s_at = sm + a.B + 1;    // [B] ring entry of the first fresh or freed page; -1: refused
@@ -62,6 +73,8 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
     const bool wide = ((reinterpret_cast<uintptr_t>(a.slots) | reinterpret_cast<uintptr_t>(a.pos)) & 15) == 0;
     const int64_t head = a.ends[0], tail = a.ends[1];
     const int64_t avail = max(int64_t(0), min(tail - head, static_cast<int64_t>(a.ring_len)));
+    const int R = a.ring_len;
+    const int head0 = static_cast<int>((head % R + R) % R), tail0 = static_cast<int>((tail % R + R) % R);
     int64_t done_x = 0, done_f = 0, taken = 0;  // taken: extras up to the last request that was granted any
     int bad = 0;
     for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
@@ -91,9 +104,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
             const bool done = k.gone && !k.bad;
             if (ok && k.extra > 0) taken = x;
             bad += !ok && !done;
-            s_at[b] = ok     ? ring_at(head + x - k.extra, a.ring_len)
-                      : done ? ring_at(tail + f - k.freed, a.ring_len)
-                             : -1;
+            s_at[b] = ok ? ring_at(head0, x - k.extra, R) : done ? ring_at(tail0, f - k.freed, R) : -1;
             if (blockIdx.x == 0) {
                 const int32_t held = a.held[b];
                 a.lens_out[b] = ok ? static_cast<int32_t>(k.total) : done ? 0 : a.lens[b];
@@ -119,22 +130,25 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
         a.info[0] = static_cast<int32_t>(taken);
         a.info[1] = bad;
     }
-    // table and ring entries: a warp a request
-    const int gw = blockIdx.x * (kPlanThreads / 32) + warp, nw = gridDim.x * (kPlanThreads / 32);
-    for (int b = gw; b < a.B; b += nw) {
-        const int at = s_at[b];
-        if (at < 0) continue;
-        int32_t *row = a.table + static_cast<int64_t>(b) * a.width;
-        const Ask k = ask_of(a, b);
-        const int held = a.held[b];
-        for (int64_t j = lane; j < k.extra; j += 32) row[held + j] = a.ring[(at + j) % a.ring_len];
-        for (int64_t j = lane; j < k.freed; j += 32) a.ring[(at + j) % a.ring_len] = row[j];
+    if (static_cast<int>(blockIdx.x) >= token_blocks) {  // table and ring entries
+        const int gw = (blockIdx.x - token_blocks) * (kPlanThreads / 32) + warp;
+        const int nw = (gridDim.x - token_blocks) * (kPlanThreads / 32);
+        for (int b = gw; b < a.B; b += nw) {
+            const int at = s_at[b];
+            if (at < 0) continue;
+            int32_t *row = a.table + static_cast<int64_t>(b) * a.width;
+            const Ask k = ask_of(a, b);
+            const int held = a.held[b];
+            for (int64_t j = lane; j < k.extra; j += 32) row[held + j] = a.ring[ring_at(at, j, R)];
+            for (int64_t j = lane; j < k.freed; j += 32) a.ring[ring_at(at, j, R)] = row[j];
+        }
+        return;
     }
     // slots: a thread four tokens in a row, which mostly share a request and a
     // page, so that the search and the table's latency are paid once for them
     const int64_t quads = (static_cast<int64_t>(a.N) + 3) / 4;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPlanThreads + tid; i < quads;
-         i += static_cast<int64_t>(gridDim.x) * kPlanThreads) {
+         i += static_cast<int64_t>(token_blocks) * kPlanThreads) {
         const int n0 = static_cast<int>(4 * i), end = s_cu[a.B];
         int64_t slot[4];
         int32_t pos[4];
@@ -159,7 +173,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
             if (j != page) {
                 page = j;
                 id = j < held ? a.table[static_cast<int64_t>(b) * a.width + j]
-                              : a.ring[(static_cast<int64_t>(at) + j - held) % a.ring_len];
+                              : a.ring[ring_at(at, j - held, R)];
             }
             slot[k] = static_cast<int64_t>(id) * a.page + (pos[k] - j * a.page);
         }
@@ -549,15 +563,17 @@ cudaError_t launch_page_plan(const PagePlanArgs &a, bool pdl, cudaStream_t strea
     static const cudaError_t attr = cudaFuncSetAttribute(
         page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (2 * ABG_MAX_REQUESTS + 1) * sizeof(int32_t));
     if (attr != cudaSuccess) return attr;
-    // four tokens a thread, a request a warp
-    const int64_t blocks =
-        std::max<int64_t>((a.N + 4ll * kPlanThreads - 1) / (4 * kPlanThreads), (32ll * a.B + kPlanThreads - 1) / kPlanThreads);
+    // four tokens a thread; a request a warp; one wave of two blocks an SM (a
+    // second wave: 12.3 us against 10.3 for the 768000 tokens)
+    const int64_t tokens = (a.N + 4ll * kPlanThreads - 1) / (4 * kPlanThreads);
+    const int table_blocks = (32 * a.B + kPlanThreads - 1) / kPlanThreads;
+    const int token_blocks = static_cast<int>(std::min<int64_t>(tokens, std::max(sm_count(), 2 * sm_count() - table_blocks)));
     // An early start deals blocks to the SMs that the launch ahead leaves first,
     // so that some get more than their share: for short grids only (768000
-    // tokens: 10.5 us, early 11.4; 384 tokens: 8.2 us, early 5.2).
-    const bool early = pdl && blocks <= sm_count() && !capturing(stream);
-    return launch_kernel(page_plan_kernel, dim3(static_cast<unsigned>(std::min<int64_t>(blocks, 2 * sm_count()))),
-                         dim3(kPlanThreads), smem, stream, early, a);
+    // tokens: 10.3 us, early 11.4; 384 tokens: 8.2 us, early 5.2).
+    const bool early = pdl && token_blocks + table_blocks <= sm_count() && !capturing(stream);
+    return launch_kernel(page_plan_kernel, dim3(static_cast<unsigned>(token_blocks + table_blocks)), dim3(kPlanThreads),
+                         smem, stream, early, a, token_blocks);
 }
 
 cudaError_t launch_tree_plan(const int32_t *parent, const int32_t *lens, const int32_t *cu, uint64_t *mask,
