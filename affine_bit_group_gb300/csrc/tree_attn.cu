@@ -18,9 +18,9 @@ constexpr int kKT = 32;  // tokens a tile
 
 // Rows of a unit: up to 4 or 16 where a request has no more, else 32.  A block
 // with a tile and 32 rows of 256 columns takes half of an SM's shared memory:
-// two blocks an SM fill the gaps between each other's barriers (f32 drafts over
-// four ragged requests of 4100 tokens: 71 us; one block of 64 rows and 64 tokens
-// 72; 8 drafts over 60000 tokens 88 against 98).
+// two blocks an SM fill the gaps between each other's barriers (8 drafts over
+// 60000 tokens, 128 columns: 88 us against 98 with one block of 64 rows and 64
+// tokens, before the scores were a warp's own; now 82).
 constexpr int kOneRows = 4, kFewRows = 16, kManyRows = 32;
 
 __device__ __forceinline__ void cp16(void *dst, const void *src, bool real) {
@@ -37,19 +37,20 @@ template <int D, int kRT>
 struct Smem {
     static constexpr int kLd = D + 4;                        // rows of Q and K start in different banks
     static constexpr int kPLd = kRT + 4;
-    static constexpr int kParts = kRT == kManyRows ? 2 : 8;  // column parts of the scores
+    static constexpr bool kRowWarps = kRT >= kFewRows;       // a warp's scores are of rows of its own
+    static constexpr int kParts = kRowWarps ? 1 : 8;         // else: column parts of the scores
     // K and V tiles on their way beside the ones in use, where two blocks fit
     static constexpr int kStages = D == 256 ? 1 : 2;
-    float q[kRT][kLd];
-    float k[kStages][kKT][kLd];
-    float v[kStages][kKT][D];
-    float p[kKT][kPLd];                       // weights, token-major
-    float part[kParts][kRT][kKT + 1];         // partial scores
-    float corr[kRT];
-    int64_t off[4][kKT];                      // row offsets of tiles in turn, in elements (-1: none)
+    alignas(16) float q[kRT][kLd];
+    alignas(16) float k[kStages][kKT][kLd];
+    alignas(16) float v[kStages][kKT][D];
+    alignas(16) float p[kKT][kPLd];                    // weights, token-major
+    float part[kParts][kRowWarps ? 1 : kRT][kKT + 1];  // partial scores
+    alignas(16) float corr[kRT];                       // read in pairs
+    int64_t off[4][kKT];                               // row offsets of tiles in turn, in elements (-1: none)
     float m[kRT], l[kRT];
     AttnScan scan;
-    uint32_t bad[ABG_MAX_SPAN / 32];          // drafts whose V holds an infinity or a NaN
+    uint32_t bad[ABG_MAX_SPAN / 32];                   // drafts whose V holds an infinity or a NaN
 };
 
 template <int D>
@@ -99,13 +100,38 @@ __device__ __forceinline__ int64_t row_offset(const abg_tree_attn_args &a, const
     return ((static_cast<int64_t>(id) * a.Hkv + s.h) * a.page + in_page) * D;
 }
 
-// One part of the work line.  Scores: up to 16 rows, a thread holds an eighth of
-// the columns of one token for all rows; 32 rows, half of the columns of two
-// rows by four tokens.  The parts meet in shared memory, where 32 lanes or
-// fewer take a row each for its maximum, weights and sum.  Weighted sums: a
-// thread holds four columns of kRPO rows, two rows to a packed pair, over every
-// kKS-th token.  Multiply-adds bound it above about 16 rows (half a multiply-add
-// a byte and row, against 11 a byte that an SM can do); below, latency and the
+// Sums over the D/8 lanes of a token group of 16 values, rows x tokens.  Half of
+// the values go to the other half of the lanes in each step; what is left of
+// them is the row and the token at index 16/R * row + token = the lane's place.
+// The rows' steps come first, of the most values: a lane's rows start from its
+// own (x[i] is row i ^ its row), so that these steps select nothing.
+template <int D, int R>
+__device__ __forceinline__ void scatter_sums(float (&x)[16], int lane) {
+#pragma unroll
+    for (int half = 8, d = D / 16; half >= (D == 64 ? 2 : 1); half /= 2, d /= 2) {
+        const bool up = half < 16 / R && lane & d;
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+            const float keep = up ? x[i + half] : x[i], send = up ? x[i] : x[i + half];
+            x[i] = keep + __shfl_xor_sync(0xffffffffu, send, d);
+        }
+    }
+}
+
+// One part of the work line.  Scores of 16 or 32 rows: a warp has 2 or 4 rows of
+// its own, a lane eight of their columns in registers; K goes past them, a token
+// to every D/8 lanes, and the lanes' sums meet by shuffles, 16 values at a time,
+// which leaves each lane the scores of one row, so that the softmax needs no
+// shared memory and no barrier before it.  (Rows of Q read from shared memory
+// again for every token took 70 us where this takes 65: 8 drafts of 8 heads on
+// four ragged f32 requests of 4100 tokens, 256 columns; 8 rows a request on 32 of
+// them 150, now 121, 3.3 TB/s.)  Up to 4 rows: a thread holds an eighth of the
+// columns of one token for all rows, and the parts meet in shared memory.
+// Weighted sums: a thread holds four columns of kRPO rows, two rows to a packed
+// pair, over every kKS-th token.  Multiply-adds bound it above about 16 rows (half
+// a multiply-add a byte and row, against 11 a byte that an SM can do): they keep
+// their units busy 47% of the time and half of the instructions are others, at 16
+// warps an SM, which is as many as the registers hold.  Below, latency and the
 // cache's bytes.
 template <int D, int kRT>
 __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant__ AttnArgs p) {
@@ -114,13 +140,21 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
     S &sm = *reinterpret_cast<S *>(raw);
     const abg_tree_attn_args &a = p.a;
     constexpr int kParts = S::kParts;
+    constexpr bool kRowWarps = S::kRowWarps;
     constexpr int kLanes = kThreads / kRT < 32 ? kThreads / kRT : 32;  // of a row's softmax
     constexpr int kEach = kKT / kLanes;                                // a lane's tokens of it
+    constexpr int kRW = kRowWarps ? kRT / (kThreads / 32) : 1;         // rows of a warp
+    constexpr int kTS = 16 / kRW;                                      // tokens of a lane at a time
     constexpr int kRPO = kRT < 8 ? kRT : 8;                            // rows of a thread's sums
     constexpr int kQuads = D / 4, kRG = kRT / kRPO, kKS = kThreads / (kQuads * kRG);
     constexpr int E = D / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int row = tid / kLanes, col = tid % kLanes;  // softmax
+    // softmax: a thread's row, and 0 in the first of the threads that share it
+    // (kRowWarps: from the lane's place that scatter_sums goes by)
+    const int place16 = D == 256 ? lane >> 1 : D == 128 ? lane & 15 : 2 * (lane & 7);
+    constexpr int kRowBits = (kRW - 1) * kTS * D / 128;  // lanes of one row differ elsewhere
+    const int row = kRowWarps ? kRW * warp + place16 / kTS : tid / kLanes;
+    const int col = kRowWarps ? lane & ~kRowBits : tid % kLanes;
     const int quad = tid % kQuads, rg = tid / kQuads % kRG, ks = tid / (kQuads * kRG);
     grid_dep_wait();
     grid_dep_launch();
@@ -130,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
     AttnSeg s;
     while (line.next(p, s)) {
         // whole warps (they shuffle) have softmax rows or not
-        const bool rows_here = (32 * warp) / kLanes < s.rows && row < kRT;
+        const bool rows_here = kRowWarps ? kRW * warp < s.rows : (32 * warp) / kLanes < s.rows && row < kRT;
         auto source = [&](const Tile &x, bool value) {
             return static_cast<const float *>(x.cache ? (value ? a.Vc : a.Kc) : (value ? a.Vd : a.Kd));
         };
@@ -171,6 +205,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
 #pragma unroll
         for (int u = 0; u < kStages; ++u) bring(u, false), bring(u, true);
         float m = -INFINITY, l = 0.0f;
+        float4 q[kRW][2];       // columns 4l .. 4l+3 and D/2 further on of a warp's rows
         float2 o[kRPO / 2][4];  // rows 2i and 2i+1, a column
 #pragma unroll
         for (int i = 0; i < kRPO / 2; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = make_float2(0.0f, 0.0f);
@@ -185,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
             cp_wait<2 * kStages - 1>();
             __syncthreads();
             // scores
-            if constexpr (kRT != kManyRows) {
+            if constexpr (!kRowWarps) {
                 const int key = tid % kKT, part = tid / kKT;
                 if (key < now.tokens) {
                     float2 acc[kRT];
@@ -204,57 +239,89 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
 #pragma unroll
                     for (int r = 0; r < kRT; ++r) sm.part[part][r][key] = acc[r].x + acc[r].y;
                 }
-            } else {
-                const int part = tid / 128, tx = tid % 8, ty = tid / 8 % 16;  // rows ty, ty+16, tokens tx+8j
-                float2 acc[2][4];
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[i][j] = make_float2(0.0f, 0.0f);
-#pragma unroll 4
-                for (int c = part * (D / kParts); c < (part + 1) * (D / kParts); c += 4) {
-                    float4 kv[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4 *>(&sm.k[st][tx + 8 * j][c]);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float4 qv = *reinterpret_cast<const float4 *>(&sm.q[ty + 16 * i][c]);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            acc[i][j] = fma2(make_float2(qv.x, qv.y), make_float2(kv[j].x, kv[j].y), acc[i][j]);
-                            acc[i][j] = fma2(make_float2(qv.z, qv.w), make_float2(kv[j].z, kv[j].w), acc[i][j]);
-                        }
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) sm.part[part][ty + 16 * i][tx + 8 * j] = acc[i][j].x + acc[i][j].y;
+                __syncthreads();
+                bring(u + kStages, false);
             }
-            __syncthreads();
-            bring(u + kStages, false);
             // softmax statistics and weights
             if (rows_here) {
                 const uint64_t *seen = nullptr;
                 if (!now.cache && row < s.rows)
                     seen = a.mask + (static_cast<int64_t>(s.req.n0) + (s.r0 + row) / p.G) * a.words;
                 float sc[kEach], top = m;
+                int at[kEach];
+                if constexpr (kRowWarps) {
+                    constexpr int kGroups = 256 / D;  // of lanes, a token each
+                    const int g = lane / (D / 8), c = 4 * (lane % (D / 8));
+                    if (u == 0)
+#pragma unroll
+                        for (int i = 0; i < kRW; ++i) {
+                            q[i][0] = *reinterpret_cast<const float4 *>(&sm.q[kRW * warp + (i ^ place16 / kTS)][c]);
+                            q[i][1] = *reinterpret_cast<const float4 *>(&sm.q[kRW * warp + (i ^ place16 / kTS)][D / 2 + c]);
+                        }
+                    constexpr int kLeft = D == 64 ? 2 : 1;
+                    constexpr int kPasses = kKT / (kTS * kGroups);
+                    float half = 0.0f;
+#pragma unroll
+                    for (int t = 0; t < kPasses; ++t) {
+                        float v[16];
+#pragma unroll
+                        for (int j = 0; j < kTS; ++j) {
+                            const float *k = &sm.k[st][(t * kGroups + g) * kTS + j][c];
+                            const float4 k0 = *reinterpret_cast<const float4 *>(k);
+                            const float4 k1 = *reinterpret_cast<const float4 *>(k + D / 2);
+#pragma unroll
+                            for (int i = 0; i < kRW; ++i) {
+                                float2 x = mul2(make_float2(q[i][0].x, q[i][0].y), make_float2(k0.x, k0.y));
+                                x = fma2(make_float2(q[i][0].z, q[i][0].w), make_float2(k0.z, k0.w), x);
+                                x = fma2(make_float2(q[i][1].x, q[i][1].y), make_float2(k1.x, k1.y), x);
+                                x = fma2(make_float2(q[i][1].z, q[i][1].w), make_float2(k1.z, k1.w), x);
+                                v[i * kTS + j] = x.x + x.y;
+                            }
+                        }
+                        scatter_sums<D, kRW>(v, lane);
+                        if constexpr (D == 256) {  // two passes' sums meet in lane pairs
+                            if (t % 2 == 0) {
+                                half = v[0];
+                            } else {
+                                const bool up = lane & 1;
+                                const float send = up ? half : v[0], keep = up ? v[0] : half;
+                                sc[t / 2] = keep + __shfl_xor_sync(0xffffffffu, send, 1);
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < kLeft; ++e) sc[t * kLeft + e] = v[e];
+                        }
+                    }
+                    const int j0 = place16 % kTS;
+#pragma unroll
+                    for (int n = 0; n < kEach; ++n)
+                        at[n] = D == 256   ? (2 * n + (lane & 1)) * kTS + j0
+                                : D == 128 ? (n * kGroups + g) * kTS + j0
+                                           : (n / 2 * kGroups + g) * kTS + j0 + n % 2;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kEach; ++j) {
+                        at[j] = col + kLanes * j;
+                        float x[kParts];
+#pragma unroll
+                        for (int h = 0; h < kParts; ++h) x[h] = sm.part[h][row][at[j]];
+#pragma unroll
+                        for (int w = kParts / 2; w >= 1; w /= 2)
+#pragma unroll
+                            for (int h = 0; h < w; ++h) x[h] = x[2 * h] + x[2 * h + 1];
+                        sc[j] = x[0];
+                    }
+                }
 #pragma unroll
                 for (int j = 0; j < kEach; ++j) {
-                    const int k = col + kLanes * j;
-                    float x[kParts];
-#pragma unroll
-                    for (int h = 0; h < kParts; ++h) x[h] = sm.part[h][row][k];
-#pragma unroll
-                    for (int w = kParts / 2; w >= 1; w /= 2)
-#pragma unroll
-                        for (int h = 0; h < w; ++h) x[h] = x[2 * h] + x[2 * h + 1];
-                    const bool in = k < now.tokens && (now.cache || (seen && attn_sees(seen, now.key0 + k)));
-                    sc[j] = in ? x[0] * p.scale2 : -INFINITY;
+                    const bool in =
+                        at[j] < now.tokens && (now.cache || (seen && attn_sees(seen, now.key0 + at[j])));
+                    sc[j] = in ? sc[j] * p.scale2 : -INFINITY;
                     top = fmaxf(top, sc[j]);
                 }
 #pragma unroll
-                for (int d = kLanes / 2; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                for (int d = 16; d >= 1; d >>= 1)
+                    if (kRowWarps ? !(d & kRowBits) : d < kLanes) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
                 const float ref = top == -INFINITY ? 0.0f : top;
                 const float corr = exp2f(m - ref);
                 float sum = 0.0f;
@@ -262,16 +329,18 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
                 for (int j = 0; j < kEach; ++j) {
                     const float e = exp2f(sc[j] - ref);
                     sum += e;
-                    sm.p[col + kLanes * j][row] = e;
+                    sm.p[at[j]][row] = e;
                 }
 #pragma unroll
-                for (int d = kLanes / 2; d >= 1; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+                for (int d = 16; d >= 1; d >>= 1)
+                    if (kRowWarps ? !(d & kRowBits) : d < kLanes) sum += __shfl_xor_sync(0xffffffffu, sum, d);
                 l = l * corr + sum;
                 m = top;
                 if (col == 0) sm.corr[row] = corr;
             }
-            cp_wait<2 * kStages - 1>();
+            cp_wait<2 * kStages - (kRowWarps ? 2 : 1)>();
             __syncthreads();
+            if constexpr (kRowWarps) bring(u + kStages, false);
             if (!now.cache) {
                 // an infinity or a NaN in a draft's V must not reach the rows
                 // that do not see it (0 * NaN): taken out here, and added at the
