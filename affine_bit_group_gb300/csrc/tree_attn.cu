@@ -14,7 +14,6 @@ namespace abg {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kKT = 32;  // tokens a tile
 
 // Rows of a unit: up to 4 or 16 where a request has no more, else 32.  A block
 // with a tile and 32 rows of 256 columns takes half of an SM's shared memory:
@@ -35,12 +34,16 @@ __device__ __forceinline__ void cp_wait() {
 
 template <int D, int kRT>
 struct Smem {
+    // Tokens a tile: what two blocks an SM have room for, since a tile costs three
+    // barriers whatever its size (64 columns: 32 tokens 46.6 us, 64 40.5; 128
+    // columns, 4 rows: two stages of 32 171 us, one of 64 140, 5.7 TB/s).
+    static constexpr int kKT = D == 256 ? 32 : 64;
     static constexpr int kLd = D + 4;                        // rows of Q and K start in different banks
     static constexpr int kPLd = kRT + 4;
     static constexpr bool kRowWarps = kRT >= kFewRows;       // a warp's scores are of rows of its own
-    static constexpr int kParts = kRowWarps ? 1 : 8;         // else: column parts of the scores
+    static constexpr int kParts = kRowWarps ? 1 : kThreads / kKT;         // else: column parts of the scores
     // K and V tiles on their way beside the ones in use, where two blocks fit
-    static constexpr int kStages = D == 256 ? 1 : 2;
+    static constexpr int kStages = D == 64 ? 2 : 1;
     alignas(16) float q[kRT][kLd];
     alignas(16) float k[kStages][kKT][kLd];
     alignas(16) float v[kStages][kKT][D];
@@ -53,7 +56,7 @@ struct Smem {
     uint32_t bad[ABG_MAX_SPAN / 32];                   // drafts whose V holds an infinity or a NaN
 };
 
-template <int D>
+template <int D, int kKT>
 __device__ __forceinline__ void load_tile(float *dst, int ld, const float *src, const int64_t *off, int tokens) {
     constexpr int kEach = kKT * (D / 4) / kThreads, kRows = kThreads / (D / 4);  // rows of a round
     const int r0 = threadIdx.x / (D / 4), c = 4 * (threadIdx.x % (D / 4));
@@ -75,6 +78,7 @@ struct Tile {
     bool cache;
     int key0, tokens;
 };
+template <int kKT>
 __device__ __forceinline__ Tile tile_at(const AttnSeg &s, int t) {
     Tile x;
     x.cache = t < s.ctiles;
@@ -139,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
     extern __shared__ __align__(16) unsigned char raw[];
     S &sm = *reinterpret_cast<S *>(raw);
     const abg_tree_attn_args &a = p.a;
-    constexpr int kParts = S::kParts;
+    constexpr int kParts = S::kParts, kKT = S::kKT;
     constexpr bool kRowWarps = S::kRowWarps;
     constexpr int kLanes = kThreads / kRT < 32 ? kThreads / kRT : 32;  // of a row's softmax
     constexpr int kEach = kKT / kLanes;                                // a lane's tokens of it
@@ -176,10 +180,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
 #pragma unroll
             for (int u = 0; u < kStages; ++u)
                 if (u < n) {
-                    const Tile x = tile_at(s, s.t0 + u);
+                    const Tile x = tile_at<kKT>(s, s.t0 + u);
                     sm.off[u][tid] = row_offset<D>(a, s, x, tid, page_of(a, s, x, tid));
                 }
-            if (kStages < n) id = page_of(a, s, tile_at(s, s.t0 + kStages), tid);
+            if (kStages < n) id = page_of(a, s, tile_at<kKT>(s, s.t0 + kStages), tid);
         }
         for (int i = tid; i < kRT * (D / 4); i += kThreads) {
             const int r = i / (D / 4), c = 4 * (i % (D / 4)), q = s.r0 + r;
@@ -193,11 +197,11 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
         __syncthreads();
         auto bring = [&](int u, bool value) {  // tile u of the stretch (Q goes with the first); a group each
             if (u < n) {
-                const Tile x = tile_at(s, s.t0 + u);
+                const Tile x = tile_at<kKT>(s, s.t0 + u);
                 if (value) {
-                    load_tile<D>(&sm.v[u % kStages][0][0], D, source(x, true), sm.off[u & 3], x.tokens);
+                    load_tile<D, kKT>(&sm.v[u % kStages][0][0], D, source(x, true), sm.off[u & 3], x.tokens);
                 } else {
-                    load_tile<D>(&sm.k[u % kStages][0][0], S::kLd, source(x, false), sm.off[u & 3], x.tokens);
+                    load_tile<D, kKT>(&sm.k[u % kStages][0][0], S::kLd, source(x, false), sm.off[u & 3], x.tokens);
                 }
             }
             cp_commit();
@@ -210,12 +214,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
 #pragma unroll
         for (int i = 0; i < kRPO / 2; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = make_float2(0.0f, 0.0f);
         for (int u = 0; u < n; ++u) {
-            const Tile now = tile_at(s, s.t0 + u);
+            const Tile now = tile_at<kKT>(s, s.t0 + u);
             const int st = u % kStages;
             // the places of tile u + kStages, and the pages of the one after it
             if (tid < kKT && u + kStages < n) {
-                sm.off[(u + kStages) & 3][tid] = row_offset<D>(a, s, tile_at(s, s.t0 + u + kStages), tid, id);
-                if (u + kStages + 1 < n) id = page_of(a, s, tile_at(s, s.t0 + u + kStages + 1), tid);
+                sm.off[(u + kStages) & 3][tid] = row_offset<D>(a, s, tile_at<kKT>(s, s.t0 + u + kStages), tid, id);
+                if (u + kStages + 1 < n) id = page_of(a, s, tile_at<kKT>(s, s.t0 + u + kStages + 1), tid);
             }
             cp_wait<2 * kStages - 1>();
             __syncthreads();
