@@ -15,12 +15,13 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// Rows of a unit: up to 4 or 16 where a request has no more, else 32.  A block
+// Rows of a unit: 4, 8 or 16 where a request has no more, else 32 (8 rows on 32
+// requests of 4100 tokens, 256 columns: in units of 16 121 us, of 8 96).  A block
 // with a tile and 32 rows of 256 columns takes half of an SM's shared memory:
 // two blocks an SM fill the gaps between each other's barriers (8 drafts over
 // 60000 tokens, 128 columns: 88 us against 98 with one block of 64 rows and 64
 // tokens, before the scores were a warp's own; now 82).
-constexpr int kOneRows = 4, kFewRows = 16, kManyRows = 32;
+constexpr int kOneRows = 4, kEightRows = 8, kFewRows = 16, kManyRows = 32;
 
 __device__ __forceinline__ void cp16(void *dst, const void *src, bool real) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(real ? 16 : 0)
@@ -35,15 +36,16 @@ __device__ __forceinline__ void cp_wait() {
 template <int D, int kRT>
 struct Smem {
     // Tokens a tile: what two blocks an SM have room for, since a tile costs three
-    // barriers whatever its size (64 columns: 32 tokens 46.6 us, 64 40.5; 128
-    // columns, 4 rows: two stages of 32 171 us, one of 64 140, 5.7 TB/s).
-    static constexpr int kKT = D == 256 ? 32 : 64;
+    // barriers whatever its size (64 columns, 32 rows: 32 tokens 46.6 us, 64 40.5,
+    // 128 in one stage 43.2; 16 rows: 32 tokens 101, 64 86, 128 79; 128 columns, 4
+    // rows: two stages of 32 171 us, one of 64 138, 5.8 TB/s).
+    static constexpr int kKT = D == 256 ? 32 : D == 128 || kRT == kManyRows ? 64 : 128;
     static constexpr int kLd = D + 4;                        // rows of Q and K start in different banks
     static constexpr int kPLd = kRT + 4;
     static constexpr bool kRowWarps = kRT >= kFewRows;       // a warp's scores are of rows of its own
-    static constexpr int kParts = kRowWarps ? 1 : kThreads / kKT;         // else: column parts of the scores
-    // K and V tiles on their way beside the ones in use, where two blocks fit
-    static constexpr int kStages = D == 64 ? 2 : 1;
+    static constexpr int kParts = kRowWarps ? 1 : kThreads / kKT;  // else: column parts of the scores
+    // K and V tiles in use and on their way
+    static constexpr int kStages = D == 64 && kRT == kManyRows ? 2 : 1;
     alignas(16) float q[kRT][kLd];
     alignas(16) float k[kStages][kKT][kLd];
     alignas(16) float v[kStages][kKT][D];
@@ -128,9 +130,10 @@ __device__ __forceinline__ void scatter_sums(float (&x)[16], int lane) {
 // which leaves each lane the scores of one row, so that the softmax needs no
 // shared memory and no barrier before it.  (Rows of Q read from shared memory
 // again for every token took 70 us where this takes 65: 8 drafts of 8 heads on
-// four ragged f32 requests of 4100 tokens, 256 columns; 8 rows a request on 32 of
-// them 150, now 121, 3.3 TB/s.)  Up to 4 rows: a thread holds an eighth of the
-// columns of one token for all rows, and the parts meet in shared memory.
+// four ragged f32 requests of 4100 tokens, 256 columns.)  Up to 8 rows: a thread
+// holds a part of the columns of one token for all rows, and the parts meet in
+// shared memory (8 rows on 32 requests of 4100 tokens: 96 us, 4.2 TB/s; with a
+// row a warp 112).
 // Weighted sums: a thread holds four columns of kRPO rows, two rows to a packed
 // pair, over every kKS-th token.  Multiply-adds bound it above about 16 rows (half
 // a multiply-add a byte and row, against 11 a byte that an SM can do): they keep
@@ -230,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
                     float2 acc[kRT];
 #pragma unroll
                     for (int r = 0; r < kRT; ++r) acc[r] = make_float2(0.0f, 0.0f);
-#pragma unroll 2
+#pragma unroll 4
                     for (int c = part * (D / kParts); c < (part + 1) * (D / kParts); c += 4) {
                         const float4 kv = *reinterpret_cast<const float4 *>(&sm.k[st][key][c]);
 #pragma unroll
@@ -451,7 +454,11 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
 }
 
 int row_tile(int64_t G, int64_t max_span) {
-    return G * max_span <= kOneRows ? kOneRows : G * max_span <= kFewRows ? kFewRows : kManyRows;
+    const int64_t rows = G * max_span;
+    return rows <= kOneRows     ? kOneRows
+           : rows <= kEightRows ? kEightRows
+           : rows <= kFewRows   ? kFewRows
+                                : kManyRows;
 }
 
 template <int D, int kRT>
@@ -486,9 +493,10 @@ cudaError_t go(AttnArgs p, void *ws, bool early, bool pdl, cudaStream_t stream) 
 // f.template operator()<D, kRT>() for the call's width and rows
 template <int D, typename F>
 auto by_rows(int rt, F f) {
-    return rt == kOneRows   ? f.template operator()<D, kOneRows>()
-           : rt == kFewRows ? f.template operator()<D, kFewRows>()
-                            : f.template operator()<D, kManyRows>();
+    return rt == kOneRows     ? f.template operator()<D, kOneRows>()
+           : rt == kEightRows ? f.template operator()<D, kEightRows>()
+           : rt == kFewRows   ? f.template operator()<D, kFewRows>()
+                              : f.template operator()<D, kManyRows>();
 }
 template <typename F>
 auto by_shape(int64_t D, int rt, F f) {

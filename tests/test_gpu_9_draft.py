@@ -310,6 +310,16 @@ def test_tree_attn(kind, Hq, Hkv, D, page, lens, spans):
     check_attn(*attn_case(1, kind, Hq, Hkv, D, page, lens, spans, gate=D != 128))
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("Hq,Hkv,spans", [
+    (5, 1, [1, 1, 1, 1, 0, 1]), (8, 1, [1, 1, 1, 1, 1, 1]), (4, 2, [4, 1, 3, 0, 2, 4]), (6, 2, [2, 2, 1, 2, 2, 1]),
+    (9, 1, [1, 1, 1, 1, 1, 1]), (8, 2, [4, 3, 1, 2, 4, 4]), (3, 3, [16, 9, 8, 5, 4, 11]), (17, 1, [1, 1, 1, 1, 1, 1]),
+])
+def test_tree_attn_few_rows_and_tiles_that_end_inside(D, Hq, Hkv, spans):
+    """5 to 17 rows a key/value head, lengths around the tiles' ends."""
+    check_attn(*attn_case(21, "f32", Hq, Hkv, D, 16, [31, 33, 64, 127, 129, 300], spans))
+
+
 @pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("spans", [[65, 128], [150, 1, 192], [256, 30]])
 def test_tree_attn_spans_past_one_mask_word(kind, spans):
