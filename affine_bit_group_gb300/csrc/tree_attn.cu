@@ -16,11 +16,11 @@ namespace {
 constexpr int kThreads = 256;
 
 // Rows of a unit: 4, 8 or 16 where a request has no more, else 32 (8 rows on 32
-// requests of 4100 tokens, 256 columns: in units of 16 121 us, of 8 96).  A block
+// requests of 4100 tokens, 256 columns: in units of 16 121 us, of 8 96, now 91).  A block
 // with a tile and 32 rows of 256 columns takes half of an SM's shared memory:
 // two blocks an SM fill the gaps between each other's barriers (8 drafts over
 // 60000 tokens, 128 columns: 88 us against 98 with one block of 64 rows and 64
-// tokens, before the scores were a warp's own; now 82).
+// tokens, before the scores were a warp's own; now 72).
 constexpr int kOneRows = 4, kEightRows = 8, kFewRows = 16, kManyRows = 32;
 
 __device__ __forceinline__ void cp16(void *dst, const void *src, bool real) {
@@ -132,8 +132,8 @@ __device__ __forceinline__ void scatter_sums(float (&x)[16], int lane) {
 // again for every token took 70 us where this takes 65: 8 drafts of 8 heads on
 // four ragged f32 requests of 4100 tokens, 256 columns.)  Up to 8 rows: a thread
 // holds a part of the columns of one token for all rows, and the parts meet in
-// shared memory (8 rows on 32 requests of 4100 tokens: 96 us, 4.2 TB/s; with a
-// row a warp 112).
+// shared memory (8 rows on 32 requests of 4100 tokens: 91 us, 4.4 TB/s; with a
+// row a warp 15 more).
 // Weighted sums: a thread holds four columns of kRPO rows, two rows to a packed
 // pair, over every kKS-th token.  Multiply-adds bound it above about 16 rows (half
 // a multiply-add a byte and row, against 11 a byte that an SM can do): they keep
@@ -369,8 +369,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[i][e] = mul2(o[i][e], f);
             }
-#pragma unroll 4
-            for (int k = rg * kRPO < s.rows ? ks : kKT; k < now.tokens; k += kKS) {
+            auto take = [&](int k) {
                 const float4 v = *reinterpret_cast<const float4 *>(&sm.v[st][k][4 * quad]);
                 const float2 vv[4] = {make_float2(v.x, v.x), make_float2(v.y, v.y), make_float2(v.z, v.z),
                                       make_float2(v.w, v.w)};
@@ -383,6 +382,14 @@ __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant
                         o[i + 1][e] = fma2(make_float2(w.z, w.w), vv[e], o[i + 1][e]);
                     }
                 }
+            };
+            if (rg * kRPO >= s.rows) {  // no rows
+            } else if (now.tokens == kKT) {  // written out (a loop of unknown length: 78.9 us where this takes 71.0)
+#pragma unroll 32
+                for (int k = 0; k < kKT; k += kKS) take(ks + k);
+            } else {
+#pragma unroll 1
+                for (int k = ks; k < now.tokens; k += kKS) take(k);
             }
             __syncthreads();
             bring(u + kStages, true);
