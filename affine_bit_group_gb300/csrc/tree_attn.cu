@@ -137,8 +137,8 @@ __device__ __forceinline__ void scatter_sums(float (&x)[16], int lane) {
 // Weighted sums: a thread holds four columns of kRPO rows, two rows to a packed
 // pair, over every kKS-th token.  Multiply-adds bound it above about 16 rows (half
 // a multiply-add a byte and row, against 11 a byte that an SM can do): they keep
-// their units busy 47% of the time and half of the instructions are others, at 16
-// warps an SM, which is as many as the registers hold.  Below, latency and the
+// their units busy 40-50% of the time and half of the instructions are others, at
+// 16 warps an SM, which is as many as the registers hold.  Below, latency and the
 // cache's bytes.
 template <int D, int kRT>
 __global__ void __launch_bounds__(kThreads, 2) attn_kernel(const __grid_constant__ AttnArgs p) {
