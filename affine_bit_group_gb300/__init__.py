@@ -138,6 +138,7 @@ def library(build_if_missing: bool = True) -> ctypes.CDLL:
             lib.abg_kv_put.argtypes = [P, P]
             lib.abg_tree_attn_workspace.argtypes = [I64, I64, I64, I64, I, ctypes.POINTER(I64)]
             lib.abg_tree_attn.argtypes = [P, P, I64, P]
+            lib.abg_selftest_tree_attn_timeout.argtypes = [P, P, I64, I, P]
             lib.abg_tree_accept_workspace.argtypes = [I64, I64, ctypes.POINTER(I64)]
             lib.abg_tree_accept.argtypes = [P, I64] + [P] * 7 + [I64] * 3 + [P, I64, P]
             lib.abg_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), I]
@@ -153,6 +154,7 @@ def library(build_if_missing: bool = True) -> ctypes.CDLL:
                       "abg_stage_graph_destroy", "abg_swiglu_mlp_static", "abg_gdn", "abg_atq",
                       "abg_device_status", "abg_set_q4mv_tuning", "abg_selftest_wait_timeout", "abg_page_plan",
                       "abg_tree_plan", "abg_kv_put", "abg_tree_attn_workspace", "abg_tree_attn",
+                      "abg_selftest_tree_attn_timeout",
                       "abg_tree_accept_workspace", "abg_tree_accept"):
                 getattr(lib, f).restype = ctypes.c_int
             _lib = lib

@@ -71,7 +71,8 @@ cudaError_t launch_tree_accept(const float *logits, int64_t ld, const int32_t *t
                                int N, int64_t V, void *ws, bool pdl, cudaStream_t stream);
 
 size_t tree_attn_bytes(int Hq, int Hkv, int D, int max_span, int type);
-cudaError_t launch_tree_attn(const abg_tree_attn_args &a, void *ws, bool pdl, cudaStream_t stream);
+// withhold: as launch_tree_attn16's
+cudaError_t launch_tree_attn(const abg_tree_attn_args &a, void *ws, bool pdl, int withhold, cudaStream_t stream);
 
 // the 16-bit kernel's device status word (OR-ed into *bits)
 cudaError_t tree_attn16_status(unsigned *bits, bool clear);

@@ -47,6 +47,37 @@ bool bounded(std::initializer_list<int64_t> f) {
 }
 cudaStream_t to_stream(void *s) { return static_cast<cudaStream_t>(s); }
 
+abg_status tree_attn(const abg_tree_attn_args *args, void *ws, int64_t ws_bytes, int withhold, void *stream) {
+    if (!args) return ABG_EINVAL;
+    const abg_tree_attn_args &a = *args;
+    if (!known_type(a.type) || (a.y_type != a.type && a.y_type != ABG_SB_F32)) return ABG_EINVAL;
+    if (a.ysum && a.y_type != ABG_SB_F32) return ABG_EINVAL;
+    if (a.words < 1 || a.words > ABG_MAX_SPAN / 64 || a.B < 1 || a.B > kMax32 - 1 || a.N < 0 || a.N > kMax32 ||
+        a.page < 1 || a.page > kMax32 || a.pages < 0 || a.pages > kMax32 || a.width < 0 || a.width > kMax32 ||
+        !bounded({a.pages, a.Hkv}) || a.pages * a.Hkv > kMax32 || !bounded({a.B, a.width, 4}) || !bounded({a.width, a.page, 2}) || a.width * a.page > kMax32 || a.drafts < a.N || a.drafts > kMax32 ||
+        a.max_span > 64 * a.words || !bounded({a.pages, a.page, a.Hkv, a.D, 4}) ||
+        !bounded({a.drafts, a.Hq, a.D, 4}))
+        return ABG_ESHAPE;
+    int64_t need = 0;
+    const abg_status st = abg_tree_attn_workspace(a.Hq, a.Hkv, a.D, a.max_span, a.type, &need);
+    if (st != ABG_OK) return st;
+    if (a.N == 0) return ABG_OK;
+    if (!a.q || !a.lens || !a.cu || !a.Kd || !a.Vd || !a.mask || !a.y || !ws) return ABG_EINVAL;
+    if ((a.width > 0 && !a.table) || (a.width > 0 && a.pages > 0 && (!a.Kc || !a.Vc))) return ABG_EINVAL;
+    if (ws_bytes < need) return ABG_ESHAPE;
+    for (const void *p : {a.q, a.Kc, a.Vc, a.Kd, a.Vd, static_cast<const void *>(a.gate),
+                          static_cast<const void *>(a.y), static_cast<const void *>(ws)})
+        if (!on(p, 16)) return ABG_EALIGN;
+    if (!on(a.table, 4) || !on(a.lens, 4) || !on(a.cu, 4) || !on(a.mask, 8) || !on(a.ysum, 4)) return ABG_EALIGN;
+    const int64_t te = elem(a.type), cache = a.pages * a.page * a.Hkv * a.D, io = a.N * a.Hq * a.D;
+    if (!apart({span(a.y, io, elem(a.y_type)), span(a.ysum, io / 64, 4), span(ws, need, 1)},
+               {span(a.q, io, te), span(a.Kc, cache, te), span(a.Vc, cache, te), span(a.table, a.B * a.width, 4),
+                span(a.lens, a.B, 4), span(a.cu, a.B + 1, 4), span(a.Kd, a.Hkv * a.drafts * a.D, te),
+                span(a.Vd, a.Hkv * a.drafts * a.D, te), span(a.mask, a.N * a.words, 8), span(a.gate, io, 4)}))
+        return ABG_EALIAS;
+    return cuda_status(launch_tree_attn(a, ws, early_launches(), withhold, to_stream(stream)), "tree_attn launch");
+}
+
 }  // namespace
 
 extern "C" {
@@ -143,34 +174,13 @@ abg_status abg_tree_attn_workspace(int64_t Hq, int64_t Hkv, int64_t D, int64_t m
 }
 
 abg_status abg_tree_attn(const abg_tree_attn_args *args, void *ws, int64_t ws_bytes, void *stream) {
-    if (!args) return ABG_EINVAL;
-    const abg_tree_attn_args &a = *args;
-    if (!known_type(a.type) || (a.y_type != a.type && a.y_type != ABG_SB_F32)) return ABG_EINVAL;
-    if (a.ysum && a.y_type != ABG_SB_F32) return ABG_EINVAL;
-    if (a.words < 1 || a.words > ABG_MAX_SPAN / 64 || a.B < 1 || a.B > kMax32 - 1 || a.N < 0 || a.N > kMax32 ||
-        a.page < 1 || a.page > kMax32 || a.pages < 0 || a.pages > kMax32 || a.width < 0 || a.width > kMax32 ||
-        !bounded({a.pages, a.Hkv}) || a.pages * a.Hkv > kMax32 || !bounded({a.B, a.width, 4}) || !bounded({a.width, a.page, 2}) || a.width * a.page > kMax32 || a.drafts < a.N || a.drafts > kMax32 ||
-        a.max_span > 64 * a.words || !bounded({a.pages, a.page, a.Hkv, a.D, 4}) ||
-        !bounded({a.drafts, a.Hq, a.D, 4}))
-        return ABG_ESHAPE;
-    int64_t need = 0;
-    const abg_status st = abg_tree_attn_workspace(a.Hq, a.Hkv, a.D, a.max_span, a.type, &need);
-    if (st != ABG_OK) return st;
-    if (a.N == 0) return ABG_OK;
-    if (!a.q || !a.lens || !a.cu || !a.Kd || !a.Vd || !a.mask || !a.y || !ws) return ABG_EINVAL;
-    if ((a.width > 0 && !a.table) || (a.width > 0 && a.pages > 0 && (!a.Kc || !a.Vc))) return ABG_EINVAL;
-    if (ws_bytes < need) return ABG_ESHAPE;
-    for (const void *p : {a.q, a.Kc, a.Vc, a.Kd, a.Vd, static_cast<const void *>(a.gate),
-                          static_cast<const void *>(a.y), static_cast<const void *>(ws)})
-        if (!on(p, 16)) return ABG_EALIGN;
-    if (!on(a.table, 4) || !on(a.lens, 4) || !on(a.cu, 4) || !on(a.mask, 8) || !on(a.ysum, 4)) return ABG_EALIGN;
-    const int64_t te = elem(a.type), cache = a.pages * a.page * a.Hkv * a.D, io = a.N * a.Hq * a.D;
-    if (!apart({span(a.y, io, elem(a.y_type)), span(a.ysum, io / 64, 4), span(ws, need, 1)},
-               {span(a.q, io, te), span(a.Kc, cache, te), span(a.Vc, cache, te), span(a.table, a.B * a.width, 4),
-                span(a.lens, a.B, 4), span(a.cu, a.B + 1, 4), span(a.Kd, a.Hkv * a.drafts * a.D, te),
-                span(a.Vd, a.Hkv * a.drafts * a.D, te), span(a.mask, a.N * a.words, 8), span(a.gate, io, 4)}))
-        return ABG_EALIAS;
-    return cuda_status(launch_tree_attn(a, ws, early_launches(), to_stream(stream)), "tree_attn launch");
+    return tree_attn(args, ws, ws_bytes, -1, stream);
+}
+
+abg_status abg_selftest_tree_attn_timeout(const abg_tree_attn_args *args, void *ws, int64_t ws_bytes, int item,
+                                          void *stream) {
+    if (item < 0 || (args && args->type == ABG_SB_F32)) return ABG_EINVAL;
+    return tree_attn(args, ws, ws_bytes, item, stream);
 }
 
 abg_status abg_tree_accept_workspace(int64_t N, int64_t V, int64_t *bytes) {

@@ -532,14 +532,14 @@ size_t tree_attn_bytes(int Hq, int Hkv, int D, int max_span, int type) {
     return type == ABG_SB_F32 ? by_shape(D, row_tile(Hq / Hkv, max_span), Bytes{}) : tree_attn16_bytes(D);
 }
 
-cudaError_t launch_tree_attn(const abg_tree_attn_args &a, void *ws, bool pdl, cudaStream_t stream) {
+cudaError_t launch_tree_attn(const abg_tree_attn_args &a, void *ws, bool pdl, int withhold, cudaStream_t stream) {
     AttnArgs p{};
     p.a = a;
     p.G = static_cast<int>(a.Hq / a.Hkv);
     p.scale2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(a.D)));
     const bool early = pdl && !capturing(stream);
     return a.type == ABG_SB_F32 ? by_shape(a.D, row_tile(p.G, a.max_span), Go{p, ws, early, pdl, stream})
-                                : launch_tree_attn16(p, ws, early, pdl, stream);
+                                : launch_tree_attn16(p, ws, early, pdl, withhold, stream);
 }
 
 }  // namespace abg

@@ -86,6 +86,7 @@ struct Smem16 {
     AttnScan scan;
     uint32_t bad[4][ABG_MAX_SPAN / 32];     // drafts whose V holds an infinity or a NaN, of stretches in turn
     uint32_t tmem;
+    int last[Shape<D>::kCopyWarps];         // last ring item that each copying warp has asked for (-1: none)
     volatile int gone;                      // a wait has given up
 };
 static_assert(sizeof(Smem16<64>) <= 227 * 1024 && sizeof(Smem16<128>) <= 227 * 1024 &&
@@ -203,8 +204,9 @@ __host__ __device__ constexpr uint32_t instr_desc(int m, int n, bool b_mn) {
 }
 
 // A wait that gives up after kWaitLimitNs, or at once when another thread of
-// the block has: the kernel then drains its copies, frees its TMEM and ends,
-// with the device status word set.
+// the block has: the kernel then waits for its copies and products in flight,
+// frees its TMEM and ends, with the device status word set.  Its units' entries
+// are written all the same, since the joining launch goes by them.
 __device__ __forceinline__ bool wait16(uint64_t *bar, uint32_t parity, volatile int *gone) {
     if (mbar_try_wait(bar, parity)) return true;
     const unsigned long long t0 = globaltimer();
@@ -257,7 +259,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(
 
 template <typename T, int D>
 __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __grid_constant__ AttnArgs p,
-                                                                      const __grid_constant__ Maps maps, int box) {
+                                                                      const __grid_constant__ Maps maps, int box,
+                                                                      int withhold) {
     using S = Shape<D>;
     constexpr int kKT = S::kKT, kSlots = S::kSlots, kCols = S::kCols, kRT = S::kRT, kGroups = S::kGroups;
     constexpr int kIssueWarp = 4 * kGroups, kCopyWarp = kIssueWarp + 1, kCopyWarps = S::kCopyWarps;
@@ -301,7 +304,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
         // Item i of the ring is brought by warp i % kCopyWarps: a tile of small
         // pages is many boxes, and a warp issues one at a time.
         // The lane's box of a tile: its row and page.  Taken before the wait
-        // for the slot, so that the table's latency is not in the way.
+        // for the slot, so that the table's latency is not in the way.  The
+        // first of these warps leaves the units' entries: it has the stretches
+        // early, and registers to spare.
+        bool left = false;
         struct At {
             int y, z;
         };
@@ -324,6 +330,10 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
         };
         int first_item = 0, last = -1;  // last: this warp's last item so far
         auto bring = [&](int t, bool value, int item) {
+            if (item == withhold) {  // the self-test: a copy that never comes
+                live = false;
+                return;
+            }
             const bool cache = t < s.ctiles;
             const int step = cache ? box : kDraftBox, boxes = (tile_tokens<kKT>(s, t) + step - 1) / step;
             const CUtensorMap *map = cache ? (value ? &maps.v : &maps.k) : (value ? &maps.vd : &maps.kd);
@@ -355,10 +365,13 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
                 bring(s.t0 + j, value, first_item + i);
             }
             first_item += 2 * n;
+            if (warp == kCopyWarp && lane == 0) line.leave_entry(p, s, blockIdx.x, left);
         }
-        if (!live)  // what was issued must have landed before the block ends
-            for (int i = last; i >= 0 && i > last - kSlots; i -= kCopyWarps)
-                mbar_wait(&bars.full[i % kSlots], (i / kSlots) & 1);
+        if (lane == 0) sm.last[warp - kCopyWarp] = last;
+        if (warp == kCopyWarp && lane == 0) {
+            while (line.next(p, s)) line.leave_entry(p, s, blockIdx.x, left);  // after a wait that gave up
+            line.end_entries(p, blockIdx.x, left);
+        }
     } else if (warp == kIssueWarp) {
         // ------------------------------------------------- the issuing warp
         // One elected lane does it all: every product waits on it, so that
@@ -435,14 +448,9 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
                 }
                 first.skip(2 * n, kSlots);
             }
-            if (!live) {  // matrix instructions in flight read this block's memory
-                tc_commit(&bars.drain);
-                mbar_wait(&bars.drain, 0);
-            }
         }
     } else {
         // ------------------------------------------------- the softmax rows
-        bool left = false;
         const int group = kGroups == 2 ? warp >> 2 : 0;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         int first_item = 0, seg = 0;
@@ -717,17 +725,31 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
                 }
                 if (mine && !whole && k0 == 0 && k1 > 0) p.part_ml[piece * kRT + r] = make_float2(M, L);
             }
-            if (tid == 0) line.leave_entry(p, s, blockIdx.x, left);
             tc_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars.o_free);
         }
-        if (tid == 0) line.end_entries(p, blockIdx.x, left);
     }
     __syncwarp();
     tc_before();
     __syncthreads();
     tc_after();
+    if (sm.gone) {
+        // Whichever wait gave up, nothing that was asked for may arrive or read
+        // after the block's end: the newest copy into each slot (the older ones
+        // have been used), and the matrix instructions.
+        if (warp == kCopyWarp && lane < kSlots) {
+            int i = -1;
+            for (int w = 0; w < kCopyWarps; ++w) i = max(i, sm.last[w]);
+            while (i >= 0 && (i % kSlots != lane || i > sm.last[i % kCopyWarps])) --i;
+            if (i >= 0) mbar_wait(&bars.full[lane], (i / kSlots) & 1);
+        }
+        if (warp == kIssueWarp && elect()) {  // the lane that issued them
+            tc_commit(&bars.drain);
+            mbar_wait(&bars.drain, 0);
+        }
+        __syncwarp();
+    }
     if (warp == kIssueWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
@@ -766,7 +788,7 @@ bool row_map(CUtensorMap *map, const void *p, int64_t D, int64_t rows, int64_t o
 }
 
 template <typename T, int D>
-cudaError_t go16(AttnArgs p, void *ws, bool early, bool pdl, cudaStream_t stream) {
+cudaError_t go16(AttnArgs p, void *ws, bool early, bool pdl, int withhold, cudaStream_t stream) {
     using S = Shape<D>;
     static const cudaError_t attr =
         cudaFuncSetAttribute(attn16_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(Smem16<D>));
@@ -790,7 +812,8 @@ cudaError_t go16(AttnArgs p, void *ws, bool early, bool pdl, cudaStream_t stream
     p.split = reinterpret_cast<AttnSplit *>(w + l.split);
     attn_entries(p, C, S::kRT);
     const cudaError_t e =
-        launch_kernel(attn16_kernel<T, D>, dim3(C), dim3(S::kThreads), sizeof(Smem16<D>), stream, early, p, m, box);
+        launch_kernel(attn16_kernel<T, D>, dim3(C), dim3(S::kThreads), sizeof(Smem16<D>), stream, early, p, m, box,
+                      withhold);
     if (e != cudaSuccess) return e;
     return launch_join<T, D, S::kRT, true>(p, C, pdl, stream);
 }
@@ -802,13 +825,14 @@ size_t tree_attn16_bytes(int D) {
     return attn_layout(sm_count(), rt, D).total;
 }
 
-cudaError_t launch_tree_attn16(const AttnArgs &p, void *ws, bool early, bool pdl, cudaStream_t stream) {
-    const bool bf = p.a.type == ABG_SB_BF16;
-    switch (p.a.D) {
-    case 64: return bf ? go16<__nv_bfloat16, 64>(p, ws, early, pdl, stream) : go16<__half, 64>(p, ws, early, pdl, stream);
-    case 128: return bf ? go16<__nv_bfloat16, 128>(p, ws, early, pdl, stream) : go16<__half, 128>(p, ws, early, pdl, stream);
-    default: return bf ? go16<__nv_bfloat16, 256>(p, ws, early, pdl, stream) : go16<__half, 256>(p, ws, early, pdl, stream);
-    }
+cudaError_t launch_tree_attn16(const AttnArgs &p, void *ws, bool early, bool pdl, int withhold, cudaStream_t stream) {
+    auto of = [&](auto zero) {
+        using T = decltype(zero);
+        return p.a.D == 64    ? go16<T, 64>(p, ws, early, pdl, withhold, stream)
+               : p.a.D == 128 ? go16<T, 128>(p, ws, early, pdl, withhold, stream)
+                              : go16<T, 256>(p, ws, early, pdl, withhold, stream);
+    };
+    return p.a.type == ABG_SB_BF16 ? of(__nv_bfloat16{}) : of(__half{});
 }
 
 // This unit's device status word (OR-ed into *bits).

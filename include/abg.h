@@ -627,7 +627,9 @@ abg_status abg_kv_put(const abg_kv_put_args *a, void *stream);
  *   max_span  the largest span (1 .. 64*words): a hint that picks the tiling
  *   ws     abg_tree_attn_workspace() bytes of device memory, for this call's
  *          stream until it is done; its contents need not be kept or cleared
- * Rows outside the spans are not written.
+ * Rows outside the spans are not written.  If a wait of the 16-bit kernel
+ * gives up (bit 256 of abg_device_status), y and ysum hold no result; nothing
+ * else is touched.
  * Sums, softmax statistics and the work split's partial results are f32.  f32
  * operands are multiplied in f32.  16-bit operands are multiplied exactly and
  * the weights p are rounded to the operands' type before they meet V, so y
@@ -651,6 +653,14 @@ typedef struct abg_tree_attn_args {
  * the device). */
 abg_status abg_tree_attn_workspace(int64_t Hq, int64_t Hkv, int64_t D, int64_t max_span, int type, int64_t *bytes);
 abg_status abg_tree_attn(const abg_tree_attn_args *a, void *ws, int64_t ws_bytes, void *stream);
+/* Failure-detection self-test: abg_tree_attn of 16-bit operands whose blocks
+ * never bring copy `item` (0, 1, ..: K and V tiles in the order of their use),
+ * so that waits run out after the 0.5 s limit in every block that has so many.
+ * Both launches end, with bits 0 and 256 of the device status word set, no copy
+ * or product in flight and the context usable; y holds no result.  A block
+ * with fewer copies finishes its part. */
+abg_status abg_selftest_tree_attn_timeout(const abg_tree_attn_args *a, void *ws, int64_t ws_bytes, int item,
+                                          void *stream);
 
 /*
  * tree_accept: the greedy check of the drafts.  best[n] is the index of the

@@ -1,0 +1,79 @@
+"""Where the draft-verification calls can go wrong: waits that give up, weights
+far below the largest, rings and pages that run out."""
+from __future__ import annotations
+
+import ctypes
+
+import numpy as np
+import pytest
+
+from helpers import host
+from test_gpu_9_draft import attn_case
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+abg = pytest.importorskip("affine_bit_group_gb300")
+
+
+# ------------------------------------------------------ waits that give up ----
+def attn_args(c):
+    """The C call's arguments for tree_attn's of a 16-bit case."""
+    ty = {torch.bfloat16: abg.SB_BF16, torch.float16: abg.SB_F16}[c["q"].dtype]
+    N, Hq, D = c["q"].shape
+    pages, Hkv, page, _ = c["Kc"].shape
+    p = {k: c[k].data_ptr() for k in ("q", "Kc", "Vc", "table", "lens", "cu", "Kd", "Vd", "mask", "y")}
+    return abg._TreeAttnArgs(**p, gate=c["gate"].data_ptr() if c["gate"] is not None else None, ysum=None,
+                             B=len(c["lens"]), N=N, Hq=Hq, Hkv=Hkv, D=D, page=page, pages=pages,
+                             width=c["table"].shape[1], drafts=c["Kd"].shape[1], words=c["mask"].shape[1],
+                             max_span=c["max_span"], type=ty, y_type=ty)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lens,spans,item", [
+    ([40000], [20], 0), ([40000], [64], 3), ([40000, 9000], [64, 30], 6),  # entries of units
+    ([700] * 300, [2] * 300, 0), ([500] * 300, [5] * 300, 5)])             # entries of blocks
+def test_tree_attn_ends_when_a_copy_never_comes(D, lens, spans, item):
+    """The waits run out; the second launch has an entry for every unit all the
+    same, so that it goes by nothing that the workspace held before; and the next
+    call is right.  The workspace starts with entries of no rows (which are
+    harmless) and a mark."""
+    c, _ = attn_case(70, "bf16", 8, 2, D, 16, lens, spans, gate=False)
+    n = abg.tree_attn_workspace(c["q"], c["Kc"], c["max_span"])
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    abg.tree_attn(**c, ws=ws)
+    want = c["y"].clone()
+    blocks = torch.cuda.get_device_properties(0).multi_processor_count
+    entries = ws[n - 24 * blocks:].view(torch.int32).view(blocks, 6)  # n0 h r0 rows first last, the last part of ws
+    ws.zero_()
+    entries[:, 0] = -77
+    assert abg.device_status(clear=True) == 0
+    a = attn_args(c)
+    assert abg.library().abg_selftest_tree_attn_timeout(ctypes.byref(a), ws.data_ptr(), n, item,
+                                                        torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    bits = abg.device_status(clear=True)
+    assert bits == 1 | 256, bits  # waits of this kernel ran out; the waits for what was in flight did not
+    rows = 256 if D < 256 else 128
+    per = -(-64 * c["mask"].shape[1] * 4 // rows)  # entries a request and head
+    e = host(entries)
+    if len(lens) * 2 * per <= blocks:
+        with_rows = [(b * 2 + h) * per + t for b, s in enumerate(spans) for h in range(2) for t in range(-(-4 * s // rows))]
+        assert (e[with_rows, 0] != -77).all()
+    else:
+        assert (e[:, 0] != -77).all()
+    written = e[(e[:, 0] != -77) & (e[:, 3] != 0)]
+    assert (written[:, 4] >= 0).all() and (written[:, 4] < written[:, 5]).all() and (written[:, 5] < blocks).all()
+    assert torch.equal(c["y"][sum(spans):], want[sum(spans):])
+    abg.tree_attn(**c, ws=ws)
+    assert torch.equal(c["y"], want) and abg.device_status(clear=True) == 0
+
+
+def test_tree_attn_selftest_refuses_what_has_no_waits():
+    c, _ = attn_case(71, "f16", 4, 2, 64, 16, [20], [3], gate=False)
+    a, ws = attn_args(c), torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
+    call = abg.library().abg_selftest_tree_attn_timeout
+    assert call(ctypes.byref(a), ws.data_ptr(), ws.numel(), -1, None) == 1
+    a.type = a.y_type = abg.SB_F32
+    assert call(ctypes.byref(a), ws.data_ptr(), ws.numel(), 0, None) == 1
+    assert call(None, ws.data_ptr(), ws.numel(), 0, None) == 1
