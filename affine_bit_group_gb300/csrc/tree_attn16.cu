@@ -452,6 +452,13 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
     } else {
         // ------------------------------------------------- the softmax rows
         const int group = kGroups == 2 ? warp >> 2 : 0;
+        // Weights are 2^(s - ref + kLift): of f16's 65504 the 2^8 that the
+        // reference may be behind leaves 2^7, which keep a weight's 11 bits
+        // down to 2^-21 of the largest instead of 2^-14, and half a unit of
+        // those below at 2^-32 of it instead of 2^-25.  The weight sum and O
+        // have the same factor, in every piece and group.  bf16 has f32's
+        // exponents.
+        constexpr float kLift = std::is_same_v<T, __half> ? 7.0f : 0.0f;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         int first_item = 0, seg = 0;
         // bit b: next phase of buffer b's s_full; phase of pv_done that the
@@ -557,7 +564,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
                             }
                         }
                     }
-                    const float sub = ref == -INFINITY ? 0.0f : ref;
+                    const float sub = ref == -INFINITY ? 0.0f : ref - kLift;
                     const float2 mul = make_float2(p.scale2, p.scale2), off = make_float2(-sub, -sub);
                     float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll

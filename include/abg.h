@@ -634,7 +634,8 @@ abg_status abg_kv_put(const abg_kv_put_args *a, void *stream);
  * operands are multiplied in f32.  16-bit operands are multiplied exactly and
  * the weights p are rounded to the operands' type before they meet V, so y
  * carries about one more rounding of that type than the formula: relative to
- * max_t |V_t|, 2^-8 (bf16) or 2^-11 (f16) at most, before y's own.
+ * max_t |V_t|, at most 2^-8 (bf16), or 2^-11 and 2^-32 for each token seen
+ * (f16, whose smallest numbers are 2^-31 of the largest weight), before y's own.
  * D = 64, 128 or 256; Hq a multiple of Hkv; pages*Hkv and width*page below 2^31;
  * every matrix 16-byte aligned.
  */

@@ -8,7 +8,7 @@ import numpy as np
 import pytest
 
 from helpers import host
-from test_gpu_9_draft import attn_case
+from test_gpu_9_draft import TYPES, U32, UNIT, attn_case, i32, i64
 
 pytestmark = pytest.mark.gpu
 
@@ -77,3 +77,42 @@ def test_tree_attn_selftest_refuses_what_has_no_waits():
     a.type = a.y_type = abg.SB_F32
     assert call(ctypes.byref(a), ws.data_ptr(), ws.numel(), 0, None) == 1
     assert call(None, ws.data_ptr(), ws.numel(), 0, None) == 1
+
+
+# ------------------------------------------------- weights far below the largest ----
+@pytest.mark.parametrize("kind", ["f16", "bf16"])
+@pytest.mark.parametrize("D", [128, 256])
+@pytest.mark.parametrize("tall", [
+    [(0, 25.4)], [(0, 24.4)], [(70000, 20.7)], [(131071, 25.4)],
+    [(0, 17.0), (90000, 24.7)], [(5, 25.4), (6, 18.0)]])  # token, log2 of its weight over the others'
+def test_tree_attn_many_weights_far_below_the_largest(kind, D, tall):
+    """131072 tokens of one score under one or two that are far above: the small
+    weights together count, though each is below 2^-14 (f16's normal range) or
+    2^-25 (half of its smallest) of the largest.  Requests that share the cache,
+    so many that most of them are not cut (a piece has a largest score of its
+    own); f32 result, one head, V = 1 where the score is small and 0 where it is
+    large."""
+    n, page, B, dtype = 131072, 128, 160, TYPES[kind]
+    K, V = (np.zeros((n, D)) for _ in range(2))
+    q = np.zeros(D)
+    q[0], V[:] = 16.0, 1.0
+    for t, lg in tall:
+        K[t, 0], V[t] = lg * np.log(2) * np.sqrt(D) / q[0], 0.0
+    K = torch.from_numpy(K).to(dtype)
+    s = K.double().numpy()[:, 0] * q[0] / np.sqrt(D)
+    w = np.exp(s - s.max())
+    want = (w * V[:, 0]).sum() / w.sum()
+
+    def pages(x):
+        return torch.as_tensor(x).to(dtype).view(n // page, 1, page, D).cuda()
+
+    y = torch.empty((B, 1, D), device="cuda")
+    draft = torch.zeros((1, B, D), dtype=dtype, device="cuda")
+    abg.tree_attn(torch.from_numpy(q).to(dtype).cuda().repeat(B, 1, 1), pages(K), pages(V),
+                  i32(np.arange(n // page)[None].repeat(B, 0)), i32([n] * B), i32(np.arange(B + 1)), draft, draft,
+                  i64(np.zeros((B, 1))), y)
+    # the weights' rounding: half a unit in the last place of each, or 2^-32 of the
+    # largest; in f32, of a sum of positive terms: a score's and a weight's few
+    # roundings, sums of 16 at a time that may be cut off (two roundings each), joins
+    bound = UNIT[kind] * 1.01 + n * 2.0**-32 + want * U32 * (2 * n / 16 + 600)
+    assert np.abs(host(y) - want).max() <= bound, (host(y).min(), host(y).max(), want, bound)
