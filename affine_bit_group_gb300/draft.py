@@ -125,11 +125,18 @@ class DraftDecoder:
         """One step: the drafts' logits, the check, and the accepted drafts' rows
         into the cache.  Returns (rows, add, last): rows[cu[b]+i] is the i-th
         accepted draft of request b, add[b] their number, last[b] the token
-        that follows them (all on the GPU)."""
+        that follows them (all on the GPU).  A request whose accepted drafts
+        find no page, or no place in its table row, is refused (info[1] counts
+        them): its rows are -1, add[b] is 0 and last[b] is its first draft's
+        token, with which it can go on once pages have been given back."""
         N = len(tok)
         best, rows = (torch.empty(N, dtype=torch.int32, device="cuda") for _ in range(2))
         tree_accept(self.logits(tok, parent, cu, max_span), tok, parent, cu, best, rows, self.add, self.last)
         slots = self._plan(self.add, cu, N)
         for i in range(len(self.dm.layers)):
             kv_put(self.Kd[i].transpose(0, 1), self.Vd[i].transpose(0, 1), self.Kc[i], self.Vc[i], slots=slots, rows=rows)
+        stored = self.lens[0] - self.lens[1]  # a refused request's length has not changed
+        rows.masked_fill_(slots < 0, -1)
+        torch.where(stored != self.add, tok[cu[:-1].clamp(max=N - 1).long()], self.last, out=self.last)
+        self.add.copy_(stored)
         return rows, self.add, self.last

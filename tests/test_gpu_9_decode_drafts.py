@@ -113,3 +113,24 @@ def test_a_step_that_runs_out_of_pages_says_so(weights):
     dec = decoder(weights, 2, pages=1)
     dec.step(i32([1, 2]), i32([-1, -1]), i32([0, 1, 2]), 1)
     assert host(dec.info).tolist() == [1, 1] and host(dec.lens[0]).tolist() == [1, 0]
+
+
+def test_a_request_that_is_refused_keeps_its_token(weights):
+    """Two requests and one page: the second is not accepted, its last token stays
+    the next step's first, and what follows is what follows without the refusal."""
+    want, _ = one_by_one(weights, [1, 2], 4, torch.float32)
+    dec = decoder(weights, 2, pages=1)
+    # request 1's second guess is right, but there is no page for either token
+    rows, add, last = dec.step(i32([1, 2, 3, want[1, 0]]), i32([-1, -1, 0, 0]), i32([0, 1, 4]), 3)
+    assert host(dec.info).tolist() == [1, 1] and host(dec.lens[0]).tolist() == [1, 0]
+    assert host(add).tolist() == [1, 0] and host(rows).tolist() == [0, -1, -1, -1]
+    assert host(last).tolist() == [want[0, 0], 2]
+    dec.release(torch.tensor([True, False]))
+    tok = last[1:].clone()
+    for i in range(4):  # the page is request 1's now; request 0 has no drafts
+        rows, add, last = dec.step(tok, i32([-1]), i32([0, 0, 1]), 1)
+        assert host(dec.info).tolist()[1] == 0 and host(add).tolist() == [0, 1]
+        assert host(last).tolist() == [-1, want[1, i]] and host(rows).tolist() == [0]
+        tok = last[1:].clone()
+    rows, add, last = dec.step(tok, i32([-1]), i32([0, 0, 1]), 1)  # a fifth token, and no second page
+    assert host(add).tolist() == [0, 0] and host(last).tolist() == [-1, want[1, 3]] and host(rows).tolist() == [-1]
