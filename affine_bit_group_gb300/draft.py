@@ -31,8 +31,9 @@ def rotation(positions: int, D: int, base: float = 10000.0):
 
 class DraftDecoder:
     """A decoder's state for `requests` requests: a paged cache of `pages` pages
-    of `page` tokens in `cache` (float32, bfloat16 or float16), and the buffers
-    of a step of at most `rows` drafts.
+    of `page` tokens in `cache` (float32, bfloat16 or float16), up to max_len
+    tokens (whole pages) a request, and the buffers of a step of at most `rows`
+    drafts.
 
     dm: the weights (decode.DeviceModel), q_rows = Hq*D and kv_rows = Hkv*D;
     embed: [vocabulary][hidden] float32; qn_w, kn_w: [D] norm weights of q and k
@@ -46,7 +47,8 @@ class DraftDecoder:
         self.Hq, self.Hkv = L["q"].rows // D, L["k"].rows // D
         ones = torch.ones(D, device="cuda")
         self.qn_w, self.kn_w = ones if qn_w is None else qn_w, ones if kn_w is None else kn_w
-        self.cos, self.sin = rotation(max_len, D)
+        width = -(-max_len // page)
+        self.cos, self.sin = rotation(width * page, D)  # a position for every token that the table holds
         kv = (len(dm.layers), pages, self.Hkv, page, D)
         self.Kc, self.Vc = torch.zeros(kv, dtype=cache, device="cuda"), torch.zeros(kv, dtype=cache, device="cuda")
         kv = (len(dm.layers), self.Hkv, rows, D)
@@ -59,7 +61,7 @@ class DraftDecoder:
         self.lens, self.held = [i32(requests), i32(requests)], [i32(requests), i32(requests)]
         self.ends = [torch.tensor([0, pages], device="cuda"), torch.zeros(2, dtype=torch.int64, device="cuda")]
         self.ring = torch.arange(pages, dtype=torch.int32, device="cuda")
-        self.table = i32(requests, -(-max_len // page))
+        self.table = i32(requests, width)
         self.info, self.last, self.add = i32(2), i32(requests), i32(requests)
 
     def _products(self, ms, x, xs):

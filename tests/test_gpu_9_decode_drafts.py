@@ -134,3 +134,17 @@ def test_a_request_that_is_refused_keeps_its_token(weights):
         tok = last[1:].clone()
     rows, add, last = dec.step(tok, i32([-1]), i32([0, 0, 1]), 1)  # a fifth token, and no second page
     assert host(add).tolist() == [0, 0] and host(last).tolist() == [-1, want[1, 3]] and host(rows).tolist() == [-1]
+
+
+def test_the_last_page_is_used_to_its_end(weights):
+    """max_len 10 in pages of 4: the table holds 12 tokens, and all of them have a
+    rotation; a thirteenth is refused."""
+    want, _ = one_by_one(weights, [7], 12, torch.float32)
+    dec = draft.DraftDecoder(*weights, D=D, requests=1, pages=4, page=4, max_len=10, rows=40)
+    tok = i32([7])
+    for i in range(12):
+        _, add, last = dec.step(tok, i32([-1]), i32([0, 1]), 1)
+        assert host(add).tolist() == [1] and host(last).tolist() == [want[0, i]], i
+        tok = last.clone()
+    dec.step(tok, i32([-1]), i32([0, 1]), 1)
+    assert host(dec.info).tolist() == [0, 1] and host(dec.lens[0]).tolist() == [12]
