@@ -74,8 +74,10 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
     const int64_t head = a.ends[0], tail = a.ends[1];
     const int64_t avail = max(int64_t(0), min(tail - head, static_cast<int64_t>(a.ring_len)));
     const int R = a.ring_len;
+    const int64_t room = R - avail;  // pages given back never lie over free ones, which others read meanwhile
     const int head0 = static_cast<int>((head % R + R) % R), tail0 = static_cast<int>((tail % R + R) % R);
-    int64_t done_x = 0, done_f = 0, taken = 0;  // taken: extras up to the last request that was granted any
+    int64_t done_x = 0, done_f = 0;
+    int64_t taken = 0, given = 0;  // extras up to the last request that was granted any, pages up to the last given back
     int bad = 0;
     for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
         const int b = b0 + tid;
@@ -101,8 +103,9 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
         done_x += all_x, done_f += all_f;
         if (b < a.B) {
             const bool ok = !k.gone && !k.bad && (k.extra == 0 || x <= avail);
-            const bool done = k.gone && !k.bad;
+            const bool done = k.gone && !k.bad && (k.freed == 0 || f <= room);
             if (ok && k.extra > 0) taken = x;
+            if (done && k.freed > 0) given = f;
             bad += !ok && !done;
             s_at[b] = ok ? ring_at(head0, x - k.extra, R) : done ? ring_at(tail0, f - k.freed, R) : -1;
             if (blockIdx.x == 0) {
@@ -118,15 +121,17 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const __grid_co
 #pragma unroll
         for (int d = 16; d >= 1; d >>= 1) {
             taken = max(taken, __shfl_xor_sync(0xffffffffu, taken, d));
+            given = max(given, __shfl_xor_sync(0xffffffffu, given, d));
             bad += __shfl_xor_sync(0xffffffffu, bad, d);
         }
-        if (lane == 0) s_sum[0][warp] = taken, s_bad[warp] = bad;
+        if (lane == 0) s_sum[0][warp] = taken, s_sum[1][warp] = given, s_bad[warp] = bad;
     }
     __syncthreads();
     if (blockIdx.x == 0 && tid == 0) {
-        for (int w = 1; w < kPlanThreads / 32; ++w) taken = max(taken, s_sum[0][w]), bad += s_bad[w];
+        for (int w = 1; w < kPlanThreads / 32; ++w)
+            taken = max(taken, s_sum[0][w]), given = max(given, s_sum[1][w]), bad += s_bad[w];
         a.ends_out[0] = head + taken;
-        a.ends_out[1] = tail + done_f;
+        a.ends_out[1] = tail + given;
         a.info[0] = static_cast<int32_t>(taken);
         a.info[1] = bad;
     }

@@ -539,8 +539,10 @@ abg_status abg_swiglu_mlp_static(const uint32_t *wg, const float *sg, const floa
  *   add exceeds its span, need or held exceeds width, lens or held is
  *   negative, or lens + add exceeds 2^31 - 1.  Pages given back go to the
  *   tail in request order (none of them is granted in the same call); a
- *   request whose held is out of range gives nothing back and counts as
- *   refused.
+ *   request whose held is out of range, or whose pages and those given back
+ *   before them do not fit in the ring beside the free ones (so none, where
+ *   ring_len is at least the number of pages that there are), gives nothing
+ *   back and counts as refused.
  *   table  in place: entries held .. need-1 of granted requests
  *   ring   in place: entries from tail on, for pages given back
  *   slots  i64 [N]  slot of token lens+i for i < add of granted requests, else -1

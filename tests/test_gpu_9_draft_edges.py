@@ -116,3 +116,38 @@ def test_tree_attn_many_weights_far_below_the_largest(kind, D, tall):
     # roundings, sums of 16 at a time that may be cut off (two roundings each), joins
     bound = UNIT[kind] * 1.01 + n * 2.0**-32 + want * U32 * (2 * n / 16 + 600)
     assert np.abs(host(y) - want).max() <= bound, (host(y).min(), host(y).max(), want, bound)
+
+
+# ------------------------------------------------------------- rings that are full ----
+def test_page_plan_refuses_pages_that_the_ring_has_no_room_for():
+    """Five entries, four of them free pages, and three requests that end: one page
+    fits, the next request's do not, and neither does one after it.  The free pages
+    stay what they are (a fourth request takes one of them in the same call)."""
+    d = dict(lens=i32([5, 40, 7, 16]), add=i32([-1, -1, -1, 1]), cu=i32([0, 0, 0, 0, 1]), held=i32([1, 3, 1, 1]),
+             ends=i64([2, 6]), ring=i32([90, 91, 92, 93, 94]), table=i32(np.arange(16).reshape(4, 4)))
+    out = dict(slots=i64([7]), pos=i32([7]), lens_out=i32([9] * 4), held_out=i32([9] * 4), ends_out=i64([9, 9]),
+               info=i32([9, 9]))
+    for _ in range(2):
+        abg.page_plan(**d, page=16, **out)
+        assert host(out["lens_out"]).tolist() == [0, 40, 7, 17] and host(out["held_out"]).tolist() == [0, 3, 1, 2]
+        assert host(out["ends_out"]).tolist() == [3, 7] and host(out["info"]).tolist() == [1, 2]
+        assert host(d["ring"]).tolist() == [90, 0, 92, 93, 94]
+        assert host(d["table"]).ravel().tolist() == [*range(13), 92, 14, 15]
+        assert host(out["slots"]).tolist() == [92 * 16] and host(out["pos"]).tolist() == [16]
+
+
+def test_page_plan_many_requests_end_in_a_small_ring():
+    """1500 requests of three pages end, and the ring has room for 1000 pages: the
+    first 333 requests' pages, over three rounds of the scan."""
+    B = 1500
+    table = i32(np.arange(4 * B).reshape(B, 4))
+    ring, ends = i32(np.full(1100, -5)), i64([50, 150])
+    lens_out, held_out, ends_out, info = i32(np.zeros(B)), i32(np.zeros(B)), i64([0, 0]), i32([0, 0])
+    abg.page_plan(i32(np.full(B, 40)), i32(np.full(B, -1)), i32(np.zeros(B + 1)), i32(np.full(B, 3)), ends, ring, table, 16,
+                  i64(np.zeros(0)), i32(np.zeros(0)), lens_out, held_out, ends_out, info)
+    n = 333
+    assert host(ends_out).tolist() == [50, 150 + 3 * n] and host(info).tolist() == [0, B - n]
+    assert host(lens_out).tolist() == [0] * n + [40] * (B - n) and host(held_out).tolist() == [0] * n + [3] * (B - n)
+    want = np.full(1100, -5)
+    want[(150 + np.arange(3 * n)) % 1100] = (4 * np.arange(n)[:, None] + np.arange(3)).ravel()
+    assert host(ring).tolist() == want.tolist()
