@@ -341,9 +341,15 @@ def _handle(stream):
     return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
-def _bytes(numel, device):
+def _bytes(numel, device, stream):
+    """A workspace out of torch's memory for the call's own stream: it is let go
+    of while the call may still run, and torch hands it out again in that
+    stream's order."""
     import torch
-    return torch.empty(numel, dtype=torch.uint8, device=device)
+    if stream is None:
+        return torch.empty(numel, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(_handle(stream), device=device)):
+        return torch.empty(numel, dtype=torch.uint8, device=device)
 
 
 def page_plan(lens, add, cu, held, ends, ring, table, page: int, slots, pos, lens_out, held_out, ends_out, info,
@@ -400,12 +406,11 @@ def tree_attn(q, Kc, Vc, table, lens, cu, Kd, Vd, mask, y, max_span: int | None 
     float32) and, with a float32 y, its 64-value group sums ysum (see
     abg_tree_attn).  max_span defaults to the most that the masks can hold.  ws
     is a uint8 tensor of tree_attn_workspace() bytes; by default the call takes
-    one from torch's allocator on the current stream (give ws for a call on
-    another stream)."""
+    one from torch's allocator, for its stream."""
     if max_span is None:
         max_span = 64 * mask.shape[1]
     if ws is None:
-        ws = _bytes(tree_attn_workspace(q, Kc, max_span), q.device)
+        ws = _bytes(tree_attn_workspace(q, Kc, max_span), q.device, stream)
     st = (_marshal or _load_marshal()).tree_attn(q, Kc, Vc, table, lens, cu, Kd, Vd, mask, y, max_span, gate, ysum, ws,
                                                  _handle(stream))
     if st:
@@ -427,7 +432,7 @@ def tree_accept(logits, tok, parent, cu, best, rows, add, last, ws=None, stream=
     number add [B], and the next tokens last [B] (see abg_tree_accept); all
     int32.  ws as in tree_attn."""
     if ws is None:
-        ws = _bytes(tree_accept_workspace(logits), logits.device)
+        ws = _bytes(tree_accept_workspace(logits), logits.device, stream)
     st = (_marshal or _load_marshal()).tree_accept(logits, tok, parent, cu, best, rows, add, last, ws, _handle(stream))
     if st:
         _check(st, "abg_tree_accept")

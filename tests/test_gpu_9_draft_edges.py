@@ -151,3 +151,35 @@ def test_page_plan_many_requests_end_in_a_small_ring():
     want = np.full(1100, -5)
     want[(150 + np.arange(3 * n)) % 1100] = (4 * np.arange(n)[:, None] + np.arange(3)).ravel()
     assert host(ring).tolist() == want.tolist()
+
+
+# ------------------------------------------------------------- other streams ----
+@pytest.mark.parametrize("handle", [False, True])
+def test_default_workspace_belongs_to_the_call_s_stream(monkeypatch, handle):
+    """A call on another stream without ws: the memory that it takes is not handed
+    out to the current stream while the call may run."""
+    c, _ = attn_case(81, "bf16", 8, 2, 128, 16, [900, 40], [9, 30], tail=0)
+    abg.tree_attn(**c)
+    want = c["y"].clone()
+    x = torch.randn((39, 5000), device="cuda")
+    tok, parent, cu = i32(np.zeros(39)), i32(np.full(39, -1)), c["cu"]
+    out = [i32(np.zeros(39)), i32(np.zeros(39)), i32([0, 0]), i32([0, 0])]
+    side, taken, plain = torch.cuda.Stream(), [], abg._bytes
+
+    def spied(*a):
+        t = plain(*a)
+        taken.append((t.data_ptr(), t.numel()))
+        return t
+
+    monkeypatch.setattr(abg, "_bytes", spied)
+    c["y"].zero_()
+    torch.cuda.synchronize()
+    stream = side.cuda_stream if handle else side
+    abg.tree_attn(**c, stream=stream)
+    abg.tree_accept(x, tok, parent, cu, *out, stream=stream)
+    assert len(taken) == 2
+    mine = [torch.empty(n, dtype=torch.uint8, device="cuda") for _, n in taken for _ in range(8)]
+    for p, n in taken:
+        assert all(m.data_ptr() + m.numel() <= p or p + n <= m.data_ptr() for m in mine)
+    side.synchronize()
+    assert torch.equal(c["y"], want) and torch.equal(out[0], x.argmax(1).int())
