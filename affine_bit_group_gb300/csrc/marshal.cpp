@@ -139,6 +139,8 @@ int tree_plan(PyObject *const *a) {
 
 // k v Kc Vc slots rows q qo qn_w kn_w cos sin pos eps stream
 int kv_put(PyObject *const *a) {
+    if ((a[10] == Py_None) != (a[11] == Py_None)) throw Wrong("cos and sin must both be given, or neither");
+    if ((a[6] == Py_None) != (a[7] == Py_None)) throw Wrong("q and qo must both be given, or neither");
     const Caches c = caches(a[2], a[3]);
     const Tensor &kt = tensor(a[0], "k");
     const ScalarType src = kt.scalar_type();

@@ -207,3 +207,17 @@ def test_binding_refuses_wrong_tensors():
     for call, words in bad_calls():
         with pytest.raises(ValueError, match=words):
             call()
+
+
+@pytest.mark.parametrize("given,words", [
+    ("sin", "cos and sin must both be given"), ("cos", "cos and sin must both be given"),
+    ("qo", "q and qo must both be given"), ("q", "q and qo must both be given")])
+def test_binding_refuses_half_of_a_pair(given, words):
+    """A rotation's sines without its cosines, or a place for q without q, is not
+    taken for none of them."""
+    import torch
+    t = dict(sin=torch.zeros(5, 32), cos=torch.zeros(5, 32), q=torch.zeros(3, 4, 64), qo=torch.zeros(3, 4, 64))
+    k = torch.zeros(3, 2, 64)
+    with pytest.raises(ValueError, match=words):
+        abg.kv_put(k, k, torch.zeros(1, 2, 8, 64), torch.zeros(1, 2, 8, 64), pos=torch.zeros(3, dtype=torch.int32),
+                   **{given: t[given]})
