@@ -84,6 +84,16 @@ void *stream_of(PyObject *o, const Tensor &t) {
     return c10::cuda::getCurrentCUDAStream(t.get_device()).stream();
 }
 
+// The library's call, without the interpreter's lock: a launch waits while the
+// stream's queue is full, and what it waits for may need the lock.
+template <typename F>
+int unlocked(F call) {
+    PyThreadState *const state = PyEval_SaveThread();
+    const int status = call();
+    PyEval_RestoreThread(state);
+    return status;
+}
+
 struct Caches {
     int type;
     ScalarType scalar;
@@ -118,13 +128,20 @@ int page_plan(PyObject *const *a) {
                  &slots = tensor(a[8], "slots");
     const int64_t B = lens.numel(), N = slots.numel(), R = ring.numel(), width = B ? table.numel() / B : 0;
     auto *lens_p = static_cast<int32_t *>(need(lens, ScalarType::Int, B, "lens"));
-    return abg_page_plan(
-        lens_p, i32(a[1], B, "add"), i32(a[2], B + 1, "cu"), i32(a[3], B, "held"),
-        need<int64_t>(a[4], ScalarType::Long, 2, "ends"), static_cast<int32_t *>(need(ring, ScalarType::Int, R, "ring")),
-        static_cast<int32_t *>(need(table, ScalarType::Int, 0, "table")),
-        static_cast<int64_t *>(need(slots, ScalarType::Long, N, "slots")), i32(a[9], N, "pos"),
-        i32(a[10], B, "lens_out"), i32(a[11], B, "held_out"), need<int64_t>(a[12], ScalarType::Long, 2, "ends_out"),
-        i32(a[13], 2, "info"), B, N, number(a[7]), width, R, stream_of(a[14], lens));
+    auto *add = i32(a[1], B, "add"), *cu = i32(a[2], B + 1, "cu"), *held = i32(a[3], B, "held");
+    auto *ends = need<int64_t>(a[4], ScalarType::Long, 2, "ends");
+    auto *ring_p = static_cast<int32_t *>(need(ring, ScalarType::Int, R, "ring"));
+    auto *table_p = static_cast<int32_t *>(need(table, ScalarType::Int, 0, "table"));
+    auto *slots_p = static_cast<int64_t *>(need(slots, ScalarType::Long, N, "slots"));
+    auto *pos = i32(a[9], N, "pos"), *lens_out = i32(a[10], B, "lens_out"), *held_out = i32(a[11], B, "held_out");
+    auto *ends_out = need<int64_t>(a[12], ScalarType::Long, 2, "ends_out");
+    auto *info = i32(a[13], 2, "info");
+    const int64_t page = number(a[7]);
+    void *stream = stream_of(a[14], lens);
+    return unlocked([&] {
+        return abg_page_plan(lens_p, add, cu, held, ends, ring_p, table_p, slots_p, pos, lens_out, held_out, ends_out,
+                             info, B, N, page, width, R, stream);
+    });
 }
 
 int tree_plan(PyObject *const *a) {
@@ -132,9 +149,13 @@ int tree_plan(PyObject *const *a) {
     const int64_t B = lens.numel(), N = parent.numel();
     if (mask.dim() != 2 || mask.size(0) != N) throw Wrong("mask must be [N][words]");
     auto *parent_p = static_cast<int32_t *>(need(parent, ScalarType::Int, N, "parent"));
-    return abg_tree_plan(parent_p, static_cast<int32_t *>(need(lens, ScalarType::Int, B, "lens")),
-                         i32(a[2], B + 1, "cu"), static_cast<uint64_t *>(need(mask, ScalarType::Long, N, "mask")),
-                         i32(a[4], N, "pos"), B, N, mask.size(1), stream_of(a[5], parent));
+    auto *lens_p = static_cast<int32_t *>(need(lens, ScalarType::Int, B, "lens"));
+    auto *cu = i32(a[2], B + 1, "cu");
+    auto *mask_p = static_cast<uint64_t *>(need(mask, ScalarType::Long, N, "mask"));
+    auto *pos = i32(a[4], N, "pos");
+    const int64_t words = mask.size(1);
+    void *stream = stream_of(a[5], parent);
+    return unlocked([&] { return abg_tree_plan(parent_p, lens_p, cu, mask_p, pos, B, N, words, stream); });
 }
 
 // k v Kc Vc slots rows q qo qn_w kn_w cos sin pos eps stream
@@ -178,7 +199,8 @@ int kv_put(PyObject *const *a) {
         throw Wrong("eps must be a number");
     }
     p.eps = static_cast<float>(eps);
-    return abg_kv_put(&p, stream_of(a[14], kt));
+    void *stream = stream_of(a[14], kt);
+    return unlocked([&] { return abg_kv_put(&p, stream); });
 }
 
 // q Kc Vc table lens cu Kd Vd mask y max_span gate ysum ws stream
@@ -206,7 +228,9 @@ int tree_attn(PyObject *const *a) {
     p.B = B, p.N = N, p.Hq = Hq, p.Hkv = c.Hkv, p.D = c.D, p.page = c.page, p.pages = c.pages;
     p.width = B ? table.numel() / B : 0, p.drafts = Kd.size(1), p.words = mask.size(1);
     p.max_span = number(a[10]), p.type = c.type;
-    return abg_tree_attn(&p, need(ws, ScalarType::Byte, 0, "ws"), ws.numel(), stream_of(a[14], q));
+    void *ws_p = need(ws, ScalarType::Byte, 0, "ws"), *stream = stream_of(a[14], q);
+    const int64_t ws_bytes = ws.numel();
+    return unlocked([&] { return abg_tree_attn(&p, ws_p, ws_bytes, stream); });
 }
 
 // logits tok parent cu best rows add last ws stream
@@ -215,10 +239,17 @@ int tree_accept(PyObject *const *a) {
     if (x.dim() != 2 || x.scalar_type() != ScalarType::Float || !x.is_cuda() || (x.stride(1) != 1 && x.size(1) > 1))
         throw Wrong("logits must be a float32 CUDA tensor [N][V] with contiguous rows");
     const int64_t N = x.size(0), V = x.size(1), B = add.numel();
-    return abg_tree_accept(static_cast<float *>(x.data_ptr()), N > 1 ? x.stride(0) : V, i32(a[1], N, "tok"),
-                           i32(a[2], N, "parent"), i32(a[3], B + 1, "cu"), i32(a[4], N, "best"), i32(a[5], N, "rows"),
-                           static_cast<int32_t *>(need(add, ScalarType::Int, B, "add")), i32(a[7], B, "last"), B, N, V,
-                           need(ws, ScalarType::Byte, 0, "ws"), ws.numel(), stream_of(a[9], x));
+    auto *logits = static_cast<float *>(x.data_ptr());
+    const int64_t ld = N > 1 ? x.stride(0) : V;
+    auto *tok = i32(a[1], N, "tok"), *parent = i32(a[2], N, "parent"), *cu = i32(a[3], B + 1, "cu");
+    auto *best = i32(a[4], N, "best"), *rows = i32(a[5], N, "rows");
+    auto *add_p = static_cast<int32_t *>(need(add, ScalarType::Int, B, "add"));
+    auto *last = i32(a[7], B, "last");
+    void *ws_p = need(ws, ScalarType::Byte, 0, "ws"), *stream = stream_of(a[9], x);
+    const int64_t ws_bytes = ws.numel();
+    return unlocked([&] {
+        return abg_tree_accept(logits, ld, tok, parent, cu, best, rows, add_p, last, B, N, V, ws_p, ws_bytes, stream);
+    });
 }
 
 template <int (*fn)(PyObject *const *), int kArgs>

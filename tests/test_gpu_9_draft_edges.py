@@ -183,3 +183,62 @@ def test_default_workspace_belongs_to_the_call_s_stream(monkeypatch, handle):
         assert all(m.data_ptr() + m.numel() <= p or p + n <= m.data_ptr() for m in mine)
     side.synchronize()
     assert torch.equal(c["y"], want) and torch.equal(out[0], x.argmax(1).int())
+
+
+# ------------------------------------------------------------ other threads ----
+SLOW = """
+#include <unistd.h>
+#define SLOW(name) int name() { usleep(300000); return 0; }
+SLOW(abg_page_plan) SLOW(abg_tree_plan) SLOW(abg_kv_put) SLOW(abg_tree_attn) SLOW(abg_tree_accept)
+"""
+TICKS = """
+import ctypes, sys, threading, time
+ctypes.CDLL(sys.argv[1], mode=ctypes.RTLD_GLOBAL)  # its calls take the place of the library's
+import torch
+sys.path[:0] = sys.argv[2:]
+import test_gpu_9_draft as t
+c, _ = t.attn_case(80, 'bf16', 4, 2, 64, 16, [20], [3], tail=0)
+z = lambda *s, dtype=torch.int32: torch.zeros(s, dtype=dtype, device='cuda')
+ws = z(99, dtype=torch.uint8)
+calls = dict(
+    page_plan=lambda: t.abg.page_plan(z(2), z(2), z(3), z(2), z(2, dtype=torch.int64), z(9), z(2, 4), 16,
+                                      z(5, dtype=torch.int64), z(5), z(2), z(2), z(2, dtype=torch.int64), z(2)),
+    tree_plan=lambda: t.abg.tree_plan(z(3), z(1), z(2), z(3, 1, dtype=torch.int64), z(3)),
+    kv_put=lambda: t.abg.kv_put(z(3, 2, 64, dtype=torch.float32), z(3, 2, 64, dtype=torch.float32),
+                                z(1, 2, 8, 64, dtype=torch.float32), z(1, 2, 8, 64, dtype=torch.float32)),
+    tree_attn=lambda: t.abg.tree_attn(**c, ws=ws),
+    tree_accept=lambda: t.abg.tree_accept(z(3, 9, dtype=torch.float32), z(3), z(3), z(2), z(3), z(3), z(1), z(1), ws=ws))
+ticks, done = [], False
+def run():
+    while not done:
+        ticks.append(time.perf_counter())
+        time.sleep(0.005)
+thread = threading.Thread(target=run)
+thread.start()
+for name, call in calls.items():
+    t0 = time.perf_counter()
+    call()
+    t1 = time.perf_counter()
+    print(name, t1 - t0, sum(t0 + 0.1 < x < t0 + 0.25 for x in ticks))
+done = True
+thread.join()
+"""
+
+
+def test_calls_let_other_threads_run(tmp_path):
+    """Calls that take long (as launches do when the queue is full) do not stop the
+    other Python threads: the library's calls are replaced by ones that sleep."""
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    (tmp_path / "slow.c").write_text(SLOW)
+    (tmp_path / "ticks.py").write_text(TICKS)
+    lib = tmp_path / "slow.so"
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", str(lib), str(tmp_path / "slow.c")], check=True)
+    out = subprocess.run([sys.executable, str(tmp_path / "ticks.py"), str(lib), os.path.dirname(here), here], check=True,
+                         timeout=120, capture_output=True, text=True).stdout.split("\n")
+    got = {name: (float(took), int(ticks)) for name, took, ticks in (line.split() for line in out if line)}
+    assert len(got) == 5
+    for name, (took, ticks) in got.items():
+        assert took > 0.25 and ticks >= 3, (name, took, ticks)
