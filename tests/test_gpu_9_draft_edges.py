@@ -242,3 +242,18 @@ def test_calls_let_other_threads_run(tmp_path):
     assert len(got) == 5
     for name, (took, ticks) in got.items():
         assert took > 0.25 and ticks >= 3, (name, took, ticks)
+
+
+# ------------------------------------------------------------- shapes of kv_put's tensors ----
+def test_kv_put_refuses_rotations_of_another_width():
+    """A rotation table with the head's whole width (each cosine twice) is not read
+    as one with half of it and twice the positions."""
+    k, pos = torch.ones((3, 1, 64), device="cuda"), i32([0, 1, 2])
+    Kc, Vc = (torch.zeros((1, 1, 3, 64), device="cuda") for _ in range(2))
+    t = {w: torch.ones((9, w), device="cuda") for w in (16, 32, 64)}
+    for cos, sin in ((64, 64), (64, 32), (32, 64), (16, 16)):
+        with pytest.raises(ValueError, match=r"cos and sin must be \[positions\]\[32\]"):
+            abg.kv_put(k, k, Kc, Vc, cos=t[cos], sin=t[sin], pos=pos)
+    assert not Kc.any() and not Vc.any()
+    abg.kv_put(k, k, Kc, Vc, cos=t[32], sin=torch.zeros_like(t[32]), pos=pos)
+    assert torch.equal(Kc, torch.ones_like(Kc))
