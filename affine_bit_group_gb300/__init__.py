@@ -110,7 +110,7 @@ def library(build_if_missing: bool = True) -> ctypes.CDLL:
             if build_if_missing:
                 from . import _build
                 if _build.stale():
-                    _build.build()
+                    _build.build(marshal=False)
             if not os.path.exists(_LIB_PATH):
                 raise RuntimeError(f"the CUDA library {_LIB_PATH} is not built")
             lib = ctypes.CDLL(_LIB_PATH)
@@ -322,10 +322,15 @@ _marshal = None  # the CPython module that takes the draft calls' tensors apart,
 
 
 def _load_marshal():
-    library()  # builds both if stale
+    library()
     import importlib
 
     import torch  # noqa: F401  (its libraries, which the module uses)
+
+    from . import _build
+    with _lock:
+        if _build.marshal_stale():
+            _build.build()
     return importlib.import_module("._marshal", __name__)  # and sets the name above
 
 
