@@ -12,6 +12,7 @@ from __future__ import annotations
 import glob
 import os
 import subprocess
+import sys
 import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -52,8 +53,29 @@ def stale() -> bool:
 
 
 def marshal_stale() -> bool:
-    """Whether _marshal.so has to be built (never without torch)."""
-    return _torch_root() is not None and _older(MARSHAL, [os.path.join(CSRC, "marshal.cpp")] + _headers())
+    """Whether _marshal.so has to be built (never without torch): also where it was
+    built for another torch or Python."""
+    return _torch_root() is not None and (_older(MARSHAL, [os.path.join(CSRC, "marshal.cpp")] + _headers()) or
+                                          _built_for() not in (None, _host()))
+
+
+def _host() -> str:
+    """The Python and the torch that the module is compiled against."""
+    version = os.path.join(_torch_root(), "version.py")
+    text = ""
+    if os.path.exists(version):
+        with open(version) as f:
+            text = f.read()
+    return f"{sys.implementation.cache_tag} {_torch_root()}\n{text}"
+
+
+def _built_for():
+    """What _host() was when the module was linked (None: not known)."""
+    note = os.path.join(OBJ, "marshal.host")
+    if not os.path.exists(note):
+        return None
+    with open(note) as f:
+        return f.read()
 
 
 def _torch_root():
@@ -99,6 +121,8 @@ def _link_marshal():
                     "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(_torch_root(), "lib"), "-ltorch_python", "-lc10_cuda",
                     "-lc10", "-ltorch_cpu"], check=True)
     os.replace(tmp, MARSHAL)
+    with open(os.path.join(OBJ, "marshal.host"), "w") as f:
+        f.write(_host())
 
 
 def build(force: bool = False, verbose: bool = False, marshal: bool = True) -> str:

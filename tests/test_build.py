@@ -76,3 +76,20 @@ def test_library_errors_are_told(tree, monkeypatch):
     with pytest.raises(RuntimeError, match="vec.cu:\nno such header"):
         _build.build()
     assert not os.path.exists(_build.LIB) and not os.path.exists(_build.MARSHAL)
+
+
+def test_binding_is_rebuilt_for_another_torch(tree, monkeypatch, tmp_path):
+    """Whatever the files' times: the module is compiled against torch's headers."""
+    pytest.importorskip("torch")
+    _build.build()
+    tree()
+    assert not _build.marshal_stale()
+    root = tmp_path / "torch"
+    root.mkdir()
+    (root / "version.py").write_text("__version__ = '2.99'\n")
+    monkeypatch.setattr(_build, "_torch_root", lambda: str(root))
+    assert _build.marshal_stale() and not _build.stale()
+    _build.build()
+    assert str(root) in tree() and not _build.marshal_stale()
+    (root / "version.py").write_text("__version__ = '3.0'\n")
+    assert _build.marshal_stale()
