@@ -589,8 +589,9 @@ abg_status abg_tree_plan(const int32_t *parent, const int32_t *lens, const int32
  *          pairs (i, i + D/2) of q and k by row pos[n] (the rows are NaN where
  *          pos[n] is outside 0 .. cos_rows-1)
  *   pos    i32 [N], with cos and sin only
- * D = 64, 128 or 256.  Two tokens of one slot leave either's row.  Rows, row
- * strides and head strides are multiples of 16 bytes.
+ * D = 64, 128 or 256.  Slots name distinct rows: what two tokens of one slot
+ * leave in it is not specified (each value is one or the other's, not all of
+ * one token).  Rows, row strides and head strides are multiples of 16 bytes.
  */
 typedef struct abg_kv_put_args {
     const void *q, *k, *v;
