@@ -120,7 +120,8 @@ Rows strided(PyObject *o, int64_t heads, int64_t D, ScalarType type, const char 
         t.stride(2) != 1)
         throw Wrong(std::string(name) + " must be a " + type_name(type) + " CUDA tensor [rows][" +
                     std::to_string(heads) + "][" + std::to_string(D) + "] with contiguous columns");
-    return {t.data_ptr(), t.size(0), t.stride(0), t.stride(1)};
+    // (the stride of a single row or head is never used, and can be anything)
+    return {t.data_ptr(), t.size(0), t.size(0) > 1 ? t.stride(0) : heads * D, heads > 1 ? t.stride(1) : D};
 }
 
 int page_plan(PyObject *const *a) {

@@ -257,3 +257,18 @@ def test_kv_put_refuses_rotations_of_another_width():
     assert not Kc.any() and not Vc.any()
     abg.kv_put(k, k, Kc, Vc, cos=t[32], sin=torch.zeros_like(t[32]), pos=pos)
     assert torch.equal(Kc, torch.ones_like(Kc))
+
+
+def test_kv_put_takes_one_row_or_head_of_any_stride():
+    """The strides of a single row and of a single head are never stepped over: a
+    view whose are no multiple of 16 bytes is as good as another."""
+    src = torch.randn(400, device="cuda")
+    k = torch.as_strided(src, (1, 2, 64), (7, 64, 1))
+    v = torch.as_strided(src, (1, 2, 64), (3, 128, 1), 16)
+    Kc, Vc = (torch.zeros((1, 2, 4, 64), device="cuda") for _ in range(2))
+    abg.kv_put(k, v, Kc, Vc)
+    assert torch.equal(Kc[0, :, 0], k[0]) and torch.equal(Vc[0, :, 0], v[0])
+    k = torch.as_strided(src, (3, 1, 64), (64, 5, 1))
+    Kc, Vc = (torch.zeros((1, 1, 4, 64), device="cuda") for _ in range(2))
+    abg.kv_put(k, k, Kc, Vc)
+    assert torch.equal(Kc[0, 0, :3], k[:, 0]) and torch.equal(Vc[0, 0, :3], k[:, 0])
