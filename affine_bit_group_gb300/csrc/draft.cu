@@ -563,7 +563,7 @@ constexpr int64_t kSlice = 4096;  // shortest slice
 
 int64_t best_slices(int64_t N, int64_t V) {
     // four blocks an SM, all at once (304 rows: 51.7 us; eight blocks 52.8)
-    const int64_t want = std::max<int64_t>(1, 4 * 152 / std::max<int64_t>(1, N));
+    const int64_t want = std::max<int64_t>(1, 4 * sm_count() / std::max<int64_t>(1, N));
     return std::max<int64_t>(1, std::min<int64_t>(want, (V + kSlice - 1) / kSlice));
 }
 
