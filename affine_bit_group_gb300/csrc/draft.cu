@@ -267,8 +267,9 @@ __global__ void __launch_bounds__(64 * W) tree_plan_kernel(const int32_t *parent
 // slot and position are already on their way.  Instructions bound it as much as
 // bytes: a lane a column pair, not a lane a column, and the heads' norm factors
 // (a division, a root and a reciprocal, each rounded) side by side in the lanes.
-// 8191 rows of 16 + 4 + 4 heads of 128, f32 to bf16: 33 us for 156 MB, 4.7 TB/s,
-// 70% of a plain copy's rate.  A lane a column took 53 us.
+// 8191 rows of 16 + 4 + 4 heads of 128, f32 to bf16: 32.7 us for 156 MB, 4.8 TB/s,
+// 70% of a plain copy's rate (35.0 without the early start).  A lane a column took
+// 53 us.
 constexpr int kPutWarps = 8;
 
 template <typename T>
@@ -459,8 +460,8 @@ __global__ void __launch_bounds__(32 * kPutWarps, D == 256 ? 2 : D == 128 ? 3 : 
 // The logits are read once, a block a slice of a row; a slice's answer is one
 // 64-bit key, the value's order in the upper half and ~index in the lower, so
 // that the largest key is the largest value at its lowest index.  Memory bounds
-// it: 304 rows of 248320, 302 MB, in 52 us (5.8 TB/s, 86% of a plain copy's rate);
-// 8 rows, 7.9 MB, in 8.5 us out of memory, less from the second-level cache.
+// it: 304 rows of 248320, 302 MB, with accept_kernel in 54.0 us (5.6 TB/s, 83% of a
+// plain copy's rate); 8 rows, 7.9 MB, in 6.4 us.
 constexpr int kBestThreads = 256;
 
 __device__ __forceinline__ uint64_t best_key(float v, uint32_t i) {
@@ -562,7 +563,7 @@ __global__ void __launch_bounds__(ABG_MAX_SPAN) accept_kernel(const int32_t *tok
 constexpr int64_t kSlice = 4096;  // shortest slice
 
 int64_t best_slices(int64_t N, int64_t V) {
-    // four blocks an SM, all at once (304 rows: 51.7 us; eight blocks 52.8)
+    // four blocks an SM, all at once (304 rows: 54.0 us; eight blocks 54.7)
     const int64_t want = std::max<int64_t>(1, 4 * sm_count() / std::max<int64_t>(1, N));
     return std::max<int64_t>(1, std::min<int64_t>(want, (V + kSlice - 1) / kSlice));
 }
@@ -580,8 +581,9 @@ cudaError_t launch_page_plan(const PagePlanArgs &a, bool pdl, cudaStream_t strea
     const int table_blocks = (32 * a.B + kPlanThreads - 1) / kPlanThreads;
     const int token_blocks = static_cast<int>(std::min<int64_t>(tokens, std::max(sm_count(), 2 * sm_count() - table_blocks)));
     // An early start deals blocks to the SMs that the launch ahead leaves first,
-    // so that some get more than their share: for short grids only (768000
-    // tokens: 10.3 us, early 11.4; 384 tokens: 8.2 us, early 5.2).
+    // so that some get more than their share: for short grids only (384 tokens:
+    // 8.2 us, early 5.2; 768000 tokens: 10.3 us, early 11.4 when one block did
+    // both kinds of work, 9.9 with the tables on blocks of their own).
     const bool early = pdl && token_blocks + table_blocks <= sm_count() && !capturing(stream);
     return launch_kernel(page_plan_kernel, dim3(static_cast<unsigned>(token_blocks + table_blocks)), dim3(kPlanThreads),
                          smem, stream, early, a, token_blocks);
@@ -641,8 +643,8 @@ cudaError_t launch_tree_accept(const float *logits, int64_t ld, const int32_t *t
     const int64_t slice = (V + slices - 1) / slices;
     uint64_t *parts = static_cast<uint64_t *>(ws);
     if (N > 0) {
-        // early where there is not work for all SMs, as page_plan (304 rows: 56.8
-        // us, early 59.3; eight rows: 8.2 us, early 6.5)
+        // early where there is not work for all SMs, as page_plan (304 rows: 54.0
+        // us, early 59.0; eight rows: 8.2 us, early 6.4)
         const bool early = pdl && slices == (V + kSlice - 1) / kSlice && !capturing(stream);
         const cudaError_t e = launch_kernel(best_kernel, dim3(static_cast<unsigned>(slices * N)), dim3(kBestThreads), 0,
                                             stream, early, logits, ld, V, slices, slice, parts);

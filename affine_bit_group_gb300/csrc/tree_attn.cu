@@ -38,7 +38,7 @@ struct Smem {
     // Tokens a tile: what two blocks an SM have room for, since a tile costs three
     // barriers whatever its size (64 columns, 32 rows: 32 tokens 46.6 us, 64 40.5,
     // 128 in one stage 43.2; 16 rows: 32 tokens 101, 64 86, 128 79; 128 columns, 4
-    // rows: two stages of 32 171 us, one of 64 138, 5.8 TB/s).
+    // rows: two stages of 32 171 us, one of 64 138, now 134.5, 6.0 TB/s).
     static constexpr int kKT = D == 256 ? 32 : D == 128 || kRT == kManyRows ? 64 : 128;
     static constexpr int kLd = D + 4;                        // rows of Q and K start in different banks
     static constexpr int kPLd = kRT + 4;
@@ -129,7 +129,7 @@ __device__ __forceinline__ void scatter_sums(float (&x)[16], int lane) {
 // to every D/8 lanes, and the lanes' sums meet by shuffles, 16 values at a time,
 // which leaves each lane the scores of one row, so that the softmax needs no
 // shared memory and no barrier before it.  (Rows of Q read from shared memory
-// again for every token took 70 us where this takes 65: 8 drafts of 8 heads on
+// again for every token took 70 us where this took 65, now 62.9: 8 drafts of 8 heads on
 // four ragged f32 requests of 4100 tokens, 256 columns.)  Up to 8 rows: a thread
 // holds a part of the columns of one token for all rows, and the parts meet in
 // shared memory (8 rows on 32 requests of 4100 tokens: 91 us, 4.4 TB/s; with a

@@ -30,10 +30,14 @@
 // to deliver them.  Rows past the unit's are not loaded, and warps without rows
 // skip the softmax.
 //
-// Measured: 24 bf16 drafts on 32 ragged requests of 12000 tokens, 592 MB, 110 us
+// Measured: 24 bf16 drafts on 32 ragged requests of 12000 tokens, 592 MB, 108.8 us
 // with the joining (5.4 TB/s, 80% of a plain copy's rate; bytes bound it); 63 f16
-// drafts on 131072 tokens of one request, 134 MB and 67.6 GFLOP, 80 us (0.85
-// PFLOP/s; the chain product, softmax, product of one row group bounds it).
+// drafts on 131071 tokens of one request, 134 MB and 67.6 GFLOP, 76.8 us (0.88
+// PFLOP/s; the chain product, softmax, product of one row group bounds it).  A box
+// costs its warp about 130 cycles, so pages whose largest power of two is small
+// are bound by their boxes: 8 bf16 drafts on 32 ragged requests of 6000 tokens, 128
+// columns, in pages of 16, 24 or 128 tokens 62-63 us, of 100 (boxes of 4) 70, of 101
+// (boxes of 1) 197.
 #include "abg_kernels.cuh"
 #include "tree_attn.cuh"
 #include "tree_attn16.cuh"
@@ -509,7 +513,7 @@ __global__ void __launch_bounds__(Shape<D>::kThreads, 1) attn16_kernel(const __g
                 if (busy) {
                     // 64 scores at a time: the last ones are read for the maximum,
                     // then again for their weights, which keeps the row in 168
-                    // registers without spills
+                    // registers
                     float x[64];
                     auto read = [&](int h) {
                         float(&lo)[32] = *reinterpret_cast<float(*)[32]>(x);
