@@ -189,8 +189,9 @@ int kv_put(PyObject *const *a) {
     p.kn_w = need_or_null<float>(a[9], ScalarType::Float, c.D, "kn_w");
     if (a[10] != Py_None) {
         const Tensor &cos = tensor(a[10], "cos"), &sin = tensor(a[11], "sin");
-        if (cos.dim() < 2 || sin.dim() < 2 || cos.size(-1) != c.D / 2 || sin.size(-1) != c.D / 2)
-            throw Wrong("cos and sin must be [positions][" + std::to_string(c.D / 2) + "]");
+        for (const Tensor *t : {&cos, &sin})  // (or flat)
+            if (t->dim() > 1 ? t->size(-1) != c.D / 2 : t->numel() % (c.D / 2) != 0)
+                throw Wrong("cos and sin must be [positions][" + std::to_string(c.D / 2) + "]");
         p.cos_rows = cos.numel() / (c.D / 2);
         p.cos = static_cast<float *>(need(cos, ScalarType::Float, p.cos_rows * (c.D / 2), "cos"));
         p.sin = need<float>(a[11], ScalarType::Float, p.cos_rows * (c.D / 2), "sin");

@@ -272,3 +272,16 @@ def test_kv_put_takes_one_row_or_head_of_any_stride():
     Kc, Vc = (torch.zeros((1, 1, 4, 64), device="cuda") for _ in range(2))
     abg.kv_put(k, k, Kc, Vc)
     assert torch.equal(Kc[0, 0, :3], k[:, 0]) and torch.equal(Vc[0, 0, :3], k[:, 0])
+
+
+def test_kv_put_takes_flat_rotation_tables():
+    k, pos = torch.randn((3, 1, 64), device="cuda"), i32([0, 2, 1])
+    ang = torch.rand((3, 32), device="cuda")
+    want, got = ([torch.zeros((1, 1, 3, 64), device="cuda") for _ in range(2)] for _ in range(2))
+    abg.kv_put(k, k, *want, cos=ang.cos(), sin=ang.sin(), pos=pos)
+    abg.kv_put(k, k, *got, cos=ang.cos(), sin=ang.sin().flatten(), pos=pos)
+    assert torch.equal(got[0], want[0])
+    abg.kv_put(k, k, *got, cos=ang.cos().flatten(), sin=ang.sin().unsqueeze(1), pos=pos)
+    assert torch.equal(got[0], want[0])
+    with pytest.raises(ValueError, match="cos and sin must be"):
+        abg.kv_put(k, k, *got, cos=ang.cos().flatten()[:95], sin=ang.sin(), pos=pos)
