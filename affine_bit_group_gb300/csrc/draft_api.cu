@@ -1,51 +1,12 @@
 // C ABI of the draft-verification calls (include/abg.h): argument validation
 // and launches.  Everything that the host can see is refused here; lengths,
 // tables and slots live on the GPU and are bounded by the kernels.
+#include "checks.cuh"
 #include "draft.cuh"
-
-#include <initializer_list>
 
 using namespace abg;
 
 namespace {
-
-constexpr int64_t kMax32 = 0x7fffffff;
-
-bool on(const void *p, uintptr_t to) { return reinterpret_cast<uintptr_t>(p) % to == 0; }
-
-struct Span {
-    uintptr_t lo, hi;
-};
-Span span(const void *p, int64_t count, size_t elem) {
-    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-    return {lo, p ? lo + static_cast<uintptr_t>(count) * elem : lo};
-}
-// No output may overlap an input or another output.
-bool apart(std::initializer_list<Span> out, std::initializer_list<Span> in) {
-    auto meet = [](Span a, Span b) { return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi; };
-    for (auto o = out.begin(); o != out.end(); ++o) {
-        for (auto p = out.begin(); p != o; ++p)
-            if (meet(*o, *p)) return false;
-        for (const Span &i : in)
-            if (meet(*o, i)) return false;
-    }
-    return true;
-}
-
-bool known_type(int t) { return t >= ABG_SB_F32 && t <= ABG_SB_F16; }
-int64_t elem(int t) { return t == ABG_SB_F32 ? 4 : 2; }
-bool known_width(int64_t D) { return D == 64 || D == 128 || D == 256; }
-// a product of positive factors that stays below 2^62
-bool bounded(std::initializer_list<int64_t> f) {
-    int64_t n = 1;
-    for (int64_t v : f) {
-        if (v < 0) return false;
-        if (v > 0 && n > (int64_t(1) << 62) / v) return false;
-        n *= v > 0 ? v : 1;
-    }
-    return true;
-}
-cudaStream_t to_stream(void *s) { return static_cast<cudaStream_t>(s); }
 
 abg_status tree_attn(const abg_tree_attn_args *args, void *ws, int64_t ws_bytes, int withhold, void *stream) {
     if (!args) return ABG_EINVAL;
