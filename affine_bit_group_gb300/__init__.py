@@ -1,7 +1,8 @@
 """Python binding of libabg.so: the GB300 affine 4-bit group-quantized
 matrix-vector product (q4mv), its activation producers (rmsq, swq, gsum), the
-decode-token stage graph, and the calls that check drafted tokens over a paged
-cache (page_plan, tree_plan, kv_put, tree_attn, tree_accept).
+decode-token stage graph, the calls that check drafted tokens over a paged
+cache (page_plan, tree_plan, kv_put, tree_attn, tree_accept), and those of a
+cache held in 4 or 8 bits (kvq_put, kvq_attn, kvq_get).
 
 This module only marshals arguments: tensors become device pointers, the
 current torch stream becomes a cudaStream_t, and status codes become
@@ -16,12 +17,13 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+import typing
 
 __all__ = [
     "TREE", "FAST", "AbgError", "library", "q4mv", "q4mv_ex", "q4mm", "gsum", "rmsq", "swq", "StageGraph", "Node",
     "device_status", "set_q4mv_tuning", "MAX_COLS", "SB_F32", "SB_BF16", "SB_F16", "SB_TYPES", "swiglu_mlp_static",
     "page_plan", "tree_plan", "kv_put", "tree_attn", "tree_attn_workspace", "tree_accept", "tree_accept_workspace",
-    "MAX_SPAN", "MAX_REQUESTS",
+    "MAX_SPAN", "MAX_REQUESTS", "KvqCache", "kvq_cache", "kvq_put", "kvq_get", "kvq_attn", "kvq_attn_workspace",
 ]
 
 TREE, FAST = 0, 1
@@ -100,6 +102,36 @@ class _TreeAttnArgs(ctypes.Structure):
                [("type", ctypes.c_int32), ("y_type", ctypes.c_int32)]
 
 
+class _KvqCache(ctypes.Structure):
+    """Mirror of struct abg_kvq_cache in include/abg.h."""
+    _fields_ = [(f, ctypes.c_void_p) for f in ("Kc", "Ks", "Vc", "Vs")] + \
+               [(f, ctypes.c_int64) for f in ("pages", "Hkv", "page", "D")] + \
+               [("bits", ctypes.c_int32), ("group", ctypes.c_int32)]
+
+
+class _KvqPutArgs(ctypes.Structure):
+    """Mirror of struct abg_kvq_put_args in include/abg.h."""
+    _fields_ = [(f, ctypes.c_void_p) for f in ("q", "k", "v")] + \
+               [(f, ctypes.c_int64) for f in ("q_row", "q_head", "k_row", "k_head", "v_row", "v_head")] + \
+               [(f, ctypes.c_void_p) for f in ("rows", "slots", "qn_w", "kn_w", "cos", "sin", "pos", "qo")] + \
+               [("c", _KvqCache)] + [(f, ctypes.c_int64) for f in ("N", "src_rows", "Hq", "cos_rows")] + \
+               [("eps", ctypes.c_float), ("src_type", ctypes.c_int32), ("q_type", ctypes.c_int32)]
+
+
+class _KvqGetArgs(ctypes.Structure):
+    """Mirror of struct abg_kvq_get_args in include/abg.h."""
+    _fields_ = [("c", _KvqCache)] + [(f, ctypes.c_void_p) for f in ("slots", "k", "v")] + \
+               [(f, ctypes.c_int64) for f in ("k_row", "k_head", "v_row", "v_head", "N")] + [("type", ctypes.c_int32)]
+
+
+class _KvqAttnArgs(ctypes.Structure):
+    """Mirror of struct abg_kvq_attn_args in include/abg.h."""
+    _fields_ = [("q", ctypes.c_void_p), ("c", _KvqCache)] + \
+               [(f, ctypes.c_void_p) for f in ("table", "lens", "cu", "Kd", "Vd", "mask", "gate", "y", "ysum")] + \
+               [(f, ctypes.c_int64) for f in ("B", "N", "Hq", "width", "drafts", "words", "max_span")] + \
+               [("type", ctypes.c_int32), ("y_type", ctypes.c_int32)]
+
+
 def library(build_if_missing: bool = True) -> ctypes.CDLL:
     """Loads libabg.so (building it with nvcc first if it is missing or stale)."""
     global _lib
@@ -141,6 +173,10 @@ def library(build_if_missing: bool = True) -> ctypes.CDLL:
             lib.abg_selftest_tree_attn_timeout.argtypes = [P, P, I64, I, P]
             lib.abg_tree_accept_workspace.argtypes = [I64, I64, ctypes.POINTER(I64)]
             lib.abg_tree_accept.argtypes = [P, I64] + [P] * 7 + [I64] * 3 + [P, I64, P]
+            lib.abg_kvq_put.argtypes = [P, P]
+            lib.abg_kvq_get.argtypes = [P, P]
+            lib.abg_kvq_attn_workspace.argtypes = [P, I64, I64, I, ctypes.POINTER(I64)]
+            lib.abg_kvq_attn.argtypes = [P, P, I64, P]
             lib.abg_device_status.argtypes = [ctypes.POINTER(ctypes.c_uint32), I]
             lib.abg_selftest_wait_timeout.argtypes = [P]
             lib.abg_set_q4mv_tuning.argtypes = [I, I, I, I]
@@ -155,7 +191,8 @@ def library(build_if_missing: bool = True) -> ctypes.CDLL:
                       "abg_device_status", "abg_set_q4mv_tuning", "abg_selftest_wait_timeout", "abg_page_plan",
                       "abg_tree_plan", "abg_kv_put", "abg_tree_attn_workspace", "abg_tree_attn",
                       "abg_selftest_tree_attn_timeout",
-                      "abg_tree_accept_workspace", "abg_tree_accept"):
+                      "abg_tree_accept_workspace", "abg_tree_accept", "abg_kvq_put", "abg_kvq_get", "abg_kvq_attn_workspace",
+                      "abg_kvq_attn"):
                 getattr(lib, f).restype = ctypes.c_int
             _lib = lib
     return _lib
@@ -442,6 +479,80 @@ def tree_accept(logits, tok, parent, cu, best, rows, add, last, ws=None, stream=
     if st:
         _check(st, "abg_tree_accept")
     return rows, add, last
+
+
+class KvqCache(typing.NamedTuple):
+    """A cache in 4 or 8 bits: words Kc, Vc int32 [pages][Hkv][page][D*bits/32] and
+    pairs (scale, bias) Ks, Vs float16 [pages][Hkv][page][D/group][2] (see
+    abg_kvq_cache).  The calls take any tuple of such tensors; bits and group are
+    those of its shapes."""
+    Kc: object
+    Ks: object
+    Vc: object
+    Vs: object
+
+
+def kvq_cache(pages: int, Hkv: int, page: int, D: int, bits: int = 4, group: int = 64, device="cuda") -> KvqCache:
+    """A KvqCache whose rows are zeros."""
+    import torch
+    if bits not in (4, 8) or group not in (32, 64) or D not in (64, 128, 256):
+        raise ValueError("bits must be 4 or 8, group 32 or 64, D 64, 128 or 256")
+
+    def words():
+        return torch.zeros((pages, Hkv, page, D * bits // 32), dtype=torch.int32, device=device)
+
+    def pairs():
+        return torch.zeros((pages, Hkv, page, D // group, 2), dtype=torch.float16, device=device)
+
+    return KvqCache(words(), pairs(), words(), pairs())
+
+
+def kvq_put(k, v, cache, slots=None, rows=None, q=None, qo=None, qn_w=None, kn_w=None, cos=None, sin=None, pos=None,
+            eps: float = 1e-6, stream=None):
+    """kv_put into a quantised cache (Kc, Ks, Vc, Vs) (see abg_kvq_put): k, v and q
+    are of one type, qo of that type or, for float32 rows, of any."""
+    st = (_marshal or _load_marshal()).kvq_put(k, v, cache, slots, rows, q, qo, qn_w, kn_w, cos, sin, pos, eps,
+                                               _handle(stream))
+    if st:
+        _check(st, "abg_kvq_put")
+    return cache
+
+
+def kvq_get(cache, k, v, slots=None, stream=None):
+    """The rows slots[n] (default n) of a quantised cache into k and v
+    [rows][Hkv][D] (any strides over rows and heads; one of them may be None),
+    float32, bfloat16 or float16 (see abg_kvq_get)."""
+    st = (_marshal or _load_marshal()).kvq_get(cache, k, v, slots, _handle(stream))
+    if st:
+        _check(st, "abg_kvq_get")
+    return k, v
+
+
+def kvq_attn_workspace(q, cache, max_span: int) -> int:
+    """Bytes of kvq_attn's workspace for queries and a cache like these."""
+    D, words, groups = q.shape[2], cache[0].shape[3], cache[1].shape[3]
+    c = _KvqCache(Hkv=cache[0].shape[1], D=D, bits=32 * words // D, group=D // max(groups, 1))
+    n = ctypes.c_int64()
+    _check(library().abg_kvq_attn_workspace(ctypes.byref(c), q.shape[1], max_span, _type_of(q, "q"), ctypes.byref(n)),
+           "abg_kvq_attn_workspace")
+    return n.value
+
+
+def kvq_attn(q, cache, table, lens, cu, Kd, Vd, mask, y, max_span: int | None = None, gate=None, ysum=None, ws=None,
+             stream=None):
+    """tree_attn over a quantised cache (Kc, Ks, Vc, Vs) (see abg_kvq_attn): q, Kd
+    and Vd are of one type, y of that type or float32.  ws is a uint8 tensor of
+    kvq_attn_workspace() bytes; by default the call takes one from torch's
+    allocator, for its stream."""
+    if max_span is None:
+        max_span = 64 * mask.shape[1]
+    if ws is None:
+        ws = _bytes(kvq_attn_workspace(q, cache, max_span), q.device, stream)
+    st = (_marshal or _load_marshal()).kvq_attn(q, cache, table, lens, cu, Kd, Vd, mask, y, max_span, gate, ysum, ws,
+                                                _handle(stream))
+    if st:
+        _check(st, "abg_kvq_attn")
+    return y
 
 
 def swiglu_mlp_static(gate, up, down, x, xsum, y, cols: int, mode: int = TREE, stream=None):

@@ -11,6 +11,11 @@ the logits agree with, `page_plan` and a `kv_put` per layer into the pages.  A
 request's first draft is its last known token, so that every step accepts at
 least one; a step whose trees are single tokens is ordinary decoding.
 
+With a cache in 4 or 8 bits, kvq_put and kvq_attn take the places of kv_put and
+tree_attn.  The drafts' rows are then quantised and read back (kvq_get) before
+the attention, so that a draft sees the others as it would see them in the cache,
+and a step of several drafts gives what as many steps of one give.
+
 All of a step's calls are queued on the current stream; nothing is read back
 between them.  The products take up to eight tokens at a time (abg_q4mm).
 """
@@ -18,9 +23,11 @@ from __future__ import annotations
 
 import torch
 
-from . import MAX_SPAN, kv_put, page_plan, q4mm, rmsq, swq, tree_accept, tree_attn, tree_attn_workspace, tree_plan
+from . import (MAX_SPAN, kv_put, kvq_attn, kvq_attn_workspace, kvq_cache, kvq_get, kvq_put, page_plan, q4mm,
+               rmsq, swq, tree_accept, tree_attn, tree_attn_workspace, tree_plan)
 
 Q4MM_TOKENS = 8  # abg_q4mm's most
+QUANTISED = {"q4": 4, "q8": 8}  # bits
 
 
 def rotation(positions: int, D: int, base: float = 10000.0):
@@ -31,9 +38,9 @@ def rotation(positions: int, D: int, base: float = 10000.0):
 
 class DraftDecoder:
     """A decoder's state for `requests` requests: a paged cache of `pages` pages
-    of `page` tokens in `cache` (float32, bfloat16 or float16), up to max_len
-    tokens (whole pages) a request, and the buffers of a step of at most `rows`
-    drafts.
+    of `page` tokens in `cache` (float32, bfloat16, float16, or "q4" or "q8": 4 or
+    8 bits in groups of `group` columns), up to max_len tokens (whole pages) a
+    request, and the buffers of a step of at most `rows` drafts.
 
     dm: the weights (decode.DeviceModel), q_rows = Hq*D and kv_rows = Hkv*D;
     embed: [vocabulary][hidden] float32; qn_w, kn_w: [D] norm weights of q and k
@@ -41,7 +48,7 @@ class DraftDecoder:
     """
 
     def __init__(self, dm, embed, D: int, requests: int, pages: int, page: int = 16, max_len: int = 4096,
-                 rows: int = 64, cache=torch.float32, eps: float = 1e-6, qn_w=None, kn_w=None):
+                 rows: int = 64, cache=torch.float32, eps: float = 1e-6, qn_w=None, kn_w=None, group: int = 64):
         self.dm, self.embed, self.D, self.page, self.eps, self.rows = dm, embed, D, page, eps, rows
         L = dm.layers[0]
         self.Hq, self.Hkv = L["q"].rows // D, L["k"].rows // D
@@ -49,10 +56,17 @@ class DraftDecoder:
         self.qn_w, self.kn_w = ones if qn_w is None else qn_w, ones if kn_w is None else kn_w
         width = -(-max_len // page)
         self.cos, self.sin = rotation(width * page, D)  # a position for every token that the table holds
-        kv = (len(dm.layers), pages, self.Hkv, page, D)
-        self.Kc, self.Vc = torch.zeros(kv, dtype=cache, device="cuda"), torch.zeros(kv, dtype=cache, device="cuda")
+        self.quantised = cache in QUANTISED
+        self.ty = torch.float32 if self.quantised else cache  # of the drafts' rows
+        if self.quantised:
+            bits = QUANTISED[cache]
+            self.caches = [kvq_cache(pages, self.Hkv, page, D, bits, group) for _ in dm.layers]
+            self.drafts = kvq_cache(1, self.Hkv, rows, D, bits, group)  # of one layer at a time
+        else:
+            kv = (len(dm.layers), pages, self.Hkv, page, D)
+            self.Kc, self.Vc = torch.zeros(kv, dtype=cache, device="cuda"), torch.zeros(kv, dtype=cache, device="cuda")
         kv = (len(dm.layers), self.Hkv, rows, D)
-        self.Kd, self.Vd = torch.zeros(kv, dtype=cache, device="cuda"), torch.zeros(kv, dtype=cache, device="cuda")
+        self.Kd, self.Vd = torch.zeros(kv, dtype=self.ty, device="cuda"), torch.zeros(kv, dtype=self.ty, device="cuda")
 
         def i32(*shape):
             return torch.zeros(shape, dtype=torch.int32, device="cuda")
@@ -103,17 +117,24 @@ class DraftDecoder:
         mask, pos = torch.empty((N, words), dtype=torch.int64, device="cuda"), torch.empty(N, dtype=torch.int32, device="cuda")
         tree_plan(parent, self.lens[0], cu, mask, pos)
         h = self.embed[tok.long()]
-        ty = self.Kc.dtype
-        qo = torch.empty((N, Hq, D), dtype=ty, device="cuda")
+        qo = torch.empty((N, Hq, D), dtype=self.ty, device="cuda")
         y, ysum = torch.empty((N, Hq, D), device="cuda"), torch.empty((N, Hq * D // 64), device="cuda")
-        ws = torch.empty(tree_attn_workspace(qo, self.Kc[0], max_span), dtype=torch.uint8, device="cuda")
+        ws = torch.empty(kvq_attn_workspace(qo, self.caches[0], max_span) if self.quantised else
+                         tree_attn_workspace(qo, self.Kc[0], max_span), dtype=torch.uint8, device="cuda")
         for i, L in enumerate(dm.layers):
             q, k, v = self._products([L["q"], L["k"], L["v"]], *self._norm(h, L["rms1"]))
-            kv_put(k.view(N, Hkv, D), v.view(N, Hkv, D), self.Kd[i].unsqueeze(0), self.Vd[i].unsqueeze(0),
-                   q=q.view(N, Hq, D), qo=qo, qn_w=self.qn_w, kn_w=self.kn_w, cos=self.cos, sin=self.sin, pos=pos,
-                   eps=self.eps)
-            tree_attn(qo, self.Kc[i], self.Vc[i], self.table, self.lens[0], cu, self.Kd[i], self.Vd[i], mask, y,
-                      max_span=max_span, ysum=ysum, ws=ws)
+            k, v = k.view(N, Hkv, D), v.view(N, Hkv, D)
+            rope = dict(q=q.view(N, Hq, D), qo=qo, qn_w=self.qn_w, kn_w=self.kn_w, cos=self.cos, sin=self.sin, pos=pos,
+                        eps=self.eps)
+            if self.quantised:
+                kvq_put(k, v, self.drafts, **rope)
+                kvq_get(self.drafts, self.Kd[i, :, :N].transpose(0, 1), self.Vd[i, :, :N].transpose(0, 1))
+                kvq_attn(qo, self.caches[i], self.table, self.lens[0], cu, self.Kd[i], self.Vd[i], mask, y,
+                         max_span=max_span, ysum=ysum, ws=ws)
+            else:
+                kv_put(k, v, self.Kd[i].unsqueeze(0), self.Vd[i].unsqueeze(0), **rope)
+                tree_attn(qo, self.Kc[i], self.Vc[i], self.table, self.lens[0], cu, self.Kd[i], self.Vd[i], mask, y,
+                          max_span=max_span, ysum=ysum, ws=ws)
             o, = self._products([L["o"]], y.view(N, Hq * D), ysum)
             gate, up = self._products([L["gate"], L["up"]], *self._norm(o, L["rms2"]))
             a = torch.cat([gate, up], 1)
@@ -136,7 +157,11 @@ class DraftDecoder:
         tree_accept(self.logits(tok, parent, cu, max_span), tok, parent, cu, best, rows, self.add, self.last)
         slots = self._plan(self.add, cu, N)
         for i in range(len(self.dm.layers)):
-            kv_put(self.Kd[i].transpose(0, 1), self.Vd[i].transpose(0, 1), self.Kc[i], self.Vc[i], slots=slots, rows=rows)
+            k, v = self.Kd[i].transpose(0, 1), self.Vd[i].transpose(0, 1)
+            if self.quantised:
+                kvq_put(k, v, self.caches[i], slots=slots, rows=rows)
+            else:
+                kv_put(k, v, self.Kc[i], self.Vc[i], slots=slots, rows=rows)
         stored = self.lens[0] - self.lens[1]  # a refused request's length has not changed
         rows.masked_fill_(slots < 0, -1)
         torch.where(stored != self.add, tok[cu[:-1].clamp(max=N - 1).long()], self.last, out=self.last)

@@ -688,6 +688,114 @@ abg_status abg_tree_accept(const float *logits, int64_t ld, const int32_t *tok, 
                            const int32_t *cu, int32_t *best, int32_t *rows, int32_t *add, int32_t *last, int64_t B,
                            int64_t N, int64_t V, void *ws, int64_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Quantised cache: the paged cache of the draft-verification calls with its
+ * rows in 4 or 8 bits, in the weights' format (value = scale*code + bias).
+ *
+ *   abg_kvq_put    rows into the cache, with kv_put's norm and rotation
+ *   abg_kvq_attn   tree_attn over such a cache
+ *   abg_kvq_get    rows of the cache read back
+ *
+ * They take the place of abg_kv_put and abg_tree_attn for the cache; the drafts
+ * of a step stay in f32, bf16 or f16 rows.  Lengths, spans, tables, slots and
+ * early starts are as there; the results are the same on every run.
+ *
+ * A row of D values of one head is D*bits/32 words and D/group factor pairs:
+ *   Kc, Vc  u32 [pages][Hkv][page][D*bits/32]  codes, low first: code j of word
+ *           k is column (32/bits)*k + j
+ *   Ks, Vs  f16 [pages][Hkv][page][D/group][2]  scale, bias of each group
+ * bits = 4 or 8, group = 32 or 64 columns, D = 64, 128 or 256, page >= 1.
+ * ------------------------------------------------------------------------- */
+typedef struct abg_kvq_cache {
+    void *Kc, *Ks, *Vc, *Vs;
+    int64_t pages, Hkv, page, D;
+    int32_t bits, group;
+} abg_kvq_cache;
+
+/*
+ * kvq_put: key and value rows of N tokens into a quantised cache, k and q with
+ * abg_atq's RMS norm and rotation (each optional).  Arguments as abg_kv_put's,
+ * but src_type is any type, and qo is of q_type: src_type, or any type where
+ * src_type is f32.
+ *   Of the f32 values x of a group (normed and rotated in f32, not rounded to
+ * 16 bits in between), each step rounded once to nearest even:
+ *     bias  = f16(min x),  scale = f16((max x - min x) / (2^bits - 1)),
+ *     code  = clamp(rint((x - bias) * (1 / scale)), 0, 2^bits - 1), 0 where
+ *             scale is 0.
+ *   A value is off by at most half a scale, the bias's rounding and 2^-11 of the
+ * group's range.  A group with a NaN or a magnitude above 65504 (f16's
+ * largest) is held as NaN: scale and bias are 0x7fff, the codes 0.
+ * The codes and factors are exact: they are the same on every run, and those of
+ * these steps done one by one in any IEEE binary32 arithmetic.
+ */
+typedef struct abg_kvq_put_args {
+    const void *q, *k, *v;
+    int64_t q_row, q_head, k_row, k_head, v_row, v_head;
+    const int32_t *rows;
+    const int64_t *slots;
+    const float *qn_w, *kn_w, *cos, *sin;
+    const int32_t *pos;
+    void *qo;
+    abg_kvq_cache c;
+    int64_t N, src_rows, Hq, cos_rows;
+    float eps;
+    int32_t src_type, q_type;
+} abg_kvq_put_args;
+abg_status abg_kvq_put(const abg_kvq_put_args *a, void *stream);
+
+/*
+ * kvq_get: the values of N rows of a quantised cache, scale*code + bias rounded
+ * once to f32 and once more to `type`.
+ *   k, v   row n, head h at k + n*k_row + h*k_head (in elements); each may be
+ *          null (not both): then it is not read
+ *   slots  i64 [N] or null: row n is slot slots[n] (null: n); a slot outside
+ *          0 .. pages*page-1 gives zeros
+ * Rows, row strides and head strides are multiples of 16 bytes; rows may not
+ * lie in one another (k_row and k_head span distinct rows).
+ */
+typedef struct abg_kvq_get_args {
+    abg_kvq_cache c;
+    const int64_t *slots;
+    void *k, *v;
+    int64_t k_row, k_head, v_row, v_head, N;
+    int32_t type;
+} abg_kvq_get_args;
+abg_status abg_kvq_get(const abg_kvq_get_args *a, void *stream);
+
+/*
+ * kvq_attn: abg_tree_attn with the cached tokens' K and V in a quantised cache;
+ * q, Kd and Vd of `type`, everything else as there.  One new token a request is
+ * a span of 1.
+ *   A page outside 0 .. pages-1 reads as zeros; a NaN in a K row that a query
+ * sees makes its result NaN, one in a V row those columns' group.  A row of q
+ * that holds a NaN or a magnitude of 2^100 or more gives NaN (0 where it sees no
+ * token).  width*page is at most 2^31 - 1024.
+ *   Sums, softmax statistics and the work split's partial results are f32.
+ * Codes are multiplied exactly, with q in f16 after a scaling of the row by a
+ * power of two: 16-bit q as it is (elements below 2^-23 of the row's largest lose
+ * bits), f32 q to 22 bits (of elements below 2^-12 of the largest: to 2^-34 of
+ * that).  The weights p*scale that meet V's codes are rounded to 11 bits for
+ * bf16, to 22 bits for f16 and f32, the smallest of either to 2^-38 of the
+ * largest scale in V.  Drafts are multiplied in f32.
+ * ws: abg_kvq_attn_workspace() bytes, as tree_attn's.
+ */
+typedef struct abg_kvq_attn_args {
+    const void *q;
+    abg_kvq_cache c;
+    const int32_t *table, *lens, *cu;
+    const void *Kd, *Vd;
+    const uint64_t *mask;
+    const float *gate;
+    void *y;
+    float *ysum;
+    int64_t B, N, Hq, width, drafts, words, max_span;
+    int32_t type, y_type;
+} abg_kvq_attn_args;
+/* Bytes of workspace; it depends on the cache's D, bits and group, type, Hq/Hkv
+ * and max_span only (and on the device).  Pointers and pages of c are not read. */
+abg_status abg_kvq_attn_workspace(const abg_kvq_cache *c, int64_t Hq, int64_t max_span, int type, int64_t *bytes);
+abg_status abg_kvq_attn(const abg_kvq_attn_args *a, void *ws, int64_t ws_bytes, void *stream);
+
 const char *abg_status_str(int status);
 /* Text of the last CUDA error seen by any call on this thread ("" if none). */
 const char *abg_last_cuda_error(void);
