@@ -55,53 +55,82 @@ __device__ __forceinline__ void store_codes(unsigned char *p, const uint32_t (&c
     }
 }
 
-// By the 16 lanes of a half warp (l: place in it; all 32 lanes call it): the row
-// u[0][0..V) at columns V*l.., u[1][..) at D/2 + V*l.. into codes and pairs; `kept`:
-// whether the row is to be written.
-template <int D>
-__device__ __forceinline__ void put_quantised(const float (&u)[2][D / 32], int l, bool kept, int bits, int group,
-                                              unsigned char *codes, __half2 *pairs) {
-    constexpr int V = D / 32;
-    float lo[2], hi[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        lo[h] = INFINITY;
-        hi[h] = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            lo[h] = fminf(lo[h], u[h][i]);
-            hi[h] = fabsf(u[h][i]) <= kLargestHalf ? fmaxf(hi[h], u[h][i]) : INFINITY;  // (a NaN too)
-        }
-    }
+// By the 16 lanes of a half warp (l: place in it; all 32 lanes call it): the rows
+// u[r][0][0..V) at columns V*l.., u[r][1][..) at D/2 + V*l.. into codes and pairs, all
+// rows' steps side by side.  rows[r]: the row's place in the cache (-1: not written)
+// of keys, or (values[r]) of values.
+template <int D, int R>
+__device__ __forceinline__ void put_quantised(const float (&u)[R][2][D / 32], int l, const int64_t (&rows)[R],
+                                              const bool (&values)[R], const abg_kvq_cache &c) {
+    constexpr int V = D / 32, C = 2 * R;  // chunks of a lane, 2 r + h
+    const int lane = threadIdx.x & 31, bits = c.bits, group = c.group;
+    float lo[C], hi[C];
     const bool joined = group > D / 2;
-    if (joined) lo[0] = lo[1] = fminf(lo[0], lo[1]), hi[0] = hi[1] = fmaxf(hi[0], hi[1]);
-    const int lanes = min(16, group / V);  // of a group's chunks of one half
-    for (int d = 1; d < lanes; d <<= 1) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            lo[h] = fminf(lo[h], __shfl_xor_sync(0xffffffffu, lo[h], d));
-            hi[h] = fmaxf(hi[h], __shfl_xor_sync(0xffffffffu, hi[h], d));
+            float &a = lo[2 * r + h], &b = hi[2 * r + h];
+            a = INFINITY, b = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                a = fminf(a, u[r][h][i]);
+                b = fabsf(u[r][h][i]) <= kLargestHalf ? fmaxf(b, u[r][h][i]) : INFINITY;  // (a NaN too)
+            }
+        }
+        if (joined) {
+            lo[2 * r] = lo[2 * r + 1] = fminf(lo[2 * r], lo[2 * r + 1]);
+            hi[2 * r] = hi[2 * r + 1] = fmaxf(hi[2 * r], hi[2 * r + 1]);
         }
     }
-    if (!kept) return;
-    const float levels = bits == 4 ? 15.0f : 255.0f;
+    // a group is at least C lanes' chunks: half of the chunks go to the other half of
+    // the lanes in each step, until lane l has that of index l mod C
+    const int lanes = min(16, group / V);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const bool bad = hi[h] == INFINITY;
-        const __half bias = bad ? __ushort_as_half(0x7fff) : __float2half_rn(lo[h]);
-        const __half scale =
-            bad ? __ushort_as_half(0x7fff) : __float2half_rn(__fdiv_rn(__fsub_rn(hi[h], lo[h]), levels));
-        const float b = __half2float(bias), s = __half2float(scale);
-        const float inv = s > 0.0f ? __frcp_rn(s) : 0.0f;  // (a NaN: 0)
-        uint32_t code[V];
+    for (int d = C / 2; d >= 1; d /= 2) {
+        const bool up = lane & d;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const float x = rintf(__fmul_rn(__fsub_rn(u[h][i], b), inv));
-            code[i] = bad ? 0u : static_cast<uint32_t>(fminf(fmaxf(x, 0.0f), levels));
+        for (int i = 0; i < d; ++i) {
+            const float a = __shfl_xor_sync(0xffffffffu, up ? lo[i] : lo[i + d], d);
+            const float b = __shfl_xor_sync(0xffffffffu, up ? hi[i] : hi[i + d], d);
+            lo[i] = fminf(up ? lo[i + d] : lo[i], a);
+            hi[i] = fmaxf(up ? hi[i + d] : hi[i], b);
         }
-        const int col = h * (D / 2) + V * l;
-        store_codes<V>(codes + col * bits / 8, code, bits);
-        if (l % lanes == 0 && !(joined && h)) pairs[col / group] = __halves2half2(scale, bias);
+    }
+    for (int d = C; d < lanes; d *= 2) {
+        lo[0] = fminf(lo[0], __shfl_xor_sync(0xffffffffu, lo[0], d));
+        hi[0] = fmaxf(hi[0], __shfl_xor_sync(0xffffffffu, hi[0], d));
+    }
+    const float levels = bits == 4 ? 15.0f : 255.0f;
+    const bool bad = hi[0] == INFINITY;
+    const __half nan = __ushort_as_half(0x7fff);
+    const __half2 own = bad ? __halves2half2(nan, nan)
+                            : __halves2half2(__float2half_rn(__fdiv_rn(__fsub_rn(hi[0], lo[0]), levels)), __float2half_rn(lo[0]));
+    const float own_inv = __low2float(own) > 0.0f ? __frcp_rn(__low2float(own)) : 0.0f;  // (a NaN: 0)
+    const uint32_t own_pair = *reinterpret_cast<const uint32_t *>(&own);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        unsigned char *codes = static_cast<unsigned char *>(values[r] ? c.Vc : c.Kc) + rows[r] * (D * bits / 8);
+        uint32_t *pairs = static_cast<uint32_t *>(values[r] ? c.Vs : c.Ks) + rows[r] * (D / group);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int from = (lane & ~(C - 1)) + 2 * r + h;
+            const uint32_t pair = __shfl_sync(0xffffffffu, own_pair, from);
+            const float inv = __shfl_sync(0xffffffffu, own_inv, from);
+            const float b = __half2float(__ushort_as_half(static_cast<unsigned short>(pair >> 16)));
+            uint32_t code[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                // clamped, then rounded to a whole number by 1.5 * 2^23 (a NaN: 0, as 0 * NaN is clamped to 0)
+                const float x = fminf(fmaxf(__fmul_rn(__fsub_rn(u[r][h][i], b), inv), 0.0f), levels);
+                code[i] = __float_as_uint(__fadd_rn(x, 12582912.0f)) & 255u;
+            }
+            const int col = h * (D / 2) + V * l;
+            if (rows[r] >= 0) {
+                store_codes<V>(codes + col * bits / 8, code, bits);
+                if (l % lanes == 0 && !(joined && h)) pairs[col / group] = pair;
+            }
+        }
     }
 }
 
@@ -113,7 +142,6 @@ __global__ void __launch_bounds__(32 * kPutWarps, D == 256 ? 2 : 3) kvq_put_kern
     const int lane = threadIdx.x & 31, l = lane & 15, half = lane >> 4;
     const int64_t units = a.N * groups, stride = static_cast<int64_t>(gridDim.x) * kPutWarps;
     const int nq = a.q ? static_cast<int>(a.Hq) : 0, nk = static_cast<int>(a.c.Hkv), heads = nq + 2 * nk;
-    const int row_bytes = D * a.c.bits / 8, row_pairs = D / a.c.group;
     // (no launch after this one starts early: some read caches and weights before they wait)
     grid_dep_wait();
     struct Token {
@@ -121,11 +149,14 @@ __global__ void __launch_bounds__(32 * kPutWarps, D == 256 ? 2 : 3) kvq_put_kern
         int32_t pos;
         int h0;
     };
+    // all tokens' last heads (keys and values, the longest work) first, so that every
+    // warp has its share of each kind
     auto token = [&](int64_t unit) {
         Token t{0, -1, -1, 0, 0};
         if (unit >= units) return t;
-        t.n = div_up_to_64(unit, groups);
-        t.h0 = static_cast<int>(unit - t.n * groups) * P::kHeads;
+        const int64_t g = div_up_to_64(unit, a.N);
+        t.n = unit - g * a.N;
+        t.h0 = (groups - 1 - static_cast<int>(g)) * P::kHeads;
         t.src = a.rows ? a.rows[t.n] : t.n;
         t.slot = a.slots ? a.slots[t.n] : t.n;
         if (a.cos) t.pos = a.pos[t.n];
@@ -175,6 +206,8 @@ __global__ void __launch_bounds__(32 * kPutWarps, D == 256 ? 2 : 3) kvq_put_kern
             const bool kept = t.slot >= 0 && t.slot < a.c.pages * a.c.page;
             const int64_t page = kept ? div_up_to_64(t.slot, a.c.page) : 0;
             const int64_t base = page * a.c.Hkv * a.c.page + (t.slot - page * a.c.page);
+            int64_t rows[kSteps];
+            bool values[kSteps];
 #pragma unroll
             for (int r = 0; r < kSteps; ++r) {
                 const int h = t.h0 + 2 * r + half;
@@ -200,65 +233,74 @@ __global__ void __launch_bounds__(32 * kPutWarps, D == 256 ? 2 : 3) kvq_put_kern
                         }
                     }
                 }
-                const bool value = h >= nq + nk;
                 if (h < nq) {
                     T *to = static_cast<T *>(a.qo) + (t.n * a.Hq + h) * D;
                     store_e<T, V>(to + V * l, u[r][0]);
                     store_e<T, V>(to + D / 2 + V * l, u[r][1]);
                 }
-                if (t.h0 + 2 * r + 1 < nq || t.h0 + 2 * r >= heads) continue;  // (the whole warp: no row of the cache)
-                const int64_t row = base + (value ? h - nq - nk : h - nq) * a.c.page;
-                put_quantised<D>(u[r], l, kept && h >= nq && h < heads, a.c.bits, a.c.group,
-                                 static_cast<unsigned char *>(value ? a.c.Vc : a.c.Kc) + row * row_bytes,
-                                 static_cast<__half2 *>(value ? a.c.Vs : a.c.Ks) + row * row_pairs);
+                values[r] = h >= nq + nk;
+                rows[r] = kept && h >= nq && h < heads ? base + (values[r] ? h - nq - nk : h - nq) * a.c.page : -1;
             }
+            if (t.h0 + P::kHeads > nq) put_quantised<D>(u, l, rows, values, a.c);  // (the whole warp, or none of it)
         }
         t = next;
     }
 }
 
 // ------------------------------------------------------------- kvq_get -----
-// A thread eight columns: one or two words and a pair in, 16 or 32 bytes out.
-// Threads go over (row, key or value, head, eight columns), the columns first, so
-// that a warp reads and writes whole rows; four such places at a time a thread, so
-// that their slots, then their words, are on their way together.
-constexpr int kGetThreads = 256, kGetEach = 4;
+// A block a tile of tokens, whose rows it finds once; then a thread eight columns at
+// a time, one or two words and a pair in, 16 or 32 bytes out, the columns first, then
+// heads, K and V, tokens, so that a warp reads and writes whole rows.  Four such
+// places at a time a thread, so that their words are on their way together.
+constexpr int kGetThreads = 256, kGetEach = 4, kGetTokens = 128;
 
-template <typename T>
+// Byte k of w as a float (0x4b000000 + c is 2^23 + c).
+template <int k>
+__device__ __forceinline__ float byte_value(uint32_t w) {
+    return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 + k)) - 8388608.0f;
+}
+
+template <typename T, int kBits>
 __global__ void __launch_bounds__(kGetThreads) kvq_get_kernel(const __grid_constant__ abg_kvq_get_args a, int kinds,
-                                                              int log_cols) {
+                                                              int log_cols, int tokens) {
+    __shared__ int64_t s_row[kGetTokens];  // of head 0; -1: none
+    const int tid = threadIdx.x, Hkv = static_cast<int>(a.c.Hkv);
+    const int per = kinds * Hkv << log_cols, log_pair = a.c.group == 32 ? 2 : 3;
+    const int64_t n0 = static_cast<int64_t>(blockIdx.x) * tokens;
+    const int here = static_cast<int>(min(static_cast<int64_t>(tokens), a.N - n0)), items = here * per;
     grid_dep_wait();  // (and nothing after this one starts early, as kvq_put)
-    const int cols = 1 << log_cols, log_pair = a.c.group == 32 ? 2 : 3;        // eights of a row and of a pair
-    const int64_t Hkv = a.c.Hkv, per = kinds * Hkv, all = a.N * per << log_cols;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * kGetThreads, slots = a.c.pages * a.c.page;
-    for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * kGetThreads + threadIdx.x; i0 < all; i0 += kGetEach * stride) {
-        int64_t n[kGetEach], slot[kGetEach];
-        int h[kGetEach], col[kGetEach];
-        bool value[kGetEach];
-#pragma unroll
-        for (int k = 0; k < kGetEach; ++k) {
-            const int64_t i = i0 + k * stride;
-            n[k] = -1;
-            if (i >= all) continue;
-            col[k] = static_cast<int>(i & (cols - 1));
-            n[k] = div_up_to_64(i >> log_cols, per);
-            const int kh = static_cast<int>((i >> log_cols) - n[k] * per);
-            value[k] = kh >= Hkv || !a.k;
-            h[k] = kh >= Hkv ? kh - static_cast<int>(Hkv) : kh;
-            slot[k] = a.slots ? a.slots[n[k]] : n[k];
+    if (tid < here) {
+        const int64_t slot = a.slots ? a.slots[n0 + tid] : n0 + tid;
+        int64_t row = -1;
+        if (slot >= 0 && slot < a.c.pages * a.c.page) {
+            const int64_t page = div_up_to_64(slot, a.c.page);
+            row = page * Hkv * a.c.page + (slot - page * a.c.page);
         }
+        s_row[tid] = row;
+    }
+    __syncthreads();
+    for (int i0 = tid; i0 < items; i0 += kGetEach * kGetThreads) {
+        int n[kGetEach], h[kGetEach], col[kGetEach];
+        bool value[kGetEach];
         uint2 w[kGetEach];
         float2 f[kGetEach];
 #pragma unroll
         for (int k = 0; k < kGetEach; ++k) {
+            const int i = i0 + k * kGetThreads;
+            n[k] = -1;
             w[k] = make_uint2(0, 0);
             f[k] = make_float2(0.0f, 0.0f);
-            if (n[k] < 0 || slot[k] < 0 || slot[k] >= slots) continue;
-            const int64_t page = div_up_to_64(slot[k], a.c.page);
-            const int64_t row = (page * Hkv + h[k]) * a.c.page + (slot[k] - page * a.c.page);
-            const int64_t at = (row << log_cols) + col[k];
+            if (i >= items) continue;
+            n[k] = static_cast<int>(static_cast<uint32_t>(i) / static_cast<uint32_t>(per));
+            const int rest = i - n[k] * per, kh = rest >> log_cols;
+            col[k] = rest & ((1 << log_cols) - 1);
+            value[k] = kh >= Hkv || !a.k;
+            h[k] = kh >= Hkv ? kh - Hkv : kh;
+            const int64_t row = s_row[n[k]];
+            if (row < 0) continue;
+            const int64_t at = ((row + h[k] * a.c.page) << log_cols) + col[k];
             const void *codes = value[k] ? a.c.Vc : a.c.Kc;
-            if (a.c.bits == 4) {
+            if constexpr (kBits == 4) {
                 w[k].x = static_cast<const uint32_t *>(codes)[at];
             } else {
                 w[k] = static_cast<const uint2 *>(codes)[at];
@@ -269,14 +311,18 @@ __global__ void __launch_bounds__(kGetThreads) kvq_get_kernel(const __grid_const
         for (int k = 0; k < kGetEach; ++k) {
             if (n[k] < 0) continue;
             float v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t code =
-                    a.c.bits == 4 ? w[k].x >> (4 * i) & 15u : (i < 4 ? w[k].x : w[k].y) >> (8 * (i % 4)) & 255u;
-                // (the product is exact: 11 and 8 bits)
-                v[i] = __fadd_rn(__fmul_rn(f[k].x, static_cast<float>(code)), f[k].y);
+            if constexpr (kBits == 4) {
+                const uint32_t even = w[k].x & 0x0f0f0f0fu, odd = w[k].x >> 4 & 0x0f0f0f0fu;
+                v[0] = byte_value<0>(even), v[1] = byte_value<0>(odd), v[2] = byte_value<1>(even), v[3] = byte_value<1>(odd);
+                v[4] = byte_value<2>(even), v[5] = byte_value<2>(odd), v[6] = byte_value<3>(even), v[7] = byte_value<3>(odd);
+            } else {
+                v[0] = byte_value<0>(w[k].x), v[1] = byte_value<1>(w[k].x), v[2] = byte_value<2>(w[k].x);
+                v[3] = byte_value<3>(w[k].x), v[4] = byte_value<0>(w[k].y), v[5] = byte_value<1>(w[k].y);
+                v[6] = byte_value<2>(w[k].y), v[7] = byte_value<3>(w[k].y);
             }
-            T *to = static_cast<T *>(value[k] ? a.v : a.k) + n[k] * (value[k] ? a.v_row : a.k_row) +
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = fmaf(f[k].x, v[i], f[k].y);  // (the product is exact: 11 and 8 bits)
+            T *to = static_cast<T *>(value[k] ? a.v : a.k) + (n0 + n[k]) * (value[k] ? a.v_row : a.k_row) +
                     h[k] * (value[k] ? a.v_head : a.k_head) + 8 * col[k];
             store_e<T, 8>(to, v);
         }
@@ -306,14 +352,21 @@ cudaError_t put(const abg_kvq_put_args &a, bool early, cudaStream_t stream) {
                           : put_d<S, T, 256>(a, early, stream);
 }
 
-template <typename T>
-cudaError_t get(const abg_kvq_get_args &a, bool pdl, cudaStream_t stream) {
+template <typename T, int kBits>
+cudaError_t get_bits(const abg_kvq_get_args &a, bool pdl, cudaStream_t stream) {
     const int kinds = (a.k != nullptr) + (a.v != nullptr);
     const int log_cols = a.c.D == 64 ? 3 : a.c.D == 128 ? 4 : 5;
-    const int64_t threads = a.N * kinds * a.c.Hkv << log_cols, each = kGetThreads * kGetEach;
-    const int64_t blocks = std::min<int64_t>((threads + each - 1) / each, 8ll * sm_count());
-    return launch_kernel(kvq_get_kernel<T>, dim3(static_cast<unsigned>(blocks)), dim3(kGetThreads), 0, stream,
-                         pdl && !capturing(stream), a, kinds, log_cols);
+    const int64_t per = kinds * a.c.Hkv << log_cols;
+    // eight places a thread, as long as there are four blocks an SM
+    const int64_t tokens = std::max<int64_t>(
+        1, std::min<int64_t>({kGetTokens, 2 * kGetEach * kGetThreads / per, a.N / (4ll * sm_count())}));
+    return launch_kernel(kvq_get_kernel<T, kBits>, dim3(static_cast<unsigned>((a.N + tokens - 1) / tokens)),
+                         dim3(kGetThreads), 0, stream, pdl && !capturing(stream), a, kinds, log_cols,
+                         static_cast<int>(tokens));
+}
+template <typename T>
+cudaError_t get(const abg_kvq_get_args &a, bool pdl, cudaStream_t stream) {
+    return a.c.bits == 4 ? get_bits<T, 4>(a, pdl, stream) : get_bits<T, 8>(a, pdl, stream);
 }
 
 }  // namespace
