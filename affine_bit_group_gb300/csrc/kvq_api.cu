@@ -14,7 +14,7 @@ bool known_format(const abg_kvq_cache &c) {
 bool cache_sizes(const abg_kvq_cache &c) {
     return c.page >= 1 && c.page <= kMax32 && c.pages >= 0 && c.pages <= kMax32 && c.Hkv >= 1 && c.Hkv <= 65536 &&
            known_width(c.D) && bounded({c.pages, c.page, c.Hkv, c.D, 4}) && bounded({c.pages, c.Hkv}) &&
-           c.pages * c.Hkv <= kMax32;
+           c.pages * c.Hkv <= kMax32 && c.pages * c.page * c.Hkv <= 2 * kMax32;
 }
 bool cache_aligned(const abg_kvq_cache &c) { return on(c.Kc, 16) && on(c.Ks, 16) && on(c.Vc, 16) && on(c.Vs, 16); }
 struct CacheSpans {

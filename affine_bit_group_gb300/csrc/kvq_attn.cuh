@@ -50,7 +50,18 @@ struct KvqAttnArgs {
     AttnArgs p;
     const unsigned char *Kc, *Vc;
     const unsigned char *Ks, *Vs;
+    uint32_t page_mul;  // t / page = (t * page_mul >> 32) >> page_shift for t < 2^31 (0: page 1)
+    int page_shift;
 };
+
+// The multiplier of a division by page: 2^(31 + s) / page rounded up, where 2^s is the
+// power of two from page on, is off by less than 1 part in 2^31.
+inline void kvq_page_division(KvqAttnArgs &x, uint32_t page) {
+    int s = 0;
+    while (s < 31 && (1u << s) < page) ++s;
+    x.page_mul = page == 1 ? 0 : static_cast<uint32_t>(((uint64_t(1) << (31 + s)) + page - 1) / page);
+    x.page_shift = s - 1;
+}
 
 constexpr int kKvqWarps = 8, kKvqThreads = 32 * kKvqWarps;
 constexpr int kKvqTile = 128;  // tokens of the work line's tiles
@@ -89,14 +100,25 @@ struct KvqShape {
     static constexpr int kSmem = kFixed + kKvqWarps * kWarpBytes;
 };
 
-template <int N>
+// N bytes to shared memory; without kWhole, zeros where they are not real
+template <int N, bool kWhole>
 __device__ __forceinline__ void kvq_cp(uint32_t dst, const void *src, bool real) {
-    if constexpr (N == 16) {
+    if constexpr (kWhole && N == 16) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    } else if constexpr (kWhole) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+    } else if constexpr (N == 16) {
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
     } else {
         asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(real ? N : 0)
                      : "memory");
     }
+}
+// 2^x by the special function unit; results below 2^-126 are 0
+__device__ __forceinline__ float kvq_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 __device__ __forceinline__ void kvq_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -210,40 +232,53 @@ __global__ void __launch_bounds__(kKvqThreads, S::kBlocks) kvq_attn_kernel(const
         const int blocks = key1 > key0 ? (key1 - key0 + kTB - 1) / kTB : 0;
         // -- copies --
         const int32_t *table = a.table + static_cast<int64_t>(s.b) * a.width;
+        auto page_at = [&](int t) {
+            return x.page_mul ? static_cast<int>(__umulhi(static_cast<uint32_t>(t), x.page_mul) >> x.page_shift) : t;
+        };
         auto page_of = [&](int blk) {  // of this lane's token
             const int t = key0 + blk * kTB + lane;
-            return blk < blocks && lane < kTB && t < key1
-                       ? table[static_cast<uint32_t>(t) / static_cast<uint32_t>(a.page)] : -1;
+            return blk < blocks && lane < kTB && t < key1 ? table[page_at(t)] : -1;
         };
         int32_t id = page_of(warp);
         auto bring = [&](int i) {  // the warp's block i, of whose pages `id` knows; a group of copies
             const int blk = warp + i * kKvqWarps;
             if (blk < blocks) {
-                const uint32_t t = static_cast<uint32_t>(key0 + blk * kTB + lane);
-                int64_t row = -1;
-                if (id >= 0 && id < a.pages)
-                    row = (static_cast<int64_t>(id) * a.Hkv + s.h) * a.page + t % static_cast<uint32_t>(a.page);
+                const int t = key0 + blk * kTB + lane, page = static_cast<int>(a.page);
+                const bool there = static_cast<uint32_t>(id) < static_cast<uint32_t>(a.pages);
+                // (a cache has fewer than 2^32 rows)
+                const uint32_t row =
+                    there ? (static_cast<uint32_t>(id) * static_cast<uint32_t>(a.Hkv) + s.h) * page + (t - page_at(t) * page) : 0;
                 id = page_of(blk + kKvqWarps);
                 const uint32_t at = ring_at + (i % kStages) * S::kStageBytes;
                 constexpr int kChunks = kRB / 16;
+                const unsigned all = __ballot_sync(0xffffffffu, there);
+                auto copy = [&](auto whole) {
+                    constexpr bool kWhole = decltype(whole)::value;
 #pragma unroll
-                for (int c = 0; c < kTB * kChunks / 32; ++c) {
-                    const int k = 32 * c + lane, tok = k / kChunks, ch = k % kChunks;
-                    const int64_t r = __shfl_sync(0xffffffffu, row, tok);
-                    const int64_t off = max(r, int64_t(0)) * kRB + 16 * ch;
-                    const uint32_t to = at + tok * kRB + 16 * (ch ^ kvq_swizzle<S>(tok));
-                    kvq_cp<16>(to, x.Kc + off, r >= 0);
-                    kvq_cp<16>(to + kTB * kRB, x.Vc + off, r >= 0);
-                }
-                if (lane < kTB) {
-                    constexpr int kEach = kFB < 16 ? kFB : 16;
-                    const uint32_t to = at + 2 * kTB * kRB + lane * kFB;
-                    const int64_t off = max(row, int64_t(0)) * kFB;
-#pragma unroll
-                    for (int c = 0; c < kFB; c += kEach) {
-                        kvq_cp<kEach>(to + c, x.Ks + off + c, row >= 0);
-                        kvq_cp<kEach>(to + kTB * kFB + c, x.Vs + off + c, row >= 0);
+                    for (int c = 0; c < kTB * kChunks / 32; ++c) {
+                        const int tok = 32 / kChunks * c + lane / kChunks, ch = lane % kChunks;
+                        const int64_t off = static_cast<uint64_t>(__shfl_sync(0xffffffffu, row, tok)) * kRB + 16 * ch;
+                        const uint32_t to = at + tok * kRB + 16 * (ch ^ kvq_swizzle<S>(tok));
+                        const bool real = kWhole || (all >> tok & 1);
+                        kvq_cp<16, kWhole>(to, x.Kc + off, real);
+                        kvq_cp<16, kWhole>(to + kTB * kRB, x.Vc + off, real);
                     }
+                    if (lane < kTB) {
+                        constexpr int kEach = kFB < 16 ? kFB : 16;
+                        const uint32_t to = at + 2 * kTB * kRB + lane * kFB;
+                        const int64_t off = static_cast<uint64_t>(row) * kFB;
+#pragma unroll
+                        for (int c = 0; c < kFB; c += kEach) {
+                            kvq_cp<kEach, kWhole>(to + c, x.Ks + off + c, there);
+                            kvq_cp<kEach, kWhole>(to + kTB * kFB + c, x.Vs + off + c, there);
+                        }
+                    }
+                };
+                constexpr unsigned kAll = kTB == 32 ? 0xffffffffu : 0xffffu;
+                if ((all & kAll) == kAll) {
+                    copy(std::true_type{});
+                } else {  // a last block, or pages that there are not: zeros
+                    copy(std::false_type{});
                 }
             }
             kvq_commit();
@@ -405,40 +440,44 @@ __global__ void __launch_bounds__(kKvqThreads, S::kBlocks) kvq_attn_kernel(const
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             sc[mt][nt][e] = fmaf(acc[mt][nt][e], f[mt][e >> 1].x,
-                                                 fmaf(f[mt][e >> 1].y, e & 1 ? qs.y : qs.x, sc[mt][nt][e]));
+                                                 g == 0 ? f[mt][e >> 1].y * (e & 1 ? qs.y : qs.x)
+                                                        : fmaf(f[mt][e >> 1].y, e & 1 ? qs.y : qs.x, sc[mt][nt][e]));
                 }
             }
-            // maxima and weights
+            // maxima and weights (sc is in units of 1/s_f until its exponential)
             const int here = key1 - key0 - blk * kTB;  // tokens of the block that are there
+            if (here < kTB) {
+#pragma unroll
+                for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                    for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (16 * mt + 8 * (e >> 1) + tok >= here) sc[mt][nt][e] = -INFINITY;
+            }
             bool grew = false;
             float corr[kNT][2];
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt) {
                 const float2 f = *reinterpret_cast<const float2 *>(s_f + nt * 8 + 2 * quad);
-                float top[2] = {m[nt][0], m[nt][1]};
-#pragma unroll
-                for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const bool in = 16 * mt + 8 * (e >> 1) + tok < here;
-                        sc[mt][nt][e] = in ? sc[mt][nt][e] * (e & 1 ? f.y : f.x) : -INFINITY;
-                        top[e & 1] = fmaxf(top[e & 1], sc[mt][nt][e]);
-                    }
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
+                    float top = fmaxf(sc[0][nt][e], sc[0][nt][2 + e]);
+                    if constexpr (kMT == 2) top = fmaxf(top, fmaxf(sc[kMT - 1][nt][e], sc[kMT - 1][nt][2 + e]));
 #pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) top[e] = fmaxf(top[e], __shfl_xor_sync(0xffffffffu, top[e], d));
-                    const float ref = top[e] == -INFINITY ? 0.0f : top[e];
-                    corr[nt][e] = exp2f(m[nt][e] - ref);
-                    grew = grew || top[e] > m[nt][e];
-                    m[nt][e] = top[e];
+                    for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                    top = fmaxf(m[nt][e], top * (e ? f.y : f.x));
+                    const float ref = top == -INFINITY ? 0.0f : top;
+                    corr[nt][e] = kvq_exp2(m[nt][e] - ref);
+                    grew = grew || top > m[nt][e];
+                    m[nt][e] = top;
                     float sum = 0.0f;
 #pragma unroll
                     for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             float &v = sc[mt][nt][2 * h + e];
-                            v = exp2f(v - ref);
+                            v = kvq_exp2(fmaf(v, e ? f.y : f.x, -ref));
                             sum += v;
                         }
                     l[nt][e] = fmaf(l[nt][e], corr[nt][e], sum);

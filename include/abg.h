@@ -704,7 +704,8 @@ abg_status abg_tree_accept(const float *logits, int64_t ld, const int32_t *tok, 
  *   Kc, Vc  u32 [pages][Hkv][page][D*bits/32]  codes, low first: code j of word
  *           k is column (32/bits)*k + j
  *   Ks, Vs  f16 [pages][Hkv][page][D/group][2]  scale, bias of each group
- * bits = 4 or 8, group = 32 or 64 columns, D = 64, 128 or 256, page >= 1.
+ * bits = 4 or 8, group = 32 or 64 columns, D = 64, 128 or 256, page >= 1, fewer than
+ * 2^32 - 1 rows (pages*Hkv*page).
  * ------------------------------------------------------------------------- */
 typedef struct abg_kvq_cache {
     void *Kc, *Ks, *Vc, *Vs;
