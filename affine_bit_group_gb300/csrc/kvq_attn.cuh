@@ -32,8 +32,8 @@
 // the weights P go from the one product's result to the other's operand by
 // movmatrix, in registers.
 //
-// Warps.  Every warp goes through blocks of 16 or 32 tokens of its own (block w, w +
-// 8, .. of the stretch), with a ring in shared memory that it fills by cp.async and
+// Warps.  Every warp goes through blocks of 16 or 32 tokens of its own (every 8th, 10th
+// or 12th of the stretch), with a ring in shared memory that it fills by cp.async and
 // its own running maxima and sums: no barrier until the stretch's end, where the
 // warps' sums meet in shared memory, and the drafts are added, in f32, a row a warp.
 #pragma once
@@ -63,7 +63,6 @@ inline void kvq_page_division(KvqAttnArgs &x, uint32_t page) {
     x.page_shift = s - 1;
 }
 
-constexpr int kKvqWarps = 8, kKvqThreads = 32 * kKvqWarps;
 constexpr int kKvqTile = 128;  // tokens of the work line's tiles
 // Rows of q from here on give NaN: their scores could pass f32's range.
 constexpr float kKvqLargestQ = 1.2676506e30f;  // 2^100
@@ -82,22 +81,28 @@ struct KvqShape {
     static constexpr int kRT = 8 * kNT;
     static constexpr int kRB = D * kBits / 8;             // bytes of a row's codes
     static constexpr int kG = D / kGroup, kFB = 4 * kG;   // groups of a row, bytes of its factors
-    static constexpr int kTB = kRB <= 64 ? 32 : 16;       // tokens of a block
+    static constexpr int kTB = kRB <= 128 && kNT * D / 4 < 128 ? 32 : 16;  // tokens of a block
     static constexpr int kMT = kTB / 16;
     static constexpr int kSteps = D / 16;                 // products of 16 columns
     static constexpr int kWords = kGroup * kBits / 128;   // words of a group in a lane
-    // blocks an SM: what the registers (D/4 of sums a row tile) and the ring leave room for
-    static constexpr int kBlocks = kNT * D / 4 > 64 || kRB == 256 ? 1 : 2;
+    // blocks an SM: what the registers leave room for, of which the sums take kNT * D / 4 a
+    // lane, and the ring
+    static constexpr int kBlocks = kNT * D / 4 <= 32 && kRB <= 64 ? 2 : 1;
+    static constexpr int kWarps = 8, kThreads = 32 * kWarps;
+    static constexpr int kL = kThreads / kRT, kE = D / kL;  // lanes of a row at the end, columns of a lane
     static constexpr int kStageBytes = kTB * 2 * (kRB + kFB);
     static constexpr int kQBytes = kSteps * kTerms * kNT * 32 * 8;
-    static constexpr int kZBytes = kNormal ? kTB * kG * 6 : 0;  // a warp's V tokens: f32 rest, f16 -(1024 + z)
-    static constexpr int kFixed = kQBytes + 4 * kRT * (kG + 1 + 2 * kKvqWarps) + kKvqWarps * kZBytes;
+    // a warp's factors of a block: f32 pairs of K and of V; f16 -(1024 + z) of V
+    static constexpr int kFacBytes = kTB * kG * (16 + (kNormal ? 2 : 0));
+    // (its place holds q's rows in f32 before)
+    static constexpr int kFacAll = std::max(kWarps * kFacBytes, kRT * (D + 4) * 4);
+    static constexpr int kFixed = kQBytes + 4 * kRT * (kG + 1 + 2 * kWarps) + kFacAll;
     static constexpr int kRoom = (kBlocks == 2 ? 113 : 226) * 1024 - kFixed - 1024;
-    static constexpr int kStages = std::min(6, kRoom / (kKvqWarps * kStageBytes));
+    static constexpr int kStages = std::min(6, kRoom / (kWarps * kStageBytes));
     static constexpr int kRowPair = 2 * D + 2;            // floats of two rows of a warp's sums
     static constexpr int kWarpBytes = std::max(kStages * kStageBytes, kRT / 2 * kRowPair * 4 + 8) / 16 * 16;
-    static_assert(kStages >= 2 && kWarpBytes * kKvqWarps <= kRoom, "the ring fits");
-    static constexpr int kSmem = kFixed + kKvqWarps * kWarpBytes;
+    static_assert(kStages >= 2 && kWarpBytes * kWarps <= kRoom, "the ring fits");
+    static constexpr int kSmem = kFixed + kWarps * kWarpBytes;
 };
 
 // N bytes to shared memory; without kWhole, zeros where they are not real
@@ -120,6 +125,9 @@ __device__ __forceinline__ float kvq_exp2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Keeps the compiler from bringing the next group's words forward: there is not a
+// register for all of them.
+__device__ __forceinline__ void kvq_fence() { __syncwarp(); }
 __device__ __forceinline__ void kvq_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void kvq_wait() {
@@ -201,32 +209,83 @@ __device__ __forceinline__ float kvq_value(const void *p, int type, int64_t at) 
                                  : __half2float(static_cast<const __half *>(p)[at]);
 }
 
+// E columns from `at` on of y, of the sums v and the weight l (attn_finish of E columns
+// a lane); all lanes call it, `mine` says which write.
+template <int E>
+__device__ __forceinline__ void kvq_finish(const abg_tree_attn_args &a, int64_t at, float (&v)[E], float l, bool mine) {
+    float sum = 0.0f;
+    if (mine) {
+        if (a.gate) {
+            float g[E];
+            load_e<float, E>(a.gate + at, g);
+#pragma unroll
+            for (int i = 0; i < E; ++i) v[i] = (l == 0.0f ? 0.0f : v[i] / l) * (1.0f / (1.0f + expf(-g[i])));
+        } else {
+#pragma unroll
+            for (int i = 0; i < E; ++i) v[i] = l == 0.0f ? 0.0f : v[i] / l;
+        }
+        if (a.y_type == ABG_SB_F32) {
+            store_e<float, E>(static_cast<float *>(a.y) + at, v);
+        } else if (a.y_type == ABG_SB_BF16) {
+            store_e<__nv_bfloat16, E>(static_cast<__nv_bfloat16 *>(a.y) + at, v);
+        } else {
+            store_e<__half, E>(static_cast<__half *>(a.y) + at, v);
+        }
+#pragma unroll
+        for (int i = 0; i < E; ++i) sum += v[i];
+    }
+    if (a.ysum) {
+#pragma unroll
+        for (int d = 1; d < 64 / E; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (mine && at % 64 == 0) a.ysum[at / 64] = sum;
+    }
+}
+
 template <typename S>
-__global__ void __launch_bounds__(kKvqThreads, S::kBlocks) kvq_attn_kernel(const __grid_constant__ KvqAttnArgs x) {
+__global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const __grid_constant__ KvqAttnArgs x) {
     constexpr int D = S::D, kNT = S::kNT, kRT = S::kRT, kRB = S::kRB, kFB = S::kFB, kG = S::kG, kTB = S::kTB;
     constexpr int kMT = S::kMT, kTerms = S::kTerms, kStages = S::kStages, kGroup = S::kGroup, kBits = S::kBits;
-    constexpr int E = D / 32, kTiles = D / 16;
+    constexpr int E = D / 32, kTiles = D / 16, kWarps = S::kWarps, kThreads = S::kThreads;
     extern __shared__ __align__(128) unsigned char raw[];
     __shared__ AttnScan scan;
+    __shared__ AttnLine<kRT, kKvqTile> s_line;  // while the blocks go by, so that no register holds them
+    __shared__ AttnSeg s_seg;
     const AttnArgs &p = x.p;
     const abg_tree_attn_args &a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, j = lane >> 2, quad = lane & 3;
     uint2 *s_q = reinterpret_cast<uint2 *>(raw);                            // [step][term][row tile][lane]
     float *s_qs = reinterpret_cast<float *>(raw + S::kQBytes);              // [kG][kRT] group sums of q
     float *s_f = s_qs + kG * kRT;                                           // [kRT] factor of a row's scores
-    float *s_m = s_f + kRT, *s_l = s_m + kKvqWarps * kRT;                   // [warp][kRT]
-    float *rest = reinterpret_cast<float *>(s_l + kKvqWarps * kRT) + warp * (S::kZBytes / 4);  // [kTB][kG]
-    __half *zero = reinterpret_cast<__half *>(rest + kTB * kG);                               // [kG][kTB], pairs
+    float *s_m = s_f + kRT, *s_l = s_m + kWarps * kRT;                   // [warp][kRT]
+    // the block's factors in f32, two groups of a token side by side: [kG / 2][kTB][2] pairs
+    float *s_qf = s_l + kWarps * kRT;                                       // [kRT][D + 4] (before the factors)
+    float2 *k_fac = reinterpret_cast<float2 *>(s_qf) + warp * (S::kFacBytes / 8);
+    float2 *v_fac = k_fac + kTB * kG;
+    __half *zero = reinterpret_cast<__half *>(v_fac + kTB * kG);            // [kG][kTB], by pairs of tokens
+    constexpr int kPair = kG > 1 ? 2 : 1;
     unsigned char *ring = raw + (S::kFixed + warp * S::kWarpBytes);
     const uint32_t ring_at = smem_u32(ring);
     static_assert(S::kFixed % 16 == 0, "the ring's alignment");
     grid_dep_wait();
     grid_dep_launch();
-    AttnLine<kRT, kKvqTile> line;
-    line.template init<kKvqThreads>(p, blockIdx.x, gridDim.x, scan);
+    // row r of a unit's q: which of q's rows of D values
+    auto q_row = [&](const AttnSeg &s, int r) {
+        const int q = s.r0 + r, draft = q / p.G;
+        return (static_cast<int64_t>(s.req.n0) + draft) * a.Hq + s.h * p.G + (q - draft * p.G);
+    };
     bool left = false;
-    AttnSeg s;
-    while (line.next(p, s)) {
+    {
+        AttnLine<kRT, kKvqTile> line;
+        line.template init<kThreads>(p, blockIdx.x, gridDim.x, scan);
+        if (tid == 0) s_line = line;
+        __syncthreads();
+    }
+    for (;;) {
+        AttnSeg s;
+        AttnLine<kRT, kKvqTile> line = s_line;
+        if (!line.next(p, s)) break;
+        __syncthreads();  // all have read the line
+        if (tid == 0) s_line = line, s_seg = s;
         const int key0 = min(s.t0, s.ctiles) * kKvqTile;
         const int key1 = min(s.req.len, min(s.t1, s.ctiles) * kKvqTile);    // cached tokens of the stretch
         const int blocks = key1 > key0 ? (key1 - key0 + kTB - 1) / kTB : 0;
@@ -241,14 +300,14 @@ __global__ void __launch_bounds__(kKvqThreads, S::kBlocks) kvq_attn_kernel(const
         };
         int32_t id = page_of(warp);
         auto bring = [&](int i) {  // the warp's block i, of whose pages `id` knows; a group of copies
-            const int blk = warp + i * kKvqWarps;
+            const int blk = warp + i * kWarps;
             if (blk < blocks) {
                 const int t = key0 + blk * kTB + lane, page = static_cast<int>(a.page);
                 const bool there = static_cast<uint32_t>(id) < static_cast<uint32_t>(a.pages);
                 // (a cache has fewer than 2^32 rows)
                 const uint32_t row =
                     there ? (static_cast<uint32_t>(id) * static_cast<uint32_t>(a.Hkv) + s.h) * page + (t - page_at(t) * page) : 0;
-                id = page_of(blk + kKvqWarps);
+                id = page_of(blk + kWarps);
                 const uint32_t at = ring_at + (i % kStages) * S::kStageBytes;
                 constexpr int kChunks = kRB / 16;
                 const unsigned all = __ballot_sync(0xffffffffu, there);
@@ -287,21 +346,23 @@ __global__ void __launch_bounds__(kKvqThreads, S::kBlocks) kvq_attn_kernel(const
         for (int i = 0; i < kStages - 1; ++i) bring(i);
         // -- q: a row a warp for its scale and sums, then the products' operands --
         if (blocks > 0) {
-            for (int r = warp; r < kRT; r += kKvqWarps) {
-                float v[E];
-                const int q = s.r0 + r;
-                float top = 0.0f;
-                if (r < s.rows) {
-                    kvq_row<E>(a.q, a.type, ((static_cast<int64_t>(s.req.n0) + q / p.G) * a.Hq + s.h * p.G + q % p.G) * D + lane * E, v);
-                } else {
+            constexpr int kRows = kRT / kWarps;  // of a warp
+            float v[kRows][E];
 #pragma unroll
-                    for (int i = 0; i < E; ++i) v[i] = 0.0f;
-                }
-                float sum = 0.0f;
+            for (int k = 0; k < kRows; ++k) {
+                const int r = k * kWarps + warp;
+#pragma unroll
+                for (int i = 0; i < E; ++i) v[k][i] = 0.0f;
+                if (r < s.rows) kvq_row<E>(a.q, a.type, q_row(s, r) * D + lane * E, v[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < kRows; ++k) {
+                const int r = k * kWarps + warp;
+                float top = 0.0f, sum = 0.0f;
 #pragma unroll
                 for (int i = 0; i < E; ++i) {
-                    top = fabsf(v[i]) < INFINITY ? fmaxf(top, fabsf(v[i])) : INFINITY;
-                    sum += v[i];
+                    top = fabsf(v[k][i]) < INFINITY ? fmaxf(top, fabsf(v[k][i])) : INFINITY;
+                    sum += v[k][i];
                 }
 #pragma unroll
                 for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -314,33 +375,27 @@ __global__ void __launch_bounds__(kKvqThreads, S::kBlocks) kvq_attn_kernel(const
                 // s_f * (s acc + b qs) is the score in base 2, acc of the scaled q and the operands
                 if (lane == 0) s_f[r] = bad ? __int_as_float(0x7fc00000) : p.scale2 * S::kUnit / up;
                 if (lane % (kGroup / E) == 0) s_qs[lane / (kGroup / E) * kRT + r] = sum * up * (1.0f / S::kUnit);
-                if (lane == 1) s_l[r] = up;  // (until the operands are made)
+#pragma unroll
+                for (int i = 0; i < E; ++i) s_qf[r * (D + 4) + lane * E + i] = v[k][i] * up;
             }
             __syncthreads();
-            for (int i = tid; i < S::kSteps * kNT * 32; i += kKvqThreads) {
+#pragma unroll 2
+            for (int i = tid; i < S::kSteps * kNT * 32; i += kThreads) {
                 const int ln = i & 31, nt = i / 32 % kNT, step = i / (32 * kNT);
-                const int r = nt * 8 + (ln >> 2), q = s.r0 + r;
                 constexpr int kPerWord = kBits == 4 ? 2 : 1;  // steps of a word
                 const int w = step / kPerWord, g = w / S::kWords, wi = w % S::kWords;
                 const int col = g * kGroup + ((ln & 3) * S::kWords + wi) * (32 / kBits) + (kBits == 4 ? 2 * (step % 2) : 0);
-                float v[4] = {};
-                if (r < s.rows) {
-                    const int64_t at = ((static_cast<int64_t>(s.req.n0) + q / p.G) * a.Hq + s.h * p.G + q % p.G) * D + col;
-                    const float up = s_l[r];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        // the pairs' columns: 0 and 4, 1 and 5 of 4 bits (the second a nibble
-                        // up: 2^4), 0 and 2, 1 and 3 of 8
-                        const float t = kvq_value(a.q, a.type, at + (k >> 1) + (k & 1) * (kBits == 4 ? 4 : 2)) * up;
-                        v[k] = k >> 1 ? t * (1.0f / S::kUpper) : t;
-                    }
-                }
+                // the pairs' columns: 0 and 4, 1 and 5 of 4 bits (the second a nibble up:
+                // 2^4), 0 and 2, 1 and 3 of 8
+                constexpr int kNext = kBits == 4 ? 4 : 2;
+                const float *from = s_qf + (nt * 8 + (ln >> 2)) * (D + 4) + col;
+                const float v0 = from[0], v1 = from[kNext], v2 = from[1] * (1.0f / S::kUpper), v3 = from[kNext + 1] * (1.0f / S::kUpper);
                 uint2 *to = s_q + ((step * kTerms) * kNT + nt) * 32 + ln;
-                const uint2 hi = make_uint2(kvq_half2(v[0], v[1]), kvq_half2(v[2], v[3]));
+                const uint2 hi = make_uint2(kvq_half2(v0, v1), kvq_half2(v2, v3));
                 *to = hi;
                 if constexpr (kTerms == 2) {
                     const float2 h0 = kvq_float2(hi.x), h1 = kvq_float2(hi.y);
-                    to[kNT * 32] = make_uint2(kvq_half2(v[0] - h0.x, v[1] - h0.y), kvq_half2(v[2] - h1.x, v[3] - h1.y));
+                    to[kNT * 32] = make_uint2(kvq_half2(v0 - h0.x, v1 - h0.y), kvq_half2(v2 - h1.x, v3 - h1.y));
                 }
             }
             __syncthreads();
@@ -349,6 +404,7 @@ __global__ void __launch_bounds__(kKvqThreads, S::kBlocks) kvq_attn_kernel(const
         float o[kTiles][kNT][4];             // columns (8 or 4 a lane of a group, two a tile) x rows 2 quad, + 1
         float l[kNT][2], m[kNT][2], bias[kG][kNT][2];
         int ev = 0;                          // the largest scale of V so far is below 2^(ev - 14)
+        float up = pow2i(28);                // 2^(28 - ev)
 #pragma unroll
         for (int i = 0; i < kTiles; ++i)
 #pragma unroll
@@ -361,20 +417,94 @@ __global__ void __launch_bounds__(kKvqThreads, S::kBlocks) kvq_attn_kernel(const
             for (int g = 0; g < kG; ++g) bias[g][nt][0] = bias[g][nt][1] = 0.0f;
         }
         const int tok = kvq_token(j);
-        for (int i = 0, blk = warp; blk < blocks; ++i, blk += kKvqWarps) {
+        for (int i = 0, blk = warp; blk < blocks; ++i, blk += kWarps) {
             kvq_wait<kStages - 2>();
             __syncwarp();  // every lane's copies have come, and the last block's place is free
             bring(i + kStages - 1);
             const unsigned char *K = ring + (i % kStages) * S::kStageBytes, *V = K + kTB * kRB, *Kf = V + kTB * kRB,
                                 *Vf = Kf + kTB * kFB;
+            // the factors, a token a lane; V's scales times a power of two that brings the
+            // largest so far to 2^13 .. 2^14
+            {
+                uint32_t kf[kG], vf[kG], big = 0;
+                if (lane < kTB) {
+#pragma unroll
+                    for (int g = 0; g < kG; ++g) {
+                        kf[g] = *reinterpret_cast<const uint32_t *>(Kf + lane * kFB + 4 * g);
+                        vf[g] = *reinterpret_cast<const uint32_t *>(Vf + lane * kFB + 4 * g);
+                        const uint32_t v = vf[g] & 0x7fffu;
+                        big = max(big, v < 0x7c00u ? v : 0u);
+                    }
+                }
+                if (__any_sync(0xffffffffu, static_cast<int>(big >> 10) > ev)) {
+                    const int ev1 = max(ev, static_cast<int>(__reduce_max_sync(0xffffffffu, big) >> 10));
+                    const float down = pow2i(ev - ev1);
+                    ev = ev1;
+                    up = pow2i(28 - ev);
+                    if constexpr (!S::kNormal) {
+#pragma unroll
+                        for (int k = 0; k < kTiles; ++k)
+#pragma unroll
+                            for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) o[k][nt][e] *= down;
+                    }
+                }
+                if (lane < kTB) {
+                    float2 kk[kG], vv[kG];
+#pragma unroll
+                    for (int g = 0; g < kG; ++g) {
+                        kk[g] = kvq_float2(kf[g]);
+                        vv[g] = kvq_float2(vf[g]);
+                        if constexpr (S::kNormal) {
+                            kk[g].y = fmaf(S::kMiddle, kk[g].x, kk[g].y);
+                            // (any z is right; no scale, or a NaN: one of the ends)
+                            const float z =
+                                fminf(fmaxf(rintf(__fdividef(-vv[g].y, vv[g].x)), 0.0f), kBits == 4 ? 15.0f : 255.0f);
+                            vv[g].y = fmaf(vv[g].x, z, vv[g].y);
+                            zero[g * kTB + (lane & ~7) + 2 * (lane & 3) + (lane >> 2 & 1)] = __float2half_rn(-1024.0f - z);
+                        }
+                        vv[g].x *= up;
+                    }
+#pragma unroll
+                    for (int g = 0; g < kG; g += kPair) {
+                        float2 *const kt = k_fac + g * kTB + lane * kPair, *const vt = v_fac + g * kTB + lane * kPair;
+                        if constexpr (kPair == 2) {
+                            *reinterpret_cast<float4 *>(kt) = make_float4(kk[g].x, kk[g].y, kk[g + 1].x, kk[g + 1].y);
+                            *reinterpret_cast<float4 *>(vt) = make_float4(vv[g].x, vv[g].y, vv[g + 1].x, vv[g + 1].y);
+                        } else {
+                            *kt = kk[g];
+                            *vt = vv[g];
+                        }
+                    }
+                }
+                __syncwarp();
+            }
+            // scale and bias of token t, groups g (even) and g + 1
+            auto factors = [&](const float2 *fac, int t, int g, float2 (&f)[2]) {
+                const float2 *from = fac + g * kTB + t * kPair;
+                if constexpr (kPair == 2) {
+                    const float4 v = *reinterpret_cast<const float4 *>(from);
+                    f[0] = make_float2(v.x, v.y), f[1] = make_float2(v.z, v.w);
+                } else {
+                    f[0] = *from;
+                }
+            };
             // scores
             float sc[kMT][kNT][4];
 #pragma unroll
             for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
                 for (int nt = 0; nt < kNT; ++nt) sc[mt][nt][0] = sc[mt][nt][1] = sc[mt][nt][2] = sc[mt][nt][3] = 0.0f;
+            float2 f2[kMT][2][2];  // of tokens tok and tok + 8, of two groups
 #pragma unroll
             for (int g = 0; g < kG; ++g) {
+                kvq_fence();
+                if (g % 2 == 0)
+#pragma unroll
+                    for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) factors(k_fac, 16 * mt + 8 * h + tok, g, f2[mt][h]);
                 uint32_t w[kMT][2][S::kWords];
 #pragma unroll
                 for (int mt = 0; mt < kMT; ++mt)
@@ -424,24 +554,17 @@ __global__ void __launch_bounds__(kKvqThreads, S::kBlocks) kvq_attn_kernel(const
                                     kvq_mma(acc[mt][nt], e[mt][0], e[mt][1], e[mt][2], e[mt][3], b);
                             }
                     }
-                float2 f[kMT][2];  // scale, bias of tokens tok and tok + 8
-#pragma unroll
-                for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        f[mt][h] = kvq_float2(*reinterpret_cast<const uint32_t *>(Kf + (16 * mt + 8 * h + tok) * kFB + 4 * g));
-                        if constexpr (S::kNormal) f[mt][h].y = fmaf(S::kMiddle, f[mt][h].x, f[mt][h].y);
-                    }
 #pragma unroll
                 for (int nt = 0; nt < kNT; ++nt) {
                     const float2 qs = *reinterpret_cast<const float2 *>(s_qs + g * kRT + nt * 8 + 2 * quad);
 #pragma unroll
                     for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            sc[mt][nt][e] = fmaf(acc[mt][nt][e], f[mt][e >> 1].x,
-                                                 g == 0 ? f[mt][e >> 1].y * (e & 1 ? qs.y : qs.x)
-                                                        : fmaf(f[mt][e >> 1].y, e & 1 ? qs.y : qs.x, sc[mt][nt][e]));
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 f = f2[mt][e >> 1][g % 2];
+                            const float qe = e & 1 ? qs.y : qs.x;
+                            sc[mt][nt][e] = fmaf(acc[mt][nt][e], f.x, g == 0 ? f.y * qe : fmaf(f.y, qe, sc[mt][nt][e]));
+                        }
                 }
             }
             // maxima and weights (sc is in units of 1/s_f until its exponential)
@@ -455,8 +578,9 @@ __global__ void __launch_bounds__(kKvqThreads, S::kBlocks) kvq_attn_kernel(const
                         for (int e = 0; e < 4; ++e)
                             if (16 * mt + 8 * (e >> 1) + tok >= here) sc[mt][nt][e] = -INFINITY;
             }
-            bool grew = false;
-            float corr[kNT][2];
+            // the rows' reference m goes up, and their sums down, where a score lies more
+            // than 1.5 above it: weights are below 2^1.5, which f16 has room for
+            bool above = false;
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt) {
                 const float2 f = *reinterpret_cast<const float2 *>(s_f + nt * 8 + 2 * quad);
@@ -464,60 +588,58 @@ __global__ void __launch_bounds__(kKvqThreads, S::kBlocks) kvq_attn_kernel(const
                 for (int e = 0; e < 2; ++e) {
                     float top = fmaxf(sc[0][nt][e], sc[0][nt][2 + e]);
                     if constexpr (kMT == 2) top = fmaxf(top, fmaxf(sc[kMT - 1][nt][e], sc[kMT - 1][nt][2 + e]));
+                    above = above || top * (e ? f.y : f.x) > m[nt][e] + 1.5f;
+                }
+            }
+            if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                    top = fmaxf(m[nt][e], top * (e ? f.y : f.x));
-                    const float ref = top == -INFINITY ? 0.0f : top;
-                    corr[nt][e] = kvq_exp2(m[nt][e] - ref);
-                    grew = grew || top > m[nt][e];
-                    m[nt][e] = top;
-                    float sum = 0.0f;
+                for (int nt = 0; nt < kNT; ++nt) {
+                    const float2 f = *reinterpret_cast<const float2 *>(s_f + nt * 8 + 2 * quad);
+                    float corr[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float top = fmaxf(sc[0][nt][e], sc[0][nt][2 + e]);
+                        if constexpr (kMT == 2) top = fmaxf(top, fmaxf(sc[kMT - 1][nt][e], sc[kMT - 1][nt][2 + e]));
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                        top = fmaxf(m[nt][e], top * (e ? f.y : f.x));
+                        corr[e] = kvq_exp2(m[nt][e] - (top == -INFINITY ? 0.0f : top));
+                        m[nt][e] = top;
+                        l[nt][e] *= corr[e];
+#pragma unroll
+                        for (int g = 0; g < kG; ++g) bias[g][nt][e] *= corr[e];
+                    }
+#pragma unroll
+                    for (int k = 0; k < kTiles; ++k)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[k][nt][e] *= corr[e & 1];
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt) {
+                const float2 f = *reinterpret_cast<const float2 *>(s_f + nt * 8 + 2 * quad);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float ref = m[nt][e] == -INFINITY ? 0.0f : m[nt][e];
 #pragma unroll
                     for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             float &v = sc[mt][nt][2 * h + e];
                             v = kvq_exp2(fmaf(v, e ? f.y : f.x, -ref));
-                            sum += v;
+                            l[nt][e] += v;
                         }
-                    l[nt][e] = fmaf(l[nt][e], corr[nt][e], sum);
                 }
             }
-            // the largest scale of V
-            uint32_t big = 0;
-            if (lane < kTB) {
-#pragma unroll
-                for (int g = 0; g < kG; ++g) {
-                    const uint32_t w = *reinterpret_cast<const uint32_t *>(Vf + lane * kFB + 4 * g), v = w & 0x7fffu;
-                    big = max(big, v < 0x7c00u ? v : 0u);
-                    if constexpr (S::kNormal) {
-                        const float2 f = kvq_float2(w);
-                        // (any z is right; no scale, or a NaN: one of the ends)
-                        const float z = fminf(fmaxf(rintf(__fdividef(-f.y, f.x)), 0.0f), kBits == 4 ? 15.0f : 255.0f);
-                        rest[lane * kG + g] = fmaf(f.x, z, f.y);
-                        zero[g * kTB + (lane & ~7) + 2 * (lane & 3) + (lane >> 2 & 1)] = __float2half_rn(-1024.0f - z);
-                    }
-                }
-            }
-            const int ev0 = static_cast<int>(__reduce_max_sync(0xffffffffu, big) >> 10), ev1 = S::kNormal ? ev0 : max(ev, ev0);
-            if constexpr (S::kNormal) __syncwarp();
-            if (__any_sync(0xffffffffu, grew) || (!S::kNormal && ev1 != ev)) {
-                const float down = S::kNormal ? 1.0f : pow2i(ev - ev1);
-#pragma unroll
-                for (int nt = 0; nt < kNT; ++nt) {
-#pragma unroll
-                    for (int g = 0; g < kG; ++g) bias[g][nt][0] *= corr[nt][0], bias[g][nt][1] *= corr[nt][1];
-                    const float c0 = corr[nt][0] * down, c1 = corr[nt][1] * down;
-#pragma unroll
-                    for (int i = 0; i < kTiles; ++i)
-                        o[i][nt][0] *= c0, o[i][nt][1] *= c1, o[i][nt][2] *= c0, o[i][nt][3] *= c1;
-                }
-            }
-            ev = ev1;
-            const float up = pow2i(28 - ev);
             // weighted sums
 #pragma unroll
             for (int g = 0; g < kG; ++g) {
+                kvq_fence();
+                if (g % 2 == 0)
+#pragma unroll
+                    for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) factors(v_fac, 16 * mt + 8 * h + tok, g, f2[mt][h]);
                 constexpr int kPart = S::kNormal ? kGroup / 16 : 1;
                 float part[kPart][kNT][4];  // of the block
                 if constexpr (S::kNormal) {
@@ -529,13 +651,6 @@ __global__ void __launch_bounds__(kKvqThreads, S::kBlocks) kvq_attn_kernel(const
                 }
 #pragma unroll
                 for (int mt = 0; mt < kMT; ++mt) {
-                    float2 f[2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        f[h] = kvq_float2(*reinterpret_cast<const uint32_t *>(Vf + (16 * mt + 8 * h + tok) * kFB + 4 * g));
-                        if constexpr (S::kNormal) f[h].y = rest[(16 * mt + 8 * h + tok) * kG + g];
-                        f[h].x *= up;
-                    }
                     uint2 b[kTerms][kNT];
 #pragma unroll
                     for (int nt = 0; nt < kNT; ++nt) {
@@ -543,8 +658,9 @@ __global__ void __launch_bounds__(kKvqThreads, S::kBlocks) kvq_attn_kernel(const
                         float v[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            v[e] = w[e] * f[e >> 1].x;
-                            bias[g][nt][e & 1] = fmaf(w[e], f[e >> 1].y, bias[g][nt][e & 1]);
+                            const float2 f = f2[mt][e >> 1][g % 2];
+                            v[e] = w[e] * f.x;
+                            bias[g][nt][e & 1] = fmaf(w[e], f.y, bias[g][nt][e & 1]);
                         }
                         const uint32_t h0 = kvq_half2(v[0], v[1]), h1 = kvq_half2(v[2], v[3]);
                         b[0][nt] = make_uint2(kvq_transpose(h0), kvq_transpose(h1));
@@ -646,115 +762,115 @@ __global__ void __launch_bounds__(kKvqThreads, S::kBlocks) kvq_attn_kernel(const
                 }
             }
         }
-        __syncthreads();
-        // -- a row a warp: the warps' sums, the drafts, the result --
-        const bool whole = s.t0 == 0 && s.t1 == s.tiles;
-        const int64_t slot = static_cast<int64_t>(2) * blockIdx.x + (s.t0 == 0);
+        // -- kL lanes a row: the warps' sums, the drafts, the result --
+        s = s_seg;
+        constexpr int kL = S::kL, kE = S::kE;
+        const int r = warp * (32 / kL) + lane / kL, ln = lane % kL;
+        const bool mine = r < s.rows;
+        const int64_t row = q_row(s, mine ? r : 0), n = static_cast<int64_t>(s.req.n0) + (s.r0 + (mine ? r : 0)) / p.G;
         const int d0 = (max(s.t0, s.ctiles) - s.ctiles) * kKvqTile, d1 = min(s.req.T, (s.t1 - s.ctiles) * kKvqTile);
-        for (int r = warp; r < s.rows; r += kKvqWarps) {
-            const int q = s.r0 + r, draft = q / p.G, hq = s.h * p.G + q % p.G;
-            const int64_t n = static_cast<int64_t>(s.req.n0) + draft;
-            float M = -INFINITY, L = 0.0f, v[E];
+        const uint64_t *mask = a.mask + n * a.words;
+        auto word = [&](int w0) {  // drafts w0 .. w0 + 63 that the row sees (kKvqTile is a multiple of 64)
+            uint64_t seen = mine && w0 < d1 ? mask[w0 >> 6] : 0;
+            if (d1 - w0 < 64) seen &= (1ull << max(d1 - w0, 0)) - 1;
+            return seen;
+        };
+        float qv[kE];
+        uint64_t seen = word(d0);  // (on its way while the warps meet, as q is)
+        if (d1 > d0 && mine) kvq_row<kE>(a.q, a.type, row * D + ln * kE, qv);
+        __syncthreads();
+        float M = -INFINITY, L = 0.0f, v[kE];
 #pragma unroll
-            for (int i = 0; i < E; ++i) v[i] = 0.0f;
-            if (blocks > 0) {
-                const int w = lane & 7;
-                const float mw = s_m[w * kRT + r], lw = s_l[w * kRT + r];
-                M = mw;
+        for (int i = 0; i < kE; ++i) v[i] = 0.0f;
+        if (blocks > 0) {
+            static_assert(kWarps == 8 && kL >= 8);
+            const float mw = s_m[(ln & 7) * kRT + r], lw = s_l[(ln & 7) * kRT + r];
+            M = mw;
 #pragma unroll
-                for (int d = 1; d < 8; d <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-                // (no maximum, but a weight: a NaN, which stays)
-                const float fw = lw == 0.0f ? 0.0f : mw == -INFINITY ? 1.0f : exp2f(mw - M);
+            for (int d = 1; d < 8; d <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+            // (no maximum, but a weight: a NaN, which stays)
+            const float fw = lw == 0.0f ? 0.0f : mw == -INFINITY ? 1.0f : exp2f(mw - M);
 #pragma unroll
-                for (int u = 0; u < kKvqWarps; ++u) {
-                    const float f = __shfl_sync(0xffffffffu, fw, u), lu = __shfl_sync(0xffffffffu, lw, u);
-                    if (f == 0.0f) continue;  // no weight: nothing to add
-                    L = fmaf(lu, f, L);
-                    const float *from = reinterpret_cast<const float *>(raw + S::kFixed + u * S::kWarpBytes) +
-                                        (r >> 1) * S::kRowPair + (r & 1) * D + lane * E;
+            for (int u = 0; u < kWarps; ++u) {
+                const float f = __shfl_sync(0xffffffffu, fw, u, kL), lu = __shfl_sync(0xffffffffu, lw, u, kL);
+                if (f == 0.0f) continue;  // no weight: nothing to add
+                L = fmaf(lu, f, L);
+                const float *from = reinterpret_cast<const float *>(raw + S::kFixed + u * S::kWarpBytes) +
+                                    (r >> 1) * S::kRowPair + (r & 1) * D + ln * kE;
 #pragma unroll
-                    for (int i = 0; i < E; i += 2) {
-                        const float2 y = *reinterpret_cast<const float2 *>(from + i);
-                        v[i] = fmaf(y.x, f, v[i]), v[i + 1] = fmaf(y.y, f, v[i + 1]);
-                    }
+                for (int i = 0; i < kE; i += 2) {
+                    const float2 y = *reinterpret_cast<const float2 *>(from + i);
+                    v[i] = fmaf(y.x, f, v[i]), v[i + 1] = fmaf(y.y, f, v[i + 1]);
                 }
-            }
-            if (d1 > d0) {
-                float qv[E];
-                kvq_row<E>(a.q, a.type, (n * a.Hq + hq) * D + lane * E, qv);
-                bool bad = false;
-#pragma unroll
-                for (int i = 0; i < E; ++i) bad = bad || !(fabsf(qv[i]) < kKvqLargestQ);
-                bad = __any_sync(0xffffffffu, bad);
-                const uint64_t *mask = a.mask + n * a.words;
-                const int64_t base = (static_cast<int64_t>(s.h) * a.drafts + s.req.n0) * D + lane * E;
-                for (int w0 = d0; w0 < d1; w0 += 64) {  // (kKvqTile is a multiple of 64)
-                    uint64_t seen = mask[w0 >> 6];
-                    if (d1 - w0 < 64) seen &= (1ull << (d1 - w0)) - 1;
-                    while (seen) {
-                        constexpr int kBatch = 4;
-                        int64_t at[kBatch];
-                        float kv[kBatch][E], vv[kBatch][E], sc[kBatch];
-#pragma unroll
-                        for (int k = 0; k < kBatch; ++k) {
-                            at[k] = seen ? base + static_cast<int64_t>(w0 + __ffsll(static_cast<long long>(seen)) - 1) * D : -1;
-                            seen &= seen - 1;
-                            if (at[k] < 0) continue;
-                            kvq_row<E>(a.Kd, a.type, at[k], kv[k]);
-                            kvq_row<E>(a.Vd, a.type, at[k], vv[k]);
-                        }
-                        float top = M;
-#pragma unroll
-                        for (int k = 0; k < kBatch; ++k) {
-                            sc[k] = 0.0f;
-                            if (at[k] >= 0)
-#pragma unroll
-                                for (int i = 0; i < E; ++i) sc[k] = fmaf(qv[i], kv[k][i], sc[k]);
-                        }
-#pragma unroll
-                        for (int d = 16; d >= 1; d >>= 1)
-#pragma unroll
-                            for (int k = 0; k < kBatch; ++k) sc[k] += __shfl_xor_sync(0xffffffffu, sc[k], d);
-#pragma unroll
-                        for (int k = 0; k < kBatch; ++k) {
-                            sc[k] = at[k] < 0 ? -INFINITY : bad ? __int_as_float(0x7fc00000) : sc[k] * p.scale2;
-                            top = fmaxf(top, sc[k]);
-                        }
-                        const float ref = top == -INFINITY ? 0.0f : top, f = exp2f(M - ref);
-                        M = top;
-                        L *= f;
-#pragma unroll
-                        for (int i = 0; i < E; ++i) v[i] *= f;
-#pragma unroll
-                        for (int k = 0; k < kBatch; ++k) {
-                            if (at[k] < 0) continue;
-                            const float w = exp2f(sc[k] - ref);
-                            L += w;
-#pragma unroll
-                            for (int i = 0; i < E; ++i) v[i] = fmaf(w, vv[k][i], v[i]);
-                        }
-                    }
-                }
-            }
-            if (whole) {
-                if (a.y_type == ABG_SB_F32) {
-                    attn_finish<float, D>(a, n, hq, v, L);
-                } else if (a.y_type == ABG_SB_BF16) {
-                    attn_finish<__nv_bfloat16, D>(a, n, hq, v, L);
-                } else {
-                    attn_finish<__half, D>(a, n, hq, v, L);
-                }
-            } else {
-                float *po = p.part_o + (slot * kRT + r) * D + lane * E;
-#pragma unroll
-                for (int i = 0; i < E; ++i) po[i] = v[i];
-                if (lane == 0) p.part_ml[slot * kRT + r] = make_float2(M, L);
             }
         }
-        if (tid == 0) line.leave_entry(p, s, blockIdx.x, left);
+        if (d1 > d0) {
+            bool bad = false;
+#pragma unroll
+            for (int i = 0; i < kE; ++i) bad = bad || (mine && !(fabsf(qv[i]) < kKvqLargestQ));
+#pragma unroll
+            for (int d = 1; d < kL; d <<= 1) bad = __shfl_xor_sync(0xffffffffu, bad, d) || bad;
+            const int64_t base = (static_cast<int64_t>(s.h) * a.drafts + s.req.n0) * D + ln * kE;
+            for (int w0 = d0; w0 < d1; w0 += 64) {
+                if (w0 > d0) seen = word(w0);
+                while (__any_sync(0xffffffffu, seen != 0)) {
+                    constexpr int kBatch = kE > 8 ? 2 : 4;
+                    int64_t at[kBatch];
+                    float kv[kBatch][kE], vv[kBatch][kE], sc[kBatch];
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        at[k] = seen ? base + static_cast<int64_t>(w0 + __ffsll(static_cast<long long>(seen)) - 1) * D : -1;
+                        seen &= seen - 1;
+                        if (at[k] < 0) continue;
+                        kvq_row<kE>(a.Kd, a.type, at[k], kv[k]);
+                        kvq_row<kE>(a.Vd, a.type, at[k], vv[k]);
+                    }
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        sc[k] = 0.0f;
+                        if (at[k] >= 0)
+#pragma unroll
+                            for (int i = 0; i < kE; ++i) sc[k] = fmaf(qv[i], kv[k][i], sc[k]);
+                    }
+#pragma unroll
+                    for (int d = kL / 2; d >= 1; d >>= 1)
+#pragma unroll
+                        for (int k = 0; k < kBatch; ++k) sc[k] += __shfl_xor_sync(0xffffffffu, sc[k], d);
+                    float top = M;
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        sc[k] = at[k] < 0 ? -INFINITY : bad ? __int_as_float(0x7fc00000) : sc[k] * p.scale2;
+                        top = fmaxf(top, sc[k]);
+                    }
+                    const float ref = top == -INFINITY ? 0.0f : top, f = exp2f(M - ref);
+                    M = top;
+                    L *= f;
+#pragma unroll
+                    for (int i = 0; i < kE; ++i) v[i] *= f;
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) {
+                        if (at[k] < 0) continue;
+                        const float w = exp2f(sc[k] - ref);
+                        L += w;
+#pragma unroll
+                        for (int i = 0; i < kE; ++i) v[i] = fmaf(w, vv[k][i], v[i]);
+                    }
+                }
+            }
+        }
+        if (s.t0 == 0 && s.t1 == s.tiles) {
+            kvq_finish<kE>(a, row * D + ln * kE, v, L, mine);
+        } else if (mine) {
+            const int64_t slot = (static_cast<int64_t>(2) * blockIdx.x + (s.t0 == 0)) * kRT + r;
+            float *po = p.part_o + slot * D + ln * kE;
+#pragma unroll
+            for (int i = 0; i < kE; i += 2) *reinterpret_cast<float2 *>(po + i) = make_float2(v[i], v[i + 1]);
+            if (ln == 0) p.part_ml[slot] = make_float2(M, L);
+        }
+        if (tid == 0) s_line.leave_entry(p, s, blockIdx.x, left);
         __syncthreads();  // the rings and the rows' factors are free
     }
-    if (tid == 0) line.end_entries(p, blockIdx.x, left);
+    if (tid == 0) s_line.end_entries(p, blockIdx.x, left);
 }
 
 template <typename S>
@@ -769,7 +885,7 @@ cudaError_t kvq_go(KvqAttnArgs x, void *ws, bool early, bool pdl, cudaStream_t s
     x.p.part_ml = reinterpret_cast<float2 *>(w + l.ml);
     x.p.split = reinterpret_cast<AttnSplit *>(w + l.split);
     attn_entries(x.p, C, S::kRT);
-    const cudaError_t e = launch_kernel(kvq_attn_kernel<S>, dim3(C), dim3(kKvqThreads), S::kSmem, stream, early, x);
+    const cudaError_t e = launch_kernel(kvq_attn_kernel<S>, dim3(C), dim3(S::kThreads), S::kSmem, stream, early, x);
     if (e != cudaSuccess) return e;
     switch (x.p.a.y_type) {
     case ABG_SB_F32: return launch_join<float, S::D, S::kRT, false>(x.p, C, pdl, stream);
