@@ -81,7 +81,7 @@ struct KvqShape {
     static constexpr int kRT = 8 * kNT;
     static constexpr int kRB = D * kBits / 8;             // bytes of a row's codes
     static constexpr int kG = D / kGroup, kFB = 4 * kG;   // groups of a row, bytes of its factors
-    static constexpr int kTB = kRB <= 128 && kNT * D / 4 < 128 ? 32 : 16;  // tokens of a block
+    static constexpr int kTB = kRB <= 128 ? 32 : 16;       // tokens of a block
     static constexpr int kMT = kTB / 16;
     static constexpr int kSteps = D / 16;                 // products of 16 columns
     static constexpr int kWords = kGroup * kBits / 128;   // words of a group in a lane
@@ -894,10 +894,13 @@ cudaError_t kvq_go(KvqAttnArgs x, void *ws, bool early, bool pdl, cudaStream_t s
     }
 }
 
-// Rows of a tile: 8, 16 or (up to 128 columns) 32, as a request and head has them;
-// more would not fit in the registers, and are tiles of their own, which read the
-// cache again.
-inline int kvq_row_tile(int64_t D, int64_t rows) { return rows <= 8 ? 8 : rows <= 16 || D == 256 ? 16 : 32; }
+// Rows of a tile: 8, or 16 where a request and head has more and D is below 256, so that
+// the sums take at most 64 registers of a lane; rows beyond are tiles of their own, which
+// read the cache again.  (128 registers of sums, at 128 columns 32 rows a tile: eight f32
+// drafts of four requests 44.7 us where two tiles take 26.7, four bf16 drafts of 32
+// requests 117 and 76.6; at 256 columns 16 rows 118 and 96.6.  At 64 columns 32 rows fit,
+// and take 50.6 us where 16 take 49.0.)
+inline int kvq_row_tile(int64_t D, int64_t rows) { return rows <= 8 || D == 256 ? 8 : 16; }
 
 // f.template operator()<Shape>() for the cache's format and a call's rows; f16 and
 // f32 queries take two terms
@@ -907,10 +910,9 @@ auto kvq_by_rows(int group, int rt, bool split, F f) {
         constexpr int G = decltype(g)::value;
         constexpr bool kSp = decltype(sp)::value;
         if constexpr (D < 256) {
-            if (rt == 32) return f.template operator()<KvqShape<D, kBits, G, 4, kSp>>();
+            if (rt == 16) return f.template operator()<KvqShape<D, kBits, G, 2, kSp>>();
         }
-        return rt == 8 ? f.template operator()<KvqShape<D, kBits, G, 1, kSp>>()
-                       : f.template operator()<KvqShape<D, kBits, G, 2, kSp>>();
+        return f.template operator()<KvqShape<D, kBits, G, 1, kSp>>();
     };
     auto sp = [&](auto g) { return split ? nt(g, std::true_type{}) : nt(g, std::false_type{}); };
     return group == 32 ? sp(std::integral_constant<int, 32>{}) : sp(std::integral_constant<int, 64>{});
