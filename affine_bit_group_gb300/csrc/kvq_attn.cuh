@@ -125,9 +125,6 @@ __device__ __forceinline__ float kvq_exp2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// Keeps the compiler from bringing the next group's words forward: there is not a
-// register for all of them.
-__device__ __forceinline__ void kvq_fence() { __syncwarp(); }
 __device__ __forceinline__ void kvq_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void kvq_wait() {
@@ -250,6 +247,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
     __shared__ AttnScan scan;
     __shared__ AttnLine<kRT, kKvqTile> s_line;  // while the blocks go by, so that no register holds them
     __shared__ AttnSeg s_seg;
+    __shared__ const int32_t *s_table;          // the request's row
     const AttnArgs &p = x.p;
     const abg_tree_attn_args &a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, j = lane >> 2, quad = lane & 3;
@@ -285,30 +283,28 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
         AttnLine<kRT, kKvqTile> line = s_line;
         if (!line.next(p, s)) break;
         __syncthreads();  // all have read the line
-        if (tid == 0) s_line = line, s_seg = s;
+        if (tid == 0) s_line = line, s_seg = s, s_table = a.table + static_cast<int64_t>(s.b) * a.width;
+        __syncthreads();
         const int key0 = min(s.t0, s.ctiles) * kKvqTile;
         const int key1 = min(s.req.len, min(s.t1, s.ctiles) * kKvqTile);    // cached tokens of the stretch
-        const int blocks = key1 > key0 ? (key1 - key0 + kTB - 1) / kTB : 0;
         // -- copies --
-        const int32_t *table = a.table + static_cast<int64_t>(s.b) * a.width;
         auto page_at = [&](int t) {
             return x.page_mul ? static_cast<int>(__umulhi(static_cast<uint32_t>(t), x.page_mul) >> x.page_shift) : t;
         };
-        auto page_of = [&](int blk) {  // of this lane's token
-            const int t = key0 + blk * kTB + lane;
-            return blk < blocks && lane < kTB && t < key1 ? table[page_at(t)] : -1;
-        };
-        int32_t id = page_of(warp);
-        auto bring = [&](int i) {  // the warp's block i, of whose pages `id` knows; a group of copies
-            const int blk = warp + i * kWarps;
-            if (blk < blocks) {
-                const int t = key0 + blk * kTB + lane, page = static_cast<int>(a.page);
+        int t_next = key0 + warp * kTB + lane;  // this lane's token of the block that is brought next
+        auto page_of = [&](int t) { return lane < kTB && t < key1 ? s_table[page_at(t)] : -1; };
+        int32_t id = page_of(t_next);           // and its page
+        auto bring = [&](int stage) {           // that block; a group of copies
+            if (t_next - lane < key1) {
+                const int page = static_cast<int>(a.page);
                 const bool there = static_cast<uint32_t>(id) < static_cast<uint32_t>(a.pages);
                 // (a cache has fewer than 2^32 rows)
-                const uint32_t row =
-                    there ? (static_cast<uint32_t>(id) * static_cast<uint32_t>(a.Hkv) + s.h) * page + (t - page_at(t) * page) : 0;
-                id = page_of(blk + kWarps);
-                const uint32_t at = ring_at + (i % kStages) * S::kStageBytes;
+                const uint32_t row = there ? (static_cast<uint32_t>(id) * static_cast<uint32_t>(a.Hkv) + s_seg.h) * page +
+                                                 (t_next - page_at(t_next) * page)
+                                           : 0;
+                t_next += kWarps * kTB;
+                id = page_of(t_next);
+                const uint32_t at = ring_at + stage * S::kStageBytes;
                 constexpr int kChunks = kRB / 16;
                 const unsigned all = __ballot_sync(0xffffffffu, there);
                 auto copy = [&](auto whole) {
@@ -345,7 +341,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
 #pragma unroll
         for (int i = 0; i < kStages - 1; ++i) bring(i);
         // -- q: a row a warp for its scale and sums, then the products' operands --
-        if (blocks > 0) {
+        if (key1 > key0) {
             constexpr int kRows = kRT / kWarps;  // of a warp
             float v[kRows][E];
 #pragma unroll
@@ -417,11 +413,12 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
             for (int g = 0; g < kG; ++g) bias[g][nt][0] = bias[g][nt][1] = 0.0f;
         }
         const int tok = kvq_token(j);
-        for (int i = 0, blk = warp; blk < blocks; ++i, blk += kWarps) {
+        int stage = 0;
+        for (int t0 = key0 + warp * kTB; t0 < key1; t0 += kWarps * kTB) {
             kvq_wait<kStages - 2>();
             __syncwarp();  // every lane's copies have come, and the last block's place is free
-            bring(i + kStages - 1);
-            const unsigned char *K = ring + (i % kStages) * S::kStageBytes, *V = K + kTB * kRB, *Kf = V + kTB * kRB,
+            bring(stage == 0 ? kStages - 1 : stage - 1);
+            const unsigned char *K = ring + stage * S::kStageBytes, *V = K + kTB * kRB, *Kf = V + kTB * kRB,
                                 *Vf = Kf + kTB * kFB;
             // the factors, a token a lane; V's scales times a power of two that brings the
             // largest so far to 2^13 .. 2^14
@@ -499,7 +496,6 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
             float2 f2[kMT][2][2];  // of tokens tok and tok + 8, of two groups
 #pragma unroll
             for (int g = 0; g < kG; ++g) {
-                kvq_fence();
                 if (g % 2 == 0)
 #pragma unroll
                     for (int mt = 0; mt < kMT; ++mt)
@@ -568,7 +564,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
                 }
             }
             // maxima and weights (sc is in units of 1/s_f until its exponential)
-            const int here = key1 - key0 - blk * kTB;  // tokens of the block that are there
+            const int here = key1 - t0;  // tokens of the block that are there
             if (here < kTB) {
 #pragma unroll
                 for (int mt = 0; mt < kMT; ++mt)
@@ -634,7 +630,6 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
             // weighted sums
 #pragma unroll
             for (int g = 0; g < kG; ++g) {
-                kvq_fence();
                 if (g % 2 == 0)
 #pragma unroll
                     for (int mt = 0; mt < kMT; ++mt)
@@ -727,11 +722,13 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
                     }
                 }
             }
+            stage = stage + 1 == kStages ? 0 : stage + 1;
         }
         kvq_wait<0>();
         __syncwarp();
         // -- the warp's sums to shared memory, in its ring --
-        if (blocks > 0) {
+        const bool cached = key1 > key0;
+        if (cached) {
             float *mine = reinterpret_cast<float *>(ring);
             const float up = S::kNormal ? 1.0f : pow2i(ev - 28) * S::kUnit;
 #pragma unroll
@@ -782,7 +779,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
         float M = -INFINITY, L = 0.0f, v[kE];
 #pragma unroll
         for (int i = 0; i < kE; ++i) v[i] = 0.0f;
-        if (blocks > 0) {
+        if (cached) {
             static_assert(kWarps == 8 && kL >= 8);
             const float mw = s_m[(ln & 7) * kRT + r], lw = s_l[(ln & 7) * kRT + r];
             M = mw;
