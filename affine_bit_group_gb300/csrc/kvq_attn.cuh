@@ -63,6 +63,7 @@ inline void kvq_page_division(KvqAttnArgs &x, uint32_t page) {
     x.page_shift = s - 1;
 }
 
+constexpr int kKvqJoin = 8;    // pieces of a row that a warp has on their way when it joins
 constexpr int kKvqTile = 128;  // tokens of the work line's tiles
 // Rows of q from here on give NaN: their scores could pass f32's range.
 constexpr float kKvqLargestQ = 1.2676506e30f;  // 2^100
@@ -89,14 +90,15 @@ struct KvqShape {
     // lane, and the ring
     static constexpr int kBlocks = kNT * D / 4 <= 32 && kRB <= 64 ? 2 : 1;
     static constexpr int kWarps = 8, kThreads = 32 * kWarps;
-    static constexpr int kL = kThreads / kRT, kE = D / kL;  // lanes of a row at the end, columns of a lane
+    static constexpr int kL = kThreads / kRT, kE = D / kL;  // lanes of a row for drafts and result, columns of a lane
     static constexpr int kStageBytes = kTB * 2 * (kRB + kFB);
     static constexpr int kQBytes = kSteps * kTerms * kNT * 32 * 8;
     // a warp's factors of a block: f32 pairs of K and of V; f16 -(1024 + z) of V
     static constexpr int kFacBytes = kTB * kG * (16 + (kNormal ? 2 : 0));
     // (its place holds q's rows in f32 before)
     static constexpr int kFacAll = std::max(kWarps * kFacBytes, kRT * (D + 4) * 4);
-    static constexpr int kFixed = kQBytes + 4 * kRT * (kG + 1 + 2 * kWarps) + kFacAll;
+    static constexpr int kPark = kBlocks == 2 ? kRT * (D + 2) * 4 : 0;  // the drafts' part of the rows' sums
+    static constexpr int kFixed = kQBytes + 4 * kRT * (kG + 1 + 2 * kWarps) + kFacAll + (kPark + 15) / 16 * 16;
     static constexpr int kRoom = (kBlocks == 2 ? 113 : 226) * 1024 - kFixed - 1024;
     static constexpr int kStages = std::min(6, kRoom / (kWarps * kStageBytes));
     static constexpr int kRowPair = 2 * D + 2;            // floats of two rows of a warp's sums
@@ -245,9 +247,12 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
     constexpr int E = D / 32, kTiles = D / 16, kWarps = S::kWarps, kThreads = S::kThreads;
     extern __shared__ __align__(128) unsigned char raw[];
     __shared__ AttnScan scan;
-    __shared__ AttnLine<kRT, kKvqTile> s_line;  // while the blocks go by, so that no register holds them
-    __shared__ AttnSeg s_seg;
-    __shared__ const int32_t *s_table;          // the request's row
+    // (in shared memory while the blocks go by, so that no register holds them)
+    using Line = AttnLine<kRT, kKvqTile>;
+    __shared__ Line s_line, s_next;           // and the next stretch's
+    __shared__ AttnSeg s_seg[2];              // this stretch and the next
+    __shared__ bool s_more;
+    __shared__ const int32_t *s_table;        // the request's row
     const AttnArgs &p = x.p;
     const abg_tree_attn_args &a = p.a;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, j = lane >> 2, quad = lane & 3;
@@ -257,6 +262,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
     float *s_m = s_f + kRT, *s_l = s_m + kWarps * kRT;                   // [warp][kRT]
     // the block's factors in f32, two groups of a token side by side: [kG / 2][kTB][2] pairs
     float *s_qf = s_l + kWarps * kRT;                                       // [kRT][D + 4] (before the factors)
+    float *s_park = reinterpret_cast<float *>(reinterpret_cast<unsigned char *>(s_qf) + S::kFacAll);  // [kRT][D], [kRT][2]
     float2 *k_fac = reinterpret_cast<float2 *>(s_qf) + warp * (S::kFacBytes / 8);
     float2 *v_fac = k_fac + kTB * kG;
     __half *zero = reinterpret_cast<__half *>(v_fac + kTB * kG);            // [kG][kTB], by pairs of tokens
@@ -273,37 +279,78 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
     };
     bool left = false;
     {
-        AttnLine<kRT, kKvqTile> line;
+        Line line;
         line.template init<kThreads>(p, blockIdx.x, gridDim.x, scan);
-        if (tid == 0) s_line = line;
+        if (tid == 0) {
+            s_more = line.next(p, s_seg[0]);
+            s_line = line;
+        }
         __syncthreads();
     }
-    for (;;) {
-        AttnSeg s;
-        AttnLine<kRT, kKvqTile> line = s_line;
-        if (!line.next(p, s)) break;
-        __syncthreads();  // all have read the line
-        if (tid == 0) s_line = line, s_seg = s, s_table = a.table + static_cast<int64_t>(s.b) * a.width;
+    for (int turn = 0;; turn ^= 1) {
+        if (!s_more) break;
+        AttnSeg s = s_seg[turn];
+        if (tid == 0) s_table = a.table + static_cast<int64_t>(s.b) * a.width;
         __syncthreads();
         const int key0 = min(s.t0, s.ctiles) * kKvqTile;
         const int key1 = min(s.req.len, min(s.t1, s.ctiles) * kKvqTile);    // cached tokens of the stretch
+        // -- what is asked for first: q, a row a warp, and the masks of the drafts' part,
+        // kL lanes a row; later they would wait behind the copies --
+        constexpr int kRows = kRT / kWarps;
+        float q[kRows][E];
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            const int r = k * kWarps + warp;
+#pragma unroll
+            for (int i = 0; i < E; ++i) q[k][i] = 0.0f;
+            if (r < s.rows) kvq_row<E>(a.q, a.type, q_row(s, r) * D + lane * E, q[k]);
+        }
+        constexpr int kL = S::kL, kE = S::kE;
+        const int r = warp * (32 / kL) + lane / kL, ln = lane % kL;
+        const bool mine = r < s.rows;
+        const int d0 = (max(s.t0, s.ctiles) - s.ctiles) * kKvqTile, d1 = min(s.req.T, (s.t1 - s.ctiles) * kKvqTile);
+        auto word = [&](int w0) -> uint64_t {  // drafts w0 .. w0 + 63 that the row sees (kKvqTile is a multiple of 64)
+            if (!mine || w0 >= d1) return 0;
+            const int64_t n = static_cast<int64_t>(s.req.n0) + (s.r0 + r) / p.G;
+            const uint64_t seen = a.mask[n * a.words + (w0 >> 6)];
+            return d1 - w0 < 64 ? seen & ((1ull << (d1 - w0)) - 1) : seen;
+        };
+        uint64_t seen = word(d0);
         // -- copies --
         auto page_at = [&](int t) {
             return x.page_mul ? static_cast<int>(__umulhi(static_cast<uint32_t>(t), x.page_mul) >> x.page_shift) : t;
         };
         int t_next = key0 + warp * kTB + lane;  // this lane's token of the block that is brought next
         auto page_of = [&](int t) { return lane < kTB && t < key1 ? s_table[page_at(t)] : -1; };
-        int32_t id = page_of(t_next);           // and its page
+        int32_t id, ids[kStages];               // and its page
+#pragma unroll
+        for (int i = 0; i < kStages; ++i) ids[i] = page_of(t_next + i * kWarps * kTB);
+        // the drafts that the row sees, some at a time: their rows on their way, then their
+        // weights and sums
+        constexpr int kBatch = kE > 4 ? 2 : 4;
+        const int64_t base = (static_cast<int64_t>(s.h) * a.drafts + s.req.n0) * D + ln * kE;
+        int64_t d_at[kBatch];
+        float d_k[kBatch][kE], d_v[kBatch][kE];
+        auto ask = [&](int w0) {
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                d_at[k] = seen ? base + static_cast<int64_t>(w0 + __ffsll(static_cast<long long>(seen)) - 1) * D : -1;
+                seen &= seen - 1;
+                if (d_at[k] < 0) continue;
+                kvq_row<kE>(a.Kd, a.type, d_at[k], d_k[k]);
+                kvq_row<kE>(a.Vd, a.type, d_at[k], d_v[k]);
+            }
+        };
+        if (d1 > d0) ask(d0);
         auto bring = [&](int stage) {           // that block; a group of copies
             if (t_next - lane < key1) {
                 const int page = static_cast<int>(a.page);
                 const bool there = static_cast<uint32_t>(id) < static_cast<uint32_t>(a.pages);
                 // (a cache has fewer than 2^32 rows)
-                const uint32_t row = there ? (static_cast<uint32_t>(id) * static_cast<uint32_t>(a.Hkv) + s_seg.h) * page +
+                const uint32_t row = there ? (static_cast<uint32_t>(id) * static_cast<uint32_t>(a.Hkv) + s_seg[turn].h) * page +
                                                  (t_next - page_at(t_next) * page)
                                            : 0;
                 t_next += kWarps * kTB;
-                id = page_of(t_next);
                 const uint32_t at = ring_at + stage * S::kStageBytes;
                 constexpr int kChunks = kRB / 16;
                 const unsigned all = __ballot_sync(0xffffffffu, there);
@@ -339,26 +386,21 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
             kvq_commit();
         };
 #pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) bring(i);
+        for (int i = 0; i < kStages - 1; ++i) {
+            id = ids[i];
+            bring(i);
+        }
+        id = ids[kStages - 1];
         // -- q: a row a warp for its scale and sums, then the products' operands --
-        if (key1 > key0) {
-            constexpr int kRows = kRT / kWarps;  // of a warp
-            float v[kRows][E];
+        {
 #pragma unroll
             for (int k = 0; k < kRows; ++k) {
-                const int r = k * kWarps + warp;
-#pragma unroll
-                for (int i = 0; i < E; ++i) v[k][i] = 0.0f;
-                if (r < s.rows) kvq_row<E>(a.q, a.type, q_row(s, r) * D + lane * E, v[k]);
-            }
-#pragma unroll
-            for (int k = 0; k < kRows; ++k) {
-                const int r = k * kWarps + warp;
+                const int qr = k * kWarps + warp;
                 float top = 0.0f, sum = 0.0f;
 #pragma unroll
                 for (int i = 0; i < E; ++i) {
-                    top = fabsf(v[k][i]) < INFINITY ? fmaxf(top, fabsf(v[k][i])) : INFINITY;
-                    sum += v[k][i];
+                    top = fabsf(q[k][i]) < INFINITY ? fmaxf(top, fabsf(q[k][i])) : INFINITY;
+                    sum += q[k][i];
                 }
 #pragma unroll
                 for (int d = 16; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
@@ -369,10 +411,11 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
                 const bool bad = top >= kKvqLargestQ, none = top == 0.0f;
                 const float up = bad || none ? 1.0f : pow2i(ex);
                 // s_f * (s acc + b qs) is the score in base 2, acc of the scaled q and the operands
-                if (lane == 0) s_f[r] = bad ? __int_as_float(0x7fc00000) : p.scale2 * S::kUnit / up;
-                if (lane % (kGroup / E) == 0) s_qs[lane / (kGroup / E) * kRT + r] = sum * up * (1.0f / S::kUnit);
+                if (lane == 1) s_l[qr] = p.scale2 / up;  // (until the drafts are done)
+                if (lane == 0) s_f[qr] = bad ? __int_as_float(0x7fc00000) : p.scale2 * S::kUnit / up;
+                if (lane % (kGroup / E) == 0) s_qs[lane / (kGroup / E) * kRT + qr] = sum * up * (1.0f / S::kUnit);
 #pragma unroll
-                for (int i = 0; i < E; ++i) s_qf[r * (D + 4) + lane * E + i] = v[k][i] * up;
+                for (int i = 0; i < E; ++i) s_qf[qr * (D + 4) + lane * E + i] = q[k][i] * up;
             }
             __syncthreads();
 #pragma unroll 2
@@ -394,7 +437,63 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
                     to[kNT * 32] = make_uint2(kvq_half2(v0 - h0.x, v1 - h0.y), kvq_half2(v2 - h1.x, v3 - h1.y));
                 }
             }
-            __syncthreads();
+        }
+        // -- the drafts --
+        float d_m = -INFINITY, d_l = 0.0f, d_o[kE];
+#pragma unroll
+        for (int i = 0; i < kE; ++i) d_o[i] = 0.0f;
+        if (d1 > d0) {
+            float qv[kE];
+#pragma unroll
+            for (int i = 0; i < kE; ++i) qv[i] = s_qf[r * (D + 4) + ln * kE + i];
+            const float f = s_f[r] == s_f[r] ? s_l[r] : __int_as_float(0x7fc00000);
+            for (int w0 = d0;;) {
+                float sc[kBatch], top = d_m;
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    sc[k] = 0.0f;
+                    if (d_at[k] >= 0)
+#pragma unroll
+                        for (int i = 0; i < kE; ++i) sc[k] = fmaf(qv[i], d_k[k][i], sc[k]);
+                }
+#pragma unroll
+                for (int d = kL / 2; d >= 1; d >>= 1)
+#pragma unroll
+                    for (int k = 0; k < kBatch; ++k) sc[k] += __shfl_xor_sync(0xffffffffu, sc[k], d);
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    sc[k] = d_at[k] < 0 ? -INFINITY : sc[k] * f;
+                    top = fmaxf(top, sc[k]);
+                }
+                const float ref = top == -INFINITY ? 0.0f : top, corr = exp2f(d_m - ref);
+                d_m = top;
+                d_l *= corr;
+#pragma unroll
+                for (int i = 0; i < kE; ++i) d_o[i] *= corr;
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    if (d_at[k] < 0) continue;
+                    const float w = exp2f(sc[k] - ref);
+                    d_l += w;
+#pragma unroll
+                    for (int i = 0; i < kE; ++i) d_o[i] = fmaf(w, d_v[k][i], d_o[i]);
+                }
+                while (!__any_sync(0xffffffffu, seen != 0) && w0 < d1) seen = word(w0 += 64);
+                if (w0 >= d1) break;
+                ask(w0);
+            }
+        }
+        if constexpr (S::kPark > 0) {
+#pragma unroll
+            for (int i = 0; i < kE; ++i) s_park[r * D + ln * kE + i] = d_o[i];
+            if (ln == 0) s_park[kRT * D + 2 * r] = d_m, s_park[kRT * D + 2 * r + 1] = d_l;
+        }
+        __syncthreads();
+        // the next stretch, whose numbers come while the blocks go by
+        if (tid == kThreads - 32) {
+            Line line = s_line;
+            s_more = line.next(p, s_seg[turn ^ 1]);
+            s_next = line;
         }
         // -- the warp's blocks --
         float o[kTiles][kNT][4];             // columns (8 or 4 a lane of a group, two a tile) x rows 2 quad, + 1
@@ -418,6 +517,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
             kvq_wait<kStages - 2>();
             __syncwarp();  // every lane's copies have come, and the last block's place is free
             bring(stage == 0 ? kStages - 1 : stage - 1);
+            id = page_of(t_next);
             const unsigned char *K = ring + stage * S::kStageBytes, *V = K + kTB * kRB, *Kf = V + kTB * kRB,
                                 *Vf = Kf + kTB * kFB;
             // the factors, a token a lane; V's scales times a power of two that brings the
@@ -759,34 +859,33 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
                 }
             }
         }
-        // -- kL lanes a row: the warps' sums, the drafts, the result --
-        s = s_seg;
-        constexpr int kL = S::kL, kE = S::kE;
-        const int r = warp * (32 / kL) + lane / kL, ln = lane % kL;
-        const bool mine = r < s.rows;
-        const int64_t row = q_row(s, mine ? r : 0), n = static_cast<int64_t>(s.req.n0) + (s.r0 + (mine ? r : 0)) / p.G;
-        const int d0 = (max(s.t0, s.ctiles) - s.ctiles) * kKvqTile, d1 = min(s.req.T, (s.t1 - s.ctiles) * kKvqTile);
-        const uint64_t *mask = a.mask + n * a.words;
-        auto word = [&](int w0) {  // drafts w0 .. w0 + 63 that the row sees (kKvqTile is a multiple of 64)
-            uint64_t seen = mine && w0 < d1 ? mask[w0 >> 6] : 0;
-            if (d1 - w0 < 64) seen &= (1ull << max(d1 - w0, 0)) - 1;
-            return seen;
-        };
-        float qv[kE];
-        uint64_t seen = word(d0);  // (on its way while the warps meet, as q is)
-        if (d1 > d0 && mine) kvq_row<kE>(a.q, a.type, row * D + ln * kE, qv);
+        // -- kL lanes a row: the warps' sums, the drafts', the result --
+        s = s_seg[turn];
         __syncthreads();
-        float M = -INFINITY, L = 0.0f, v[kE];
+        float M, L, v[kE];
+        if constexpr (S::kPark > 0) {
 #pragma unroll
-        for (int i = 0; i < kE; ++i) v[i] = 0.0f;
+            for (int i = 0; i < kE; ++i) v[i] = s_park[r * D + ln * kE + i];
+            M = s_park[kRT * D + 2 * r], L = s_park[kRT * D + 2 * r + 1];
+        } else {
+#pragma unroll
+            for (int i = 0; i < kE; ++i) v[i] = d_o[i];
+            M = d_m, L = d_l;
+        }
         if (cached) {
             static_assert(kWarps == 8 && kL >= 8);
             const float mw = s_m[(ln & 7) * kRT + r], lw = s_l[(ln & 7) * kRT + r];
-            M = mw;
+            float top = mw;
 #pragma unroll
-            for (int d = 1; d < 8; d <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+            for (int d = 1; d < 8; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            top = fmaxf(top, M);
             // (no maximum, but a weight: a NaN, which stays)
-            const float fw = lw == 0.0f ? 0.0f : mw == -INFINITY ? 1.0f : exp2f(mw - M);
+            const float fw = lw == 0.0f ? 0.0f : mw == -INFINITY ? 1.0f : exp2f(mw - top);
+            const float fd = L == 0.0f ? 0.0f : M == -INFINITY ? 1.0f : exp2f(M - top);
+            M = top;
+            L = L == 0.0f ? 0.0f : L * fd;
+#pragma unroll
+            for (int i = 0; i < kE; ++i) v[i] = fd == 0.0f ? 0.0f : v[i] * fd;
 #pragma unroll
             for (int u = 0; u < kWarps; ++u) {
                 const float f = __shfl_sync(0xffffffffu, fw, u, kL), lu = __shfl_sync(0xffffffffu, lw, u, kL);
@@ -801,62 +900,8 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
                 }
             }
         }
-        if (d1 > d0) {
-            bool bad = false;
-#pragma unroll
-            for (int i = 0; i < kE; ++i) bad = bad || (mine && !(fabsf(qv[i]) < kKvqLargestQ));
-#pragma unroll
-            for (int d = 1; d < kL; d <<= 1) bad = __shfl_xor_sync(0xffffffffu, bad, d) || bad;
-            const int64_t base = (static_cast<int64_t>(s.h) * a.drafts + s.req.n0) * D + ln * kE;
-            for (int w0 = d0; w0 < d1; w0 += 64) {
-                if (w0 > d0) seen = word(w0);
-                while (__any_sync(0xffffffffu, seen != 0)) {
-                    constexpr int kBatch = kE > 8 ? 2 : 4;
-                    int64_t at[kBatch];
-                    float kv[kBatch][kE], vv[kBatch][kE], sc[kBatch];
-#pragma unroll
-                    for (int k = 0; k < kBatch; ++k) {
-                        at[k] = seen ? base + static_cast<int64_t>(w0 + __ffsll(static_cast<long long>(seen)) - 1) * D : -1;
-                        seen &= seen - 1;
-                        if (at[k] < 0) continue;
-                        kvq_row<kE>(a.Kd, a.type, at[k], kv[k]);
-                        kvq_row<kE>(a.Vd, a.type, at[k], vv[k]);
-                    }
-#pragma unroll
-                    for (int k = 0; k < kBatch; ++k) {
-                        sc[k] = 0.0f;
-                        if (at[k] >= 0)
-#pragma unroll
-                            for (int i = 0; i < kE; ++i) sc[k] = fmaf(qv[i], kv[k][i], sc[k]);
-                    }
-#pragma unroll
-                    for (int d = kL / 2; d >= 1; d >>= 1)
-#pragma unroll
-                        for (int k = 0; k < kBatch; ++k) sc[k] += __shfl_xor_sync(0xffffffffu, sc[k], d);
-                    float top = M;
-#pragma unroll
-                    for (int k = 0; k < kBatch; ++k) {
-                        sc[k] = at[k] < 0 ? -INFINITY : bad ? __int_as_float(0x7fc00000) : sc[k] * p.scale2;
-                        top = fmaxf(top, sc[k]);
-                    }
-                    const float ref = top == -INFINITY ? 0.0f : top, f = exp2f(M - ref);
-                    M = top;
-                    L *= f;
-#pragma unroll
-                    for (int i = 0; i < kE; ++i) v[i] *= f;
-#pragma unroll
-                    for (int k = 0; k < kBatch; ++k) {
-                        if (at[k] < 0) continue;
-                        const float w = exp2f(sc[k] - ref);
-                        L += w;
-#pragma unroll
-                        for (int i = 0; i < kE; ++i) v[i] = fmaf(w, vv[k][i], v[i]);
-                    }
-                }
-            }
-        }
         if (s.t0 == 0 && s.t1 == s.tiles) {
-            kvq_finish<kE>(a, row * D + ln * kE, v, L, mine);
+            kvq_finish<kE>(a, q_row(s, mine ? r : 0) * D + ln * kE, v, L, mine);
         } else if (mine) {
             const int64_t slot = (static_cast<int64_t>(2) * blockIdx.x + (s.t0 == 0)) * kRT + r;
             float *po = p.part_o + slot * D + ln * kE;
@@ -864,7 +909,10 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
             for (int i = 0; i < kE; i += 2) *reinterpret_cast<float2 *>(po + i) = make_float2(v[i], v[i + 1]);
             if (ln == 0) p.part_ml[slot] = make_float2(M, L);
         }
-        if (tid == 0) s_line.leave_entry(p, s, blockIdx.x, left);
+        if (tid == 0) {
+            s_line.leave_entry(p, s, blockIdx.x, left);
+            s_line = s_next;
+        }
         __syncthreads();  // the rings and the rows' factors are free
     }
     if (tid == 0) s_line.end_entries(p, blockIdx.x, left);
@@ -885,9 +933,9 @@ cudaError_t kvq_go(KvqAttnArgs x, void *ws, bool early, bool pdl, cudaStream_t s
     const cudaError_t e = launch_kernel(kvq_attn_kernel<S>, dim3(C), dim3(S::kThreads), S::kSmem, stream, early, x);
     if (e != cudaSuccess) return e;
     switch (x.p.a.y_type) {
-    case ABG_SB_F32: return launch_join<float, S::D, S::kRT, false>(x.p, C, pdl, stream);
-    case ABG_SB_BF16: return launch_join<__nv_bfloat16, S::D, S::kRT, false>(x.p, C, pdl, stream);
-    default: return launch_join<__half, S::D, S::kRT, false>(x.p, C, pdl, stream);
+    case ABG_SB_F32: return launch_join<float, S::D, S::kRT, false, kKvqJoin>(x.p, C, pdl, stream);
+    case ABG_SB_BF16: return launch_join<__nv_bfloat16, S::D, S::kRT, false, kKvqJoin>(x.p, C, pdl, stream);
+    default: return launch_join<__half, S::D, S::kRT, false, kKvqJoin>(x.p, C, pdl, stream);
     }
 }
 

@@ -303,7 +303,7 @@ __device__ __forceinline__ int64_t attn_piece_at(int64_t piece, int r, int q) {
 // meet in shared memory.  Latency bounds it: the pieces of 152 blocks, of 96 rows
 // of 128 columns, take 11.7 us on their own out of memory, of 256 rows 13.9; after
 // the first launch, out of the second-level cache, 3-5.
-template <typename T, int D, int kRT, bool kByQuad, int kWarps>
+template <typename T, int D, int kRT, bool kByQuad, int kWarps, int kBatch>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnArgs p) {
     constexpr int E = D / 32, kRows = 8 / kWarps;
     __shared__ __align__(16) float s_o[8][D];
@@ -323,7 +323,6 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
         const int r = r0 + warp / kWarps;
         float m = -INFINITY, L = 0.0f, o[E] = {};
         if (r < s.rows) {
-            constexpr int kBatch = 4;
             for (int k0 = sub; k0 < pieces; k0 += kBatch * kWarps) {
                 float2 ml[kBatch];
                 float v[kBatch][E];
@@ -399,8 +398,8 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
 }
 
 // The joining launch, early (it waits for the first).  Few units are many
-// pieces each: more warps a row.
-template <typename T, int D, int kRT, bool kByQuad>
+// pieces each: more warps a row.  kBatch: pieces that a warp loads at a time.
+template <typename T, int D, int kRT, bool kByQuad, int kBatch = 4>
 cudaError_t launch_join(const AttnArgs &p, int C, bool pdl, cudaStream_t stream) {
     const int64_t units = p.per_head ? p.units : C, span_rows = p.a.max_span * p.G;
     const int64_t rows = std::min<int64_t>(kRT, span_rows);
@@ -409,7 +408,7 @@ cudaError_t launch_join(const AttnArgs &p, int C, bool pdl, cudaStream_t stream)
     auto go = [&](auto w) {
         constexpr int kWarps = decltype(w)::value;
         const dim3 grid(static_cast<unsigned>(units), static_cast<unsigned>((rows * kWarps + 7) / 8));
-        return launch_kernel(attn_join_kernel<T, D, kRT, kByQuad, kWarps>, grid, dim3(256), 0, stream, pdl, p);
+        return launch_kernel(attn_join_kernel<T, D, kRT, kByQuad, kWarps, kBatch>, grid, dim3(256), 0, stream, pdl, p);
     };
     return pieces > 32  ? go(std::integral_constant<int, 8>{})
            : pieces > 6 ? go(std::integral_constant<int, 4>{})
