@@ -24,34 +24,48 @@ constexpr float kLargestHalf = 65504.0f;
 // V*l .. V*l+V-1 of a head (V = D/32) and the ones D/2 further on.  A group is then
 // in 4, 8 or 16 lanes' chunks of one half of the columns, or (64 columns a row, one
 // group) in all 16 lanes' both chunks, and its least and largest value meet by
-// shuffles; the lanes then quantise and pack their own columns.
+// shuffles; the lanes then quantise and pack their own columns.  Instructions bound it
+// (3700 a token of 16 + 4 + 4 heads, of which kv_put's steps are 2500): 8191 such rows of
+// 128 columns, f32 to 4 bits, with q in bf16, in 43 us (139 MB, 3.2 TB/s; kv_put to bf16
+// 33).  Three blocks an SM, in 80 registers, spill and take 50.
 constexpr int kPutWarps = 8;
 
-// V codes of `bits` bits, low first, to p (V*bits/8 bytes, aligned to as many).
-template <int V>
-__device__ __forceinline__ void store_codes(unsigned char *p, const uint32_t (&code)[V], int bits) {
-    if (bits == 4) {
-        uint32_t w = 0;
+// Least and largest; a NaN stays.
+__device__ __forceinline__ float least(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float largest(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// N codes of kBits bits, low first, in a word, of whole numbers x + 1.5 * 2^23: their bits
+// are 0x4b400000 + x.
+template <int kBits, int N>
+__device__ __forceinline__ uint32_t code_word(const float *x) {
+    uint32_t w = 0, over = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) w |= code[i] << (4 * i);
-        if constexpr (V == 2) {
-            *p = static_cast<unsigned char>(w);
-        } else if constexpr (V == 4) {
-            *reinterpret_cast<uint16_t *>(p) = static_cast<uint16_t>(w);
-        } else {
-            *reinterpret_cast<uint32_t *>(p) = w;
-        }
+    for (int i = 0; i < N; ++i) {
+        w += __float_as_uint(x[i]) << (kBits * i);
+        over += 0x4b400000u << (kBits * i);
+    }
+    return w - over;
+}
+// V codes to p (V*kBits/8 bytes, aligned to as many).
+template <int kBits, int V>
+__device__ __forceinline__ void store_codes(unsigned char *p, const float (&x)[V]) {
+    constexpr int kBytes = V * kBits / 8;
+    if constexpr (kBytes == 1) {
+        *p = static_cast<unsigned char>(code_word<kBits, V>(x));
+    } else if constexpr (kBytes == 2) {
+        *reinterpret_cast<uint16_t *>(p) = static_cast<uint16_t>(code_word<kBits, V>(x));
+    } else if constexpr (kBytes == 4) {
+        *reinterpret_cast<uint32_t *>(p) = code_word<kBits, V>(x);
     } else {
-        uint32_t w[(V + 3) / 4] = {};
-#pragma unroll
-        for (int i = 0; i < V; ++i) w[i / 4] |= code[i] << (8 * (i % 4));
-        if constexpr (V == 2) {
-            *reinterpret_cast<uint16_t *>(p) = static_cast<uint16_t>(w[0]);
-        } else if constexpr (V == 4) {
-            *reinterpret_cast<uint32_t *>(p) = w[0];
-        } else {
-            *reinterpret_cast<uint2 *>(p) = make_uint2(w[0], w[1]);
-        }
+        *reinterpret_cast<uint2 *>(p) = make_uint2(code_word<kBits, V / 2>(x), code_word<kBits, V / 2>(x + V / 2));
     }
 }
 
@@ -73,14 +87,11 @@ __device__ __forceinline__ void put_quantised(const float (&u)[R][2][D / 32], in
             float &a = lo[2 * r + h], &b = hi[2 * r + h];
             a = INFINITY, b = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                a = fminf(a, u[r][h][i]);
-                b = fabsf(u[r][h][i]) <= kLargestHalf ? fmaxf(b, u[r][h][i]) : INFINITY;  // (a NaN too)
-            }
+            for (int i = 0; i < V; ++i) a = least(a, u[r][h][i]), b = largest(b, u[r][h][i]);
         }
         if (joined) {
-            lo[2 * r] = lo[2 * r + 1] = fminf(lo[2 * r], lo[2 * r + 1]);
-            hi[2 * r] = hi[2 * r + 1] = fmaxf(hi[2 * r], hi[2 * r + 1]);
+            lo[2 * r] = lo[2 * r + 1] = least(lo[2 * r], lo[2 * r + 1]);
+            hi[2 * r] = hi[2 * r + 1] = largest(hi[2 * r], hi[2 * r + 1]);
         }
     }
     // a group is at least C lanes' chunks: half of the chunks go to the other half of
@@ -93,16 +104,16 @@ __device__ __forceinline__ void put_quantised(const float (&u)[R][2][D / 32], in
         for (int i = 0; i < d; ++i) {
             const float a = __shfl_xor_sync(0xffffffffu, up ? lo[i] : lo[i + d], d);
             const float b = __shfl_xor_sync(0xffffffffu, up ? hi[i] : hi[i + d], d);
-            lo[i] = fminf(up ? lo[i + d] : lo[i], a);
-            hi[i] = fmaxf(up ? hi[i + d] : hi[i], b);
+            lo[i] = least(up ? lo[i + d] : lo[i], a);
+            hi[i] = largest(up ? hi[i + d] : hi[i], b);
         }
     }
     for (int d = C; d < lanes; d *= 2) {
-        lo[0] = fminf(lo[0], __shfl_xor_sync(0xffffffffu, lo[0], d));
-        hi[0] = fmaxf(hi[0], __shfl_xor_sync(0xffffffffu, hi[0], d));
+        lo[0] = least(lo[0], __shfl_xor_sync(0xffffffffu, lo[0], d));
+        hi[0] = largest(hi[0], __shfl_xor_sync(0xffffffffu, hi[0], d));
     }
     const float levels = bits == 4 ? 15.0f : 255.0f;
-    const bool bad = hi[0] == INFINITY;
+    const bool bad = !(hi[0] <= kLargestHalf && lo[0] >= -kLargestHalf);
     const __half nan = __ushort_as_half(0x7fff);
     const __half2 own = bad ? __halves2half2(nan, nan)
                             : __halves2half2(__float2half_rn(__fdiv_rn(__fsub_rn(hi[0], lo[0]), levels)), __float2half_rn(lo[0]));
@@ -118,16 +129,22 @@ __device__ __forceinline__ void put_quantised(const float (&u)[R][2][D / 32], in
             const uint32_t pair = __shfl_sync(0xffffffffu, own_pair, from);
             const float inv = __shfl_sync(0xffffffffu, own_inv, from);
             const float b = __half2float(__ushort_as_half(static_cast<unsigned short>(pair >> 16)));
-            uint32_t code[V];
+            const float2 back = make_float2(-b, -b), times = make_float2(inv, inv), whole = make_float2(12582912.0f, 12582912.0f);
+            float x[V];
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                // clamped, then rounded to a whole number by 1.5 * 2^23 (a NaN: 0, as 0 * NaN is clamped to 0)
-                const float x = fminf(fmaxf(__fmul_rn(__fsub_rn(u[r][h][i], b), inv), 0.0f), levels);
-                code[i] = __float_as_uint(__fadd_rn(x, 12582912.0f)) & 255u;
+            for (int i = 0; i < V; i += 2) {
+                // clamped (a NaN to 0), then rounded to a whole number by 1.5 * 2^23
+                const float2 y = mul2(add2(make_float2(u[r][h][i], u[r][h][i + 1]), back), times);
+                const float2 z = add2(make_float2(fminf(fmaxf(y.x, 0.0f), levels), fminf(fmaxf(y.y, 0.0f), levels)), whole);
+                x[i] = z.x, x[i + 1] = z.y;
             }
             const int col = h * (D / 2) + V * l;
             if (rows[r] >= 0) {
-                store_codes<V>(codes + col * bits / 8, code, bits);
+                if (bits == 4) {
+                    store_codes<4>(codes + col / 2, x);
+                } else {
+                    store_codes<8>(codes + col, x);
+                }
                 if (l % lanes == 0 && !(joined && h)) pairs[col / group] = pair;
             }
         }
@@ -135,7 +152,7 @@ __device__ __forceinline__ void put_quantised(const float (&u)[R][2][D / 32], in
 }
 
 template <typename S, typename T, int D>
-__global__ void __launch_bounds__(32 * kPutWarps, D == 256 ? 2 : 3) kvq_put_kernel(
+__global__ void __launch_bounds__(32 * kPutWarps, 2) kvq_put_kernel(
     const __grid_constant__ abg_kvq_put_args a, int groups) {
     using P = Put<D>;
     constexpr int V = P::V, kSteps = P::kSteps;
@@ -248,10 +265,13 @@ __global__ void __launch_bounds__(32 * kPutWarps, D == 256 ? 2 : 3) kvq_put_kern
 }
 
 // ------------------------------------------------------------- kvq_get -----
-// A block a tile of tokens, whose rows it finds once; then a thread eight columns at
-// a time, one or two words and a pair in, 16 or 32 bytes out, the columns first, then
-// heads, K and V, tokens, so that a warp reads and writes whole rows.  Four such
-// places at a time a thread, so that their words are on their way together.
+// A thread eight columns of a key or value head, for token after token: one or two words
+// and a pair in, 16 or 32 bytes out, so that all but a token's row is known before the
+// first.  A block's threads have a token's heads side by side, and as many tokens as there
+// is room for; four of a thread's tokens at a time, so that their words are on their way
+// together.  Instructions bound it: 32768 tokens of 4 heads of 128, 4 bits to bf16, in
+// 17.6 us (86 MB, 4.9 TB/s); with every place found on its own 24.4, with the codes made
+// floats by conversions and 64-bit divisions 40.6.
 constexpr int kGetThreads = 256, kGetEach = 4, kGetTokens = 128;
 
 // Byte k of w as a float (0x4b000000 + c is 2^23 + c).
@@ -260,56 +280,59 @@ __device__ __forceinline__ float byte_value(uint32_t w) {
     return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 + k)) - 8388608.0f;
 }
 
+// per: places of eight columns of a token (key or value, head, columns); side: tokens side
+// by side in a block; tokens: of a block
 template <typename T, int kBits>
-__global__ void __launch_bounds__(kGetThreads) kvq_get_kernel(const __grid_constant__ abg_kvq_get_args a, int kinds,
-                                                              int log_cols, int tokens) {
-    __shared__ int64_t s_row[kGetTokens];  // of head 0; -1: none
-    const int tid = threadIdx.x, Hkv = static_cast<int>(a.c.Hkv);
-    const int per = kinds * Hkv << log_cols, log_pair = a.c.group == 32 ? 2 : 3;
+__global__ void __launch_bounds__(kGetThreads) kvq_get_kernel(const __grid_constant__ abg_kvq_get_args a, int log_cols,
+                                                              int per, int side, int tokens) {
+    __shared__ uint32_t s_row[kGetTokens];  // of head 0 (a cache has fewer than 2^32 rows); ~0: none
+    const int tid = threadIdx.x, Hkv = static_cast<int>(a.c.Hkv), log_pair = a.c.group == 32 ? 2 : 3;
     const int64_t n0 = static_cast<int64_t>(blockIdx.x) * tokens;
-    const int here = static_cast<int>(min(static_cast<int64_t>(tokens), a.N - n0)), items = here * per;
+    const int here = static_cast<int>(min(static_cast<int64_t>(tokens), a.N - n0));
+    int first = 0, place = blockIdx.y * kGetThreads + tid;  // the thread's first token, and its place in a token
+    if (per < kGetThreads) first = tid / per, place = tid - first * per;
+    const int col = place & ((1 << log_cols) - 1), kh = place >> log_cols;
+    const bool value = kh >= Hkv || !a.k;
+    const int h = kh >= Hkv ? kh - Hkv : kh;
+    const int64_t at0 = ((h * a.c.page) << log_cols) + col;
+    const uint32_t *codes = static_cast<const uint32_t *>(value ? a.c.Vc : a.c.Kc) + at0 * (kBits / 4);
+    const __half2 *pairs = static_cast<const __half2 *>(value ? a.c.Vs : a.c.Ks) + (at0 >> log_pair);
+    const int log_words = log_cols + (kBits == 8), log_pairs = log_cols - log_pair;
+    const int64_t step = value ? a.v_row : a.k_row;
+    T *to = static_cast<T *>(value ? a.v : a.k) + (n0 + first) * step + h * (value ? a.v_head : a.k_head) + 8 * col;
     grid_dep_wait();  // (and nothing after this one starts early, as kvq_put)
     if (tid < here) {
         const int64_t slot = a.slots ? a.slots[n0 + tid] : n0 + tid;
-        int64_t row = -1;
+        uint32_t row = ~0u;
         if (slot >= 0 && slot < a.c.pages * a.c.page) {
             const int64_t page = div_up_to_64(slot, a.c.page);
-            row = page * Hkv * a.c.page + (slot - page * a.c.page);
+            row = static_cast<uint32_t>(page * Hkv * a.c.page + (slot - page * a.c.page));
         }
         s_row[tid] = row;
     }
     __syncthreads();
-    for (int i0 = tid; i0 < items; i0 += kGetEach * kGetThreads) {
-        int n[kGetEach], h[kGetEach], col[kGetEach];
-        bool value[kGetEach];
+    if (first >= side || place >= per) return;
+    for (int n = first; n < here; n += kGetEach * side) {
         uint2 w[kGetEach];
-        float2 f[kGetEach];
+        __half2 f[kGetEach];
 #pragma unroll
         for (int k = 0; k < kGetEach; ++k) {
-            const int i = i0 + k * kGetThreads;
-            n[k] = -1;
             w[k] = make_uint2(0, 0);
-            f[k] = make_float2(0.0f, 0.0f);
-            if (i >= items) continue;
-            n[k] = static_cast<int>(static_cast<uint32_t>(i) / static_cast<uint32_t>(per));
-            const int rest = i - n[k] * per, kh = rest >> log_cols;
-            col[k] = rest & ((1 << log_cols) - 1);
-            value[k] = kh >= Hkv || !a.k;
-            h[k] = kh >= Hkv ? kh - Hkv : kh;
-            const int64_t row = s_row[n[k]];
-            if (row < 0) continue;
-            const int64_t at = ((row + h[k] * a.c.page) << log_cols) + col[k];
-            const void *codes = value[k] ? a.c.Vc : a.c.Kc;
+            f[k] = __float2half2_rn(0.0f);
+            if (n + k * side >= here) continue;
+            const uint32_t row = s_row[n + k * side];
+            if (row == ~0u) continue;
+            const uint32_t *from = codes + (static_cast<uint64_t>(row) << log_words);
             if constexpr (kBits == 4) {
-                w[k].x = static_cast<const uint32_t *>(codes)[at];
+                w[k].x = *from;
             } else {
-                w[k] = static_cast<const uint2 *>(codes)[at];
+                w[k] = *reinterpret_cast<const uint2 *>(from);
             }
-            f[k] = __half22float2(static_cast<const __half2 *>(value[k] ? a.c.Vs : a.c.Ks)[at >> log_pair]);
+            f[k] = pairs[static_cast<uint64_t>(row) << log_pairs];
         }
 #pragma unroll
         for (int k = 0; k < kGetEach; ++k) {
-            if (n[k] < 0) continue;
+            if (n + k * side >= here) continue;
             float v[8];
             if constexpr (kBits == 4) {
                 const uint32_t even = w[k].x & 0x0f0f0f0fu, odd = w[k].x >> 4 & 0x0f0f0f0fu;
@@ -320,11 +343,11 @@ __global__ void __launch_bounds__(kGetThreads) kvq_get_kernel(const __grid_const
                 v[3] = byte_value<3>(w[k].x), v[4] = byte_value<0>(w[k].y), v[5] = byte_value<1>(w[k].y);
                 v[6] = byte_value<2>(w[k].y), v[7] = byte_value<3>(w[k].y);
             }
+            const float2 sb = __half22float2(f[k]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = fmaf(f[k].x, v[i], f[k].y);  // (the product is exact: 11 and 8 bits)
-            T *to = static_cast<T *>(value[k] ? a.v : a.k) + (n0 + n[k]) * (value[k] ? a.v_row : a.k_row) +
-                    h[k] * (value[k] ? a.v_head : a.k_head) + 8 * col[k];
+            for (int i = 0; i < 8; ++i) v[i] = fmaf(sb.x, v[i], sb.y);  // (the product is exact: 11 and 8 bits)
             store_e<T, 8>(to, v);
+            to += side * step;
         }
     }
 }
@@ -356,12 +379,14 @@ template <typename T, int kBits>
 cudaError_t get_bits(const abg_kvq_get_args &a, bool pdl, cudaStream_t stream) {
     const int kinds = (a.k != nullptr) + (a.v != nullptr);
     const int log_cols = a.c.D == 64 ? 3 : a.c.D == 128 ? 4 : 5;
-    const int64_t per = kinds * a.c.Hkv << log_cols;
-    // eight places a thread, as long as there are four blocks an SM
-    const int64_t tokens = std::max<int64_t>(
-        1, std::min<int64_t>({kGetTokens, 2 * kGetEach * kGetThreads / per, a.N / (4ll * sm_count())}));
-    return launch_kernel(kvq_get_kernel<T, kBits>, dim3(static_cast<unsigned>((a.N + tokens - 1) / tokens)),
-                         dim3(kGetThreads), 0, stream, pdl && !capturing(stream), a, kinds, log_cols,
+    const int per = kinds * static_cast<int>(a.c.Hkv) << log_cols;
+    const int side = std::min(std::max(1, kGetThreads / per), kGetTokens / 8), parts = (per + kGetThreads - 1) / kGetThreads;
+    // eight tokens a thread, as long as there are eight blocks an SM
+    const int64_t each = std::max<int64_t>(1, std::min<int64_t>(8, a.N * parts / side / (8ll * sm_count())));
+    const int64_t tokens = each * side;
+    return launch_kernel(kvq_get_kernel<T, kBits>,
+                         dim3(static_cast<unsigned>((a.N + tokens - 1) / tokens), static_cast<unsigned>(parts)),
+                         dim3(kGetThreads), 0, stream, pdl && !capturing(stream), a, log_cols, per, side,
                          static_cast<int>(tokens));
 }
 template <typename T>

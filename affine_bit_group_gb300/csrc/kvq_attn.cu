@@ -44,6 +44,8 @@ cudaError_t launch_kvq_attn(const abg_kvq_attn_args &a, void *ws, bool pdl, cuda
     x.p.scale2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(a.c.D)));
     x.Kc = static_cast<const unsigned char *>(a.c.Kc), x.Vc = static_cast<const unsigned char *>(a.c.Vc);
     x.Ks = static_cast<const unsigned char *>(a.c.Ks), x.Vs = static_cast<const unsigned char *>(a.c.Vs);
+    // (without pages nothing is read, but a copy of no bytes still has an address)
+    if (a.c.pages == 0) x.Kc = x.Vc = x.Ks = x.Vs = static_cast<const unsigned char *>(a.q);
     kvq_page_division(x, static_cast<uint32_t>(a.c.page));
     const bool early = pdl && !capturing(stream), split = a.type != ABG_SB_BF16;
     const int rt = kvq_row_tile(a.c.D, x.p.G * a.max_span), group = a.c.group;

@@ -727,7 +727,8 @@ typedef struct abg_kvq_cache {
  * group's range.  A group with a NaN or a magnitude above 65504 (f16's
  * largest) is held as NaN: scale and bias are 0x7fff, the codes 0.
  * The codes and factors are exact: they are the same on every run, and those of
- * these steps done one by one in any IEEE binary32 arithmetic.
+ * these steps done one by one in any IEEE binary32 arithmetic (of zeros of both
+ * signs -0 is the least).
  */
 typedef struct abg_kvq_put_args {
     const void *q, *k, *v;
@@ -768,7 +769,8 @@ abg_status abg_kvq_get(const abg_kvq_get_args *a, void *stream);
  * q, Kd and Vd of `type`, everything else as there.  One new token a request is
  * a span of 1.
  *   A page outside 0 .. pages-1 reads as zeros; a NaN in a K row that a query
- * sees makes its result NaN, one in a V row those columns' group.  A row of q
+ * sees makes its result NaN, one in a V row those columns' group (an infinite
+ * factor, which kvq_put never writes, may do so too).  A row of q
  * that holds a NaN or a magnitude of 2^100 or more gives NaN (0 where it sees no
  * token).  width*page is at most 2^31 - 1024.
  *   Sums, softmax statistics and the work split's partial results are f32.
