@@ -32,10 +32,20 @@
 // the weights P go from the one product's result to the other's operand by
 // movmatrix, in registers.
 //
-// Warps.  Every warp goes through blocks of 16 or 32 tokens of its own (every 8th, 10th
-// or 12th of the stretch), with a ring in shared memory that it fills by cp.async and
-// its own running maxima and sums: no barrier until the stretch's end, where the
-// warps' sums meet in shared memory, and the drafts are added, in f32, a row a warp.
+// Warps.  Every warp goes through blocks of 16 or 32 tokens of its own (every eighth of
+// the stretch), with a ring in shared memory that it fills by cp.async and its own
+// reference and sums: no barrier until the stretch's end, where the warps' sums meet in
+// shared memory.  The drafts are multiplied in f32, a few lanes a row, while the first
+// blocks are on their way, and what a stretch needs besides is asked for before its
+// copies, behind which it would wait.
+//
+// What bounds it.  64 requests of up to 16000 tokens, 16 heads over 4 of 128 columns, 4
+// bits, take 104 us for 441 MB (4.2 TB/s): copies alone take about 70, the rest without
+// copies about 75, with 600 instructions a warp for 32 tokens, half of them for taking the
+// codes apart, and no one of them that shortens the call by more than 6 us when it is left
+// out; launches, the joining and two beginnings and ends a block are 15 of it.  In 8 bits 48
+// requests of 9001 tokens of 256 columns take 69 us (354 MB, 5.1 TB/s), one f16 token over
+// 131071 28 us (75 MB), one over 2000 13 to 15 us, the latency of two launches.
 #pragma once
 
 #include "kv_rows.cuh"
@@ -73,8 +83,8 @@ struct KvqShape {
     static constexpr int D = D_, kBits = kBits_, kGroup = kGroup_;
     static constexpr int kNT = kNT_;                      // query rows, by 8
     static constexpr int kTerms = kSplit_ ? 2 : 1;        // f16 terms of q and of P
-    // two terms: codes as normal numbers around 0 (K's c - kMiddle, V's c - z), a block's
-    // products summed on their own; else codes as subnormal numbers, one sum
+    // two terms: codes as normal numbers around 0 (K's c - kMiddle, V's c - z), else as
+    // subnormal ones
     static constexpr bool kNormal = kSplit_;
     static constexpr float kMiddle = kNormal ? (kBits == 4 ? 8.0f : 128.0f) : 0.0f;
     static constexpr float kUnit = kNormal ? 1.0f : 16777216.0f;             // 1 / the operand's value of a code 1
@@ -86,9 +96,11 @@ struct KvqShape {
     static constexpr int kMT = kTB / 16;
     static constexpr int kSteps = D / 16;                 // products of 16 columns
     static constexpr int kWords = kGroup * kBits / 128;   // words of a group in a lane
-    // blocks an SM: what the registers leave room for, of which the sums take kNT * D / 4 a
-    // lane, and the ring
-    static constexpr int kBlocks = kNT * D / 4 <= 32 && kRB <= 64 ? 2 : 1;
+    // Blocks an SM.  The sums take kNT * D / 4 registers of a lane, and where these are 32 or
+    // 64, 8 warps of 255 registers do as much as 12 or 16 that spill (4 bits in groups of 32,
+    // 128 columns, 48 requests: one block 75.7 us, two 85.5, one of 12 warps 79.0; groups of
+    // 64, 64 requests: 104.9, 103.3, 102.9).
+    static constexpr int kBlocks = kNT * D / 4 <= 16 && kRB <= 64 ? 2 : 1;
     static constexpr int kWarps = 8, kThreads = 32 * kWarps;
     static constexpr int kL = kThreads / kRT, kE = D / kL;  // lanes of a row for drafts and result, columns of a lane
     static constexpr int kStageBytes = kTB * 2 * (kRB + kFB);
@@ -139,6 +151,12 @@ __device__ __forceinline__ void kvq_mma(float (&d)[4], uint32_t a0, uint32_t a1,
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y));
 }
+// d = a b
+__device__ __forceinline__ void kvq_mma0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint2 b) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b.x), "r"(b.y), "f"(0.0f));
+}
 __device__ __forceinline__ uint32_t kvq_transpose(uint32_t a) {
     uint32_t d;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
@@ -177,7 +195,8 @@ __device__ __forceinline__ int kvq_token(int i) { return (i >> 1) + 4 * (i & 1);
 
 // Which 16-byte place of a row of the ring a chunk lies in: the rows of one load in
 // different banks (counted over all 32 lanes of every load of both products: no
-// conflicts left, but for 8 bits in groups of 64 of a 64-column row, 24 for 16).
+// conflicts left, but for 8 bits in groups of 64 of a 64-column row, 24 for 16).  An XOR of
+// t's lowest three bits, so that the place of a sum of tokens is the XOR of theirs.
 template <typename S>
 __device__ __forceinline__ int kvq_swizzle(int t) {
     constexpr bool narrow = S::kGroup == 32 && S::kBits == 4;
@@ -499,7 +518,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
         float o[kTiles][kNT][4];             // columns (8 or 4 a lane of a group, two a tile) x rows 2 quad, + 1
         float l[kNT][2], m[kNT][2], bias[kG][kNT][2];
         int ev = 0;                          // the largest scale of V so far is below 2^(ev - 14)
-        float up = pow2i(28);                // 2^(28 - ev)
+        float up = pow2i(28), down = pow2i(-28) * S::kUnit;  // 2^(28 - ev), and back for the products' results
 #pragma unroll
         for (int i = 0; i < kTiles; ++i)
 #pragma unroll
@@ -534,18 +553,9 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
                     }
                 }
                 if (__any_sync(0xffffffffu, static_cast<int>(big >> 10) > ev)) {
-                    const int ev1 = max(ev, static_cast<int>(__reduce_max_sync(0xffffffffu, big) >> 10));
-                    const float down = pow2i(ev - ev1);
-                    ev = ev1;
+                    ev = max(ev, static_cast<int>(__reduce_max_sync(0xffffffffu, big) >> 10));
                     up = pow2i(28 - ev);
-                    if constexpr (!S::kNormal) {
-#pragma unroll
-                        for (int k = 0; k < kTiles; ++k)
-#pragma unroll
-                            for (int nt = 0; nt < kNT; ++nt)
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) o[k][nt][e] *= down;
-                    }
+                    down = pow2i(ev - 28) * S::kUnit;
                 }
                 if (lane < kTB) {
                     float2 kk[kG], vv[kG];
@@ -589,10 +599,6 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
             };
             // scores
             float sc[kMT][kNT][4];
-#pragma unroll
-            for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-                for (int nt = 0; nt < kNT; ++nt) sc[mt][nt][0] = sc[mt][nt][1] = sc[mt][nt][2] = sc[mt][nt][3] = 0.0f;
             float2 f2[kMT][2][2];  // of tokens tok and tok + 8, of two groups
 #pragma unroll
             for (int g = 0; g < kG; ++g) {
@@ -620,10 +626,6 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
                         }
                     }
                 float acc[kMT][kNT][4];
-#pragma unroll
-                for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-                    for (int nt = 0; nt < kNT; ++nt) acc[mt][nt][0] = acc[mt][nt][1] = acc[mt][nt][2] = acc[mt][nt][3] = 0.0f;
                 constexpr int kPerWord = kBits == 4 ? 2 : 1;
 #pragma unroll
                 for (int wi = 0; wi < S::kWords; ++wi)
@@ -646,8 +648,13 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
                             for (int nt = 0; nt < kNT; ++nt) {
                                 const uint2 b = s_q[((step * kTerms + term) * kNT + nt) * 32 + lane];
 #pragma unroll
-                                for (int mt = 0; mt < kMT; ++mt)
-                                    kvq_mma(acc[mt][nt], e[mt][0], e[mt][1], e[mt][2], e[mt][3], b);
+                                for (int mt = 0; mt < kMT; ++mt) {
+                                    if (wi == 0 && hh == 0 && term == 0) {
+                                        kvq_mma0(acc[mt][nt], e[mt][0], e[mt][1], e[mt][2], e[mt][3], b);
+                                    } else {
+                                        kvq_mma(acc[mt][nt], e[mt][0], e[mt][1], e[mt][2], e[mt][3], b);
+                                    }
+                                }
                             }
                     }
 #pragma unroll
@@ -735,18 +742,12 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
                     for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) factors(v_fac, 16 * mt + 8 * h + tok, g, f2[mt][h]);
-                constexpr int kPart = S::kNormal ? kGroup / 16 : 1;
-                float part[kPart][kNT][4];  // of the block
-                if constexpr (S::kNormal) {
-#pragma unroll
-                    for (int nt = 0; nt < kNT; ++nt) {
-#pragma unroll
-                        for (int i = 0; i < kPart; ++i) part[i][nt][0] = part[i][nt][1] = part[i][nt][2] = part[i][nt][3] = 0.0f;
-                    }
-                }
+                constexpr int kCols = kGroup / 8, kColWords = kCols * kBits > 32 ? kCols * kBits / 32 : 1;
+                uint2 b[kMT][kTerms][kNT];
+                uint32_t u[kMT][4][kColWords];
+                __half2 z[kMT][2];
 #pragma unroll
                 for (int mt = 0; mt < kMT; ++mt) {
-                    uint2 b[kTerms][kNT];
 #pragma unroll
                     for (int nt = 0; nt < kNT; ++nt) {
                         const float *w = sc[mt][nt];
@@ -758,68 +759,67 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
                             bias[g][nt][e & 1] = fmaf(w[e], f.y, bias[g][nt][e & 1]);
                         }
                         const uint32_t h0 = kvq_half2(v[0], v[1]), h1 = kvq_half2(v[2], v[3]);
-                        b[0][nt] = make_uint2(kvq_transpose(h0), kvq_transpose(h1));
+                        b[mt][0][nt] = make_uint2(kvq_transpose(h0), kvq_transpose(h1));
                         if constexpr (kTerms == 2) {
                             const float2 r0 = kvq_float2(h0), r1 = kvq_float2(h1);
-                            b[1][nt] = make_uint2(kvq_transpose(kvq_half2(v[0] - r0.x, v[1] - r0.y)),
-                                                  kvq_transpose(kvq_half2(v[2] - r1.x, v[3] - r1.y)));
+                            b[mt][1][nt] = make_uint2(kvq_transpose(kvq_half2(v[0] - r0.x, v[1] - r0.y)),
+                                                      kvq_transpose(kvq_half2(v[2] - r1.x, v[3] - r1.y)));
                         }
                     }
-                    __half2 z[2];  // of tokens quad and + 4, + 8 and + 12
+                    // the lane's columns of the group, of tokens quad, + 4, + 8, + 12, and where their codes
+                    // are counted from
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        // (the group's and the token's part of the chunk's place are the same for all lanes)
+                        const int off = kCols * kBits / 8 * j & ~3, same = g * (kGroup * kBits / 128) ^ kvq_swizzle<S>(4 * (k & 1));
+                        const unsigned char *from = V + (16 * mt + 4 * k) * kRB + quad * kRB + (off & 15) +
+                                                    (((off >> 4) ^ kvq_swizzle<S>(quad) ^ same) << 4);
+                        if constexpr (kColWords == 2) {
+                            const uint2 v = *reinterpret_cast<const uint2 *>(from);
+                            u[mt][k][0] = v.x, u[mt][k][1] = v.y;
+                        } else {
+                            u[mt][k][0] = *reinterpret_cast<const uint32_t *>(from);
+                        }
+                    }
                     if constexpr (S::kNormal) {
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
-                            z[k] = *reinterpret_cast<const __half2 *>(zero + g * kTB + 16 * mt + 8 * k + 2 * quad);
+                            z[mt][k] = *reinterpret_cast<const __half2 *>(zero + g * kTB + 16 * mt + 8 * k + 2 * quad);
                     }
-                    // the lane's columns of the group, of those tokens
-                    constexpr int kCols = kGroup / 8;
-                    uint32_t u[4][kCols * kBits / 32 > 0 ? kCols * kBits / 32 : 1];
+                }
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int t = quad + 4 * k;
-                        const int off = g * (kGroup * kBits / 8) + (kCols * kBits / 8 * j & ~3);
-                        const unsigned char *from =
-                            V + (16 * mt + t) * kRB + (((off >> 4) ^ kvq_swizzle<S>(t)) << 4) + (off & 15);
-                        if constexpr (kCols * kBits == 64) {
-                            const uint2 v = *reinterpret_cast<const uint2 *>(from);
-                            u[k][0] = v.x, u[k][1] = v.y;
-                        } else {
-                            u[k][0] = *reinterpret_cast<const uint32_t *>(from);
-                        }
-                    }
+                for (int i = 0; i < kGroup / 16; ++i) {  // columns 2 i and 2 i + 1 of the lane's
+                    float part[kNT][4];                  // of the block
 #pragma unroll
-                    for (int i = 0; i < kGroup / 16; ++i) {  // columns 2 i and 2 i + 1 of the lane's
+                    for (int mt = 0; mt < kMT; ++mt) {
                         uint32_t e[4];
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {  // tokens quad and + 4, then + 8 and + 12
-                            if constexpr (kBits == 4) {
-                                // four columns of both tokens
-                                const uint32_t pick = kGroup == 32 ? (j & 1 ? 0x7632u : 0x5410u) : i >= 2 ? 0x7632u : 0x5410u;
-                                const uint32_t v = __byte_perm(u[2 * k][0], u[2 * k + 1][0], pick) >> (8 * (i % 2));
-                                e[2 * k] = kvq_operand<S, false>(v, z[k]), e[2 * k + 1] = kvq_operand<S, true>(v, z[k]);
-                            } else {
-                                const uint32_t v = __byte_perm(u[2 * k][i / 2], u[2 * k + 1][i / 2], i % 2 ? 0x7632u : 0x5410u);
-                                e[2 * k] = kvq_operand<S, false>(v, z[k]), e[2 * k + 1] = kvq_operand<S, true>(v, z[k]);
-                            }
+                            // 4 bits: four columns of both tokens; 8: two
+                            const int word = kBits == 4 ? 0 : i / 2;
+                            const bool upper = kBits == 8 ? i % 2 : kGroup == 32 ? j & 1 : i >= 2;
+                            uint32_t v = __byte_perm(u[mt][2 * k][word], u[mt][2 * k + 1][word], upper ? 0x7632u : 0x5410u);
+                            if (kBits == 4) v >>= 8 * (i % 2);
+                            e[2 * k] = kvq_operand<S, false>(v, z[mt][k]), e[2 * k + 1] = kvq_operand<S, true>(v, z[mt][k]);
                         }
 #pragma unroll
                         for (int term = 0; term < kTerms; ++term)
 #pragma unroll
-                            for (int nt = 0; nt < kNT; ++nt)
-                                kvq_mma(S::kNormal ? part[S::kNormal ? i : 0][nt] : o[g * (kGroup / 16) + i][nt], e[0], e[1],
-                                        e[2], e[3], b[term][nt]);
+                            for (int nt = 0; nt < kNT; ++nt) {
+                                if (mt == 0 && term == 0) {
+                                    kvq_mma0(part[nt], e[0], e[1], e[2], e[3], b[mt][term][nt]);
+                                } else {
+                                    kvq_mma(part[nt], e[0], e[1], e[2], e[3], b[mt][term][nt]);
+                                }
+                            }
                     }
-                }
-                if constexpr (S::kNormal) {
-                    const float down = pow2i(ev - 28);
 #pragma unroll
-                    for (int nt = 0; nt < kNT; ++nt) {
+                    for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-                        for (int i = 0; i < kPart; ++i)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                o[g * (kGroup / 16) + i][nt][e] = fmaf(part[i][nt][e], down, o[g * (kGroup / 16) + i][nt][e]);
-                    }
+                        for (int e = 0; e < 4; ++e) {
+                            float &sum = o[g * (kGroup / 16) + i][nt][e];
+                            sum = fmaf(part[nt][e], e < 2 ? down : down * (1.0f / S::kUpper), sum);
+                        }
                 }
             }
             stage = stage + 1 == kStages ? 0 : stage + 1;
@@ -830,7 +830,6 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
         const bool cached = key1 > key0;
         if (cached) {
             float *mine = reinterpret_cast<float *>(ring);
-            const float up = S::kNormal ? 1.0f : pow2i(ev - 28) * S::kUnit;
 #pragma unroll
             for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
@@ -850,12 +849,10 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
                 for (int i = 0; i < kTiles; ++i) {
                     constexpr int kPer = kGroup / 16;
                     const int g = i / kPer, col = g * kGroup + (kGroup / 8) * j + 2 * (i % kPer);
-                    constexpr float kOdd = 1.0f / S::kUpper;
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
                         *reinterpret_cast<float2 *>(mine + (nt * 4 + quad) * S::kRowPair + e * D + col) =
-                            make_float2(fmaf(o[i][nt][e], up, bias[g][nt][e]),
-                                        fmaf(o[i][nt][2 + e] * kOdd, up, bias[g][nt][e]));
+                            make_float2(o[i][nt][e] + bias[g][nt][e], o[i][nt][2 + e] + bias[g][nt][e]);
                 }
             }
         }
