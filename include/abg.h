@@ -779,7 +779,9 @@ abg_status abg_kvq_get(const abg_kvq_get_args *a, void *stream);
  * bits), f32 q to 22 bits (of elements below 2^-12 of the largest: to 2^-34 of
  * that).  The weights p*scale that meet V's codes are rounded to 11 bits for
  * bf16, to 22 bits for f16 and f32, the smallest of either to 2^-38 of the
- * largest scale in V.  Drafts are multiplied in f32.
+ * largest scale in V.  The tensor cores cut the sums of a block's products (up to
+ * 32 tokens, 64 columns) off at about 2^-17 of the largest for bf16, at 2^-23 for
+ * f16 and f32.  Drafts are multiplied in f32.
  * ws: abg_kvq_attn_workspace() bytes, as tree_attn's.
  */
 typedef struct abg_kvq_attn_args {

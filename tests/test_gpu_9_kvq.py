@@ -577,6 +577,112 @@ def test_pages_past_two_to_the_32_columns(bits, group):
     check_attn(c, "bf16")
 
 
+def test_a_cache_without_pages_and_requests_without_tokens():
+    """No page at all, tables of no width, empty spans: only the drafts count; a
+    row that has none is not written."""
+    for kind in ("bf16", "f32"):
+        c, k = attn_case(60, kind, 4, 64, 4, 2, 64, 16, [0, 0, 0], [2, 0, 1], gate=False)
+        want, _ = check_attn(dict(c, y=c["y"].clone()), k)
+        empty = abg.kvq_cache(0, 2, 16, 64)
+        for table in (c["table"], i32(np.zeros((3, 0)))):
+            y = torch.full_like(c["y"], 5.0)
+            abg.kvq_attn(**dict(c, cache=empty, table=table, lens=i32([40, 7, 2**31 - 1]) if table.numel() == 0 else c["lens"], y=y))
+            assert np.array_equal(wide(y), want)
+    rows = torch.ones((3, 2, 64), device="cuda")
+    abg.kvq_put(rows, rows, empty)
+    abg.kvq_get(empty, rows, None, slots=i64([0, 1, 2]))
+    assert not rows.any()
+    abg.kvq_put(rows[:0], rows[:0], empty)
+    abg.kvq_get(empty, rows[:0], None)
+
+
+def test_lengths_that_are_out_of_range():
+    """A negative length is 0; one past the table's width ends at its last token."""
+    c, k = attn_case(61, "bf16", 4, 64, 8, 2, 128, 16, [64, 32, 48], [1, 2, 1], gate=False)
+    check_attn(dict(c, lens=i32([-5, 2**31 - 1, 48]), table=i32(np.where(host(c["table"]) < 0, -1, host(c["table"])))), k)
+
+
+@pytest.mark.parametrize("bits,group", [(4, 64), (8, 32)])
+def test_rows_between_other_rows(bits, group):
+    """Sources and results inside wider rows, heads before rows, one head alone."""
+    rng = np.random.default_rng([70, bits])
+    N, Hkv, D = 19, 3, 128
+    wide_rows = dev(rng.standard_normal((N, 3 * Hkv + 2, D + 16)).astype(np.float32))
+    k, v = wide_rows[:, 1:1 + 2 * Hkv:2, :D], wide_rows[:, 2 * Hkv:3 * Hkv, 16:]
+    cache = abg.kvq_cache(2, Hkv, 13, D, bits, group)
+    abg.kvq_put(k, v, cache)
+    for i, x in ((0, k), (2, v)):
+        words, pairs = ref.quantise(host(x.contiguous()), bits, group)
+        got = [a.transpose(0, 2, 1, *range(3, a.ndim)).reshape(26, Hkv, *a.shape[3:])[:N] for a in arrays(cache)[i:i + 2]]
+        same_bits(got[0], words)
+        same_bits(got[1], pairs)
+    ko, vo = torch.empty((N, Hkv, D), device="cuda"), torch.empty((N, Hkv, D), device="cuda")
+    abg.kvq_get(cache, ko, vo)
+    out = torch.zeros_like(wide_rows)
+    abg.kvq_get(cache, out[:, 1:1 + 2 * Hkv:2, :D], None)
+    abg.kvq_get(cache, None, out[:, 2 * Hkv:3 * Hkv, 16:])
+    assert torch.equal(out[:, 1:1 + 2 * Hkv:2, :D], ko) and torch.equal(out[:, 2 * Hkv:3 * Hkv, 16:], vo)
+    out[:, 1:1 + 2 * Hkv:2, :D] = 0
+    out[:, 2 * Hkv:3 * Hkv, 16:] = 0
+    assert not out.any()
+
+
+def test_early_start_off_gives_the_same_bits(tmp_path):
+    """ABG_PDL=0 in a process of its own: plain stream order, the same results."""
+    import os
+    import subprocess
+    import sys
+    prog = tmp_path / "run.py"
+    prog.write_text(
+        "import sys, torch\n"
+        f"sys.path[:0] = {[os.path.dirname(os.path.dirname(os.path.abspath(__file__))), os.path.dirname(os.path.abspath(__file__))]!r}\n"
+        "import test_gpu_9_kvq as t\n"
+        "out = []\n"
+        "for kind, bits in (('f32', 4), ('bf16', 8), ('f16', 4)):\n"
+        "    c, _ = t.attn_case(60, kind, bits, 64, 8, 2, 128, 16, [900, 40], [9, 30], tail=0)\n"
+        "    k = torch.arange(2 * 2 * 128, device='cuda').view(2, 2, 128).float().sin()\n"
+        "    for i in range(3):\n"
+        "        t.abg.kvq_put(k * (i + 1), k, c['cache'], slots=t.i64([3, 18]))\n"
+        "        t.abg.kvq_attn(**c)\n"
+        "    ko = torch.empty_like(k)\n"
+        "    t.abg.kvq_get(c['cache'], ko, None, slots=t.i64([3, 18]))\n"
+        "    out += [c['y'].cpu(), ko.cpu()]\n"
+        "torch.save(out, sys.argv[1])\n")
+    got = []
+    for v in ("0", "1"):
+        path = tmp_path / v
+        env = dict(os.environ, ABG_PDL=v)
+        subprocess.run([sys.executable, str(prog), str(path)], check=True, env=env, timeout=120)
+        got.append(torch.load(path))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def test_first_call_inside_a_capture():
+    """A process whose first call of each kernel is recorded: nothing that a call
+    sets up once is a stream operation."""
+    import os
+    import subprocess
+    import sys
+    here = os.path.dirname(os.path.abspath(__file__))
+    subprocess.run([sys.executable, "-c",
+                    "import sys, torch\n"
+                    f"sys.path[:0] = {[os.path.dirname(here), here]!r}\n"
+                    "import test_gpu_9_kvq as t\n"
+                    "c, k = t.attn_case(30, 'bf16', 8, 32, 8, 2, 64, 16, [300, 90], [6, 4], tail=0)\n"
+                    "ws = torch.empty(t.abg.kvq_attn_workspace(c['q'], c['cache'], c['max_span']), dtype=torch.uint8, device='cuda')\n"
+                    "ko = torch.empty((2, 2, 64), device='cuda')\n"
+                    "g = torch.cuda.CUDAGraph()\n"
+                    "with torch.cuda.graph(g):\n"
+                    "    t.abg.kvq_attn(**c, ws=ws)\n"
+                    "    t.abg.kvq_get(c['cache'], ko, None)\n"
+                    "g.replay()\n"
+                    "y, r = c['y'].clone(), ko.clone()\n"
+                    "t.check_attn(c, k)\n"
+                    "t.abg.kvq_get(c['cache'], ko, None)\n"
+                    "assert torch.equal(y, c['y']) and torch.equal(r.nan_to_num(7.0), ko.nan_to_num(7.0))\n"],
+                   check=True, timeout=120)
+
+
 # --------------------------------------------------------------- refusals ----
 def test_binding_refuses_wrong_tensors_on_the_device():
     c, _ = attn_case(40, "bf16", 4, 64, 4, 2, 64, 16, [20], [3], tail=0)
