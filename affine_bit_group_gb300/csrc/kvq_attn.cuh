@@ -40,7 +40,7 @@
 // copies, behind which it would wait.
 //
 // What bounds it.  64 requests of up to 16000 tokens, 16 heads over 4 of 128 columns, 4
-// bits, take 104 us for 441 MB (4.2 TB/s): copies alone take about 70, the rest without
+// bits, take 101 us for 441 MB (4.4 TB/s): copies alone take about 70, the rest without
 // copies about 75, with 600 instructions a warp for 32 tokens, half of them for taking the
 // codes apart, and no one of them that shortens the call by more than 6 us when it is left
 // out; launches, the joining and two beginnings and ends a block are 15 of it.  In 8 bits 48
@@ -96,11 +96,13 @@ struct KvqShape {
     static constexpr int kMT = kTB / 16;
     static constexpr int kSteps = D / 16;                 // products of 16 columns
     static constexpr int kWords = kGroup * kBits / 128;   // words of a group in a lane
-    // Blocks an SM.  The sums take kNT * D / 4 registers of a lane, and where these are 32 or
-    // 64, 8 warps of 255 registers do as much as 12 or 16 that spill (4 bits in groups of 32,
-    // 128 columns, 48 requests: one block 75.7 us, two 85.5, one of 12 warps 79.0; groups of
-    // 64, 64 requests: 104.9, 103.3, 102.9).
-    static constexpr int kBlocks = kNT * D / 4 <= 16 && kRB <= 64 ? 2 : 1;
+    // Blocks an SM.  The sums take kNT * D / 4 registers of a lane; up to 32, two blocks of
+    // 128 registers that go through 16 tokens at a time do more than one that goes through
+    // 32 (64 requests, 128 columns, 4 bits: 100.9 us for 104.5; 16 rows of 64 columns 47.7
+    // for 49.6), and more than two that go through 32 and spill (103.3; 85.5 for 74.8 in
+    // groups of 32).  With 64, two would spill, and 12 warps of 168 registers do no more.
+    static constexpr int kBlocks = kNT * D / 4 <= 32 && kRB <= 64 ? 2 : 1;
+    static constexpr int kMP = kBlocks == 2 ? 1 : kMT;    // 16-token tiles of a block side by side
     static constexpr int kWarps = 8, kThreads = 32 * kWarps;
     static constexpr int kL = kThreads / kRT, kE = D / kL;  // lanes of a row for drafts and result, columns of a lane
     static constexpr int kStageBytes = kTB * 2 * (kRB + kFB);
@@ -262,7 +264,7 @@ __device__ __forceinline__ void kvq_finish(const abg_tree_attn_args &a, int64_t 
 template <typename S>
 __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const __grid_constant__ KvqAttnArgs x) {
     constexpr int D = S::D, kNT = S::kNT, kRT = S::kRT, kRB = S::kRB, kFB = S::kFB, kG = S::kG, kTB = S::kTB;
-    constexpr int kMT = S::kMT, kTerms = S::kTerms, kStages = S::kStages, kGroup = S::kGroup, kBits = S::kBits;
+    constexpr int kMT = S::kMT, kMP = S::kMP, kTerms = S::kTerms, kStages = S::kStages, kGroup = S::kGroup, kBits = S::kBits;
     constexpr int E = D / 32, kTiles = D / 16, kWarps = S::kWarps, kThreads = S::kThreads;
     extern __shared__ __align__(128) unsigned char raw[];
     __shared__ AttnScan scan;
@@ -599,48 +601,50 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
             };
             // scores
             float sc[kMT][kNT][4];
-            float2 f2[kMT][2][2];  // of tokens tok and tok + 8, of two groups
+            float2 f2[kMP][2][2];  // of tokens tok and tok + 8, of two groups
+#pragma unroll
+            for (int m0 = 0; m0 < kMT; m0 += kMP) {
 #pragma unroll
             for (int g = 0; g < kG; ++g) {
                 if (g % 2 == 0)
 #pragma unroll
-                    for (int mt = 0; mt < kMT; ++mt)
+                    for (int mt = m0; mt < m0 + kMP; ++mt)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) factors(k_fac, 16 * mt + 8 * h + tok, g, f2[mt][h]);
-                uint32_t w[kMT][2][S::kWords];
+                        for (int h = 0; h < 2; ++h) factors(k_fac, 16 * mt + 8 * h + tok, g, f2[mt - m0][h]);
+                uint32_t w[kMP][2][S::kWords];
 #pragma unroll
-                for (int mt = 0; mt < kMT; ++mt)
+                for (int mt = m0; mt < m0 + kMP; ++mt)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int off = g * (kGroup * kBits / 8) + quad * (4 * S::kWords);
                         const unsigned char *from =
                             K + (16 * mt + 8 * h + tok) * kRB + (((off >> 4) ^ kvq_swizzle<S>(tok)) << 4) + (off & 15);
                         if constexpr (S::kWords == 1) {
-                            w[mt][h][0] = *reinterpret_cast<const uint32_t *>(from);
+                            w[mt - m0][h][0] = *reinterpret_cast<const uint32_t *>(from);
                         } else if constexpr (S::kWords == 2) {
                             const uint2 v = *reinterpret_cast<const uint2 *>(from);
-                            w[mt][h][0] = v.x, w[mt][h][1] = v.y;
+                            w[mt - m0][h][0] = v.x, w[mt - m0][h][1] = v.y;
                         } else {
                             const uint4 v = *reinterpret_cast<const uint4 *>(from);
-                            w[mt][h][0] = v.x, w[mt][h][1] = v.y, w[mt][h][2] = v.z, w[mt][h][3] = v.w;
+                            w[mt - m0][h][0] = v.x, w[mt - m0][h][1] = v.y, w[mt - m0][h][2] = v.z, w[mt - m0][h][3] = v.w;
                         }
                     }
-                float acc[kMT][kNT][4];
+                float acc[kMP][kNT][4];
                 constexpr int kPerWord = kBits == 4 ? 2 : 1;
 #pragma unroll
                 for (int wi = 0; wi < S::kWords; ++wi)
 #pragma unroll
                     for (int hh = 0; hh < kPerWord; ++hh) {
                         const int step = (g * S::kWords + wi) * kPerWord + hh;
-                        uint32_t e[kMT][4];
+                        uint32_t e[kMP][4];
 #pragma unroll
-                        for (int mt = 0; mt < kMT; ++mt)
+                        for (int mt = m0; mt < m0 + kMP; ++mt)
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
-                                const uint32_t v = w[mt][h][wi] >> (8 * hh);
+                                const uint32_t v = w[mt - m0][h][wi] >> (8 * hh);
                                 const __half2 from = __float2half2_rn(-1024.0f - S::kMiddle);
-                                e[mt][h] = kvq_operand<S, false>(v, from);
-                                e[mt][2 + h] = kvq_operand<S, true>(v, from);
+                                e[mt - m0][h] = kvq_operand<S, false>(v, from);
+                                e[mt - m0][2 + h] = kvq_operand<S, true>(v, from);
                             }
 #pragma unroll
                         for (int term = 0; term < kTerms; ++term)
@@ -648,11 +652,11 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
                             for (int nt = 0; nt < kNT; ++nt) {
                                 const uint2 b = s_q[((step * kTerms + term) * kNT + nt) * 32 + lane];
 #pragma unroll
-                                for (int mt = 0; mt < kMT; ++mt) {
+                                for (int mt = m0; mt < m0 + kMP; ++mt) {
                                     if (wi == 0 && hh == 0 && term == 0) {
-                                        kvq_mma0(acc[mt][nt], e[mt][0], e[mt][1], e[mt][2], e[mt][3], b);
+                                        kvq_mma0(acc[mt - m0][nt], e[mt - m0][0], e[mt - m0][1], e[mt - m0][2], e[mt - m0][3], b);
                                     } else {
-                                        kvq_mma(acc[mt][nt], e[mt][0], e[mt][1], e[mt][2], e[mt][3], b);
+                                        kvq_mma(acc[mt - m0][nt], e[mt - m0][0], e[mt - m0][1], e[mt - m0][2], e[mt - m0][3], b);
                                     }
                                 }
                             }
@@ -661,14 +665,15 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
                 for (int nt = 0; nt < kNT; ++nt) {
                     const float2 qs = *reinterpret_cast<const float2 *>(s_qs + g * kRT + nt * 8 + 2 * quad);
 #pragma unroll
-                    for (int mt = 0; mt < kMT; ++mt)
+                    for (int mt = m0; mt < m0 + kMP; ++mt)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float2 f = f2[mt][e >> 1][g % 2];
+                            const float2 f = f2[mt - m0][e >> 1][g % 2];
                             const float qe = e & 1 ? qs.y : qs.x;
-                            sc[mt][nt][e] = fmaf(acc[mt][nt][e], f.x, g == 0 ? f.y * qe : fmaf(f.y, qe, sc[mt][nt][e]));
+                            sc[mt][nt][e] = fmaf(acc[mt - m0][nt][e], f.x, g == 0 ? f.y * qe : fmaf(f.y, qe, sc[mt][nt][e]));
                         }
                 }
+            }
             }
             // maxima and weights (sc is in units of 1/s_f until its exponential)
             const int here = key1 - t0;  // tokens of the block that are there
@@ -736,33 +741,35 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
             }
             // weighted sums
 #pragma unroll
+            for (int m0 = 0; m0 < kMT; m0 += kMP) {
+#pragma unroll
             for (int g = 0; g < kG; ++g) {
                 if (g % 2 == 0)
 #pragma unroll
-                    for (int mt = 0; mt < kMT; ++mt)
+                    for (int mt = m0; mt < m0 + kMP; ++mt)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) factors(v_fac, 16 * mt + 8 * h + tok, g, f2[mt][h]);
+                        for (int h = 0; h < 2; ++h) factors(v_fac, 16 * mt + 8 * h + tok, g, f2[mt - m0][h]);
                 constexpr int kCols = kGroup / 8, kColWords = kCols * kBits > 32 ? kCols * kBits / 32 : 1;
-                uint2 b[kMT][kTerms][kNT];
-                uint32_t u[kMT][4][kColWords];
-                __half2 z[kMT][2];
+                uint2 b[kMP][kTerms][kNT];
+                uint32_t u[kMP][4][kColWords];
+                __half2 z[kMP][2];
 #pragma unroll
-                for (int mt = 0; mt < kMT; ++mt) {
+                for (int mt = m0; mt < m0 + kMP; ++mt) {
 #pragma unroll
                     for (int nt = 0; nt < kNT; ++nt) {
                         const float *w = sc[mt][nt];
                         float v[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float2 f = f2[mt][e >> 1][g % 2];
+                            const float2 f = f2[mt - m0][e >> 1][g % 2];
                             v[e] = w[e] * f.x;
                             bias[g][nt][e & 1] = fmaf(w[e], f.y, bias[g][nt][e & 1]);
                         }
                         const uint32_t h0 = kvq_half2(v[0], v[1]), h1 = kvq_half2(v[2], v[3]);
-                        b[mt][0][nt] = make_uint2(kvq_transpose(h0), kvq_transpose(h1));
+                        b[mt - m0][0][nt] = make_uint2(kvq_transpose(h0), kvq_transpose(h1));
                         if constexpr (kTerms == 2) {
                             const float2 r0 = kvq_float2(h0), r1 = kvq_float2(h1);
-                            b[mt][1][nt] = make_uint2(kvq_transpose(kvq_half2(v[0] - r0.x, v[1] - r0.y)),
+                            b[mt - m0][1][nt] = make_uint2(kvq_transpose(kvq_half2(v[0] - r0.x, v[1] - r0.y)),
                                                       kvq_transpose(kvq_half2(v[2] - r1.x, v[3] - r1.y)));
                         }
                     }
@@ -776,40 +783,40 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
                                                     (((off >> 4) ^ kvq_swizzle<S>(quad) ^ same) << 4);
                         if constexpr (kColWords == 2) {
                             const uint2 v = *reinterpret_cast<const uint2 *>(from);
-                            u[mt][k][0] = v.x, u[mt][k][1] = v.y;
+                            u[mt - m0][k][0] = v.x, u[mt - m0][k][1] = v.y;
                         } else {
-                            u[mt][k][0] = *reinterpret_cast<const uint32_t *>(from);
+                            u[mt - m0][k][0] = *reinterpret_cast<const uint32_t *>(from);
                         }
                     }
                     if constexpr (S::kNormal) {
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
-                            z[mt][k] = *reinterpret_cast<const __half2 *>(zero + g * kTB + 16 * mt + 8 * k + 2 * quad);
+                            z[mt - m0][k] = *reinterpret_cast<const __half2 *>(zero + g * kTB + 16 * mt + 8 * k + 2 * quad);
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < kGroup / 16; ++i) {  // columns 2 i and 2 i + 1 of the lane's
                     float part[kNT][4];                  // of the block
 #pragma unroll
-                    for (int mt = 0; mt < kMT; ++mt) {
+                    for (int mt = m0; mt < m0 + kMP; ++mt) {
                         uint32_t e[4];
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {  // tokens quad and + 4, then + 8 and + 12
                             // 4 bits: four columns of both tokens; 8: two
                             const int word = kBits == 4 ? 0 : i / 2;
                             const bool upper = kBits == 8 ? i % 2 : kGroup == 32 ? j & 1 : i >= 2;
-                            uint32_t v = __byte_perm(u[mt][2 * k][word], u[mt][2 * k + 1][word], upper ? 0x7632u : 0x5410u);
+                            uint32_t v = __byte_perm(u[mt - m0][2 * k][word], u[mt - m0][2 * k + 1][word], upper ? 0x7632u : 0x5410u);
                             if (kBits == 4) v >>= 8 * (i % 2);
-                            e[2 * k] = kvq_operand<S, false>(v, z[mt][k]), e[2 * k + 1] = kvq_operand<S, true>(v, z[mt][k]);
+                            e[2 * k] = kvq_operand<S, false>(v, z[mt - m0][k]), e[2 * k + 1] = kvq_operand<S, true>(v, z[mt - m0][k]);
                         }
 #pragma unroll
                         for (int term = 0; term < kTerms; ++term)
 #pragma unroll
                             for (int nt = 0; nt < kNT; ++nt) {
-                                if (mt == 0 && term == 0) {
-                                    kvq_mma0(part[nt], e[0], e[1], e[2], e[3], b[mt][term][nt]);
+                                if (mt == m0 && term == 0) {
+                                    kvq_mma0(part[nt], e[0], e[1], e[2], e[3], b[mt - m0][term][nt]);
                                 } else {
-                                    kvq_mma(part[nt], e[0], e[1], e[2], e[3], b[mt][term][nt]);
+                                    kvq_mma(part[nt], e[0], e[1], e[2], e[3], b[mt - m0][term][nt]);
                                 }
                             }
                     }
@@ -821,6 +828,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
                             sum = fmaf(part[nt][e], e < 2 ? down : down * (1.0f / S::kUpper), sum);
                         }
                 }
+            }
             }
             stage = stage + 1 == kStages ? 0 : stage + 1;
         }
