@@ -25,9 +25,9 @@ constexpr float kLargestHalf = 65504.0f;
 // in 4, 8 or 16 lanes' chunks of one half of the columns, or (64 columns a row, one
 // group) in all 16 lanes' both chunks, and its least and largest value meet by
 // shuffles; the lanes then quantise and pack their own columns.  Instructions bound it
-// (3700 a token of 16 + 4 + 4 heads, of which kv_put's steps are 2500): 8191 such rows of
-// 128 columns, f32 to 4 bits, with q in bf16, in 43 us (139 MB, 3.2 TB/s; kv_put to bf16
-// 33).  Three blocks an SM, in 80 registers, spill and take 50.
+// (3000 a token of 16 + 4 + 4 heads; kv_put 2500): 8191 such rows of 128 columns, f32 to 4
+// bits, with q in bf16, in 42 us (139 MB, 3.3 TB/s; kv_put to bf16 33).  Three blocks an
+// SM, in 80 registers, spill and take 50.
 constexpr int kPutWarps = 8;
 
 // Least and largest; a NaN stays.
@@ -40,6 +40,22 @@ __device__ __forceinline__ float largest(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
+}
+
+// Pairwise tree of V squares (chunk_tree's, the products in pairs).
+template <int V>
+__device__ __forceinline__ float square_tree(const float (&u)[V]) {
+    float x[V];
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+        const float2 y = mul2(make_float2(u[i], u[i + 1]), make_float2(u[i], u[i + 1]));
+        x[i] = y.x, x[i + 1] = y.y;
+    }
+#pragma unroll
+    for (int k = V / 2; k >= 1; k >>= 1)
+#pragma unroll
+        for (int i = 0; i < k; ++i) x[i] = __fadd_rn(x[2 * i], x[2 * i + 1]);
+    return x[0];
 }
 
 // N codes of kBits bits, low first, in a word, of whole numbers x + 1.5 * 2^23: their bits
@@ -209,7 +225,7 @@ __global__ void __launch_bounds__(32 * kPutWarps, 2) kvq_put_kernel(
                 float ss = 0.0f;
 #pragma unroll
                 for (int r = 0; r < kSteps; ++r) {
-                    const float lo = chunk_tree<V>(u[r][0]), hi = chunk_tree<V>(u[r][1]);
+                    const float lo = square_tree<V>(u[r][0]), hi = square_tree<V>(u[r][1]);
                     // even lanes go on with the lower columns' sum, odd ones with the upper's
                     const float away = __shfl_xor_sync(0xffffffffu, l & 1 ? lo : hi, 1);
                     float sum = __fadd_rn(l & 1 ? hi : lo, away);
@@ -236,17 +252,22 @@ __global__ void __launch_bounds__(32 * kPutWarps, 2) kvq_put_kernel(
                         load_e<float, V>(w + V * l, wv[0]);
                         load_e<float, V>(w + D / 2 + V * l, wv[1]);
 #pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            u[r][0][i] = __fmul_rn(__fmul_rn(u[r][0][i], f), wv[0][i]);
-                            u[r][1][i] = __fmul_rn(__fmul_rn(u[r][1][i], f), wv[1][i]);
-                        }
+                        for (int h2 = 0; h2 < 2; ++h2)
+#pragma unroll
+                            for (int i = 0; i < V; i += 2) {
+                                const float2 y = mul2(mul2(make_float2(u[r][h2][i], u[r][h2][i + 1]), make_float2(f, f)),
+                                                      make_float2(wv[h2][i], wv[h2][i + 1]));
+                                u[r][h2][i] = y.x, u[r][h2][i + 1] = y.y;
+                            }
                     }
                     if (a.cos) {
 #pragma unroll
-                        for (int i = 0; i < V; ++i) {
-                            const float x = u[r][0][i], y = u[r][1][i];
-                            u[r][0][i] = __fsub_rn(__fmul_rn(x, c[i]), __fmul_rn(y, s[i]));
-                            u[r][1][i] = __fadd_rn(__fmul_rn(y, c[i]), __fmul_rn(x, s[i]));
+                        for (int i = 0; i < V; i += 2) {  // (scalar sums: a packed one could be contracted)
+                            const float2 x = make_float2(u[r][0][i], u[r][0][i + 1]), y = make_float2(u[r][1][i], u[r][1][i + 1]);
+                            const float2 cc = make_float2(c[i], c[i + 1]), ss = make_float2(s[i], s[i + 1]);
+                            const float2 xc = mul2(x, cc), ys = mul2(y, ss), yc = mul2(y, cc), xs = mul2(x, ss);
+                            u[r][0][i] = __fsub_rn(xc.x, ys.x), u[r][0][i + 1] = __fsub_rn(xc.y, ys.y);
+                            u[r][1][i] = __fadd_rn(yc.x, xs.x), u[r][1][i + 1] = __fadd_rn(yc.y, xs.y);
                         }
                     }
                 }
@@ -270,14 +291,14 @@ __global__ void __launch_bounds__(32 * kPutWarps, 2) kvq_put_kernel(
 // first.  A block's threads have a token's heads side by side, and as many tokens as there
 // is room for; four of a thread's tokens at a time, so that their words are on their way
 // together.  Instructions bound it: 32768 tokens of 4 heads of 128, 4 bits to bf16, in
-// 17.6 us (86 MB, 4.9 TB/s); with every place found on its own 24.4, with the codes made
+// 17.2 us (86 MB, 5.0 TB/s); with every place found on its own 24.4, with the codes made
 // floats by conversions and 64-bit divisions 40.6.
 constexpr int kGetThreads = 256, kGetEach = 4, kGetTokens = 128;
 
-// Byte k of w as a float (0x4b000000 + c is 2^23 + c).
+// Byte k of w plus 2^23, as a float (0x4b000000 + c).
 template <int k>
 __device__ __forceinline__ float byte_value(uint32_t w) {
-    return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 + k)) - 8388608.0f;
+    return __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 + k));
 }
 
 // per: places of eight columns of a token (key or value, head, columns); side: tokens side
@@ -345,7 +366,11 @@ __global__ void __launch_bounds__(kGetThreads) kvq_get_kernel(const __grid_const
             }
             const float2 sb = __half22float2(f[k]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = fmaf(sb.x, v[i], sb.y);  // (the product is exact: 11 and 8 bits)
+            for (int i = 0; i < 8; i += 2) {  // (the product is exact: 11 and 8 bits)
+                const float2 y = fma2(make_float2(sb.x, sb.x), add2(make_float2(v[i], v[i + 1]), make_float2(-8388608.0f, -8388608.0f)),
+                                      make_float2(sb.y, sb.y));
+                v[i] = y.x, v[i + 1] = y.y;
+            }
             store_e<T, 8>(to, v);
             to += side * step;
         }
