@@ -25,9 +25,9 @@ constexpr float kLargestHalf = 65504.0f;
 // in 4, 8 or 16 lanes' chunks of one half of the columns, or (64 columns a row, one
 // group) in all 16 lanes' both chunks, and its least and largest value meet by
 // shuffles; the lanes then quantise and pack their own columns.  Instructions bound it
-// (3000 a token of 16 + 4 + 4 heads; kv_put 2500): 8191 such rows of 128 columns, f32 to 4
-// bits, with q in bf16, in 42 us (139 MB, 3.3 TB/s; kv_put to bf16 33).  Three blocks an
-// SM, in 80 registers, spill and take 50.
+// (2600 a token of 16 + 4 + 4 heads; kv_put 2500): 8191 such rows of 128 columns, f32 to 4
+// bits, with q in bf16, in 38 us (139 MB, 3.7 TB/s; kv_put to bf16 33).  With the bits read
+// from the arguments and one address a chunk it took 42.
 constexpr int kPutWarps = 8;
 
 // Least and largest; a NaN stays.
@@ -89,11 +89,11 @@ __device__ __forceinline__ void store_codes(unsigned char *p, const float (&x)[V
 // u[r][0][0..V) at columns V*l.., u[r][1][..) at D/2 + V*l.. into codes and pairs, all
 // rows' steps side by side.  rows[r]: the row's place in the cache (-1: not written)
 // of keys, or (values[r]) of values.
-template <int D, int R>
+template <int D, int kBits, int R>
 __device__ __forceinline__ void put_quantised(const float (&u)[R][2][D / 32], int l, const int64_t (&rows)[R],
                                               const bool (&values)[R], const abg_kvq_cache &c) {
     constexpr int V = D / 32, C = 2 * R;  // chunks of a lane, 2 r + h
-    const int lane = threadIdx.x & 31, bits = c.bits, group = c.group;
+    const int lane = threadIdx.x & 31, group = c.group, log_group = group == 32 ? 5 : 6;
     float lo[C], hi[C];
     const bool joined = group > D / 2;
 #pragma unroll
@@ -124,50 +124,52 @@ __device__ __forceinline__ void put_quantised(const float (&u)[R][2][D / 32], in
             hi[i] = largest(up ? hi[i + d] : hi[i], b);
         }
     }
-    for (int d = C; d < lanes; d *= 2) {
-        lo[0] = least(lo[0], __shfl_xor_sync(0xffffffffu, lo[0], d));
-        hi[0] = largest(hi[0], __shfl_xor_sync(0xffffffffu, hi[0], d));
+    if (lanes > C) {  // (twice as many)
+        lo[0] = least(lo[0], __shfl_xor_sync(0xffffffffu, lo[0], C));
+        hi[0] = largest(hi[0], __shfl_xor_sync(0xffffffffu, hi[0], C));
     }
-    const float levels = bits == 4 ? 15.0f : 255.0f;
+    constexpr float levels = kBits == 4 ? 15.0f : 255.0f;
     const bool bad = !(hi[0] <= kLargestHalf && lo[0] >= -kLargestHalf);
     const __half nan = __ushort_as_half(0x7fff);
     const __half2 own = bad ? __halves2half2(nan, nan)
                             : __halves2half2(__float2half_rn(__fdiv_rn(__fsub_rn(hi[0], lo[0]), levels)), __float2half_rn(lo[0]));
     const float own_inv = __low2float(own) > 0.0f ? __frcp_rn(__low2float(own)) : 0.0f;  // (a NaN: 0)
     const uint32_t own_pair = *reinterpret_cast<const uint32_t *>(&own);
+    const bool first = (l & (lanes - 1)) == 0;  // of a group's lanes
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        unsigned char *codes = static_cast<unsigned char *>(values[r] ? c.Vc : c.Kc) + rows[r] * (D * bits / 8);
-        uint32_t *pairs = static_cast<uint32_t *>(values[r] ? c.Vs : c.Ks) + rows[r] * (D / group);
+        float x[2][V];
+        uint32_t pair[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int from = (lane & ~(C - 1)) + 2 * r + h;
-            const uint32_t pair = __shfl_sync(0xffffffffu, own_pair, from);
+            pair[h] = __shfl_sync(0xffffffffu, own_pair, from);
             const float inv = __shfl_sync(0xffffffffu, own_inv, from);
-            const float b = __half2float(__ushort_as_half(static_cast<unsigned short>(pair >> 16)));
+            const float b = __half2float(__ushort_as_half(static_cast<unsigned short>(pair[h] >> 16)));
             const float2 back = make_float2(-b, -b), times = make_float2(inv, inv), whole = make_float2(12582912.0f, 12582912.0f);
-            float x[V];
 #pragma unroll
             for (int i = 0; i < V; i += 2) {
                 // clamped (a NaN to 0), then rounded to a whole number by 1.5 * 2^23
                 const float2 y = mul2(add2(make_float2(u[r][h][i], u[r][h][i + 1]), back), times);
                 const float2 z = add2(make_float2(fminf(fmaxf(y.x, 0.0f), levels), fminf(fmaxf(y.y, 0.0f), levels)), whole);
-                x[i] = z.x, x[i + 1] = z.y;
+                x[h][i] = z.x, x[h][i + 1] = z.y;
             }
-            const int col = h * (D / 2) + V * l;
-            if (rows[r] >= 0) {
-                if (bits == 4) {
-                    store_codes<4>(codes + col / 2, x);
-                } else {
-                    store_codes<8>(codes + col, x);
-                }
-                if (l % lanes == 0 && !(joined && h)) pairs[col / group] = pair;
+        }
+        if (rows[r] >= 0) {
+            unsigned char *codes =
+                static_cast<unsigned char *>(values[r] ? c.Vc : c.Kc) + rows[r] * (D * kBits / 8) + V * l * kBits / 8;
+            store_codes<kBits>(codes, x[0]);
+            store_codes<kBits>(codes + D / 2 * kBits / 8, x[1]);
+            if (first) {
+                uint32_t *pairs = static_cast<uint32_t *>(values[r] ? c.Vs : c.Ks) + ((rows[r] * D + V * l) >> log_group);
+                pairs[0] = pair[0];
+                if (!joined) pairs[(D / 2) >> log_group] = pair[1];
             }
         }
     }
 }
 
-template <typename S, typename T, int D>
+template <typename S, typename T, int D, int kBits>
 __global__ void __launch_bounds__(32 * kPutWarps, 2) kvq_put_kernel(
     const __grid_constant__ abg_kvq_put_args a, int groups) {
     using P = Put<D>;
@@ -279,7 +281,7 @@ __global__ void __launch_bounds__(32 * kPutWarps, 2) kvq_put_kernel(
                 values[r] = h >= nq + nk;
                 rows[r] = kept && h >= nq && h < heads ? base + (values[r] ? h - nq - nk : h - nq) * a.c.page : -1;
             }
-            if (t.h0 + P::kHeads > nq) put_quantised<D>(u, l, rows, values, a.c);  // (the whole warp, or none of it)
+            if (t.h0 + P::kHeads > nq) put_quantised<D, kBits>(u, l, rows, values, a.c);  // (the whole warp, or none of it)
         }
         t = next;
     }
@@ -377,12 +379,12 @@ __global__ void __launch_bounds__(kGetThreads) kvq_get_kernel(const __grid_const
     }
 }
 
-template <typename S, typename T, int D>
+template <typename S, typename T, int D, int kBits>
 cudaError_t put_d(const abg_kvq_put_args &a, bool early, cudaStream_t stream) {
     // as many blocks as fit at once
     static const int fit = [] {
         int per = 0;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kvq_put_kernel<S, T, D>, 32 * kPutWarps, 0) !=
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kvq_put_kernel<S, T, D, kBits>, 32 * kPutWarps, 0) !=
             cudaSuccess)
             per = 1;
         return std::max(per, 1) * sm_count();
@@ -390,14 +392,18 @@ cudaError_t put_d(const abg_kvq_put_args &a, bool early, cudaStream_t stream) {
     const int heads = static_cast<int>((a.q ? a.Hq : 0) + 2 * a.c.Hkv);
     const int groups = (heads + Put<D>::kHeads - 1) / Put<D>::kHeads;
     const int64_t blocks = (a.N * groups + kPutWarps - 1) / kPutWarps;
-    return launch_kernel(kvq_put_kernel<S, T, D>, dim3(static_cast<unsigned>(std::min<int64_t>(blocks, fit))),
+    return launch_kernel(kvq_put_kernel<S, T, D, kBits>, dim3(static_cast<unsigned>(std::min<int64_t>(blocks, fit))),
                          dim3(32 * kPutWarps), 0, stream, early, a, groups);
+}
+template <typename S, typename T, int kBits>
+cudaError_t put_bits(const abg_kvq_put_args &a, bool early, cudaStream_t stream) {
+    return a.c.D == 64    ? put_d<S, T, 64, kBits>(a, early, stream)
+           : a.c.D == 128 ? put_d<S, T, 128, kBits>(a, early, stream)
+                          : put_d<S, T, 256, kBits>(a, early, stream);
 }
 template <typename S, typename T>
 cudaError_t put(const abg_kvq_put_args &a, bool early, cudaStream_t stream) {
-    return a.c.D == 64    ? put_d<S, T, 64>(a, early, stream)
-           : a.c.D == 128 ? put_d<S, T, 128>(a, early, stream)
-                          : put_d<S, T, 256>(a, early, stream);
+    return a.c.bits == 4 ? put_bits<S, T, 4>(a, early, stream) : put_bits<S, T, 8>(a, early, stream);
 }
 
 template <typename T, int kBits>
