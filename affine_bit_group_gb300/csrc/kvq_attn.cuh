@@ -884,17 +884,18 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
 #pragma unroll
             for (int d = 1; d < 8; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
             top = fmaxf(top, M);
-            // (no maximum, but a weight: a NaN, which stays)
-            const float fw = lw == 0.0f ? 0.0f : mw == -INFINITY ? 1.0f : exp2f(mw - top);
-            const float fd = L == 0.0f ? 0.0f : M == -INFINITY ? 1.0f : exp2f(M - top);
+            // (no maximum, but a weight: a NaN, which stays, as one that is far below does)
+            const float fw = mw == -INFINITY ? 1.0f : exp2f(mw - top);
+            const float fd = M == -INFINITY ? 1.0f : exp2f(M - top);
+            const bool none = L == 0.0f;
             M = top;
-            L = L == 0.0f ? 0.0f : L * fd;
+            L *= fd;
 #pragma unroll
-            for (int i = 0; i < kE; ++i) v[i] = fd == 0.0f ? 0.0f : v[i] * fd;
+            for (int i = 0; i < kE; ++i) v[i] = none ? 0.0f : v[i] * fd;
 #pragma unroll
             for (int u = 0; u < kWarps; ++u) {
                 const float f = __shfl_sync(0xffffffffu, fw, u, kL), lu = __shfl_sync(0xffffffffu, lw, u, kL);
-                if (f == 0.0f) continue;  // no weight: nothing to add
+                if (lu == 0.0f) continue;  // no token: nothing to add
                 L = fmaf(lu, f, L);
                 const float *from = reinterpret_cast<const float *>(raw + S::kFixed + u * S::kWarpBytes) +
                                     (r >> 1) * S::kRowPair + (r & 1) * D + ln * kE;

@@ -392,6 +392,34 @@ def test_kvq_attn_nan_stays_where_it_is_seen(kind, D):
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("tokens,top,bad", [(600, 5, 40), (600, 40, 5), (600, 5, 590), (20000, 5, 19990), (20000, 19990, 5),
+                                            (20000, 12000, 5)])
+def test_kvq_attn_nan_far_below_the_largest_score_stays(kind, tokens, top, bad):
+    """A NaN in a row that another warp, block or piece outweighs by 2^800."""
+    c, k = attn_case(14, kind, 4, 32, 4, 2, 128, 16, [tokens], [2], gate=False)
+    Kw, Kp, Vw, Vp = (a.copy() for a in arrays(c["cache"]))
+
+    def at(t):
+        return host(c["table"])[0][t // 16], slice(None), t % 16
+
+    Kp[(*at(np.arange(tokens)), 0, slice(None))] = 0.0
+    Kp[(*at(top), 0, 1)] = 40.0
+    q = c["q"].clone()
+    q[..., :32] = 5.0
+    Vp[at(bad)[0], 1, at(bad)[2], 2, 0] = np.nan
+    y = torch.zeros_like(c["y"])
+    abg.kvq_attn(**dict(c, cache=as_cache(Kw, Kp, Vw, Vp), q=q, y=y))
+    got = wide(y)[:2]
+    nan = np.zeros(got.shape, bool)
+    nan[:, 2:, 64:96] = True
+    assert np.array_equal(np.isnan(got), nan)
+    Kp[at(bad)[0], 0, at(bad)[2], 3, 1] = np.nan
+    abg.kvq_attn(**dict(c, cache=as_cache(Kw, Kp, Vw, Vp), q=q, y=y))
+    nan[:, :2] = True
+    assert np.array_equal(np.isnan(wide(y)[:2]), nan)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("bits,group", [(4, 32), (8, 64)])
 def test_kvq_attn_scores_far_apart_and_scales_of_all_sizes(kind, bits, group):
     """Scores that grow along the sequence (every block raises the maximum) and
