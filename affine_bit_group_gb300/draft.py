@@ -14,7 +14,10 @@ least one; a step whose trees are single tokens is ordinary decoding.
 With a cache in 4 or 8 bits, kvq_put and kvq_attn take the places of kv_put and
 tree_attn.  The drafts' rows are then quantised and read back (kvq_get) before
 the attention, so that a draft sees the others as it would see them in the cache,
-and a step of several drafts gives what as many steps of one give.
+and a step of several drafts gives what as many steps of one give.  The accepted
+ones are quantised into the cache from the same products again, since rows that
+were read back need not have the codes that they came from (of a group far from 0
+the bias's rounding is many scales).
 
 All of a step's calls are queued on the current stream; nothing is read back
 between them.  The products take up to eight tokens at a time (abg_q4mm).
@@ -65,7 +68,7 @@ class DraftDecoder:
         else:
             kv = (len(dm.layers), pages, self.Hkv, page, D)
             self.Kc, self.Vc = torch.zeros(kv, dtype=cache, device="cuda"), torch.zeros(kv, dtype=cache, device="cuda")
-        kv = (len(dm.layers), self.Hkv, rows, D)
+        kv = (1 if self.quantised else len(dm.layers), self.Hkv, rows, D)
         self.Kd, self.Vd = torch.zeros(kv, dtype=self.ty, device="cuda"), torch.zeros(kv, dtype=self.ty, device="cuda")
 
         def i32(*shape):
@@ -109,7 +112,8 @@ class DraftDecoder:
     def logits(self, tok, parent, cu, max_span: int):
         """Logits [N][vocabulary] of the drafts tok [N] (int32) with parents
         parent [N] and spans cu [requests+1]; their key and value rows are left
-        in Kd, Vd."""
+        in Kd, Vd, or with a quantised cache before norm and rotation in products,
+        and their positions in pos."""
         dm, D, Hq, Hkv, N = self.dm, self.D, self.Hq, self.Hkv, len(tok)
         if not 0 < N <= self.rows or not 0 < max_span <= MAX_SPAN:
             raise ValueError(f"1 to {self.rows} drafts, spans of 1 to {MAX_SPAN}")
@@ -121,15 +125,17 @@ class DraftDecoder:
         y, ysum = torch.empty((N, Hq, D), device="cuda"), torch.empty((N, Hq * D // 64), device="cuda")
         ws = torch.empty(kvq_attn_workspace(qo, self.caches[0], max_span) if self.quantised else
                          tree_attn_workspace(qo, self.Kc[0], max_span), dtype=torch.uint8, device="cuda")
+        self.products, self.pos = [], pos
         for i, L in enumerate(dm.layers):
             q, k, v = self._products([L["q"], L["k"], L["v"]], *self._norm(h, L["rms1"]))
             k, v = k.view(N, Hkv, D), v.view(N, Hkv, D)
             rope = dict(q=q.view(N, Hq, D), qo=qo, qn_w=self.qn_w, kn_w=self.kn_w, cos=self.cos, sin=self.sin, pos=pos,
                         eps=self.eps)
             if self.quantised:
+                self.products.append((k, v))
                 kvq_put(k, v, self.drafts, **rope)
-                kvq_get(self.drafts, self.Kd[i, :, :N].transpose(0, 1), self.Vd[i, :, :N].transpose(0, 1))
-                kvq_attn(qo, self.caches[i], self.table, self.lens[0], cu, self.Kd[i], self.Vd[i], mask, y,
+                kvq_get(self.drafts, self.Kd[0, :, :N].transpose(0, 1), self.Vd[0, :, :N].transpose(0, 1))
+                kvq_attn(qo, self.caches[i], self.table, self.lens[0], cu, self.Kd[0], self.Vd[0], mask, y,
                          max_span=max_span, ysum=ysum, ws=ws)
             else:
                 kv_put(k, v, self.Kd[i].unsqueeze(0), self.Vd[i].unsqueeze(0), **rope)
@@ -156,12 +162,13 @@ class DraftDecoder:
         best, rows = (torch.empty(N, dtype=torch.int32, device="cuda") for _ in range(2))
         tree_accept(self.logits(tok, parent, cu, max_span), tok, parent, cu, best, rows, self.add, self.last)
         slots = self._plan(self.add, cu, N)
-        for i in range(len(self.dm.layers)):
-            k, v = self.Kd[i].transpose(0, 1), self.Vd[i].transpose(0, 1)
-            if self.quantised:
-                kvq_put(k, v, self.caches[i], slots=slots, rows=rows)
-            else:
-                kv_put(k, v, self.Kc[i], self.Vc[i], slots=slots, rows=rows)
+        if self.quantised:
+            pos = self.pos[rows.clamp(min=0).long()]
+            for (k, v), cache in zip(self.products, self.caches):
+                kvq_put(k, v, cache, slots=slots, rows=rows, kn_w=self.kn_w, cos=self.cos, sin=self.sin, pos=pos, eps=self.eps)
+        else:
+            for i in range(len(self.dm.layers)):
+                kv_put(self.Kd[i].transpose(0, 1), self.Vd[i].transpose(0, 1), self.Kc[i], self.Vc[i], slots=slots, rows=rows)
         stored = self.lens[0] - self.lens[1]  # a refused request's length has not changed
         rows.masked_fill_(slots < 0, -1)
         torch.where(stored != self.add, tok[cu[:-1].clamp(max=N - 1).long()], self.last, out=self.last)

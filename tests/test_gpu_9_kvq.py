@@ -801,3 +801,40 @@ def test_draft_decoder_over_a_quantised_cache(cache, group):
         if i == 0:  # the first layer's rows depend on the tokens and positions alone
             assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
     assert abg.device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("cache", ["q4", "q8"])
+def test_draft_decoder_holds_the_rows_that_the_drafts_saw(cache):
+    """Value rows far from 0 against their spread, whose bias rounds by many scales:
+    quantised again after being read back they would have other codes."""
+    from affine_bit_group_gb300 import decode, draft, synth
+    V, D, n = 700, 64, 5
+    model, _ = synth.decode_model(seed=41, n_layers=2, hidden=512, mlp=512, head_rows=V, q_rows=4 * D, kv_rows=2 * D)
+    dm = decode.DeviceModel.upload(model)
+    rng = np.random.default_rng(42)
+    for L in dm.layers:  # all rows of V's matrix are its first one, but for one bias
+        for t in (L["v"].w, L["v"].scale, L["v"].bias):
+            m = t.view(2 * D, -1)
+            m[:] = m[0].clone()
+        L["v"].bias.view(2 * D, -1)[:, 0] += dev((1e-4 * rng.standard_normal(2 * D)).astype(np.float32)).to(L["v"].bias.dtype)
+    embed = dev(rng.standard_normal((V, 512)).astype(np.float32))
+
+    def decoder():
+        return draft.DraftDecoder(dm, embed, D=D, requests=1, pages=8, page=4, max_len=32, rows=8, cache=cache)
+
+    one, chain = decoder(), [7]
+    for _ in range(n):
+        chain.append(int(one.step(i32(chain[-1:]), i32([-1]), i32([0, 1]), 1)[2]))
+    dec = decoder()
+    rows, add, last = dec.step(i32(chain[:n]), i32(range(-1, n - 1)), i32([0, n]), n)
+    assert host(rows).tolist() == list(range(n)) and host(add).tolist() == [n] and host(last).tolist() == chain[n:]
+    # the last layer's drafts are still there
+    table, t = host(dec.table)[0], np.arange(n)
+    for held, cached in zip(dec.drafts, dec.caches[-1]):
+        want, got = (host(x.view(torch.int32)) for x in (held, cached))
+        assert np.array_equal(got[table[t // 4], :, t % 4], want[0, :, :n].swapaxes(0, 1))
+    if cache == "q8":  # (and are such rows; in 4 bits these happen to keep their codes)
+        k, v = (torch.empty((n, 2, D), device="cuda") for _ in range(2))
+        abg.kvq_get(dec.drafts, k, v)
+        again = abg.kvq_put(k, v, abg.kvq_cache(1, 2, 8, D, 8, 64))
+        assert not torch.equal(again.Vc[:, :, :n], dec.drafts.Vc[:, :, :n])
