@@ -131,7 +131,8 @@ abg_status abg_kvq_attn(const abg_kvq_attn_args *args, void *ws, int64_t ws_byte
     if (a.ysum && a.y_type != ABG_SB_F32) return ABG_EINVAL;
     if (!cache_sizes(c) || a.words < 1 || a.words > ABG_MAX_SPAN / 64 || a.B < 1 || a.B > kMax32 - 1 || a.N < 0 ||
         a.N > kMax32 || a.width < 0 || a.width > kMax32 || !bounded({a.B, a.width, 4}) ||
-        !bounded({a.width, c.page, 2}) || a.width * c.page > kMax32 - 1023 || a.drafts < a.N || a.drafts > kMax32 ||
+        // (a kernel's token numbers pass the last cached one by up to 1535)
+        !bounded({a.width, c.page, 2}) || a.width * c.page > kMax32 - 2047 || a.drafts < a.N || a.drafts > kMax32 ||
         a.max_span > 64 * a.words || a.Hq < 1 || a.Hq > 65536 || !bounded({a.drafts, a.Hq, c.D, 4}))
         return ABG_ESHAPE;
     int64_t need = 0;

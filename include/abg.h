@@ -724,7 +724,7 @@ typedef struct abg_kvq_cache {
  *     code  = clamp(rint((x - bias) * (1 / scale)), 0, 2^bits - 1), 0 where
  *             scale is 0.
  *   A value is off by at most half a scale, the bias's rounding and 2^-11 of the
- * group's range.  A group with a NaN or a magnitude above 65504 (f16's
+ * group's range (or (2^bits - 1)*2^-25, where the scale is below 2^-14).  A group with a NaN or a magnitude above 65504 (f16's
  * largest) is held as NaN: scale and bias are 0x7fff, the codes 0.
  * The codes and factors are exact: they are the same on every run, and those of
  * these steps done one by one in any IEEE binary32 arithmetic (of zeros of both
@@ -772,7 +772,7 @@ abg_status abg_kvq_get(const abg_kvq_get_args *a, void *stream);
  * sees makes its result NaN, one in a V row those columns' group (an infinite
  * factor, which kvq_put never writes, may do so too).  A row of q
  * that holds a NaN or a magnitude of 2^100 or more gives NaN (0 where it sees no
- * token).  width*page is at most 2^31 - 1024.
+ * token).  width*page is at most 2^31 - 2048.
  *   Sums, softmax statistics and the work split's partial results are f32.
  * Codes are multiplied exactly, with q in f16 after a scaling of the row by a
  * power of two: 16-bit q as it is (elements below 2^-23 of the row's largest lose

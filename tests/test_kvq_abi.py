@@ -103,7 +103,7 @@ WS = A + 16 * STEP
     (dict(q=A + 4 * STEP + 8), EALIGN), (dict(gate=A + 11 * STEP + 4), EALIGN), (dict(mask=A + 10 * STEP + 4), EALIGN),
     (dict(table=A + 5 * STEP + 2), EALIGN), (dict(ysum=A + 13 * STEP + 2), EALIGN), (dict(y=A + 4 * STEP), EALIAS),
     (dict(y=A), EALIAS), (dict(y=A + 3 * STEP), EALIAS), (dict(ysum=A + 12 * STEP + 16), EALIAS), (dict(y=WS + 1024), EALIAS),
-    (dict(Vd=WS), EALIAS)])
+    (dict(Vd=WS), EALIAS), (dict(N=0, width=2**27 - 64, page=16), ESHAPE), (dict(N=0, width=2**27 - 128, page=16), OK)])
 def test_kvq_attn_refuses(lib, change, status):
     assert call(lib, "abg_kvq_attn", abg._KvqAttnArgs, ATTN, change, WS, 1 << 40, None) == status
 
