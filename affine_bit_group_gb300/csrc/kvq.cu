@@ -24,10 +24,12 @@ constexpr float kLargestHalf = 65504.0f;
 // V*l .. V*l+V-1 of a head (V = D/32) and the ones D/2 further on.  A group is then
 // in 4, 8 or 16 lanes' chunks of one half of the columns, or (64 columns a row, one
 // group) in all 16 lanes' both chunks, and its least and largest value meet by
-// shuffles; the lanes then quantise and pack their own columns.  Instructions bound it
-// (2600 a token of 16 + 4 + 4 heads; kv_put 2500): 8191 such rows of 128 columns, f32 to 4
-// bits, with q in bf16, in 38 us (139 MB, 3.7 TB/s; kv_put to bf16 33).  With the bits read
-// from the arguments and one address a chunk it took 42.
+// shuffles; the lanes then quantise and pack their own columns.  A warp's next rows and
+// rotations come to shared memory by cp.async meanwhile, each lane's own.  Instructions
+// bound it (2500 a token of 16 + 4 + 4 heads, with 16 warps an SM to hide their latency):
+// 8191 such rows of 128 columns, f32 to 4 bits, with q in bf16, in 31.5 us (139 MB, 4.4
+// TB/s; kv_put to bf16 33).  Loaded only when their turn came they took 38; with heads'
+// places and 64-bit divisions for each token 34.6.
 constexpr int kPutWarps = 8;
 
 // Least and largest; a NaN stays.
@@ -87,10 +89,10 @@ __device__ __forceinline__ void store_codes(unsigned char *p, const float (&x)[V
 
 // By the 16 lanes of a half warp (l: place in it; all 32 lanes call it): the rows
 // u[r][0][0..V) at columns V*l.., u[r][1][..) at D/2 + V*l.. into codes and pairs, all
-// rows' steps side by side.  rows[r]: the row's place in the cache (-1: not written)
+// rows' steps side by side.  rows[r]: the row's place in the cache (~0: not written)
 // of keys, or (values[r]) of values.
 template <int D, int kBits, int R>
-__device__ __forceinline__ void put_quantised(const float (&u)[R][2][D / 32], int l, const int64_t (&rows)[R],
+__device__ __forceinline__ void put_quantised(const float (&u)[R][2][D / 32], int l, const uint32_t (&rows)[R],
                                               const bool (&values)[R], const abg_kvq_cache &c) {
     constexpr int V = D / 32, C = 2 * R;  // chunks of a lane, 2 r + h
     const int lane = threadIdx.x & 31, group = c.group, log_group = group == 32 ? 5 : 6;
@@ -155,13 +157,15 @@ __device__ __forceinline__ void put_quantised(const float (&u)[R][2][D / 32], in
                 x[h][i] = z.x, x[h][i + 1] = z.y;
             }
         }
-        if (rows[r] >= 0) {
-            unsigned char *codes =
-                static_cast<unsigned char *>(values[r] ? c.Vc : c.Kc) + rows[r] * (D * kBits / 8) + V * l * kBits / 8;
+        if (rows[r] != ~0u) {
+            unsigned char *codes = static_cast<unsigned char *>(values[r] ? c.Vc : c.Kc) +
+                                   static_cast<uint64_t>(rows[r]) * (D * kBits / 8) + V * l * kBits / 8;
             store_codes<kBits>(codes, x[0]);
             store_codes<kBits>(codes + D / 2 * kBits / 8, x[1]);
             if (first) {
-                uint32_t *pairs = static_cast<uint32_t *>(values[r] ? c.Vs : c.Ks) + ((rows[r] * D + V * l) >> log_group);
+                uint32_t *pairs = static_cast<uint32_t *>(values[r] ? c.Vs : c.Ks) +
+                                  (static_cast<uint64_t>(rows[r]) << (D == 64 ? 6 : D == 128 ? 7 : 8) >> log_group) +
+                                  (V * l >> log_group);
                 pairs[0] = pair[0];
                 if (!joined) pairs[(D / 2) >> log_group] = pair[1];
             }
@@ -169,56 +173,140 @@ __device__ __forceinline__ void put_quantised(const float (&u)[R][2][D / 32], in
     }
 }
 
+// What the lanes of a warp copy for themselves: `chunks` runs of kBytes a lane, in pieces
+// of up to 16 bytes, a piece of all lanes side by side.
+template <int kBytes>
+struct Pieces {
+    static constexpr int kPiece = std::min(kBytes, 16), kParts = kBytes / kPiece;
+    __device__ static __forceinline__ void bring(uint32_t to, int chunk, int lane, const void *from) {
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            const uint32_t at = to + (chunk * kParts + i) * 32 * kPiece + lane * kPiece;
+            const char *p = static_cast<const char *>(from) + i * kPiece;
+            if constexpr (kPiece == 16) {
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(p) : "memory");
+            } else {
+                asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(p), "n"(kPiece) : "memory");
+            }
+        }
+    }
+    template <typename S, int V>
+    __device__ static __forceinline__ void take(const unsigned char *from, int chunk, int lane, float (&v)[V]) {
+        static_assert(V * sizeof(S) == kBytes);
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+            float t[V / kParts];
+            load_e<S, V / kParts>(
+                reinterpret_cast<const S *>(from + (chunk * kParts + i) * 32 * kPiece + lane * kPiece), t);
+#pragma unroll
+            for (int k = 0; k < V / kParts; ++k) v[i * (V / kParts) + k] = t[k];
+        }
+    }
+};
+
+template <typename S, int D>
+struct PutRing {  // two units of each warp: their rows and rotations (the warps' first ones, then their second)
+    using Rows = Pieces<Put<D>::V * sizeof(S)>;
+    using Turn = Pieces<Put<D>::V * 4>;
+    static constexpr int kRows = 2 * Put<D>::kSteps * 32 * Put<D>::V * static_cast<int>(sizeof(S));
+    static constexpr int kUnit = kRows + 32 * Put<D>::V * 4;
+    static constexpr int kStage = kPutWarps * kUnit;
+};
+
+// A warp's way through the units (token n, group of heads g), tokens first.
+struct PutWalk {
+    uint64_t page_mul;  // 2^64 / page rounded up (page 1: 0): slot / page = page_mul * slot >> 64 for slots below 2^32
+    uint32_t dn;        // from one of a warp's units to its next: tokens
+    int dg, groups;     // and groups; all groups
+};
+
 template <typename S, typename T, int D, int kBits>
 __global__ void __launch_bounds__(32 * kPutWarps, 2) kvq_put_kernel(
-    const __grid_constant__ abg_kvq_put_args a, int groups) {
+    const __grid_constant__ abg_kvq_put_args a, const __grid_constant__ PutWalk walk) {
     using P = Put<D>;
+    using Ring = PutRing<S, D>;
     constexpr int V = P::V, kSteps = P::kSteps;
+    extern __shared__ __align__(16) unsigned char raw[];
     const int lane = threadIdx.x & 31, l = lane & 15, half = lane >> 4;
-    const int64_t units = a.N * groups, stride = static_cast<int64_t>(gridDim.x) * kPutWarps;
+    unsigned char *ring = raw + (threadIdx.x >> 5) * Ring::kUnit;
     const int nq = a.q ? static_cast<int>(a.Hq) : 0, nk = static_cast<int>(a.c.Hkv), heads = nq + 2 * nk;
     // (no launch after this one starts early: some read caches and weights before they wait)
     grid_dep_wait();
     struct Token {
-        int64_t n, src, slot;
+        uint32_t n;
+        int32_t src;  // -1: none
+        int64_t slot;
         int32_t pos;
-        int h0;
+        int h0;       // first head; below 0: no unit
     };
     // all tokens' last heads (keys and values, the longest work) first, so that every
     // warp has its share of each kind
-    auto token = [&](int64_t unit) {
-        Token t{0, -1, -1, 0, 0};
-        if (unit >= units) return t;
-        const int64_t g = div_up_to_64(unit, a.N);
-        t.n = unit - g * a.N;
-        t.h0 = (groups - 1 - static_cast<int>(g)) * P::kHeads;
-        t.src = a.rows ? a.rows[t.n] : t.n;
-        t.slot = a.slots ? a.slots[t.n] : t.n;
-        if (a.cos) t.pos = a.pos[t.n];
+    const uint32_t N = static_cast<uint32_t>(a.N), unit = blockIdx.x * kPutWarps + (threadIdx.x >> 5);
+    int g = static_cast<int>(unit / N);
+    uint32_t n = unit - g * N;
+    auto token = [&] {
+        Token t{n, -1, -1, 0, (walk.groups - 1 - g) * P::kHeads};
+        if (t.h0 >= 0) {
+            t.src = a.rows ? a.rows[n] : static_cast<int32_t>(n);
+            if (t.src >= a.src_rows) t.src = -1;
+            t.slot = a.slots ? a.slots[n] : n;
+            if (a.cos) t.pos = a.pos[n];
+        }
+        n += walk.dn, g += walk.dg;
+        if (n >= N) n -= N, ++g;
         return t;
     };
-    int64_t unit = static_cast<int64_t>(blockIdx.x) * kPutWarps + (threadIdx.x >> 5);
-    Token t = token(unit);
-    for (; unit < units; unit += stride) {
-        const Token next = token(unit + stride);
-        if (t.src >= 0 && t.src < a.src_rows) {
-            float u[kSteps][2][V], c[V], s[V];
+    // a unit's rows and (the lower half's lanes cos, the upper's sin) rotations on their
+    // way; at[r]: the lane's columns of its head of row 0
+    const S *at[kSteps];
+    int at_h0 = -1;
+    auto bring = [&](const Token &t, int stage) {
+        if (t.src >= 0) {
+            if (t.h0 != at_h0) {
+                at_h0 = t.h0;
+#pragma unroll
+                for (int r = 0; r < kSteps; ++r) {
+                    const int h = t.h0 + 2 * r + half;
+                    at[r] = V * l + (h < nq        ? static_cast<const S *>(a.q) + h * a.q_head
+                                     : h < nq + nk ? static_cast<const S *>(a.k) + (h - nq) * a.k_head
+                                                   : static_cast<const S *>(a.v) + min(h - nq - nk, nk - 1) * a.v_head);
+                }
+            }
+            const uint32_t to = smem_u32(ring) + stage * Ring::kStage;
+            const int64_t in_q = t.src * a.q_row, in_k = t.src * a.k_row, in_v = t.src * a.v_row;
 #pragma unroll
             for (int r = 0; r < kSteps; ++r) {
                 const int h = t.h0 + 2 * r + half;
-                if (h >= heads) continue;
-                const S *p = h < nq        ? static_cast<const S *>(a.q) + t.src * a.q_row + h * a.q_head
-                             : h < nq + nk ? static_cast<const S *>(a.k) + t.src * a.k_row + (h - nq) * a.k_head
-                                           : static_cast<const S *>(a.v) + t.src * a.v_row + (h - nq - nk) * a.v_head;
-                load_e<S, V>(p + V * l, u[r][0]);
-                load_e<S, V>(p + D / 2 + V * l, u[r][1]);
+                const S *p = at[r] + (h < nq ? in_q : h < nq + nk ? in_k : in_v);  // (past the last head: the last again)
+                Ring::Rows::bring(to, 2 * r, lane, p);
+                Ring::Rows::bring(to, 2 * r + 1, lane, p + D / 2);
+            }
+            if (a.cos && t.h0 < nq + nk && t.pos >= 0 && t.pos < a.cos_rows)
+                Ring::Turn::bring(to + Ring::kRows, 0, lane,
+                                  (half ? a.sin : a.cos) + t.pos * static_cast<int64_t>(D / 2) + V * l);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    Token t = token(), next = token();
+    bring(t, 0);
+    for (int stage = 0; t.h0 >= 0; stage ^= 1) {
+        __syncwarp();  // the other place has been read
+        bring(next, stage ^ 1);
+        const Token after = token();
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncwarp();
+        if (t.src >= 0) {
+            const unsigned char *from = ring + stage * Ring::kStage;
+            float u[kSteps][2][V], c[V], s[V];
+#pragma unroll
+            for (int r = 0; r < kSteps; ++r) {
+                Ring::Rows::template take<S, V>(from, 2 * r, lane, u[r][0]);
+                Ring::Rows::template take<S, V>(from, 2 * r + 1, lane, u[r][1]);
             }
             if (a.cos && t.h0 < nq + nk) {
-                const bool in = t.pos >= 0 && t.pos < a.cos_rows;
-                const int64_t at = (in ? t.pos : 0) * static_cast<int64_t>(D / 2) + V * l;
-                load_e<float, V>(a.cos + at, c);
-                load_e<float, V>(a.sin + at, s);
-                if (!in)
+                Ring::Turn::template take<float, V>(from + Ring::kRows, 0, l, c);
+                Ring::Turn::template take<float, V>(from + Ring::kRows, 0, l + 16, s);
+                if (!(t.pos >= 0 && t.pos < a.cos_rows))
 #pragma unroll
                     for (int i = 0; i < V; ++i) c[i] = s[i] = __int_as_float(0x7fc00000);
             }
@@ -239,9 +327,12 @@ __global__ void __launch_bounds__(32 * kPutWarps, 2) kvq_put_kernel(
                 factor = __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(ss, static_cast<float>(D)), a.eps)));
             }
             const bool kept = t.slot >= 0 && t.slot < a.c.pages * a.c.page;
-            const int64_t page = kept ? div_up_to_64(t.slot, a.c.page) : 0;
-            const int64_t base = page * a.c.Hkv * a.c.page + (t.slot - page * a.c.page);
-            int64_t rows[kSteps];
+            // (a cache has fewer than 2^32 - 1 rows)
+            const uint32_t slot = static_cast<uint32_t>(t.slot), page_size = static_cast<uint32_t>(a.c.page);
+            const uint64_t low = (walk.page_mul & 0xffffffffu) * slot >> 32, page64 = ((walk.page_mul >> 32) * slot + low) >> 32;
+            const uint32_t page = walk.page_mul ? static_cast<uint32_t>(page64) : slot;
+            const uint32_t base = page * (nk * page_size) + (slot - page * page_size);
+            uint32_t rows[kSteps];
             bool values[kSteps];
 #pragma unroll
             for (int r = 0; r < kSteps; ++r) {
@@ -274,16 +365,16 @@ __global__ void __launch_bounds__(32 * kPutWarps, 2) kvq_put_kernel(
                     }
                 }
                 if (h < nq) {
-                    T *to = static_cast<T *>(a.qo) + (t.n * a.Hq + h) * D;
+                    T *to = static_cast<T *>(a.qo) + (static_cast<int64_t>(t.n) * nq + h) * D;
                     store_e<T, V>(to + V * l, u[r][0]);
                     store_e<T, V>(to + D / 2 + V * l, u[r][1]);
                 }
                 values[r] = h >= nq + nk;
-                rows[r] = kept && h >= nq && h < heads ? base + (values[r] ? h - nq - nk : h - nq) * a.c.page : -1;
+                rows[r] = kept && h >= nq && h < heads ? base + (values[r] ? h - nq - nk : h - nq) * page_size : ~0u;
             }
             if (t.h0 + P::kHeads > nq) put_quantised<D, kBits>(u, l, rows, values, a.c);  // (the whole warp, or none of it)
         }
-        t = next;
+        t = next, next = after;
     }
 }
 
@@ -381,19 +472,25 @@ __global__ void __launch_bounds__(kGetThreads) kvq_get_kernel(const __grid_const
 
 template <typename S, typename T, int D, int kBits>
 cudaError_t put_d(const abg_kvq_put_args &a, bool early, cudaStream_t stream) {
+    using Ring = PutRing<S, D>;
+    const auto kernel = kvq_put_kernel<S, T, D, kBits>;
+    static const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * Ring::kStage);
+    if (attr != cudaSuccess) return attr;
     // as many blocks as fit at once
-    static const int fit = [] {
+    static const int fit = [&] {
         int per = 0;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kvq_put_kernel<S, T, D, kBits>, 32 * kPutWarps, 0) !=
-            cudaSuccess)
-            per = 1;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, 32 * kPutWarps, 2 * Ring::kStage) != cudaSuccess) per = 1;
         return std::max(per, 1) * sm_count();
     }();
     const int heads = static_cast<int>((a.q ? a.Hq : 0) + 2 * a.c.Hkv);
     const int groups = (heads + Put<D>::kHeads - 1) / Put<D>::kHeads;
     const int64_t blocks = (a.N * groups + kPutWarps - 1) / kPutWarps;
-    return launch_kernel(kvq_put_kernel<S, T, D, kBits>, dim3(static_cast<unsigned>(std::min<int64_t>(blocks, fit))),
-                         dim3(32 * kPutWarps), 0, stream, early, a, groups);
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(blocks, fit));
+    const uint64_t stride = uint64_t(grid) * kPutWarps, N = static_cast<uint64_t>(a.N), page = static_cast<uint64_t>(a.c.page);
+    const PutWalk walk{page == 1 ? 0 : ~uint64_t(0) / page + 1, static_cast<uint32_t>(stride % N), static_cast<int>(stride / N),
+                       groups};
+    return launch_kernel(kernel, dim3(grid), dim3(32 * kPutWarps), blocks <= fit ? Ring::kStage : 2 * Ring::kStage, stream,
+                         early, a, walk);
 }
 template <typename S, typename T, int kBits>
 cudaError_t put_bits(const abg_kvq_put_args &a, bool early, cudaStream_t stream) {
