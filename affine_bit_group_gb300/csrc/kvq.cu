@@ -228,7 +228,8 @@ __global__ void __launch_bounds__(32 * kPutWarps, 2) kvq_put_kernel(
     constexpr int V = P::V, kSteps = P::kSteps;
     extern __shared__ __align__(16) unsigned char raw[];
     const int lane = threadIdx.x & 31, l = lane & 15, half = lane >> 4;
-    unsigned char *ring = raw + (threadIdx.x >> 5) * Ring::kUnit;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // (known to be the same for all lanes)
+    unsigned char *ring = raw + warp * Ring::kUnit;
     const int nq = a.q ? static_cast<int>(a.Hq) : 0, nk = static_cast<int>(a.c.Hkv), heads = nq + 2 * nk;
     // (no launch after this one starts early: some read caches and weights before they wait)
     grid_dep_wait();
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(32 * kPutWarps, 2) kvq_put_kernel(
     };
     // all tokens' last heads (keys and values, the longest work) first, so that every
     // warp has its share of each kind
-    const uint32_t N = static_cast<uint32_t>(a.N), unit = blockIdx.x * kPutWarps + (threadIdx.x >> 5);
+    const uint32_t N = static_cast<uint32_t>(a.N), unit = blockIdx.x * kPutWarps + warp;
     int g = static_cast<int>(unit / N);
     uint32_t n = unit - g * N;
     auto token = [&] {
