@@ -81,6 +81,43 @@ def test_kvq_put_is_its_steps_one_by_one(bits, group, kind, qkind, N, Hq, Hkv, D
     assert np.all(np.abs(got.reshape(g.shape) - g) <= room * (1 + 1e-6) + 2.0**-24)  # (2^-25: f16's smallest, of both)
 
 
+@pytest.mark.parametrize("kind,qkind,N,Hq,Hkv,D,page,bits,group", [
+    ("f32", "bf16", 9001, 3, 1, 128, 16, 4, 64), ("bf16", "bf16", 3001, 5, 5, 64, 7, 8, 32),
+    ("f32", "f32", 1100, 16, 4, 256, 48, 4, 32), ("f16", "f16", 1301, 7, 2, 256, 1, 8, 64),
+    ("f32", "f16", 17, 512, 512, 64, 5, 4, 64)])
+def test_kvq_put_of_more_units_than_warps(kind, qkind, N, Hq, Hkv, D, page, bits, group):
+    test_kvq_put_is_its_steps_one_by_one(bits, group, kind, qkind, N, Hq, Hkv, D, page, True, True)
+
+
+@pytest.mark.parametrize("kind,qkind", [("f32", "bf16"), ("bf16", "bf16"), ("f16", "f16")])
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 9, 3), (128, 4, 2), (256, 2, 1)])
+def test_kvq_put_in_one_call_and_in_small_ones(kind, qkind, D, Hq, Hkv):
+    """Rows and positions that there are not among them."""
+    rng = np.random.default_rng([D, Hq])
+    N, R, P, pages, page = 6007, 501, 90, 400, 16
+    qkv = torch.from_numpy(rng.standard_normal((R, Hq + 2 * Hkv, D)).astype(np.float32)).to(TYPES[kind]).cuda()
+    rows, pos = rng.integers(0, R, N), rng.integers(0, P, N)
+    rows[rng.random(N) < 0.2] = -1
+    rows[::97], rows[::89] = R, -2**31
+    pos[::31], pos[::37] = P, -1
+    slots = rng.permutation(pages * page)[:N]
+    slots[::41] = -5
+    rows, pos, slots = i32(rows), i32(pos), i64(slots)
+    w, cos, sin = (dev(rng.standard_normal(n).astype(np.float32)) for n in (D, P * D // 2, P * D // 2))
+    got = []
+    for step in (N, 50):
+        cache = abg.kvq_cache(pages, Hkv, page, D, 8, 32)
+        qo = torch.full((N, Hq, D), 7.0, dtype=TYPES[qkind], device="cuda")
+        for n in range(0, N, step):
+            s = slice(n, n + step)
+            abg.kvq_put(qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:], cache, slots=slots[s], rows=rows[s].clone(), q=qkv[:, :Hq],
+                        qo=qo[s], qn_w=w, kn_w=w, cos=cos, sin=sin, pos=pos[s].clone())
+        got.append([*cache, qo])
+    for one, many in zip(*got):
+        same_bits(host(one.view(torch.int16)), host(many.view(torch.int16)), "one call")
+    assert bool((got[0][4][host(rows) == -1] == 7.0).all()) and bool(got[0][4][host(rows) >= 0].float().abs().sum() != 0)
+
+
 @pytest.mark.parametrize("bits", [4, 8])
 @pytest.mark.parametrize("group", [32, 64])
 @pytest.mark.parametrize("D", [64, 128, 256])
