@@ -26,8 +26,8 @@ constexpr float kLargestHalf = 65504.0f;
 // group) in all 16 lanes' both chunks, and its least and largest value meet by
 // shuffles; the lanes then quantise and pack their own columns.  A warp's next rows and
 // rotations come to shared memory by cp.async meanwhile, each lane's own.  Instructions
-// bound it (2500 a token of 16 + 4 + 4 heads, with 16 warps an SM to hide their latency):
-// 8191 such rows of 128 columns, f32 to 4 bits, with q in bf16, in 31.5 us (139 MB, 4.4
+// bound it (2400 a token of 16 + 4 + 4 heads, with 16 warps an SM to hide their latency):
+// 8191 such rows of 128 columns, f32 to 4 bits, with q in bf16, in 31.2 us (139 MB, 4.5
 // TB/s; kv_put to bf16 33).  Loaded only when their turn came they took 38; with heads'
 // places and 64-bit divisions for each token 34.6.
 constexpr int kPutWarps = 8;
