@@ -19,18 +19,30 @@ namespace {
 constexpr float kLargestHalf = 65504.0f;
 
 // ------------------------------------------------------------- kvq_put -----
-// kv_put's lanes and steps up to the rotated row: a warp a token and 8 of its
-// heads (4 of 256 columns), two at a time, lane l of a half warp with columns
+// kv_put's lanes and steps up to the rotated row: a warp a token and 4 of its
+// heads, two at a time, lane l of a half warp with columns
 // V*l .. V*l+V-1 of a head (V = D/32) and the ones D/2 further on.  A group is then
 // in 4, 8 or 16 lanes' chunks of one half of the columns, or (64 columns a row, one
 // group) in all 16 lanes' both chunks, and its least and largest value meet by
 // shuffles; the lanes then quantise and pack their own columns.  A warp's next rows and
 // rotations come to shared memory by cp.async meanwhile, each lane's own.  Instructions
-// bound it (2400 a token of 16 + 4 + 4 heads, with 16 warps an SM to hide their latency):
-// 8191 such rows of 128 columns, f32 to 4 bits, with q in bf16, in 31.2 us (139 MB, 4.5
-// TB/s; kv_put to bf16 33).  Loaded only when their turn came they took 38; with heads'
-// places and 64-bit divisions for each token 34.6.
+// bound it, and their latency: 8191 tokens of 16 + 4 + 4 heads of 128 columns, f32 to 4
+// bits, with q in bf16, in 30.9 us (139 MB, 4.5 TB/s; kv_put to bf16 33); with 8 heads a warp,
+// for which two blocks an SM have registers, 31.2, with four blocks, which spill, 33.5.
+// Loaded only when their turn came the rows took 38, with heads' places and 64-bit
+// divisions for each token 34.6.  Calls so short that no warp has a second unit take two
+// heads a warp and load them to registers: 8 tokens of 8 + 2 + 2 heads of 256 columns 3.0 us
+// for 3.4, with the ring 4.1.
 constexpr int kPutWarps = 8;
+
+// kOnce: no warp has a second unit.
+template <int D, bool kOnce>
+struct PutUnit {
+    static constexpr int V = D / 32;                // columns of a chunk
+    static constexpr int kSteps = kOnce ? 1 : 2;    // heads of a half warp
+    static constexpr int kHeads = 2 * kSteps;
+    static constexpr int kBlocks = kOnce ? 4 : 3;   // an SM
+};
 
 // Least and largest; a NaN stays.
 __device__ __forceinline__ float least(float a, float b) {
@@ -126,9 +138,9 @@ __device__ __forceinline__ void put_quantised(const float (&u)[R][2][D / 32], in
             hi[i] = largest(up ? hi[i + d] : hi[i], b);
         }
     }
-    if (lanes > C) {  // (twice as many)
-        lo[0] = least(lo[0], __shfl_xor_sync(0xffffffffu, lo[0], C));
-        hi[0] = largest(hi[0], __shfl_xor_sync(0xffffffffu, hi[0], C));
+    for (int d = C; d < lanes; d *= 2) {
+        lo[0] = least(lo[0], __shfl_xor_sync(0xffffffffu, lo[0], d));
+        hi[0] = largest(hi[0], __shfl_xor_sync(0xffffffffu, hi[0], d));
     }
     constexpr float levels = kBits == 4 ? 15.0f : 255.0f;
     const bool bad = !(hi[0] <= kLargestHalf && lo[0] >= -kLargestHalf);
@@ -206,10 +218,11 @@ struct Pieces {
 
 template <typename S, int D>
 struct PutRing {  // two units of each warp: their rows and rotations (all warps' first ones, then their second ones)
-    using Rows = Pieces<Put<D>::V * sizeof(S)>;
-    using Turn = Pieces<Put<D>::V * 4>;
-    static constexpr int kRows = 2 * Put<D>::kSteps * 32 * Put<D>::V * static_cast<int>(sizeof(S));
-    static constexpr int kUnit = kRows + 32 * Put<D>::V * 4;
+    static constexpr int V = D / 32;
+    using Rows = Pieces<V * sizeof(S)>;
+    using Turn = Pieces<V * 4>;
+    static constexpr int kRows = 2 * PutUnit<D, false>::kSteps * 32 * V * static_cast<int>(sizeof(S));
+    static constexpr int kUnit = kRows + 32 * V * 4;
     static constexpr int kStage = kPutWarps * kUnit;
 };
 
@@ -220,11 +233,10 @@ struct PutWalk {
     int dg, groups;     // and groups; all groups
 };
 
-// kOnce: a warp has one unit at most, which it loads to registers.
 template <typename S, typename T, int D, int kBits, bool kOnce>
-__global__ void __launch_bounds__(32 * kPutWarps, 2) kvq_put_kernel(
+__global__ void __launch_bounds__(32 * kPutWarps, PutUnit<D, kOnce>::kBlocks) kvq_put_kernel(
     const __grid_constant__ abg_kvq_put_args a, const __grid_constant__ PutWalk walk) {
-    using P = Put<D>;
+    using P = PutUnit<D, kOnce>;
     using Ring = PutRing<S, D>;
     constexpr int V = P::V, kSteps = P::kSteps;
     extern __shared__ __align__(16) unsigned char raw[];
@@ -496,30 +508,37 @@ __global__ void __launch_bounds__(kGetThreads) kvq_get_kernel(const __grid_const
     }
 }
 
-template <typename S, typename T, int D, int kBits>
-cudaError_t put_d(const abg_kvq_put_args &a, bool early, cudaStream_t stream) {
-    using Ring = PutRing<S, D>;
-    const auto kernel = kvq_put_kernel<S, T, D, kBits, false>;
-    static const cudaError_t attr =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * Ring::kStage);
-    if (attr != cudaSuccess) return attr;
+// kOnce: false if the call is too long for it
+template <typename S, typename T, int D, int kBits, bool kOnce>
+bool put_units(const abg_kvq_put_args &a, bool early, cudaStream_t stream, cudaError_t &e) {
+    constexpr int kSmem = kOnce ? 0 : 2 * PutRing<S, D>::kStage, kHeads = PutUnit<D, kOnce>::kHeads;
+    const auto kernel = kvq_put_kernel<S, T, D, kBits, kOnce>;
+    static const cudaError_t attr = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (attr != cudaSuccess) {
+        e = attr;
+        return true;
+    }
     // as many blocks as fit at once
     static const int fit = [&] {
         int per = 0;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, 32 * kPutWarps, 2 * Ring::kStage) != cudaSuccess) per = 1;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, 32 * kPutWarps, kSmem) != cudaSuccess) per = 1;
         return std::max(per, 1) * sm_count();
     }();
-    const int heads = static_cast<int>((a.q ? a.Hq : 0) + 2 * a.c.Hkv);
-    const int groups = (heads + Put<D>::kHeads - 1) / Put<D>::kHeads;
+    const int heads = static_cast<int>((a.q ? a.Hq : 0) + 2 * a.c.Hkv), groups = (heads + kHeads - 1) / kHeads;
     const int64_t blocks = (a.N * groups + kPutWarps - 1) / kPutWarps;
+    if (kOnce && blocks > fit) return false;
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>(blocks, fit));
     const uint64_t stride = uint64_t(grid) * kPutWarps, N = static_cast<uint64_t>(a.N), page = static_cast<uint64_t>(a.c.page);
     const PutWalk walk{page == 1 ? 0 : ~uint64_t(0) / page + 1, static_cast<uint32_t>(stride % N), static_cast<int>(stride / N),
                        groups};
-    // (without the ring: one f32 unit of 256 columns a warp 3.4 us for 4.1, of 64 columns in 16 bits 3.3 for 3.3)
-    return blocks <= fit ? launch_kernel(kvq_put_kernel<S, T, D, kBits, true>, dim3(grid), dim3(32 * kPutWarps), 0, stream, early,
-                                         a, walk)
-                         : launch_kernel(kernel, dim3(grid), dim3(32 * kPutWarps), 2 * Ring::kStage, stream, early, a, walk);
+    e = launch_kernel(kernel, dim3(grid), dim3(32 * kPutWarps), kSmem, stream, early, a, walk);
+    return true;
+}
+template <typename S, typename T, int D, int kBits>
+cudaError_t put_d(const abg_kvq_put_args &a, bool early, cudaStream_t stream) {
+    cudaError_t e = cudaSuccess;
+    if (!put_units<S, T, D, kBits, true>(a, early, stream, e)) put_units<S, T, D, kBits, false>(a, early, stream, e);
+    return e;
 }
 template <typename S, typename T, int kBits>
 cudaError_t put_bits(const abg_kvq_put_args &a, bool early, cudaStream_t stream) {
