@@ -77,6 +77,8 @@ constexpr int kKvqJoin = 8;    // pieces of a row that a warp has on their way w
 constexpr int kKvqTile = 128;  // tokens of the work line's tiles
 // Rows of q from here on give NaN: their scores could pass f32's range.
 constexpr float kKvqLargestQ = 1.2676506e30f;  // 2^100
+// A score (in base 2) whose product with the row's factor rounds by up to 2^-2.
+constexpr float kKvqFar = 4194304.0f;  // 2^22
 
 template <int D_, int kBits_, int kGroup_, int kNT_, bool kSplit_>
 struct KvqShape {
@@ -675,7 +677,9 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
                 }
             }
             }
-            // maxima and weights (sc is in units of 1/s_f until its exponential)
+            // maxima and weights: sc and m are in units of 1/s_f, so that the largest score is m
+            // itself and not m as a product rounds it (which from 2^23 on could be off by a
+            // weight that passes f16's range, or by all of the weights)
             const int here = key1 - t0;  // tokens of the block that are there
             if (here < kTB) {
 #pragma unroll
@@ -696,7 +700,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
                 for (int e = 0; e < 2; ++e) {
                     float top = fmaxf(sc[0][nt][e], sc[0][nt][2 + e]);
                     if constexpr (kMT == 2) top = fmaxf(top, fmaxf(sc[kMT - 1][nt][e], sc[kMT - 1][nt][2 + e]));
-                    above = above || top * (e ? f.y : f.x) > m[nt][e] + 1.5f;
+                    above = above || (top - m[nt][e]) * (e ? f.y : f.x) > 1.5f;
                 }
             }
             if (__any_sync(0xffffffffu, above)) {
@@ -710,8 +714,8 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
                         if constexpr (kMT == 2) top = fmaxf(top, fmaxf(sc[kMT - 1][nt][e], sc[kMT - 1][nt][2 + e]));
 #pragma unroll
                         for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                        top = fmaxf(m[nt][e], top * (e ? f.y : f.x));
-                        corr[e] = kvq_exp2(m[nt][e] - (top == -INFINITY ? 0.0f : top));
+                        top = fmaxf(m[nt][e], top);
+                        corr[e] = kvq_exp2((m[nt][e] - (top == -INFINITY ? 0.0f : top)) * (e ? f.y : f.x));
                         m[nt][e] = top;
                         l[nt][e] *= corr[e];
 #pragma unroll
@@ -734,7 +738,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             float &v = sc[mt][nt][2 * h + e];
-                            v = kvq_exp2(fmaf(v, e ? f.y : f.x, -ref));
+                            v = kvq_exp2((v - ref) * (e ? f.y : f.x));
                             l[nt][e] += v;
                         }
                 }
@@ -883,9 +887,13 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
             float top = mw;
 #pragma unroll
             for (int d = 1; d < 8; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            top = fmaxf(top, M);
+            const float f = s_f[r];
+            top = fmaxf(__fmul_rn(top, f), M);
+            // what the rounding of a moderate maximum took is in the weights; that of a far one
+            // is not, as it could be all of them
+            const float over = fabsf(top) < kKvqFar ? fmaf(mw, f, -top) : __fsub_rn(__fmul_rn(mw, f), top);
             // (no maximum, but a weight: a NaN, which stays, as one that is far below does)
-            const float fw = mw == -INFINITY ? 1.0f : exp2f(mw - top);
+            const float fw = mw == -INFINITY ? 1.0f : exp2f(over);
             const float fd = M == -INFINITY ? 1.0f : exp2f(M - top);
             const bool none = L == 0.0f;
             M = top;
@@ -894,15 +902,15 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
             for (int i = 0; i < kE; ++i) v[i] = none ? 0.0f : v[i] * fd;
 #pragma unroll
             for (int u = 0; u < kWarps; ++u) {
-                const float f = __shfl_sync(0xffffffffu, fw, u, kL), lu = __shfl_sync(0xffffffffu, lw, u, kL);
+                const float fu = __shfl_sync(0xffffffffu, fw, u, kL), lu = __shfl_sync(0xffffffffu, lw, u, kL);
                 if (lu == 0.0f) continue;  // no token: nothing to add
-                L = fmaf(lu, f, L);
+                L = fmaf(lu, fu, L);
                 const float *from = reinterpret_cast<const float *>(raw + S::kFixed + u * S::kWarpBytes) +
                                     (r >> 1) * S::kRowPair + (r & 1) * D + ln * kE;
 #pragma unroll
                 for (int i = 0; i < kE; i += 2) {
                     const float2 y = *reinterpret_cast<const float2 *>(from + i);
-                    v[i] = fmaf(y.x, f, v[i]), v[i + 1] = fmaf(y.y, f, v[i + 1]);
+                    v[i] = fmaf(y.x, fu, v[i]), v[i + 1] = fmaf(y.y, fu, v[i + 1]);
                 }
             }
         }

@@ -525,6 +525,57 @@ def test_kvq_attn_many_weights_far_below_the_largest(kind, tall):
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("bits,group", FORMATS)
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_kvq_attn_scores_whose_rounding_moves_a_weight(kind, bits, group, sign):
+    """Rows of q up to 2^95, so that a score's last bit is worth many powers of two:
+    the largest score has all the weight, and rows of moderate scores beside them
+    are as exact as alone.  K is a bias of whole numbers, each once, in its first
+    group, where q is constant, and q is 0 elsewhere."""
+    c, _ = attn_case(15, kind, bits, group, 4, 2, 128, 16, [700], [6], gate=False, y32=True, tail=0)
+    rng = np.random.default_rng([80, bits, group])
+    Kw, Kp, Vw, Vp = (a.copy() for a in arrays(c["cache"]))
+    t = np.arange(700)
+    at = host(c["table"])[0][t // 16], slice(None), t % 16
+    bias = sign * (1 + rng.permutation(1500)[:700])
+    Kp[(*at, 0, 0)], Kp[(*at, 0, 1)] = 0.0, bias[:, None]
+    top = np.array([-6, 10, 12, 13, 14, 11] if kind == "f16" else [-6, 16, 18, 23, 30, 95])
+    q = np.zeros((6, 4, 128))
+    q[..., :group] = (rng.uniform(1, 2, (6, 4)) * 2.0 ** top[:, None])[..., None]
+    Kd = np.zeros((2, 9, 128))
+    Kd[:, :6, :group] = 3008.0 if sign > 0 else -0.25  # above all of the cache's
+    c.update(q=torch.from_numpy(q).to(TYPES[kind]).cuda(), Kd=torch.from_numpy(Kd).to(TYPES[kind]).cuda(),
+             cache=as_cache(Kw, Kp, Vw, Vp))
+    (K, _), (V, Vmag) = ref.values(Kw, Kp, bits), ref.values(Vw, Vp, bits)
+    Vd, far = wide(c["Vd"]), top > 0
+    for own in (False, True):
+        mask = np.where(own, 1 << np.arange(6), 0)[:, None]
+        y = torch.full_like(c["y"], 5.0)
+        abg.kvq_attn(**dict(c, mask=i64(mask), y=y))
+        got = wide(y).reshape(6, 2, 2, 128)  # of two query heads a cached head
+        if own:
+            want, mag = Vd[:, :6].swapaxes(0, 1)[:, :, None], np.abs(Vd[:, :6]).swapaxes(0, 1)[:, :, None]
+        else:
+            w = int(np.argmax(bias))
+            want, mag = (x[host(c["table"])[0][w // 16], :, w % 16][None, :, None] for x in (V, Vmag))
+        # one weight that is not 0: rounded, as its scale times it and the products, to 11 or 22 bits and cut off
+        # at 2^-17 or 2^-23 (twice each), and some sixteen steps in f32 from there to the quotient
+        bound = mag * (2.0**-11 + 2 * 2.0**-17 if kind == "bf16" else 2.0**-22 + 2 * 2.0**-23) + mag * 16 * U32
+        err = np.abs(got - want)
+        assert (err <= bound)[far].all(), (own, top, np.nanmax(err / mag, axis=(1, 2, 3)), np.isnan(got).any(axis=(1, 2, 3)))
+        if not own:
+            # the row of moderate scores: f32 steps of a score's magnitude (as check_attn's)
+            exact, terms = (draft_ref.tree_attn(f(wide(c["q"])), k, v, host(c["table"]), host(c["lens"]), host(c["cu"]),
+                                                f(wide(c["Kd"])), f(Vd), bits_of(i64(mask)))[i]
+                            for i, f, k, v in ((0, np.array, K, V), (1, np.abs, np.nan_to_num(ref.values(Kw, Kp, bits)[1]),
+                                                                     np.nan_to_num(Vmag))))
+            high, mags = terms[..., :1], terms[..., 1:]
+            room = high * (U32 * (2 * (2 * (128 + 8) + 4) * mags + 4 * (64 + 700 / 16 + 600)) +
+                           ((2.0**-11 if kind == "bf16" else 2.0**-22) + 700 * 2.0**-38) * 1.01)
+            assert (np.abs(wide(y) - exact) <= room)[~far].all()
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
 def test_kvq_attn_is_the_same_on_every_run_and_on_other_streams(kind):
     c, k = attn_case(13, kind, 4, 64, 8, 2, 128, 16, [5000, 70, 900], [4, 3, 1])
     abg.kvq_attn(**c)
