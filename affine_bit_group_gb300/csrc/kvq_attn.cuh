@@ -521,8 +521,10 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
         // -- the warp's blocks --
         float o[kTiles][kNT][4];             // columns (8 or 4 a lane of a group, two a tile) x rows 2 quad, + 1
         float l[kNT][2], m[kNT][2], bias[kG][kNT][2];
-        int ev = 0;                          // the largest scale of V so far is below 2^(ev - 14)
-        float up = pow2i(28), down = pow2i(-28) * S::kUnit;  // 2^(28 - ev), and back for the products' results
+        // up brings the largest scale of V so far to 2^13 .. 2^14, down its products' results
+        // back; one of these f16 bits is twice as large or more (at first: any that is not 0)
+        float up = pow2i(37), down = pow2i(-37) * S::kUnit;
+        uint32_t larger = 1;
 #pragma unroll
         for (int i = 0; i < kTiles; ++i)
 #pragma unroll
@@ -556,10 +558,13 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
                         big = max(big, v < 0x7c00u ? v : 0u);
                     }
                 }
-                if (__any_sync(0xffffffffu, static_cast<int>(big >> 10) > ev)) {
-                    ev = max(ev, static_cast<int>(__reduce_max_sync(0xffffffffu, big) >> 10));
-                    up = pow2i(28 - ev);
-                    down = pow2i(ev - 28) * S::kUnit;
+                if (__any_sync(0xffffffffu, big >= larger)) {
+                    // (as a f32, where f16's subnormal numbers have exponents of their own)
+                    const float top = kvq_float2(__reduce_max_sync(0xffffffffu, big)).x;
+                    const int ev = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+                    up = pow2i(13 - ev);
+                    down = pow2i(ev - 13) * S::kUnit;
+                    larger = __half_as_ushort(__float2half_rn(pow2i(ev + 1)));
                 }
                 if (lane < kTB) {
                     float2 kk[kG], vv[kG];

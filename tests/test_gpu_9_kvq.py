@@ -575,6 +575,36 @@ def test_kvq_attn_scores_whose_rounding_moves_a_weight(kind, bits, group, sign):
             assert (np.abs(wide(y) - exact) <= room)[~far].all()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("scale", [-24, -20, -16, -14])
+@pytest.mark.parametrize("tall", [[(0, 28.5)], [(5, 30.0), (6, 18.0)]])
+def test_kvq_attn_many_small_weights_and_small_scales(kind, scale, tall):
+    """test_kvq_attn_many_weights_far_below_the_largest with V's scale a power of two
+    down to f16's smallest: the same result times it."""
+    n, page, B, D = 131072, 128, 320, 64
+    pairs = [np.zeros((n // page, 1, page, 1, 2), np.float16) for _ in range(2)]
+    words = [np.zeros((n // page, 1, page, 8), np.uint32) for _ in range(2)]
+    words[1][:] = 0x11111111
+    pairs[1][..., 0] = 2.0**scale
+    q = np.zeros((B, 1, D), np.float32)
+    q[..., 0] = 16.0
+    for t, lg in tall:
+        pairs[0][t // page, 0, t % page, 0, 1] = lg * np.log(2) * np.sqrt(D) / 16.0  # K is the bias; q sums to 16
+        words[1][t // page, 0, t % page] = 0
+    s = pairs[0][..., 0, 1].astype(np.float64).ravel() * 16 / np.sqrt(D)
+    w = np.exp(s - s.max())
+    want = (w * (words[1][..., 0] > 0).ravel()).sum() / w.sum()
+    y = torch.empty((B, 1, D), device="cuda")
+    draft = torch.zeros((1, B, D), dtype=TYPES[kind], device="cuda")
+    abg.kvq_attn(torch.from_numpy(q).to(TYPES[kind]).cuda(), as_cache(words[0], pairs[0], words[1], pairs[1]),
+                 i32(np.arange(n // page)[None].repeat(B, 0)), i32([n] * B), i32(np.arange(B + 1)), draft, draft,
+                 i64(np.zeros((B, 1))), y)
+    # as there, all of it in units of the scale
+    bound = (2.0**-11 if kind == "bf16" else 2.0**-22) * 1.01 * want + n * 2.0**-38 + want * U32 * (2 * n / 16 + 600)
+    got = host(y).astype(np.float64) * 2.0**-scale
+    assert np.abs(got - want).max() <= bound, (got.min(), got.max(), want, bound)
+
+
 @pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
 def test_kvq_attn_is_the_same_on_every_run_and_on_other_streams(kind):
     c, k = attn_case(13, kind, 4, 64, 8, 2, 128, 16, [5000, 70, 900], [4, 3, 1])
