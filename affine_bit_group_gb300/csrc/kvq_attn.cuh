@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
                 const bool bad = top >= kKvqLargestQ, none = top == 0.0f;
                 const float up = bad || none ? 1.0f : pow2i(ex);
                 // s_f * (s acc + b qs) is the score in base 2, acc of the scaled q and the operands
-                if (lane == 1) s_l[qr] = p.scale2 / up;  // (until the drafts are done)
+                if (lane == 1) s_l[qr] = 1.0f / up;  // (until the drafts are done)
                 if (lane == 0) s_f[qr] = bad ? __int_as_float(0x7fc00000) : p.scale2 * S::kUnit / up;
                 if (lane % (kGroup / E) == 0) s_qs[lane / (kGroup / E) * kRT + qr] = sum * up * (1.0f / S::kUnit);
 #pragma unroll
@@ -468,8 +468,8 @@ __global__ void __launch_bounds__(S::kThreads, S::kBlocks) kvq_attn_kernel(const
         if (d1 > d0) {
             float qv[kE];
 #pragma unroll
-            for (int i = 0; i < kE; ++i) qv[i] = s_qf[r * (D + 4) + ln * kE + i];
-            const float f = s_f[r] == s_f[r] ? s_l[r] : __int_as_float(0x7fc00000);
+            for (int i = 0; i < kE; ++i) qv[i] = s_qf[r * (D + 4) + ln * kE + i] * s_l[r];  // (as it was: K has f32's range)
+            const float f = s_f[r] == s_f[r] ? p.scale2 : __int_as_float(0x7fc00000);
             for (int w0 = d0;;) {
                 float sc[kBatch], top = d_m;
 #pragma unroll

@@ -605,6 +605,16 @@ def test_kvq_attn_many_small_weights_and_small_scales(kind, scale, tall):
     assert np.abs(got - want).max() <= bound, (got.min(), got.max(), want, bound)
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_kvq_attn_large_draft_keys_under_small_queries(kind, D):
+    """Drafts' K of 2^116 with q of 2^-80, whose products would pass f32's range with q
+    brought up to f16's, and the other way round: finite results."""
+    c, k = attn_case(16, kind, 4, 32, 4, 2, D, 16, [100, 0], [5, 9], gate=False)
+    for q, e in ((2.0**-80, 2.0**116), (2.0**-115, 2.0**115), (2.0**60, 2.0**-60)):
+        check_attn(dict(c, q=c["q"] * q, Kd=c["Kd"] * e, y=c["y"].clone(), lens=i32([100 if q < 1 else 0, 0])), k)
+
+
 @pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
 def test_kvq_attn_is_the_same_on_every_run_and_on_other_streams(kind):
     c, k = attn_case(13, kind, 4, 64, 8, 2, 128, 16, [5000, 70, 900], [4, 3, 1])
