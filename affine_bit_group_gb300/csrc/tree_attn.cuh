@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
                 const float f = L == 0.0f ? 0.0f : exp2f(m - ref);
                 L *= f;
 #pragma unroll
-                for (int e = 0; e < E; ++e) o[e] = f == 0.0f && o[e] == o[e] ? 0.0f : o[e] * f;  // (a NaN stays)
+                for (int e = 0; e < E; ++e) o[e] *= f;  // (without weight o is 0; a NaN stays, as infinity * 0)
 #pragma unroll
                 for (int w = 1; w < kWarps; ++w) {
                     const float2 ml = s_ml[warp + w];

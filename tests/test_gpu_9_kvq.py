@@ -616,6 +616,30 @@ def test_kvq_attn_large_draft_keys_under_small_queries(kind, D):
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("tiles", [16, 17, 18, 40, 120])
+def test_kvq_attn_infinity_far_below_the_largest_score_stays(kind, tiles):
+    """An infinite value of a draft, in the unit's last piece, that another piece
+    outweighs by 2^800: infinite or (infinity times 0) NaN, whichever of a row's warps
+    joins its piece, and never a number."""
+    tokens = 128 * tiles
+    c, k = attn_case(17, kind, 4, 32, 4, 2, 128, 16, [tokens], [1], gate=False, tail=0)
+    Kw, Kp, Vw, Vp = (a.copy() for a in arrays(c["cache"]))
+    q, Kd, Vd = c["q"].clone(), c["Kd"].clone(), c["Vd"].clone()
+    q[..., :32], Kd[:], c["mask"] = 5.0, 0.0, i64([[1]])
+    Vd[0, 0, 70], Vd[1, 0, 5] = float("inf"), float("-inf")
+    want = np.zeros((1, 4, 128), bool)
+    want[:, :2, 70] = want[:, 2:, 5] = True
+    every = np.arange(tokens)
+    Kp[host(c["table"])[0][every // 16], :, every % 16, 0] = 0.0
+    for top in (5, 700, 1300, tokens - 5):
+        p = Kp.copy()
+        p[host(c["table"])[0][top // 16], :, top % 16, 0, 1] = 40.0
+        y = torch.zeros_like(c["y"])
+        abg.kvq_attn(**dict(c, cache=as_cache(Kw, p, Vw, Vp), q=q, Kd=Kd, Vd=Vd, y=y))
+        assert np.array_equal(~np.isfinite(wide(y)), want), top
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16", "f16"])
 def test_kvq_attn_is_the_same_on_every_run_and_on_other_streams(kind):
     c, k = attn_case(13, kind, 4, 64, 8, 2, 128, 16, [5000, 70, 900], [4, 3, 1])
     abg.kvq_attn(**c)
