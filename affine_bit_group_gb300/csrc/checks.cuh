@@ -5,7 +5,10 @@
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
+#include <cstdlib>
 #include <initializer_list>
+#include <utility>
 
 namespace abg {
 
@@ -44,6 +47,42 @@ inline bool bounded(std::initializer_list<int64_t> f) {
         n *= v > 0 ? v : 1;
     }
     return true;
+}
+
+// [N] rows of H heads of D columns, at these strides (that of a single row or head
+// does not count).
+struct RowStrides {
+    int64_t row, head;
+};
+// Rows that do not lie in one another: the heads of a row side by side before the
+// next row, or the rows of a head before the next.
+inline bool rows_apart(RowStrides s, int64_t N, int64_t H, int64_t D) {
+    return (N == 1 && H == 1) || ((H == 1 || s.head >= D) && (N == 1 || s.row >= (H - 1) * s.head + D)) ||
+           ((N == 1 || s.row >= D) && (H == 1 || s.head >= (N - 1) * s.row + D));
+}
+// Whether two such sets of rows (each rows_apart), the second `off` >= 0 columns on, have
+// no column in common.  Exact at the same strides: the distances between their rows are
+// off + i*row + j*head, |i| < N, |j| < H, and none is below D.  At other ones only where
+// each row of the one (all its heads) lies between two of the other's, or each head (all
+// its rows) between two heads.
+inline bool rows_between(int64_t off, RowStrides a, RowStrides b, int64_t N, int64_t H, int64_t D) {
+    if ((N == 1 || a.row == b.row) && (H == 1 || a.head == b.head)) {
+        // the shorter of the two axes step by step, the next multiples of the other one's stride
+        int64_t n = N, step = N == 1 ? 0 : a.row, h = H, each = H == 1 ? 0 : a.head;
+        if (n < h) std::swap(n, h), std::swap(step, each);
+        for (int64_t j = 1 - h; j < h; ++j) {
+            const int64_t x = off + j * each;  // x - i*step, 1 - n <= i < n
+            const int64_t low = n == 1 ? 0 : std::clamp(x / step - (x % step < 0), 1 - n, n - 2);
+            for (int64_t i = low; i <= low + (n > 1); ++i)
+                if (std::abs(x - i * step) < D) return false;
+        }
+        return true;
+    }
+    auto within = [off](int64_t a_period, int64_t b_period, int64_t a_extent, int64_t b_extent) {
+        return a_period > 0 && a_period == b_period && off % a_period >= a_extent && off % a_period + b_extent <= a_period;
+    };
+    return within(a.row, b.row, (H - 1) * a.head + D, (H - 1) * b.head + D) ||
+           within(a.head, b.head, (N - 1) * a.row + D, (N - 1) * b.row + D);
 }
 inline cudaStream_t to_stream(void *s) { return static_cast<cudaStream_t>(s); }
 

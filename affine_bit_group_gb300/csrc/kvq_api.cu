@@ -26,13 +26,6 @@ CacheSpans spans_of(const abg_kvq_cache &c) {
             span(c.Vc, codes, static_cast<size_t>(c.bits)), span(c.Vs, pairs, 4)};
 }
 
-// Rows [N] of H heads at these strides that do not lie in one another: the heads
-// of a row side by side before the next row, or the rows of a head before the next.
-bool rows_apart(int64_t N, int64_t row, int64_t H, int64_t head, int64_t D) {
-    return (N == 1 && H == 1) || ((H == 1 || head >= D) && (N == 1 || row >= (H - 1) * head + D)) ||
-           ((N == 1 || row >= D) && (H == 1 || head >= (N - 1) * row + D));
-}
-
 }  // namespace
 
 extern "C" {
@@ -93,8 +86,8 @@ abg_status abg_kvq_get(const abg_kvq_get_args *args, void *stream) {
     if (!on(a.k, 16) || !on(a.v, 16) || !on(a.slots, 8) || !cache_aligned(c)) return ABG_EALIGN;
     for (int64_t st : {a.k ? a.k_row : 0, a.k ? a.k_head : 0, a.v ? a.v_row : 0, a.v ? a.v_head : 0})
         if (st * e % 16 != 0) return ABG_EALIGN;
-    if ((a.k && !rows_apart(a.N, a.k_row, c.Hkv, a.k_head, c.D)) ||
-        (a.v && !rows_apart(a.N, a.v_row, c.Hkv, a.v_head, c.D)))
+    if ((a.k && !rows_apart({a.k_row, a.k_head}, a.N, c.Hkv, c.D)) ||
+        (a.v && !rows_apart({a.v_row, a.v_head}, a.N, c.Hkv, c.D)))
         return ABG_EALIAS;
     const int64_t ke = (c.Hkv - 1) * a.k_head + c.D, ve = (c.Hkv - 1) * a.v_head + c.D;  // of one row's heads
     const Span ks = span(a.k, (a.N - 1) * a.k_row + ke, static_cast<size_t>(e)),
@@ -103,13 +96,12 @@ abg_status abg_kvq_get(const abg_kvq_get_args *args, void *stream) {
     for (const Span &out : {a.k ? ks : none, a.v ? vs : none})
         if (!apart({out}, {s.Kc, s.Ks, s.Vc, s.Vs, span(a.slots, a.N, 8)})) return ABG_EALIAS;
     if (a.k && a.v && !apart({ks, vs}, {})) {
-        // k and v of one buffer: a row of the one beside that of the other, or a head beside a head
+        // k and v of one buffer
         const bool k_first = ks.lo < vs.lo;
         const int64_t off = static_cast<int64_t>(k_first ? vs.lo - ks.lo : ks.lo - vs.lo) / e;
-        const int64_t one = k_first ? ke : ve, two = k_first ? ve : ke, row = a.k_row, head = a.k_head;
-        const bool rows = row > 0 && off % row >= one && off % row + two <= row;
-        const bool heads = head > 0 && row % head == 0 && head == a.v_head && off % head >= c.D && off % head + c.D <= head;
-        if (row != a.v_row || !(rows || heads)) return ABG_EALIAS;
+        const RowStrides k{a.k_row, a.k_head}, v{a.v_row, a.v_head};
+        if (!(k_first ? rows_between(off, k, v, a.N, c.Hkv, c.D) : rows_between(off, v, k, a.N, c.Hkv, c.D)))
+            return ABG_EALIAS;
     }
     return cuda_status(launch_kvq_get(a, early_launches(), to_stream(stream)), "kvq_get launch");
 }

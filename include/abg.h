@@ -754,6 +754,9 @@ abg_status abg_kvq_put(const abg_kvq_put_args *a, void *stream);
  *          0 .. pages*page-1 gives zeros
  * Rows, row strides and head strides are multiples of 16 bytes; rows may not
  * lie in one another (k_row and k_head span distinct rows).
+ * k and v may lie in one buffer, between one another's rows or heads: at the same
+ * strides wherever no two rows meet (a single row's or head's stride does not
+ * count), at others where whole rows or heads of the one lie between the other's.
  */
 typedef struct abg_kvq_get_args {
     abg_kvq_cache c;

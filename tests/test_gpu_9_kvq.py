@@ -230,6 +230,36 @@ def test_kvq_get_without_slots_and_of_every_code():
             assert np.array_equal(host(got), want)
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("Hkv", [1, 2, 3])
+@pytest.mark.parametrize("N", [1, 2, 5])
+def test_kvq_get_into_one_buffer(kind, Hkv, N):
+    """k and v between one another in one buffer: heads in turn (in rows with room at
+    their end too), heads before rows with k and v in turn or side by side, and every
+    other place as it was."""
+    rng = np.random.default_rng([90, Hkv, N])
+    D, T = 64, TYPES[kind]
+    cache = as_cache(*random_cache(rng, 2, Hkv, 4, D, 4, 32))
+    slots = i64(rng.permutation(8)[:N])
+    want = [torch.empty((N, Hkv, D), dtype=T, device="cuda") for _ in range(2)]
+    abg.kvq_get(cache, *want, slots=slots)
+    for shape, parts in (((N, 2 * Hkv, D), lambda b: (b[:, 0::2], b[:, 1::2])),
+                         ((N, 2 * Hkv + 1, D), lambda b: (b[:, 1::2], b[:, 0:2 * Hkv:2])),
+                         ((N, 2 * Hkv + 1, D), lambda b: (b[:, Hkv + 1:], b[:, :Hkv])),
+                         ((Hkv, N, 2, D), lambda b: (b[:, :, 0].transpose(0, 1), b[:, :, 1].transpose(0, 1))),
+                         ((Hkv, 2, N, D), lambda b: (b[:, 1].transpose(0, 1), b[:, 0].transpose(0, 1))),
+                         ((Hkv, N + 1, 3, D), lambda b: (b[:, :N, 2].transpose(0, 1), b[:, 1:, 0].transpose(0, 1)))):
+        got, exp = (torch.full(shape, 7.0, dtype=T, device="cuda") for _ in range(2))
+        abg.kvq_get(cache, *parts(got), slots=slots)
+        for to, x in zip(parts(exp), want):
+            to.copy_(x)
+        assert torch.equal(got, exp), shape
+    if N > 1:
+        both = torch.zeros((N, 2 * Hkv, D), dtype=T, device="cuda")
+        with pytest.raises(abg.AbgError, match="output overlaps"):
+            abg.kvq_get(cache, both[:, :Hkv], both[:, Hkv - 1:2 * Hkv - 1], slots=slots)
+
+
 # --------------------------------------------------------------- kvq_attn ----
 def attn_case(seed, kind, bits, group, Hq, Hkv, D, page, lens, spans, words=None, gate=True, y32=False, tail=2, qscale=2.0):
     """Inputs (device) of one call: random pages, masks of random trees, NaN

@@ -88,6 +88,59 @@ def test_kvq_get_refuses(lib, change, status):
     assert call(lib, "abg_kvq_get", abg._KvqGetArgs, GET, change, None) == status
 
 
+def test_kvq_get_rows_of_one_buffer_are_refused_where_they_meet_and_only_there(tmp_path):
+    """The check's rule against every column written out: all places of v's rows
+    beside k's, at equal strides exactly; at others never accepted where they meet."""
+    prog = tmp_path / "rows.cpp"
+    prog.write_text(r"""
+#include "checks.cuh"
+#include <cstdio>
+#include <vector>
+using namespace abg;
+static bool meet(int64_t off, RowStrides a, RowStrides b, int64_t N, int64_t H, int64_t D) {
+    std::vector<char> at(4096, 0);
+    for (int64_t n = 0; n < N; ++n)
+        for (int64_t h = 0; h < H; ++h)
+            for (int64_t d = 0; d < D; ++d) at[n * a.row + h * a.head + d] = 1;
+    for (int64_t n = 0; n < N; ++n)
+        for (int64_t h = 0; h < H; ++h)
+            for (int64_t d = 0; d < D; ++d)
+                if (off + n * b.row + h * b.head + d < 4096 && at[off + n * b.row + h * b.head + d]) return true;
+    return false;
+}
+int main() {
+    const int64_t D = 2;
+    long wrong = 0, apart = 0, met = 0, mixed = 0;
+    for (int64_t N = 1; N <= 4; ++N)
+        for (int64_t H = 1; H <= 4; ++H)
+            for (int64_t row = 0; row <= 26; ++row)
+                for (int64_t head = 0; head <= 26; ++head) {
+                    const RowStrides a{row, head};
+                    if (!rows_apart(a, N, H, D)) continue;
+                    for (int64_t off = 0; off < (N - 1) * row + (H - 1) * head + D; ++off) {
+                        // a single row's or head's stride is any number
+                        const RowStrides b{N == 1 ? 7 : row, H == 1 ? 5 : head};
+                        const bool m = meet(off, a, b, N, H, D);
+                        wrong += rows_between(off, a, b, N, H, D) == m;
+                        ++(m ? met : apart);
+                        for (int64_t other = 0; other <= 12; other += 3)
+                            for (const RowStrides &c : {RowStrides{row, other}, RowStrides{other, head}, RowStrides{other, other}})
+                                if (rows_apart(c, N, H, D) && rows_between(off, a, c, N, H, D)) {
+                                    wrong += meet(off, a, c, N, H, D);
+                                    ++mixed;
+                                }
+                    }
+                }
+    std::printf("%ld %d %d %d\n", wrong, apart > 1000, met > 1000, mixed > 1000);
+}
+""")
+    exe = tmp_path / "rows"
+    subprocess.run(["g++", "-std=c++17", "-O1", "-I", os.path.join(ROOT, "affine_bit_group_gb300", "csrc"), "-I",
+                    "/usr/local/cuda/include", str(prog), "-o", str(exe)], check=True)
+    out = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout
+    assert out.split() == ["0", "1", "1", "1"]
+
+
 ATTN = dict(q=A + 4 * STEP, table=A + 5 * STEP, lens=A + 6 * STEP, cu=A + 7 * STEP, Kd=A + 8 * STEP, Vd=A + 9 * STEP,
             mask=A + 10 * STEP, gate=A + 11 * STEP, y=A + 12 * STEP, ysum=A + 13 * STEP, B=3, N=20, Hq=8, width=4, drafts=20,
             words=1, max_span=9, type=1, y_type=0)
