@@ -270,6 +270,26 @@ __global__ void __launch_bounds__(64 * W) tree_plan_kernel(const int32_t *parent
 // 53 us.
 constexpr int kPutWarps = 8;
 
+template <int D>
+struct Put {
+    static constexpr int V = D / 32;                    // columns of a chunk
+    static constexpr int kSteps = D == 256 ? 2 : 4;
+    static constexpr int kHeads = 2 * kSteps;           // of a unit
+};
+
+// Pairwise tree of V values.
+template <int V>
+__device__ __forceinline__ float chunk_tree(const float (&u)[V]) {
+    float x[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) x[i] = __fmul_rn(u[i], u[i]);
+#pragma unroll
+    for (int k = V / 2; k >= 1; k >>= 1)
+#pragma unroll
+        for (int i = 0; i < k; ++i) x[i] = __fadd_rn(x[2 * i], x[2 * i + 1]);
+    return x[0];
+}
+
 template <typename S, typename T, int D>
 __global__ void __launch_bounds__(32 * kPutWarps, D == 256 ? 2 : D == 128 ? 3 : 4) kv_put_kernel(
     const __grid_constant__ abg_kv_put_args a, int groups) {

@@ -1,5 +1,5 @@
-// Rows of keys, values and queries as kv_put and kvq_put take them: loads and
-// stores of a lane's columns, and the pairwise tree of their squares.
+// Rows of keys, values and queries: loads and stores of a thread's columns in
+// the three types, and the division that finds a token's page.
 #pragma once
 
 #include "abg_dev.cuh"
@@ -67,26 +67,6 @@ __device__ __forceinline__ void store_e(T *p, const float (&v)[E]) {
 #pragma unroll
         for (int i = 0; i < kBytes / 16; ++i) reinterpret_cast<uint4 *>(p)[i] = reinterpret_cast<uint4 *>(t)[i];
     }
-}
-
-template <int D>
-struct Put {
-    static constexpr int V = D / 32;                    // columns of a chunk
-    static constexpr int kSteps = D == 256 ? 2 : 4;
-    static constexpr int kHeads = 2 * kSteps;           // of a unit
-};
-
-// Pairwise tree of V values.
-template <int V>
-__device__ __forceinline__ float chunk_tree(const float (&u)[V]) {
-    float x[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = __fmul_rn(u[i], u[i]);
-#pragma unroll
-    for (int k = V / 2; k >= 1; k >>= 1)
-#pragma unroll
-        for (int i = 0; i < k; ++i) x[i] = __fadd_rn(x[2 * i], x[2 * i + 1]);
-    return x[0];
 }
 
 }  // namespace abg

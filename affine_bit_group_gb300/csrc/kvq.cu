@@ -56,7 +56,7 @@ __device__ __forceinline__ float largest(float a, float b) {
     return r;
 }
 
-// Pairwise tree of V squares (chunk_tree's, the products in pairs).
+// Pairwise tree of V squares, as kv_put's, the products in pairs.
 template <int V>
 __device__ __forceinline__ float square_tree(const float (&u)[V]) {
     float x[V];

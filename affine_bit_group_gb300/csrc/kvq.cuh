@@ -1,4 +1,4 @@
-// The quantised cache's row format and the host launchers of its kernels.
+// Host launchers of the quantised cache's kernels (kvq.cu, kvq_attn.cu).
 #pragma once
 
 #include "../../include/abg.h"

@@ -225,11 +225,6 @@ __device__ __forceinline__ void kvq_row(const void *p, int type, int64_t at, flo
         load_e<__half, E>(static_cast<const __half *>(p) + at, v);
     }
 }
-__device__ __forceinline__ float kvq_value(const void *p, int type, int64_t at) {
-    return type == ABG_SB_F32    ? static_cast<const float *>(p)[at]
-           : type == ABG_SB_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[at])
-                                 : __half2float(static_cast<const __half *>(p)[at]);
-}
 
 // E columns from `at` on of y, of the sums v and the weight l (attn_finish of E columns
 // a lane); all lanes call it, `mine` says which write.
