@@ -26,9 +26,12 @@ constexpr float kLargestHalf = 65504.0f;
 // group) in all 16 lanes' both chunks, and its least and largest value meet by
 // shuffles; the lanes then quantise and pack their own columns.  A warp's next rows and
 // rotations come to shared memory by cp.async meanwhile, each lane's own.  Instructions
-// bound it, and their latency: 8191 tokens of 16 + 4 + 4 heads of 128 columns, f32 to 4
-// bits, with q in bf16, in 30.9 us (139 MB, 4.5 TB/s; kv_put to bf16 33); with 8 heads a warp,
-// for which two blocks an SM have registers, 31.2, with four blocks, which spill, 33.5.
+// and their latency bound it alike: 8191 tokens of 16 + 4 + 4 heads of 128 columns, f32 to 4
+// bits, with q in bf16, in 30.9 us (143 MB, 4.6 TB/s; kv_put to bf16 33) and 25.9 M warp
+// instructions; with 8 heads a warp, for which two blocks an SM have registers, 20.3 M in
+// 31.2, with four blocks, which spill, 33.5.  (Of f32 rows of 256 columns the ring has room
+// for two of the three blocks: 8 + 2 + 2 heads 46.0 us, 45.1 compiled for two, q in f32 53.0
+// either way; of bf16 rows 26.5 for three, 26.8 for two.)
 // Loaded only when their turn came the rows took 38, with heads' places and 64-bit
 // divisions for each token 34.6.  Calls so short that no warp has a second unit take two
 // heads a warp and load them to registers: 8 tokens of 8 + 2 + 2 heads of 256 columns 3.0 us

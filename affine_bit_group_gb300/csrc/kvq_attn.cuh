@@ -40,7 +40,7 @@
 // copies, behind which it would wait.
 //
 // What bounds it.  64 requests of up to 16000 tokens, 16 heads over 4 of 128 columns, 4
-// bits, take 101 us for 441 MB (4.4 TB/s): copies alone take about 70, the rest without
+// bits, take 102 us for 441 MB (4.3 TB/s): copies alone take about 70, the rest without
 // copies about 75, with 600 instructions a warp for 32 tokens, half of them for taking the
 // codes apart, and no one of them that shortens the call by more than 6 us when it is left
 // out; launches, the joining and two beginnings and ends a block are 15 of it.  In 8 bits 48
@@ -99,10 +99,23 @@ struct KvqShape {
     static constexpr int kSteps = D / 16;                 // products of 16 columns
     static constexpr int kWords = kGroup * kBits / 128;   // words of a group in a lane
     // Blocks an SM.  The sums take kNT * D / 4 registers of a lane; up to 32, two blocks of
-    // 128 registers that go through 16 tokens at a time do more than one that goes through
-    // 32 (64 requests, 128 columns, 4 bits: 100.9 us for 104.5; 16 rows of 64 columns 47.7
-    // for 49.6), and more than two that go through 32 and spill (103.3; 85.5 for 74.8 in
-    // groups of 32).  With 64, two would spill, and 12 warps of 168 registers do no more.
+    // 128 registers that go through 16 tokens at a time stand against one of up to 255 that
+    // goes through 32.  64 requests of 8000 tokens, us of two and of one, bf16 / f32 queries:
+    //   64 columns,  8 rows, 4 bits, groups of 64    78 and 102 / 108 and 129
+    //                                groups of 32    86 and 105 / 123 and 141
+    //                        8 bits, groups of 64    98 and 122 / 119 and 145
+    //                                groups of 32   101 and 121 / 132 and 151
+    //   64 columns, 16 rows, 4 bits, groups of 64   137 and 141 / 185 and 168
+    //                                groups of 32   178 and 151 / 230 and 196
+    //                        8 bits, groups of 64   148 and 162 / 200 and 188
+    //                                groups of 32   212 and 171 / 247 and 209
+    //   128 columns, 8 rows, 4 bits, groups of 64    74 and  75 / 106 and 107
+    //                                groups of 32    86 and  86 / 122 and 122
+    // The 16-row shapes of 64 columns spill 84 to 344 bytes a thread in two blocks, and only
+    // bf16 in groups of 64 gains by them all the same; those of 128 columns spill 60 to 140.
+    // Two blocks that go through 32 tokens at a time spill more (128 columns, bf16, groups of
+    // 64: 103 us for 101; of 32: 86 for 75).  With 64 registers of sums, two blocks would spill
+    // all the more, and 12 warps of 168 registers do no more.
     static constexpr int kBlocks = kNT * D / 4 <= 32 && kRB <= 64 ? 2 : 1;
     static constexpr int kMP = kBlocks == 2 ? 1 : kMT;    // 16-token tiles of a block side by side
     static constexpr int kWarps = 8, kThreads = 32 * kWarps;

@@ -724,8 +724,9 @@ typedef struct abg_kvq_cache {
  *     code  = clamp(rint((x - bias) * (1 / scale)), 0, 2^bits - 1), 0 where
  *             scale is 0.
  *   A value is off by at most half a scale, the bias's rounding and 2^-11 of the
- * group's range (or (2^bits - 1)*2^-25, where the scale is below 2^-14).  A group with a NaN or a magnitude above 65504 (f16's
- * largest) is held as NaN: scale and bias are 0x7fff, the codes 0.
+ * group's range (or (2^bits - 1)*2^-25, where the scale is below 2^-14).  A group
+ * with a NaN or a magnitude above 65504 (f16's largest) is held as NaN: scale and
+ * bias are 0x7fff, the codes 0.
  * The codes and factors are exact: they are the same on every run, and those of
  * these steps done one by one in any IEEE binary32 arithmetic (of zeros of both
  * signs -0 is the least).
@@ -781,10 +782,16 @@ abg_status abg_kvq_get(const abg_kvq_get_args *a, void *stream);
  * power of two: 16-bit q as it is (elements below 2^-23 of the row's largest lose
  * bits), f32 q to 22 bits (of elements below 2^-12 of the largest: to 2^-34 of
  * that).  The weights p*scale that meet V's codes are rounded to 11 bits for
- * bf16, to 22 bits for f16 and f32, the smallest of either to 2^-38 of the
- * largest scale in V.  The tensor cores cut the sums of a block's products (up to
+ * bf16 (whatever y's type), to 22 bits for f16 and f32, the smallest of either to
+ * 2^-38 of the largest scale in V.  The tensor cores cut the sums of a block's products (up to
  * 32 tokens, 64 columns) off at about 2^-17 of the largest for bf16, at 2^-23 for
  * f16 and f32.  Drafts are multiplied in f32.
+ *   The time grows with a request and head's rows (its span times Hq/Hkv): each 16
+ * (8 at D = 256) go through the cache and its codes once more.  For bf16 and f16
+ * queries it is shorter than abg_tree_attn's over the same rows in 16 bits up to 16
+ * rows (8 at D = 256; 16 rows of f16 over 8 bits: as long) and longer from 32 on,
+ * several times at 64 and more; for f32 ones it is a quarter to half of
+ * abg_tree_attn's, and as much for a span of 256 over a few thousand tokens.
  * ws: abg_kvq_attn_workspace() bytes, as tree_attn's.
  */
 typedef struct abg_kvq_attn_args {
